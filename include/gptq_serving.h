@@ -1,0 +1,66 @@
+/*
+ * gptq_serving.h - C ABI of the serving operators around the product on stored codes
+ * (AMD Instinct MI355X, gfx950).
+ *
+ * gptq.h makes a layer's codes, scales and zeros and holds the plain product on them
+ * (gptq_quantized_linear).  The operators here stand next to that product when such
+ * layers are served: the norm that feeds it with 8-bit rows, the product on 8-bit rows,
+ * the product with low-rank adapters of many requests beside it, and a whole
+ * mixture-of-experts layer whose experts are stored layers.
+ *
+ * Conventions: those of gptq.h (device pointers unless said otherwise, caller-owned
+ * buffers and workspaces, row-major matrices, all work enqueued on `stream` of the
+ * current device, nothing allocated, no synchronization, argument errors returned before
+ * anything is enqueued).  Every call can be captured into a graph.  No call uses
+ * atomics on results, so equal calls give equal bits.  Calls that may overlap in time
+ * must not share outputs or workspaces; graphs that share a workspace must not be
+ * replayed at the same time.  Rows need no alignment; pitches are in elements.
+ */
+#ifndef GPTQ_SERVING_MI355X_H
+#define GPTQ_SERVING_MI355X_H
+
+#include "gptq.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * RMS norm with the residual's addition, written as 8-bit rows with one scale each.
+ * For every row, with T = x_dtype:
+ *     h     = T(x + residual)                (h = x without a residual)
+ *     p_c   = h_c weight_c,  rstd = 1 / sqrt(mean_c h_c^2 + eps)
+ *     am    = max_c |p_c|
+ *     q_c   = 127 p_c / am rounded to nearest, ties to even
+ *     scale = am rstd / 127                  (fp32; 1 when am = 0, and then q = 0)
+ * so q_c scale is the normalised value p_c rstd to within half a scale.  rstd cancels
+ * from q: for 16-bit x the codes are the exact roundings for these inputs, whatever the
+ * order of the sum (fp32 x: of a quotient in 64 bits).  The squares are summed in 64
+ * bits.  A row with an infinity or a NaN among its p gets q = 0 and scale = NaN, so that
+ * a product on it gives NaN.
+ *
+ *  x             n_tokens x d, pitch ldx >= d, dtype x_dtype
+ *  residual      NULL, or n_tokens x d, pitch ld_residual, dtype x_dtype
+ *  weight        d values, dtype w_dtype: x_dtype or GPTQ_F32
+ *  residual_out  NULL, or n_tokens x d, pitch ld_residual_out, dtype x_dtype: h
+ *  normed        NULL, or n_tokens x d, pitch ld_normed, dtype x_dtype: T(p_c rstd)
+ *  q             n_tokens x d int8, pitch ldq
+ *  scale         n_tokens fp32
+ * residual_out and normed may each be the buffer of x or of residual with its pitch (not
+ * both the same one); no other outputs and inputs may overlap.
+ * Errors: negative sizes, a pitch below d, eps negative or NaN, a bad dtype, a NULL
+ * needed pointer -> GPTQ_ERR_INVALID_ARG; n_tokens > 65535 * 64 = 4194240 or
+ * d > 2^30 -> GPTQ_ERR_UNSUPPORTED.  n_tokens == 0 or d == 0 is a no-op.
+ */
+gptq_status gptqs_rmsnorm_int8(const void* x, gptq_dtype x_dtype, int64_t ldx,
+                               const void* residual, int64_t ld_residual,
+                               const void* weight, gptq_dtype w_dtype, float eps,
+                               int64_t n_tokens, int64_t d,
+                               void* residual_out, int64_t ld_residual_out,
+                               void* normed, int64_t ld_normed,
+                               int8_t* q, int64_t ldq, float* scale, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* GPTQ_SERVING_MI355X_H */

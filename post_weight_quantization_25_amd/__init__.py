@@ -74,6 +74,9 @@ def _load():
         "gptq_quantized_linear": (ctypes.c_int, [vp, vp, vp, i64, i64, i32, i32, vp, ctypes.c_int, i64, i64,
                                                  vp, ctypes.c_int, vp]),
         "gptq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
+        # include/gptq_serving.h
+        "gptqs_rmsnorm_int8": (ctypes.c_int, [vp, ctypes.c_int, i64, vp, i64, vp, ctypes.c_int, ctypes.c_float, i64,
+                                              i64, vp, i64, vp, i64, vp, i64, vp, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -486,3 +489,6 @@ def check_info(info: torch.Tensor, what: str = "gptq"):
                                  "expired (device overloaded or preempted); results are undefined")
     if v < 0:
         raise GptqError(ERR_NONFINITE, f"{what}: {status_string(ERR_NONFINITE)}")
+
+
+from .serving import Int8Rows, rmsnorm_int8  # noqa: E402,F401  (uses the names above)

@@ -1,0 +1,27 @@
+// Host-side launchers of the serving operators (internal to the library).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gptq_serving.h"
+
+namespace gptq {
+
+// Most tokens of a call: their tiles are on the grid's y extent (at most 65535 tiles of 64),
+// and one 1024-thread workgroup per token stays below 2^32 threads.
+constexpr int64_t SERVE_MAX_TOKENS = (int64_t)65535 * 64;
+
+struct NormArgs {
+    const void* x; int64_t ldx;
+    const void* r; int64_t ldr;          // residual, or nullptr
+    const void* w;
+    float eps;
+    int64_t n, d;
+    void* h; int64_t ldh;                // T(x + r), or nullptr
+    void* y; int64_t ldy;                // T(p rstd), or nullptr
+    int8_t* q; int64_t ldq;
+    float* scale;
+};
+gptq_status norm_launch(const NormArgs& a, gptq_dtype xt, gptq_dtype wt, hipStream_t s);
+
+}  // namespace gptq

@@ -1,0 +1,107 @@
+"""The serving operators (C ABI in ``include/gptq_serving.h``): the norm that writes 8-bit
+rows, the product on stored codes with 8-bit rows, the product with low-rank adapters
+beside it, and a mixture-of-experts layer on stored codes.
+
+Argument checks and marshalling only, as in the package's module.  Work is queued on
+``stream`` (default: the current stream of the operands' device, which need not be the
+current device); buffers made here are allocated on that stream.
+"""
+from __future__ import annotations
+
+from dataclasses import dataclass
+
+import torch
+
+from . import _DT, _check, _tensor, lib
+
+
+class _On:
+    """The operands' device made current and ``stream`` made the current stream, where they
+    are not already; gives the stream's handle."""
+
+    def __init__(self, device, stream):
+        self._inner = []
+        if device.index != torch.cuda.current_device():
+            self._inner.append(torch.cuda.device(device))
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, the operands on {device}")
+            self._inner.append(torch.cuda.stream(stream))
+        self._device = device
+
+    def __enter__(self):
+        for c in self._inner:
+            c.__enter__()
+        return torch.cuda.current_stream(self._device).cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self._inner):
+            c.__exit__(*exc)
+
+
+def _rows(t: torch.Tensor, name: str, dtype=None, shape=None, device=None) -> int:
+    """A 2-D device tensor of rows with unit column stride; its row pitch in elements."""
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D device tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must have dtype {dtype}, not {t.dtype}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other operands on {device}")
+    n, d = t.shape
+    s0, s1 = t.stride()
+    if n == 0 or d == 0:
+        return d
+    if (s1 != 1 and d > 1) or (s0 < d and n > 1):
+        raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
+    return max(s0, d)
+
+
+@dataclass
+class Int8Rows:
+    """Rows of 8-bit codes with one scale each: row t stands for q[t] * scale[t]."""
+    q: torch.Tensor          # int8, n_tokens x d (rows may be strided)
+    scale: torch.Tensor      # float32, n_tokens
+
+
+def rmsnorm_int8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
+                 residual_out: torch.Tensor | None = None, normed: torch.Tensor | None = None,
+                 out: Int8Rows | None = None, stream=None):
+    """h = x + residual; RMS norm of h times ``weight``, as 8-bit rows (gptqs_rmsnorm_int8).
+    Returns (Int8Rows, h); h is x itself without a residual, else ``residual_out`` (made
+    here when not given; it may be ``residual`` or ``x``).  ``normed``: a buffer of x's
+    dtype that also receives the normalised rows (it may be ``x`` or ``residual``, not
+    ``residual_out``).  Rows may be strided."""
+    if x.dtype not in _DT:
+        raise ValueError("x must be f32/bf16/f16")
+    dev, dt = x.device, x.dtype
+    ldx = _rows(x, "x")
+    shape = n, d = tuple(x.shape)
+    _tensor(weight, "weight", (dt, torch.float32), (d,), dev)
+    ldr = 0 if residual is None else _rows(residual, "residual", dt, shape, dev)
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    if normed is not None:
+        ldn = _rows(normed, "normed", dt, shape, dev)
+        if residual_out is not None and normed.data_ptr() == residual_out.data_ptr() and n and d:
+            raise ValueError("normed and residual_out must be different buffers")
+    with _On(dev, stream) as s:
+        if residual is not None and residual_out is None:
+            residual_out = torch.empty(shape, dtype=dt, device=dev)
+        ldo = 0 if residual_out is None else _rows(residual_out, "residual_out", dt, shape, dev)
+        for o, ldo_, name in ((residual_out, ldo, "residual_out"), (normed, 0 if normed is None else ldn, "normed")):
+            for i, ldi in ((x, ldx), (residual, ldr)):
+                if o is not None and i is not None and o.data_ptr() == i.data_ptr() and ldo_ != ldi and n > 1:
+                    raise ValueError(f"{name} shares a buffer with an input of another row pitch")
+        if out is None:
+            out = Int8Rows(torch.empty(shape, dtype=torch.int8, device=dev),
+                           torch.empty(n, dtype=torch.float32, device=dev))
+        ldq = _rows(out.q, "out.q", torch.int8, shape, dev)
+        _tensor(out.scale, "out.scale", torch.float32, (n,), dev)
+        _check(lib.gptqs_rmsnorm_int8(
+            x.data_ptr(), _DT[dt], ldx, None if residual is None else residual.data_ptr(), ldr, weight.data_ptr(),
+            _DT[weight.dtype], eps, n, d, None if residual_out is None else residual_out.data_ptr(), ldo,
+            None if normed is None else normed.data_ptr(), 0 if normed is None else ldn, out.q.data_ptr(), ldq,
+            out.scale.data_ptr(), s), "gptqs_rmsnorm_int8")
+    return out, (x if residual is None else residual_out)
