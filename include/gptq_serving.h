@@ -60,6 +60,25 @@ gptq_status gptqs_rmsnorm_int8(const void* x, gptq_dtype x_dtype, int64_t ldx,
                                void* normed, int64_t ld_normed,
                                int8_t* q, int64_t ldq, float* scale, void* stream);
 
+/*
+ * The product on stored codes with 8-bit rows:
+ *   y[t][r] = x_scale[t] sum_g S16[r][g] sum_{c in g} xq[t][c] (u[r][c] - z[r][g]).
+ * The products run on the int8 matrix cores: u - z (u - 128 for 8-bit codes) is taken in
+ * 8 bits with z rounded to a whole number in [-112, 127], and what that leaves of z
+ * enters as (the rest) * sum_c xq; integer sums are exact, groups are added in fp32.
+ *
+ *  codes, scales_f16, zeros_f16   as for gptq_quantized_linear: bits 3, 4 or 8,
+ *             group_size 32, 64, 128, 0 (per row) or -1 (per tensor, as 0).
+ *  xq         n_tokens x d_col int8 (values -128 .. 127), pitch ldx >= d_col.
+ *  x_scale    n_tokens fp32.
+ *  y          n_tokens x d_row, pitch d_row, dtype y_dtype; written, not read.
+ * Errors: as gptq_quantized_linear; another group_size -> GPTQ_ERR_UNSUPPORTED.
+ */
+gptq_status gptqs_linear_int8(const uint8_t* codes, const uint16_t* scales_f16, const uint16_t* zeros_f16,
+                              int64_t d_row, int64_t d_col, int32_t bits, int32_t group_size,
+                              const int8_t* xq, int64_t ldx, const float* x_scale, int64_t n_tokens,
+                              void* y, gptq_dtype y_dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

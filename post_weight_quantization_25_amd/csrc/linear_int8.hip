@@ -1,0 +1,90 @@
+// The product on stored codes with 8-bit rows (gptqs_linear_int8):
+//   y[t][r] = xs[t] sum_g S[r][g] sum_{c in g} xq[t][c] (u[r][c] - z[r][g]),
+// integer products on v_mfma_i32_16x16x64_i8 (exact), groups added in fp32.
+//
+// Small batches (tile_kernel): bound by the codes' bytes and, at one token, by the latency
+// of one round trip.  A workgroup of 8 waves owns 16 RB rows and 16 NTT tokens; its waves
+// take the rows' 128-column chunks in turn and meet in LDS at the end.
+
+#include "serving.h"
+#include "stored_tile.h"
+
+namespace gptq {
+
+constexpr int TW = 8;    // waves per workgroup
+
+struct Int8Args {
+    Stored L; int64_t d_row;
+    const int8_t* x; int64_t ldx; int64_t n;
+    const float* xs;
+    void* y; gptq_dtype yt;
+};
+
+template <int CB, int RUN, int NTT, int RB>
+__global__ __launch_bounds__(64 * TW) void int8_tile_kernel(Int8Args a) {
+    constexpr int CPW = NTT == 1 ? 2 : 1;
+    __shared__ float red[TW][NTT * RB][4][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15;
+    const int64_t row0 = (int64_t)blockIdx.x * 16 * RB, tok0 = (int64_t)blockIdx.y * 16 * NTT;
+    int64_t row[RB];
+    const uint8_t* xrow[NTT];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+        const int64_t r = row0 + 16 * rb + n16;
+        row[rb] = r < a.d_row ? r : a.d_row - 1;                 // rows past the end re-read the last
+    }
+#pragma unroll
+    for (int tt = 0; tt < NTT; ++tt) {
+        int64_t t = tok0 + 16 * tt + n16;
+        t = t < a.n ? t : a.n - 1;                               // a repeated token past the end
+        xrow[tt] = reinterpret_cast<const uint8_t*>(a.x) + t * a.ldx;
+    }
+    f32x4_t acc[NTT][RB];
+#pragma unroll
+    for (int tt = 0; tt < NTT; ++tt)
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) acc[tt][rb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    stored_accumulate<X_I8, CB, RUN, NTT, RB, CPW>(acc, a.L, row, xrow, wave, TW, (int)((a.L.d_col + SCK - 1) / SCK));
+#pragma unroll
+    for (int tt = 0; tt < NTT; ++tt)
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) red[wave][tt * RB + rb][i][lane] = acc[tt][rb][i];
+    __syncthreads();
+    for (int o = threadIdx.x; o < NTT * RB * 256; o += 64 * TW) {
+        const int tr = o >> 8, m = (o >> 4) & 15, n = o & 15, tt = tr / RB, rb = tr % RB;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < TW; ++w) v += red[w][tr][m & 3][n + 16 * (m >> 2)];
+        const int64_t t = tok0 + 16 * tt + m, r = row0 + 16 * rb + n;
+        if (t < a.n && r < a.d_row) store_out(a.y, a.yt, t * a.d_row + r, a.xs[t] * v);
+    }
+}
+
+template <int CB, int RUN>
+static gptq_status launch(const Int8Args& a, hipStream_t s) {
+    const unsigned g16 = (unsigned)((a.d_row + 15) / 16), g32 = (unsigned)((a.d_row + 31) / 32);
+    auto tiles = [&](int per) { return (unsigned)((a.n + per - 1) / per); };
+    if (a.n <= 16) int8_tile_kernel<CB, RUN, 1, 1><<<dim3(g16, 1), 64 * TW, 0, s>>>(a);
+    else if (a.n <= 32) int8_tile_kernel<CB, RUN, 2, 1><<<dim3(g16, 1), 64 * TW, 0, s>>>(a);
+    else int8_tile_kernel<CB, RUN, 4, 2><<<dim3(g32, tiles(64)), 64 * TW, 0, s>>>(a);
+    GPTQ_LAUNCH_CHECK();
+    return GPTQ_OK;
+}
+
+template <int CB>
+static gptq_status launch_runs(const Int8Args& a, int group, hipStream_t s) {
+    return group == 32 ? launch<CB, 8>(a, s) : group == 64 ? launch<CB, 16>(a, s) : launch<CB, 32>(a, s);
+}
+
+gptq_status linear_int8_launch(const uint8_t* codes, const uint16_t* scales, const uint16_t* zeros, int64_t d_row,
+                               int64_t d_col, int bits, int group, const int8_t* x, int64_t ldx, const float* xs,
+                               int64_t n, void* y, gptq_dtype yt, hipStream_t s) {
+    Int8Args a;
+    a.L = stored_layer(codes, scales, zeros, d_col, bits, group);
+    a.d_row = d_row; a.x = x; a.ldx = ldx; a.n = n; a.xs = xs; a.y = y; a.yt = yt;
+    return bits == 3 ? launch_runs<3>(a, group, s) : bits == 4 ? launch_runs<4>(a, group, s) : launch_runs<8>(a, group, s);
+}
+
+}  // namespace gptq

@@ -24,4 +24,8 @@ struct NormArgs {
 };
 gptq_status norm_launch(const NormArgs& a, gptq_dtype xt, gptq_dtype wt, hipStream_t s);
 
+gptq_status linear_int8_launch(const uint8_t* codes, const uint16_t* scales, const uint16_t* zeros, int64_t d_row,
+                               int64_t d_col, int bits, int group, const int8_t* x, int64_t ldx, const float* xs,
+                               int64_t n, void* y, gptq_dtype yt, hipStream_t s);
+
 }  // namespace gptq

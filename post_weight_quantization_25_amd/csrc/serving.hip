@@ -8,6 +8,18 @@ using namespace gptq;
 
 static bool valid_dtype(gptq_dtype t) { return t == GPTQ_F32 || t == GPTQ_BF16 || t == GPTQ_F16; }
 
+// Settings of a stored layer that the serving products take; group -1 (per tensor) becomes 0.
+static gptq_status check_stored(int64_t d_col, int32_t bits, int32_t& group) {
+    if (group == -1) group = 0;
+    if (group < 0) return GPTQ_ERR_INVALID_ARG;
+    if (bits != 3 && bits != 4 && bits != 8) return GPTQ_ERR_UNSUPPORTED;
+    if (group > 0 && d_col % group != 0) return GPTQ_ERR_INVALID_ARG;
+    if (group != 0 && group != 32 && group != 64 && group != 128) return GPTQ_ERR_UNSUPPORTED;
+    if (bits <= 4 && (d_col & 1)) return GPTQ_ERR_INVALID_ARG;
+    if (bits == 3 && (d_col & 7)) return GPTQ_ERR_INVALID_ARG;
+    return GPTQ_OK;
+}
+
 #pragma GCC visibility push(default)
 extern "C" {
 
@@ -28,6 +40,21 @@ gptq_status gptqs_rmsnorm_int8(const void* x, gptq_dtype x_dtype, int64_t ldx, c
     a.n = n_tokens; a.d = d; a.h = residual_out; a.ldh = ld_residual_out; a.y = normed; a.ldy = ld_normed;
     a.q = q; a.ldq = ldq; a.scale = scale;
     return norm_launch(a, x_dtype, w_dtype, (hipStream_t)stream);
+}
+
+gptq_status gptqs_linear_int8(const uint8_t* codes, const uint16_t* scales_f16, const uint16_t* zeros_f16,
+                              int64_t d_row, int64_t d_col, int32_t bits, int32_t group_size, const int8_t* xq,
+                              int64_t ldx, const float* x_scale, int64_t n_tokens, void* y, gptq_dtype y_dtype,
+                              void* stream) {
+    if (d_row < 0 || d_col < 0 || n_tokens < 0 || !valid_dtype(y_dtype)) return GPTQ_ERR_INVALID_ARG;
+    const gptq_status st = check_stored(d_col, bits, group_size);
+    if (st != GPTQ_OK) return st;
+    if (d_row == 0 || d_col == 0 || n_tokens == 0) return GPTQ_OK;
+    if (!codes || !scales_f16 || !zeros_f16 || !xq || !x_scale || !y || ldx < d_col) return GPTQ_ERR_INVALID_ARG;
+    if (d_row > 2147483647LL / 64 || d_col > 2147483647LL / 64 || n_tokens > SERVE_MAX_TOKENS)
+        return GPTQ_ERR_UNSUPPORTED;
+    return linear_int8_launch(codes, scales_f16, zeros_f16, d_row, d_col, bits, group_size, xq, ldx, x_scale, n_tokens,
+                              y, y_dtype, (hipStream_t)stream);
 }
 
 }  // extern "C"

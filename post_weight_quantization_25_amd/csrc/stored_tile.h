@@ -1,0 +1,302 @@
+// Products of 16-token tiles with 16-row blocks of a stored layer on the matrix cores,
+// shared by the serving kernels (8-bit and 16-bit activations).
+//
+// A chunk is 128 columns of a row.  A piece is the part of a chunk that has one scale:
+// 128 columns (groups of whole chunks, or one scale per row), 64 or 32.  Lane l of a wave
+// holds, of every piece, the RUN = piece / 4 columns RUN (l / 16) .. + RUN - 1 of weight
+// row l % 16 and of token l % 16, so that each column of the piece enters one product
+// once; which k a column has inside a product is the same on both sides and changes
+// nothing else.  The sums of a piece (exact integers for 8-bit activations) are scaled by
+// S and added in fp32.
+//
+// Zeros: the operand is u - zc with zc = z rounded to a whole number and clamped so that
+// u - zc is exact in the operand's type (8 bits: u - 128 for 8-bit codes, zc in -112 ..
+// 127 for narrower ones; 16 bits: |u - zc| <= 256).  z - zc is 0 for the quantizer's usual
+// zeros; where it is not, (z - zc) sum x is taken off the piece, with sum x from a product
+// of the same activations with ones, so every zero is served with exact operands.
+#pragma once
+#include "common.h"
+
+namespace gptq {
+
+constexpr int SCK = 128;                      // columns per chunk
+constexpr int X_I8 = 0, X_BF16 = 1, X_F16 = 2;
+
+typedef int32_t i32x4_t __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+
+template <int X> constexpr int xbytes() { return X == X_I8 ? 1 : 2; }
+
+// ---- codes of RUN consecutive columns, as stored
+template <int CB, int RUN>
+struct Raw { uint32_t w[(CB * RUN + 31) / 32]; };
+
+template <int CB, int RUN>
+GPTQ_DEV Raw<CB, RUN> load_raw(const uint8_t* p) {    // any alignment
+    Raw<CB, RUN> r;
+    r.w[(CB * RUN + 31) / 32 - 1] = 0;
+    __builtin_memcpy(r.w, p, CB * RUN / 8);
+    return r;
+}
+
+// The first n of RUN columns (the others 0); n <= 0 reads nothing.
+template <int CB, int RUN>
+GPTQ_DEV Raw<CB, RUN> load_raw_tail(const uint8_t* p, int n) {
+    Raw<CB, RUN> r;
+#pragma unroll
+    for (int i = 0; i < (CB * RUN + 31) / 32; ++i) r.w[i] = 0;
+    const int nb = n > 0 ? (n * CB + 7) / 8 : 0;
+#pragma unroll
+    for (int i = 0; i < CB * RUN / 8; ++i)
+        if (i < nb) r.w[i / 4] |= (uint32_t)p[i] << (8 * (i & 3));
+    return r;
+}
+
+// Columns 4 j .. 4 j + 3 as unsigned bytes.
+template <int CB, int RUN>
+GPTQ_DEV uint32_t code_bytes4(const Raw<CB, RUN>& r, int j) {
+    if constexpr (CB == 8) {
+        return r.w[j];
+    } else if constexpr (CB == 4) {
+        const uint32_t w = r.w[j >> 1], lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
+        return __builtin_amdgcn_perm(hi, lo, (j & 1) ? 0x07030602u : 0x05010400u);
+    } else {
+        const int bit = 12 * j, k = bit >> 5, sh = bit & 31;
+        uint32_t x = r.w[k] >> sh;
+        if (sh > 20) x |= r.w[k + 1] << (32 - sh);
+        x &= 0xFFFu;
+        x = (x | (x << 10)) & 0x003F003Fu;
+        return (x | (x << 5)) & 0x07070707u;
+    }
+}
+
+// The whole-number part of a zero that the operand takes, and as the decoders use it.
+template <int X, int CB>
+GPTQ_DEV float zero_part(float z) {
+    if constexpr (X == X_I8) return CB == 8 ? 128.f : fminf(fmaxf(rintf(z), -112.f), 127.f);
+    else return fminf(fmaxf(rintf(z), CB == 8 ? -1.f : -240.f), CB == 8 ? 255.f : 240.f);
+}
+
+// u - zc of four columns as signed bytes; zz = zc times 0x01010101.
+template <int CB>
+GPTQ_DEV uint32_t minus_zero_i8(uint32_t u4, uint32_t zz) {
+    if constexpr (CB == 8) return u4 ^ 0x80808080u;
+    else return ((u4 | 0x80808080u) - zz) ^ 0x80808080u;   // each byte 128 + u - zc in 0 .. 255: no borrow
+}
+
+// u - zc of four columns in a 16-bit type, two per word.
+template <int X>
+GPTQ_DEV void minus_zero_16(uint32_t u4, float zc, uint32_t (&o)[2]) {
+    if constexpr (X == X_F16) {
+        // 0x6400 | u is 1024 + u; 1024 + zc and the difference are whole numbers below 2048
+        const _Float16 s = (_Float16)(1024.f + zc);
+        const f16x2_t zz = {s, s};
+        o[0] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, __builtin_amdgcn_perm(0x64646464u, u4, 0x04010400u)) - zz);
+        o[1] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, __builtin_amdgcn_perm(0x64646464u, u4, 0x04030402u)) - zz);
+    } else {
+        const f32x2_t a = {(float)(u4 & 0xFFu) - zc, (float)((u4 >> 8) & 0xFFu) - zc};
+        const f32x2_t b = {(float)((u4 >> 16) & 0xFFu) - zc, (float)(u4 >> 24) - zc};
+        o[0] = __builtin_bit_cast(uint32_t, __builtin_convertvector(a, bf16x2_t));
+        o[1] = __builtin_bit_cast(uint32_t, __builtin_convertvector(b, bf16x2_t));
+    }
+}
+
+// ---- one product: 16-byte operands (8 bytes for 8-bit activations with 32-column pieces)
+template <int X> struct Acc { typedef f32x4_t t; };
+template <> struct Acc<X_I8> { typedef i32x4_t t; };
+
+template <int X>
+GPTQ_DEV typename Acc<X>::t mfma16(u32x4_t a, u32x4_t b, typename Acc<X>::t c) {
+    if constexpr (X == X_I8)
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, a), __builtin_bit_cast(i32x4_t, b), c, 0, 0, 0);
+    else if constexpr (X == X_BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+}
+
+GPTQ_DEV i32x4_t mfma8_i8(uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1, i32x4_t c) {
+    const long a = (long)(((uint64_t)a1 << 32) | a0), b = (long)(((uint64_t)b1 << 32) | b0);
+    return __builtin_amdgcn_mfma_i32_16x16x32_i8(a, b, c, 0, 0, 0);
+}
+
+template <int X>
+GPTQ_DEV constexpr uint32_t ones_word() { return X == X_I8 ? 0x01010101u : X == X_BF16 ? 0x3F803F80u : 0x3C003C00u; }
+
+// ---- activations of RUN columns
+template <int X, int RUN>
+struct XRun { uint32_t w[RUN * xbytes<X>() / 4]; };
+
+template <int X, int RUN>
+GPTQ_DEV XRun<X, RUN> load_x(const uint8_t* p) {
+    XRun<X, RUN> r;
+    __builtin_memcpy(r.w, p, RUN * xbytes<X>());
+    return r;
+}
+
+template <int X, int RUN>
+GPTQ_DEV XRun<X, RUN> load_x_tail(const uint8_t* p, int n) {   // zeros from column n on
+    XRun<X, RUN> r;
+#pragma unroll
+    for (int i = 0; i < RUN * xbytes<X>() / 4; ++i) r.w[i] = 0;
+    if constexpr (X == X_I8) {
+#pragma unroll
+        for (int i = 0; i < RUN; ++i)
+            if (i < n) r.w[i / 4] |= (uint32_t)p[i] << (8 * (i & 3));
+    } else {
+#pragma unroll
+        for (int i = 0; i < RUN; ++i)
+            if (i < n) r.w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
+    }
+    return r;
+}
+
+// The stored layer as the kernels take it.
+struct Stored {
+    const uint8_t* codes; int64_t code_ld;             // bytes per row
+    const uint16_t* scales; const uint16_t* zeros;     // fp16, rows x n_groups
+    int64_t d_col;
+    int n_groups, cpg;                                 // cpg: chunks per group (128-column pieces)
+};
+
+// Sums of RB blocks of 16 weight rows with NTT tiles of 16 tokens over the chunks c0, c0 +
+// step, .. below nck: acc[tt][rb], lane l's value i the output of weight row l % 16 and
+// token 4 (l / 16) + i.  row[rb]: the lane's weight row; xrow[tt]: the lane's token's
+// first element.  CPW chunks are loaded before their arithmetic begins.
+template <int X, int CB, int RUN, int NTT, int RB, int CPW>
+GPTQ_DEV void stored_accumulate(f32x4_t (&acc)[NTT][RB], const Stored& L, const int64_t (&row)[RB],
+                                const uint8_t* const (&xrow)[NTT], int c0, int step, int nck) {
+    constexpr int P = 32 / RUN;               // pieces per chunk
+    constexpr int XB = xbytes<X>();
+    const int q = (threadIdx.x & 63) >> 4;
+    for (int cb = c0; cb < nck; cb += step * CPW) {
+        Raw<CB, RUN> cw[CPW][RB][P];
+        XRun<X, RUN> xw[CPW][NTT][P];
+        uint16_t S16[CPW][RB][P], Z16[CPW][RB][P];
+#pragma unroll
+        for (int j = 0; j < CPW; ++j) {
+            const int c = cb + step * j < nck ? cb + step * j : cb;   // chunks past the end re-read the first
+            const bool full = (int64_t)(c + 1) * SCK <= L.d_col;
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const int64_t col = (int64_t)c * SCK + p * 4 * RUN + q * RUN;
+                const int64_t left = L.d_col - col;
+                int g = RUN == 32 ? c / L.cpg : c * P + p;
+                g = g < L.n_groups ? g : L.n_groups - 1;
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb) {
+                    const uint8_t* src = L.codes + row[rb] * L.code_ld + col / 8 * CB;
+                    cw[j][rb][p] = full ? load_raw<CB, RUN>(src) : load_raw_tail<CB, RUN>(src, (int)(left < RUN ? left : RUN));
+                    S16[j][rb][p] = L.scales[row[rb] * L.n_groups + g];
+                    Z16[j][rb][p] = L.zeros[row[rb] * L.n_groups + g];
+                }
+#pragma unroll
+                for (int tt = 0; tt < NTT; ++tt) {
+                    const uint8_t* src = xrow[tt] + col * XB;
+                    xw[j][tt][p] = full ? load_x<X, RUN>(src) : load_x_tail<X, RUN>(src, (int)(left < RUN ? left : RUN));
+                }
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);    // keep every load above the arithmetic
+#pragma unroll
+        for (int j = 0; j < CPW; ++j) {
+            if (cb + step * j >= nck) break;  // wave-uniform
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb) {
+                    const float S = f16_bits_to_f32(S16[j][rb][p]), z = f16_bits_to_f32(Z16[j][rb][p]);
+                    const float zc = zero_part<X, CB>(z), rz = z - zc;
+                    typedef typename Acc<X>::t sum_t;
+                    // sum x where some zero has a rest, as fp32; a block of its own, with no
+                    // branch between a product and the reads of its result: this compiler
+                    // counts the wait that such a read needs along one of the two paths
+                    float xs[NTT][4];
+#pragma unroll
+                    for (int tt = 0; tt < NTT; ++tt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) xs[tt][i] = 0.f;
+                    if (__ballot(!(rz == 0.f)) != 0) {
+                        const uint32_t w1 = ones_word<X>();
+                        sum_t s[NTT];
+#pragma unroll
+                        for (int tt = 0; tt < NTT; ++tt) {
+                            s[tt] = sum_t{0, 0, 0, 0};
+                            const uint32_t* a = xw[j][tt][p].w;
+                            if constexpr (X == X_I8 && RUN == 8) {
+                                s[tt] = mfma8_i8(a[0], a[1], w1, w1, s[tt]);
+                            } else {
+#pragma unroll
+                                for (int t = 0; t < RUN * xbytes<X>() / 16; ++t)
+                                    s[tt] = mfma16<X>(u32x4_t{a[4 * t], a[4 * t + 1], a[4 * t + 2], a[4 * t + 3]},
+                                                      u32x4_t{w1, w1, w1, w1}, s[tt]);
+                            }
+                        }
+#pragma unroll
+                        for (int tt = 0; tt < NTT; ++tt)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) xs[tt][i] = (float)s[tt][i];
+                    }
+                    sum_t cs[NTT];
+#pragma unroll
+                    for (int tt = 0; tt < NTT; ++tt) cs[tt] = sum_t{0, 0, 0, 0};
+                    if constexpr (X == X_I8 && RUN == 8) {
+                        const uint32_t zz = (uint32_t)((int)zc * 0x01010101);
+                        const uint32_t b0 = minus_zero_i8<CB>(code_bytes4<CB, RUN>(cw[j][rb][p], 0), zz);
+                        const uint32_t b1 = minus_zero_i8<CB>(code_bytes4<CB, RUN>(cw[j][rb][p], 1), zz);
+#pragma unroll
+                        for (int tt = 0; tt < NTT; ++tt) cs[tt] = mfma8_i8(xw[j][tt][p].w[0], xw[j][tt][p].w[1], b0, b1, cs[tt]);
+                    } else {
+#pragma unroll
+                        for (int t = 0; t < RUN * xbytes<X>() / 16; ++t) {
+                            u32x4_t b;
+                            if constexpr (X == X_I8) {
+                                const uint32_t zz = (uint32_t)((int)zc * 0x01010101);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    b[e] = minus_zero_i8<CB>(code_bytes4<CB, RUN>(cw[j][rb][p], 4 * t + e), zz);
+                            } else {
+                                uint32_t lo[2], hi[2];
+                                minus_zero_16<X>(code_bytes4<CB, RUN>(cw[j][rb][p], 2 * t), zc, lo);
+                                minus_zero_16<X>(code_bytes4<CB, RUN>(cw[j][rb][p], 2 * t + 1), zc, hi);
+                                b = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+                            }
+#pragma unroll
+                            for (int tt = 0; tt < NTT; ++tt) {
+                                const uint32_t* a = xw[j][tt][p].w + 4 * t;
+                                cs[tt] = mfma16<X>(u32x4_t{a[0], a[1], a[2], a[3]}, b, cs[tt]);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int tt = 0; tt < NTT; ++tt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            acc[tt][rb][i] = fmaf(S, fmaf(-rz, xs[tt][i], (float)cs[tt][i]), acc[tt][rb][i]);
+                }
+            }
+        }
+    }
+}
+
+GPTQ_DEV void store_out(void* y, gptq_dtype t, int64_t idx, float v) {
+    if (t == GPTQ_F32) reinterpret_cast<float*>(y)[idx] = v;
+    else if (t == GPTQ_BF16) reinterpret_cast<uint16_t*>(y)[idx] = f32_to_bf16_bits(v);
+    else reinterpret_cast<uint16_t*>(y)[idx] = f32_to_f16_bits(v);
+}
+
+// Host: the stored layer's layout; group 0 = one scale per row.
+inline Stored stored_layer(const uint8_t* codes, const uint16_t* scales, const uint16_t* zeros, int64_t d_col, int bits,
+                           int group) {
+    Stored L;
+    L.codes = codes; L.code_ld = bits == 3 ? d_col / 8 * 3 : bits == 4 ? d_col / 2 : d_col;
+    L.scales = scales; L.zeros = zeros; L.d_col = d_col;
+    L.n_groups = group > 0 ? (int)(d_col / group) : 1;
+    const int64_t nck = (d_col + SCK - 1) / SCK;
+    L.cpg = group > 0 ? 1 : (int)nck;      // of the 128-column pieces; groups are 128 or the row
+    return L;
+}
+
+}  // namespace gptq

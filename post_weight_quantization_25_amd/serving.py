@@ -12,7 +12,7 @@ from dataclasses import dataclass
 
 import torch
 
-from . import _DT, _check, _tensor, lib
+from . import _DT, Quantized, _check, _check_quantized, _dev, _tensor, lib
 
 
 class _On:
@@ -105,3 +105,41 @@ def rmsnorm_int8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor |
             None if normed is None else normed.data_ptr(), 0 if normed is None else ldn, out.q.data_ptr(), ldq,
             out.scale.data_ptr(), s), "gptqs_rmsnorm_int8")
     return out, (x if residual is None else residual_out)
+
+
+def _stored(q: Quantized, name: str, device) -> int:
+    """q is a layer on an integer grid with whole arrays on ``device``; its rows."""
+    if q.fp4:
+        raise ValueError(f"{name} is on the E2M1 grid; the products read integer-grid codes")
+    _dev(q.codes, f"{name}.codes")
+    d_row = q.codes.shape[0]
+    _check_quantized(q, name, d_row, device)
+    return d_row
+
+
+def _out(out, n: int, d_row: int, out_dtype, device):
+    if out is None:
+        if out_dtype not in _DT:
+            raise ValueError("out_dtype must be f32/bf16/f16")
+        return torch.empty((n, d_row), dtype=out_dtype, device=device)
+    _tensor(out, "out", tuple(_DT), (n, d_row), device)
+    return out
+
+
+def linear_int8(q: Quantized, x: Int8Rows, out_dtype=torch.float32, out: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """y = (x.q * x.scale) What^T on the stored format and the 8-bit rows (gptqs_linear_int8):
+    int8 products, exact integer sums per group, fp32 across groups.  x.q may be strided."""
+    dev = x.q.device
+    ldx = _rows(x.q, "x.q", torch.int8)
+    n, d_col = x.q.shape
+    if d_col != q.d_col:
+        raise ValueError(f"x.q has {d_col} columns, the layer {q.d_col}")
+    _tensor(x.scale, "x.scale", torch.float32, (n,), dev)
+    d_row = _stored(q, "q", dev)
+    with _On(dev, stream) as s:
+        out = _out(out, n, d_row, out_dtype, dev)
+        _check(lib.gptqs_linear_int8(q.codes.data_ptr(), q.scales.data_ptr(), q.zeros.data_ptr(), d_row, d_col, q.bits,
+                                     q.group_size, x.q.data_ptr(), ldx, x.scale.data_ptr(), n, out.data_ptr(),
+                                     _DT[out.dtype], s), "gptqs_linear_int8")
+    return out

@@ -21,6 +21,7 @@ vp, i64, i32, sz, dt = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c
 SIG = {
     "gptqs_rmsnorm_int8": (dt, [vp, dt, i64, vp, i64, vp, dt, ctypes.c_float, i64, i64, vp, i64, vp, i64, vp, i64, vp,
                                 vp]),
+    "gptqs_linear_int8": (dt, [vp, vp, vp, i64, i64, i32, i32, vp, i64, vp, i64, vp, dt, vp]),
 }
 
 
@@ -77,3 +78,28 @@ def test_norm_argument_errors(lib):
     assert call(d=(1 << 30) + 1, ldx=1 << 31, ldq=1 << 31) == UNSUPPORTED
     assert call(n=0, x=None, w=None, q=None, s=None) == OK
     assert call(d=0, x=None, w=None, q=None, s=None) == OK
+
+
+def stored_errors(call):
+    """What every product on a stored layer refuses: call(bits=, G=, d_col=)."""
+    assert call(bits=5) == UNSUPPORTED
+    assert call(G=16, d_col=256) == UNSUPPORTED and call(G=256, d_col=256) == UNSUPPORTED
+    assert call(G=128, d_col=320) == INVALID_ARG           # the group does not divide the width
+    assert call(G=-2) == INVALID_ARG
+    assert call(G=0, d_col=255) == INVALID_ARG             # odd width, two codes per byte
+    assert call(G=0, d_col=252, bits=3) == INVALID_ARG     # 3-bit rows are whole 8-code groups
+
+
+def test_int8_argument_errors(lib):
+    def call(codes=FAKE, S=FAKE, Z=FAKE, d_row=4, d_col=256, bits=4, G=128, x=FAKE, ldx=512, xs=FAKE, n=2, y=FAKE, yt=F32):
+        return lib.gptqs_linear_int8(codes, S, Z, d_row, d_col, bits, G, x, ldx, xs, n, y, yt, None)
+
+    stored_errors(call)
+    assert call(yt=7) == INVALID_ARG and call(n=-1) == INVALID_ARG and call(d_row=-1) == INVALID_ARG
+    assert call(ldx=255) == INVALID_ARG
+    for name in ("codes", "S", "Z", "x", "xs", "y"):
+        assert call(**{name: None}) == INVALID_ARG, name
+    assert call(n=65535 * 64 + 1) == UNSUPPORTED
+    assert call(d_row=2 ** 31 // 64) == UNSUPPORTED
+    assert call(n=0, codes=None, x=None, y=None) == OK
+    assert call(d_row=0, codes=None, x=None, y=None) == OK
