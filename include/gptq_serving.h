@@ -79,6 +79,36 @@ gptq_status gptqs_linear_int8(const uint8_t* codes, const uint16_t* scales_f16, 
                               const int8_t* xq, int64_t ldx, const float* x_scale, int64_t n_tokens,
                               void* y, gptq_dtype y_dtype, void* stream);
 
+/*
+ * A projection on stored codes, shared by all tokens, with a low-rank adapter per token
+ * beside it:
+ *   y[t] = What x[t] + scaling[a] B[a] (A[a] x[t]),  a = adapter_ids[t];
+ * a token whose id is outside 0 .. n_adapters - 1 (by convention -1) takes What x[t]
+ * alone.  Tokens may come in any order; runs of tokens with one adapter are cheapest.
+ * A x is summed in fp32; scaling A x enters the second product in fp32 (small batches) or
+ * as two bfloat16 parts.
+ *
+ *  codes, scales_f16, zeros_f16, d_row, d_col, bits, group_size   as gptqs_linear_int8.
+ *  x            n_tokens x d_col, pitch ldx >= d_col, dtype x_dtype: GPTQ_BF16 or GPTQ_F16
+ *  A            n_adapters x rank x d_col, dtype x_dtype
+ *  B            n_adapters x d_row x rank, dtype x_dtype
+ *  adapter_ids  n_tokens int32
+ *  scaling      n_adapters fp32, or NULL for 1
+ *  y            n_tokens x d_row, pitch d_row, dtype y_dtype
+ *  ws           at least gptqs_linear_lora_workspace_size(n_tokens, d_col, rank) bytes,
+ *               4-byte aligned; contents on entry are ignored
+ * Errors: as gptqs_linear_int8; x_dtype GPTQ_F32 -> GPTQ_ERR_UNSUPPORTED; rank outside
+ * 1 .. 256 or n_adapters < 0 -> GPTQ_ERR_INVALID_ARG; a missing, misaligned or short
+ * workspace -> GPTQ_ERR_WORKSPACE.  n_adapters == 0: A, B and ws may be NULL.
+ */
+size_t gptqs_linear_lora_workspace_size(int64_t n_tokens, int64_t d_col, int32_t rank);
+gptq_status gptqs_linear_lora(const uint8_t* codes, const uint16_t* scales_f16, const uint16_t* zeros_f16,
+                              int64_t d_row, int64_t d_col, int32_t bits, int32_t group_size,
+                              const void* x, gptq_dtype x_dtype, int64_t n_tokens, int64_t ldx,
+                              const void* A, const void* B, int32_t n_adapters, int32_t rank,
+                              const int32_t* adapter_ids, const float* scaling,
+                              void* y, gptq_dtype y_dtype, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -78,6 +78,9 @@ def _load():
         "gptqs_rmsnorm_int8": (ctypes.c_int, [vp, ctypes.c_int, i64, vp, i64, vp, ctypes.c_int, ctypes.c_float, i64,
                                               i64, vp, i64, vp, i64, vp, i64, vp, vp]),
         "gptqs_linear_int8": (ctypes.c_int, [vp, vp, vp, i64, i64, i32, i32, vp, i64, vp, i64, vp, ctypes.c_int, vp]),
+        "gptqs_linear_lora_workspace_size": (sz, [i64, i64, i32]),
+        "gptqs_linear_lora": (ctypes.c_int, [vp, vp, vp, i64, i64, i32, i32, vp, ctypes.c_int, i64, i64, vp, vp, i32, i32,
+                                             vp, vp, vp, ctypes.c_int, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -492,4 +495,4 @@ def check_info(info: torch.Tensor, what: str = "gptq"):
         raise GptqError(ERR_NONFINITE, f"{what}: {status_string(ERR_NONFINITE)}")
 
 
-from .serving import Int8Rows, linear_int8, rmsnorm_int8  # noqa: E402,F401  (uses the names above)
+from .serving import Int8Rows, linear_int8, linear_lora, linear_lora_workspace_size, rmsnorm_int8  # noqa: E402,F401  (uses the names above)

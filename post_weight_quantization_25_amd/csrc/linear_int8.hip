@@ -68,7 +68,7 @@ static gptq_status launch(const Int8Args& a, hipStream_t s) {
     auto tiles = [&](int per) { return (unsigned)((a.n + per - 1) / per); };
     if (a.n <= 16) int8_tile_kernel<CB, RUN, 1, 1><<<dim3(g16, 1), 64 * TW, 0, s>>>(a);
     else if (a.n <= 32) int8_tile_kernel<CB, RUN, 2, 1><<<dim3(g16, 1), 64 * TW, 0, s>>>(a);
-    else int8_tile_kernel<CB, RUN, 4, 2><<<dim3(g32, tiles(64)), 64 * TW, 0, s>>>(a);
+    else int8_tile_kernel<CB, RUN, 4, RUN == 8 ? 1 : 2><<<dim3(RUN == 8 ? g16 : g32, tiles(64)), 64 * TW, 0, s>>>(a);
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
 }

@@ -1,0 +1,234 @@
+// A shared projection on stored codes with a low-rank adapter per token beside it
+// (gptqs_linear_lora):
+//   y[t] = What x[t] + s_a B_a (A_a x[t]),  a = ids[t].
+//
+// Two launches.  lora_shrink_kernel forms v[t] = A_a x[t] on the matrix cores: a workgroup
+// takes 16 tokens and a share of the columns, and for each distinct adapter among its
+// tokens multiplies all 16 by that adapter's rows and keeps the rows of the tokens that
+// have it (a run of tokens with one adapter costs one product).  The shares' sums go to
+// the workspace, fp32, and are added in a fixed order by the readers.  Then the
+// projection's kernel adds s_a B_a v to its own sums before its one rounding, so the
+// adapters cost no extra pass over y.  Selecting rows, rather than multiplying by zero,
+// keeps an infinity or a NaN of one adapter away from the tokens of the others.
+
+#include "serving.h"
+#include "stored_tile.h"
+
+namespace gptq {
+
+constexpr int TW = 8;         // waves per workgroup of the projection
+constexpr int SW = 4;         // waves per workgroup of the shrink product
+constexpr int SHARE = 512;    // columns of one share's step: 128 per wave
+constexpr int RCH = 64;       // ranks held in LDS at a time by the projection's epilogue
+
+struct LoraArgs {
+    Stored L; int64_t d_row;
+    const uint16_t* x; int64_t ldx; int64_t n;
+    const uint16_t* A; const uint16_t* B; int n_adapters; int rank;   // rank 0: no adapters
+    const int32_t* ids; const float* scaling;
+    float* v; int splits; int64_t share;   // v: splits x n x rank; share: columns per split
+    void* y; gptq_dtype yt;
+};
+
+// The adapter of token t: -1 past the last token or outside the table.
+GPTQ_DEV int adapter_of(const LoraArgs& a, int64_t t) {
+    const int id = t < a.n ? a.ids[t] : -1;
+    return id >= 0 && id < a.n_adapters ? id : -1;
+}
+
+template <int X>
+__global__ __launch_bounds__(64 * SW) void lora_shrink_kernel(LoraArgs a) {
+    __shared__ float red[SW][4][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15, q = lane >> 4;
+    const int64_t tok0 = (int64_t)blockIdx.x * 16;
+    const int64_t t = tok0 + n16 < a.n ? tok0 + n16 : a.n - 1;
+    const int id = adapter_of(a, tok0 + n16);
+    const uint8_t* xrow = reinterpret_cast<const uint8_t*>(a.x + t * a.ldx);
+    const int64_t col_a = (int64_t)blockIdx.y * a.share;
+    const int64_t col_b = col_a + a.share < a.L.d_col ? col_a + a.share : a.L.d_col;
+    const int rt = blockIdx.z;                                   // 16 ranks
+    const int k = 16 * rt + n16 < a.rank ? 16 * rt + n16 : a.rank - 1;
+    f32x4_t out = {0.f, 0.f, 0.f, 0.f};
+    uint32_t todo = (uint32_t)__ballot(id >= 0) & 0xFFFFu;
+    while (todo) {                                               // wave-uniform
+        const int ad = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
+        const uint32_t mine = (uint32_t)__ballot(id == ad) & 0xFFFFu;
+        todo &= ~mine;
+        const uint8_t* arow = reinterpret_cast<const uint8_t*>(a.A + ((int64_t)ad * a.rank + k) * a.L.d_col);
+        f32x4_t cs = {0.f, 0.f, 0.f, 0.f};
+        for (int64_t c0 = col_a + 128 * wave; c0 < col_b; c0 += SHARE) {
+            u32x4_t xf[4], af[4];
+            const int64_t col = c0 + 32 * q;                     // the lane's 32 columns of 128
+            if (c0 + 128 <= col_b) {
+                const XRun<X, 32> xr = load_x<X, 32>(xrow + 2 * col), ar = load_x<X, 32>(arow + 2 * col);
+                __builtin_memcpy(xf, xr.w, 64);
+                __builtin_memcpy(af, ar.w, 64);
+            } else {
+                const int left = (int)(col_b - col < 32 ? col_b - col : 32);
+                const XRun<X, 32> xr = load_x_tail<X, 32>(xrow + 2 * col, left), ar = load_x_tail<X, 32>(arow + 2 * col, left);
+                __builtin_memcpy(xf, xr.w, 64);
+                __builtin_memcpy(af, ar.w, 64);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) cs = mfma16<X>(xf[e], af[e], cs);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[i] = (mine >> (4 * q + i)) & 1 ? cs[i] : out[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[wave][i][lane] = out[i];
+    __syncthreads();
+    const int m = threadIdx.x >> 4, n = threadIdx.x & 15;        // token m, rank n of the tile
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < SW; ++w) v += red[w][m & 3][n + 16 * (m >> 2)];
+    if (tok0 + m < a.n && 16 * rt + n < a.rank)
+        a.v[((int64_t)blockIdx.y * a.n + tok0 + m) * a.rank + 16 * rt + n] = v;
+}
+
+template <int X>
+GPTQ_DEV float elem16(uint16_t b) { return X == X_BF16 ? bf16_bits_to_f32(b) : f16_bits_to_f32(b); }
+
+template <int X, int CB, int RUN, int NTT, int RB>
+__global__ __launch_bounds__(64 * TW) void lora_tile_kernel(LoraArgs a) {
+    constexpr int CPW = NTT == 1 ? 2 : 1;
+    constexpr int PER = NTT * RB * 256 / (64 * TW) > 0 ? NTT * RB * 256 / (64 * TW) : 1;   // outputs per thread
+    __shared__ float red[TW][NTT * RB][4][64];
+    __shared__ float vs[16 * NTT][RCH + 1];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15;
+    const int64_t row0 = (int64_t)blockIdx.x * 16 * RB, tok0 = (int64_t)blockIdx.y * 16 * NTT;
+    int64_t row[RB];
+    const uint8_t* xrow[NTT];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+        const int64_t r = row0 + 16 * rb + n16;
+        row[rb] = r < a.d_row ? r : a.d_row - 1;
+    }
+#pragma unroll
+    for (int tt = 0; tt < NTT; ++tt) {
+        int64_t t = tok0 + 16 * tt + n16;
+        t = t < a.n ? t : a.n - 1;
+        xrow[tt] = reinterpret_cast<const uint8_t*>(a.x + t * a.ldx);
+    }
+    f32x4_t acc[NTT][RB];
+#pragma unroll
+    for (int tt = 0; tt < NTT; ++tt)
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) acc[tt][rb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    stored_accumulate<X, CB, RUN, NTT, RB, CPW>(acc, a.L, row, xrow, wave, TW, (int)((a.L.d_col + SCK - 1) / SCK));
+#pragma unroll
+    for (int tt = 0; tt < NTT; ++tt)
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) red[wave][tt * RB + rb][i][lane] = acc[tt][rb][i];
+
+    // the thread's outputs: o = threadIdx.x + 64 TW k
+    float delta[PER];
+    int id[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int o = threadIdx.x + 64 * TW * k, tr = o >> 8;
+        delta[k] = 0.f;
+        id[k] = a.rank && tr < NTT * RB ? adapter_of(a, tok0 + 16 * (tr / RB) + ((o >> 4) & 15)) : -1;
+    }
+    for (int k0 = 0; k0 < a.rank; k0 += RCH) {
+        const int kn = a.rank - k0 < RCH ? a.rank - k0 : RCH;
+        __syncthreads();
+        for (int e = threadIdx.x; e < 16 * NTT * kn; e += 64 * TW) {
+            const int m = e / kn, k = e % kn;
+            const int64_t t = tok0 + m;
+            float v = 0.f;
+            if (t < a.n) {
+                for (int s = 0; s < a.splits; ++s) v += a.v[((int64_t)s * a.n + t) * a.rank + k0 + k];
+                const int ad = adapter_of(a, t);
+                if (a.scaling && ad >= 0) v *= a.scaling[ad];
+            }
+            vs[m][k] = v;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int o = threadIdx.x + 64 * TW * k, tr = o >> 8, m = 16 * (tr / RB) + ((o >> 4) & 15);
+            const int64_t r = row0 + 16 * (tr % RB) + (o & 15);
+            if (id[k] < 0 || r >= a.d_row) continue;
+            const uint16_t* b = a.B + ((int64_t)id[k] * a.d_row + r) * a.rank + k0;
+            int e = 0;
+            for (; e + 8 <= kn; e += 8) {
+                uint16_t w[8];
+                __builtin_memcpy(w, b + e, 16);
+#pragma unroll
+                for (int f = 0; f < 8; ++f) delta[k] = fmaf(vs[m][e + f], elem16<X>(w[f]), delta[k]);
+            }
+            for (; e < kn; ++e) delta[k] = fmaf(vs[m][e], elem16<X>(b[e]), delta[k]);
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int o = threadIdx.x + 64 * TW * k, tr = o >> 8, m = (o >> 4) & 15, n = o & 15;
+        if (tr >= NTT * RB) continue;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < TW; ++w) v += red[w][tr][m & 3][n + 16 * (m >> 2)];
+        const int64_t t = tok0 + 16 * (tr / RB) + m, r = row0 + 16 * (tr % RB) + n;
+        if (id[k] >= 0) v += delta[k];
+        if (t < a.n && r < a.d_row) store_out(a.y, a.yt, t * a.d_row + r, v);
+    }
+}
+
+template <int X, int CB, int RUN>
+static gptq_status launch(const LoraArgs& a, hipStream_t s) {
+    const unsigned g16 = (unsigned)((a.d_row + 15) / 16), g32 = (unsigned)((a.d_row + 31) / 32);
+    auto tiles = [&](int per) { return (unsigned)((a.n + per - 1) / per); };
+    if (a.n <= 16) lora_tile_kernel<X, CB, RUN, 1, 1><<<dim3(g16, 1), 64 * TW, 0, s>>>(a);
+    else if (a.n <= 32) lora_tile_kernel<X, CB, RUN, 2, 1><<<dim3(g16, 1), 64 * TW, 0, s>>>(a);
+    else lora_tile_kernel<X, CB, RUN, 4, RUN == 8 ? 1 : 2><<<dim3(RUN == 8 ? g16 : g32, tiles(64)), 64 * TW, 0, s>>>(a);
+    GPTQ_LAUNCH_CHECK();
+    return GPTQ_OK;
+}
+
+template <int X, int CB>
+static gptq_status launch_runs(const LoraArgs& a, int group, hipStream_t s) {
+    return group == 32 ? launch<X, CB, 8>(a, s) : group == 64 ? launch<X, CB, 16>(a, s) : launch<X, CB, 32>(a, s);
+}
+
+template <int X>
+static gptq_status launch_bits(const LoraArgs& a, int bits, int group, hipStream_t s) {
+    if (a.rank) {
+        const dim3 grid((unsigned)((a.n + 15) / 16), (unsigned)a.splits, (unsigned)((a.rank + 15) / 16));
+        lora_shrink_kernel<X><<<grid, 64 * SW, 0, s>>>(a);
+        GPTQ_LAUNCH_CHECK();
+    }
+    return bits == 3 ? launch_runs<X, 3>(a, group, s) : bits == 4 ? launch_runs<X, 4>(a, group, s) : launch_runs<X, 8>(a, group, s);
+}
+
+// Shares of the columns: enough workgroups to fill the device, none below 512 columns.
+static int lora_splits(int64_t n, int64_t d_col, int rank) {
+    const int64_t tiles = (n + 15) / 16 * ((rank + 15) / 16), most = (d_col + SHARE - 1) / SHARE;
+    const int64_t want = (512 + tiles - 1) / tiles;
+    const int64_t s = want < most ? want : most;
+    return (int)(s < 1 ? 1 : s < 64 ? s : 64);
+}
+
+size_t lora_ws_bytes(int64_t n, int64_t d_col, int rank) {
+    return (size_t)lora_splits(n, d_col, rank) * (size_t)n * (size_t)rank * sizeof(float);
+}
+
+gptq_status linear_lora_launch(const uint8_t* codes, const uint16_t* scales, const uint16_t* zeros, int64_t d_row,
+                               int64_t d_col, int bits, int group, const void* x, gptq_dtype xt, int64_t n, int64_t ldx,
+                               const void* A, const void* B, int n_adapters, int rank, const int32_t* ids,
+                               const float* scaling, void* y, gptq_dtype yt, void* ws, hipStream_t s) {
+    LoraArgs a;
+    a.L = stored_layer(codes, scales, zeros, d_col, bits, group);
+    a.d_row = d_row; a.x = (const uint16_t*)x; a.ldx = ldx; a.n = n;
+    a.A = (const uint16_t*)A; a.B = (const uint16_t*)B; a.n_adapters = n_adapters;
+    a.rank = n_adapters > 0 ? rank : 0;
+    a.ids = ids; a.scaling = scaling; a.v = (float*)ws;
+    a.splits = a.rank ? lora_splits(n, d_col, rank) : 0;
+    a.share = a.rank ? ((d_col + SHARE - 1) / SHARE + a.splits - 1) / a.splits * SHARE : 0;
+    a.y = y; a.yt = yt;
+    return xt == GPTQ_BF16 ? launch_bits<X_BF16>(a, bits, group, s) : launch_bits<X_F16>(a, bits, group, s);
+}
+
+}  // namespace gptq

@@ -28,4 +28,11 @@ gptq_status linear_int8_launch(const uint8_t* codes, const uint16_t* scales, con
                                int64_t d_col, int bits, int group, const int8_t* x, int64_t ldx, const float* xs,
                                int64_t n, void* y, gptq_dtype yt, hipStream_t s);
 
+constexpr int LORA_MAX_RANK = 256;
+size_t lora_ws_bytes(int64_t n, int64_t d_col, int rank);
+gptq_status linear_lora_launch(const uint8_t* codes, const uint16_t* scales, const uint16_t* zeros, int64_t d_row,
+                               int64_t d_col, int bits, int group, const void* x, gptq_dtype xt, int64_t n, int64_t ldx,
+                               const void* A, const void* B, int n_adapters, int rank, const int32_t* ids,
+                               const float* scaling, void* y, gptq_dtype yt, void* ws, hipStream_t s);
+
 }  // namespace gptq

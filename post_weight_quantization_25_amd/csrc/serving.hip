@@ -57,5 +57,32 @@ gptq_status gptqs_linear_int8(const uint8_t* codes, const uint16_t* scales_f16, 
                               y, y_dtype, (hipStream_t)stream);
 }
 
+size_t gptqs_linear_lora_workspace_size(int64_t n_tokens, int64_t d_col, int32_t rank) {
+    if (n_tokens <= 0 || d_col <= 0 || rank < 1 || rank > LORA_MAX_RANK) return 0;
+    return lora_ws_bytes(n_tokens, d_col, rank);
+}
+
+gptq_status gptqs_linear_lora(const uint8_t* codes, const uint16_t* scales_f16, const uint16_t* zeros_f16,
+                              int64_t d_row, int64_t d_col, int32_t bits, int32_t group_size, const void* x,
+                              gptq_dtype x_dtype, int64_t n_tokens, int64_t ldx, const void* A, const void* B,
+                              int32_t n_adapters, int32_t rank, const int32_t* adapter_ids, const float* scaling,
+                              void* y, gptq_dtype y_dtype, void* ws, size_t ws_bytes, void* stream) {
+    if (d_row < 0 || d_col < 0 || n_tokens < 0 || !valid_dtype(x_dtype) || !valid_dtype(y_dtype))
+        return GPTQ_ERR_INVALID_ARG;
+    if (n_adapters < 0 || (n_adapters > 0 && (rank < 1 || rank > LORA_MAX_RANK))) return GPTQ_ERR_INVALID_ARG;
+    const gptq_status st = check_stored(d_col, bits, group_size);
+    if (st != GPTQ_OK) return st;
+    if (x_dtype == GPTQ_F32) return GPTQ_ERR_UNSUPPORTED;
+    if (d_row == 0 || d_col == 0 || n_tokens == 0) return GPTQ_OK;
+    if (!codes || !scales_f16 || !zeros_f16 || !x || !y || ldx < d_col) return GPTQ_ERR_INVALID_ARG;
+    if (n_adapters > 0 && (!A || !B || !adapter_ids)) return GPTQ_ERR_INVALID_ARG;
+    if (d_row > 2147483647LL / 64 || d_col > 2147483647LL / 64 || n_tokens > SERVE_MAX_TOKENS)
+        return GPTQ_ERR_UNSUPPORTED;
+    if (n_adapters > 0 && (!ws || (reinterpret_cast<uintptr_t>(ws) & 3) || ws_bytes < lora_ws_bytes(n_tokens, d_col, rank)))
+        return GPTQ_ERR_WORKSPACE;
+    return linear_lora_launch(codes, scales_f16, zeros_f16, d_row, d_col, bits, group_size, x, x_dtype, n_tokens, ldx,
+                              A, B, n_adapters, rank, adapter_ids, scaling, y, y_dtype, ws, (hipStream_t)stream);
+}
+
 }  // extern "C"
 #pragma GCC visibility pop

@@ -125,6 +125,13 @@ GPTQ_DEV i32x4_t mfma8_i8(uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1, i3
 template <int X>
 GPTQ_DEV constexpr uint32_t ones_word() { return X == X_I8 ? 0x01010101u : X == X_BF16 ? 0x3F803F80u : 0x3C003C00u; }
 
+// Ends a conditional block of products: their results are settled behind it.  This compiler
+// (clang 22) counts the wait between a product and a later use of its registers along only
+// one of the paths that meet behind a branch, so results that leave the block are waited
+// for here: 16 wait states, more than any of these products needs (12).
+template <typename V>
+GPTQ_DEV void settle(V& v) { asm volatile("s_nop 7\n\ts_nop 7" : "+v"(v)); }
+
 // ---- activations of RUN columns
 template <int X, int RUN>
 struct XRun { uint32_t w[RUN * xbytes<X>() / 4]; };
@@ -210,9 +217,7 @@ GPTQ_DEV void stored_accumulate(f32x4_t (&acc)[NTT][RB], const Stored& L, const 
                     const float S = f16_bits_to_f32(S16[j][rb][p]), z = f16_bits_to_f32(Z16[j][rb][p]);
                     const float zc = zero_part<X, CB>(z), rz = z - zc;
                     typedef typename Acc<X>::t sum_t;
-                    // sum x where some zero has a rest, as fp32; a block of its own, with no
-                    // branch between a product and the reads of its result: this compiler
-                    // counts the wait that such a read needs along one of the two paths
+                    // sum x where some zero has a rest, as fp32
                     float xs[NTT][4];
 #pragma unroll
                     for (int tt = 0; tt < NTT; ++tt)
@@ -235,9 +240,11 @@ GPTQ_DEV void stored_accumulate(f32x4_t (&acc)[NTT][RB], const Stored& L, const 
                             }
                         }
 #pragma unroll
-                        for (int tt = 0; tt < NTT; ++tt)
+                        for (int tt = 0; tt < NTT; ++tt) {
+                            settle(s[tt]);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) xs[tt][i] = (float)s[tt][i];
+                        }
                     }
                     sum_t cs[NTT];
 #pragma unroll

@@ -12,7 +12,7 @@ from dataclasses import dataclass
 
 import torch
 
-from . import _DT, Quantized, _check, _check_quantized, _dev, _tensor, lib
+from . import _DT, Quantized, _check, _check_quantized, _dev, _tensor, _workspace, lib
 
 
 class _On:
@@ -142,4 +142,40 @@ def linear_int8(q: Quantized, x: Int8Rows, out_dtype=torch.float32, out: torch.T
         _check(lib.gptqs_linear_int8(q.codes.data_ptr(), q.scales.data_ptr(), q.zeros.data_ptr(), d_row, d_col, q.bits,
                                      q.group_size, x.q.data_ptr(), ldx, x.scale.data_ptr(), n, out.data_ptr(),
                                      _DT[out.dtype], s), "gptqs_linear_int8")
+    return out
+
+
+def linear_lora_workspace_size(n_tokens: int, d_col: int, rank: int) -> int:
+    return lib.gptqs_linear_lora_workspace_size(n_tokens, d_col, rank)
+
+
+def linear_lora(q: Quantized, x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ids: torch.Tensor,
+                scaling: torch.Tensor | None = None, out_dtype=torch.float32, out: torch.Tensor | None = None,
+                ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y[t] = What x[t] + scaling[a] B[a] (A[a] x[t]), a = ids[t] (gptqs_linear_lora): the
+    projection is shared, the adapters (A: n_adapters x rank x d_col, B: n_adapters x d_row
+    x rank, x's dtype) are the tokens' own; a token whose id (int32) is outside the table
+    takes the projection alone.  x (bf16/f16) may be strided."""
+    dev, dt = x.device, x.dtype
+    ldx = _rows(x, "x")
+    n, d_col = x.shape
+    if dt not in (torch.bfloat16, torch.float16) or d_col != q.d_col:
+        raise ValueError(f"x must be bf16/f16 with the layer's {q.d_col} columns")
+    d_row = _stored(q, "q", dev)
+    if A.dim() != 3 or B.dim() != 3:
+        raise ValueError("A and B must be n_adapters x rank x d_col and n_adapters x d_row x rank")
+    m, rank, _ = A.shape
+    _tensor(A, "A", dt, (m, rank, d_col), dev)
+    _tensor(B, "B", dt, (m, d_row, rank), dev)
+    _tensor(ids, "ids", torch.int32, (n,), dev)
+    if scaling is not None:
+        _tensor(scaling, "scaling", torch.float32, (m,), dev)
+    with _On(dev, stream) as s:
+        out = _out(out, n, d_row, out_dtype, dev)
+        ws = _workspace(linear_lora_workspace_size(n, d_col, rank) if m else 0, dev, ws)
+        _check(lib.gptqs_linear_lora(q.codes.data_ptr(), q.scales.data_ptr(), q.zeros.data_ptr(), d_row, d_col, q.bits,
+                                     q.group_size, x.data_ptr(), _DT[dt], n, ldx, A.data_ptr(), B.data_ptr(), m, rank,
+                                     ids.data_ptr(), None if scaling is None else scaling.data_ptr(), out.data_ptr(),
+                                     _DT[out.dtype], None if ws is None else ws.data_ptr(),
+                                     0 if ws is None else ws.numel(), s), "gptqs_linear_lora")
     return out

@@ -44,3 +44,13 @@ def out_rounding(ref, t):
         return 0.0
     fi = torch.finfo(t)
     return fi.eps / 2 * ref.abs() + fi.smallest_normal * fi.eps / 2
+
+
+def zero_parts(q, x):
+    """S sum_c |x_c| (|u - zc| + |z - zc|), zc the whole number next to z within 240 of 0 (255
+    for 8-bit codes): what the 16-bit products add up, per token and row."""
+    u = o.unpack(q.codes.cpu().numpy(), q.bits).astype(np.float64)
+    rep = u.shape[1] // q.scales.shape[1]
+    S, Z = (np.repeat(t.cpu().numpy().astype(np.float64), rep, axis=1) for t in (q.scales, q.zeros))
+    zc = np.clip(np.rint(Z), -1 if q.bits == 8 else -240, 255 if q.bits == 8 else 240)
+    return x.abs() @ torch.from_numpy(S * (np.abs(u - zc) + np.abs(Z - zc))).t()

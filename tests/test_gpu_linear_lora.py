@@ -1,0 +1,168 @@
+"""gptqs_linear_lora against its definition in 64 bits.
+
+Tolerance.  Products of 16-bit values are exact in fp32; an addition is taken at one unit
+in the last place (2^-23: the matrix cores are not assumed to round to nearest).
+ * The projection: every column enters one fp32 sum as x (u - zc), and the zero's rest as
+   rz sum x, so with M = S sum |x| (|u - zc| + |rz|) the error is at most (d_col + 64)
+   2^-23 M (64: pieces' scaling and the waves' sums, as for the plain product).
+ * The adapter: v = A x is off by at most (d_col + 64) 2^-23 sum |x| |A|, the second
+   product adds rank + 8 additions and the split of v into two bfloat16 parts 2^-18 of it:
+   with D = |s| sum_k |B| (|A| |x|), at most ((d_col + rank + 72) 2^-23 + 2^-18) D.
+ * Half a step of a 16-bit output."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from gpu_helpers import log
+from serving_helpers import BF, F32, HF, out_rounding, stored, zero_parts
+
+pytestmark = pytest.mark.gpu
+
+
+def adapters(m, rank, d_row, d_col, dt, seed):
+    gen = torch.Generator().manual_seed(seed)
+    return ((torch.randn(m, rank, d_col, generator=gen) * d_col ** -0.5).to(dt).cuda(),
+            torch.randn(m, d_row, rank, generator=gen).to(dt).cuda(), (0.5 + torch.rand(m, generator=gen)).cuda())
+
+
+def compare(y, q, What, x, A, B, ids, scaling, yt):
+    x, A, B = (t.cpu().double() for t in (x, A, B))
+    s = torch.ones(A.shape[0]).double() if scaling is None else scaling.cpu().double()
+    ref, mag = x @ What.t(), zero_parts(q, x)
+    d_col, rank = x.shape[1], A.shape[1]
+    bound = (d_col + 64) * 2.0 ** -23 * mag
+    ids = ids.cpu()
+    for a in range(A.shape[0]):
+        t = torch.nonzero(ids == a)[:, 0]
+        ref[t] += s[a] * (x[t] @ A[a].t()) @ B[a].t()
+        D = s[a].abs() * (x[t].abs() @ A[a].abs().t()) @ B[a].abs().t()
+        bound[t] += ((d_col + rank + 72) * 2.0 ** -23 + 2.0 ** -18) * D
+    bound = bound * (1 + 2.0 ** -10) + out_rounding(ref, yt)
+    err = (y.cpu().double() - ref).abs()
+    log(f"  max |err| / bound = {float((err / bound.clamp_min(1e-300)).max()):.3f}")
+    assert y.dtype == yt and bool((err <= bound).all())
+
+
+def some_ids(n, m, kind, seed=0):
+    rng = np.random.default_rng([seed, n, m])
+    if kind == "mixed":
+        v = rng.integers(-1, m, size=n)
+    elif kind == "runs":
+        v = np.repeat(rng.integers(-1, m, size=n // 23 + 1), 23)[:n]
+    elif kind == "one":
+        v = np.full(n, m - 1)
+    elif kind == "none":
+        v = np.full(n, -1)
+    else:   # values outside the table count as none
+        v = rng.choice([-2 ** 31, -7, m, 2 ** 31 - 1, 0], size=n)
+    return torch.from_numpy(v.astype(np.int32)).cuda()
+
+
+CASES = [
+    # d_row, d_col, bits, group, n, dtype, y dtype, adapters, rank, ids, zeros
+    (4096, 4096, 4, 128, 1, BF, BF, 8, 16, "one", "whole"), (17, 64, 4, 32, 1, HF, F32, 1, 1, "one", "whole"),
+    (300, 512, 4, 128, 3, BF, F32, 2, 8, "mixed", "whole"), (33, 1024, 4, 64, 16, HF, HF, 16, 20, "mixed", "whole"),
+    (64, 256, 3, 32, 2, BF, F32, 3, 4, "mixed", "whole"), (128, 256, 8, 64, 7, HF, BF, 4, 33, "mixed", "whole"),
+    (100, 250, 4, 0, 5, BF, F32, 3, 7, "mixed", "fraction"), (97, 333, 8, 0, 19, BF, F32, 5, 16, "mixed", "whole"),
+    (50, 200, 3, 0, 17, HF, F32, 2, 64, "runs", "symmetric"), (31, 8, 3, 0, 2, BF, F32, 2, 2, "one", "whole"),
+    (272, 384, 3, 128, 33, HF, HF, 40, 16, "mixed", "whole"), (40, 96, 4, 32, 20, BF, F32, 3, 100, "mixed", "far"),
+    (70, 192, 8, 64, 31, BF, F32, 2, 256, "mixed", "far"), (130, 640, 4, 128, 64, BF, F32, 9, 65, "runs", "fraction"),
+    (96, 512, 4, 64, 50, HF, F32, 4, 16, "none", "far"), (96, 512, 4, 128, 50, HF, F32, 4, 16, "outside", "whole"),
+    (200, 1100, 4, 0, 100, BF, BF, 6, 16, "runs", "whole"), (129, 4098, 4, 0, 130, HF, F32, 3, 32, "mixed", "fraction"),
+    (513, 1024, 4, 128, 257, BF, F32, 8, 16, "runs", "whole"), (260, 896, 4, 32, 300, HF, F32, 30, 48, "mixed", "whole"),
+    (255, 576, 4, 64, 333, BF, BF, 4, 13, "runs", "far"), (384, 1111, 8, 0, 200, BF, F32, 2, 128, "one", "whole"),
+    (300, 1000, 3, 0, 290, HF, F32, 5, 16, "runs", "symmetric"), (1001, 2048, 3, 128, 520, BF, BF, 7, 16, "runs", "whole"),
+    (640, 512, 8, 32, 700, HF, F32, 3, 200, "mixed", "fraction"), (1111, 1024, 4, 128, 1030, BF, BF, 64, 32, "mixed", "whole"),
+]
+
+
+@pytest.mark.parametrize("d_row,d_col,bits,group,n,dt,yt,m,rank,kind,zeros", CASES)
+def test_lora_parity(d_row, d_col, bits, group, n, dt, yt, m, rank, kind, zeros):
+    import post_weight_quantization_25_amd as g
+    log(f"lora {d_row}x{d_col} bits={bits} g={group} n={n} {dt} m={m} rank={rank} {kind} zeros={zeros}")
+    q, What = stored(d_row, d_col, bits, group, 1, zeros)
+    A, B, s = adapters(m, rank, d_row, d_col, dt, 4)
+    x = torch.randn(n, d_col, generator=torch.Generator().manual_seed(n)).to(dt).cuda()
+    ids = some_ids(n, m, kind)
+    s = None if kind == "one" else s
+    y = g.linear_lora(q, x, A, B, ids, s, out_dtype=yt)
+    torch.cuda.synchronize()
+    compare(y, q, What, x, A, B, ids, s, yt)
+    assert torch.equal(g.linear_lora(q, x, A, B, ids, s, out_dtype=yt), y)
+
+
+@pytest.mark.parametrize("n", [1, 30, 60, 200])
+def test_lora_without_adapters_is_the_projection(n):
+    """No adapters at all, or no token with one: the shared projection, bit for bit the same."""
+    import post_weight_quantization_25_amd as g
+    q, What = stored(150, 384, 4, 128, 5)
+    A, B, s = adapters(3, 16, 150, 384, BF, 1)
+    x = torch.randn(n, 384, generator=torch.Generator().manual_seed(1)).to(BF).cuda()
+    y0 = g.linear_lora(q, x, A[:0], B[:0], some_ids(n, 3, "one"), None)
+    y1 = g.linear_lora(q, x, A, B, some_ids(n, 3, "none"), s)
+    assert torch.equal(y0, y1)
+    compare(y0, q, What, x, A, B, some_ids(n, 3, "none"), s, F32)
+
+
+@pytest.mark.parametrize("n", [5, 40, 300])
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_lora_bad_adapters_stay_with_their_tokens(n, dt):
+    """NaNs and infinities in one adapter, one token and one weight row change nothing else."""
+    import post_weight_quantization_25_amd as g
+    d_row, d_col, m, rank = 150, 384, 4, 16
+    q, _ = stored(d_row, d_col, 4, 128, 5)
+    A, B, s = adapters(m, rank, d_row, d_col, dt, 2)
+    x = torch.randn(n, d_col, generator=torch.Generator().manual_seed(1)).to(dt).cuda()
+    ids = some_ids(n, m, "mixed", 3)
+    y = g.linear_lora(q, x, A, B, ids, s)
+    A2, B2, x2 = A.clone(), B.clone(), x.clone()
+    A2[1, 3, 7] = float("nan")
+    B2[2, 9, 1] = float("inf")
+    x2[n // 2, 5] = float("inf")
+    q.scales[11, 1] = float("nan")
+    y2 = g.linear_lora(q, x2, A2, B2, ids, s)
+    bad = torch.zeros(n, d_row, dtype=torch.bool, device="cuda")
+    bad[ids == 1] = True
+    bad[ids == 2, 9] = True
+    bad[n // 2] = True
+    bad[:, 11] = True
+    assert torch.equal(y2[~bad], y[~bad]) and not bool(torch.isfinite(y2[bad]).any())
+
+
+@pytest.mark.parametrize("n", [2, 40, 300])
+def test_lora_large_and_small_intermediates(n):
+    """A x beyond fp16's range, and far below its smallest normal number: v is not an fp16 value."""
+    import post_weight_quantization_25_amd as g
+    d_row, d_col, m, rank = 64, 256, 2, 16
+    q, What = stored(d_row, d_col, 4, 128, 5)
+    A, B, s = adapters(m, rank, d_row, d_col, HF, 2)
+    for up, down in ((3e4, 1e-4), (1e-5, 1e3)):
+        A2, B2 = (A.float() * up).to(HF), (B.float() * down).to(HF)
+        x = torch.randn(n, d_col, generator=torch.Generator().manual_seed(1)).to(HF).cuda()
+        ids = some_ids(n, m, "runs", 3)
+        compare(g.linear_lora(q, x, A2, B2, ids, s), q, What, x, A2, B2, ids, s, F32)
+
+
+@pytest.mark.parametrize("n", [2, 70])
+def test_lora_strides_workspace_and_refusals(n):
+    import post_weight_quantization_25_amd as g
+    d_row, d_col, m, rank = 150, 384, 4, 12
+    q, What = stored(d_row, d_col, 4, 128, 5)
+    A, B, s = adapters(m, rank, d_row, d_col, HF, 2)
+    x = torch.randn(n, d_col, generator=torch.Generator().manual_seed(1)).to(HF).cuda()
+    ids = some_ids(n, m, "mixed")
+    buf = torch.full((n, d_col + 3), float("nan"), dtype=HF, device="cuda")
+    buf[:, 1:1 + d_col] = x
+    need = g.linear_lora_workspace_size(n, d_col, rank)
+    ws = torch.full((need + 64,), 0xFF, dtype=torch.uint8, device="cuda")     # NaN bits on entry
+    out = torch.full((n + 2, d_row), 7.0, device="cuda")
+    y = g.linear_lora(q, buf[:, 1:1 + d_col], A, B, ids, s, out=out[1:1 + n], ws=ws)
+    compare(y, q, What, x, A, B, ids, s, F32)
+    assert bool((ws[need:] == 0xFF).all()) and bool((out[0] == 7).all()) and bool((out[n + 1] == 7).all())
+    for bad in (dict(x=x.float()), dict(A=A[:, :, :64]), dict(B=B.to(BF)), dict(ids=ids.long()), dict(ids=ids[:1]),
+                dict(scaling=s[:1]), dict(B=B.transpose(1, 2).contiguous().transpose(1, 2))):
+        kw = {**dict(x=x, A=A, B=B, ids=ids, scaling=s), **bad}
+        with pytest.raises(ValueError):
+            g.linear_lora(q, kw["x"], kw["A"], kw["B"], kw["ids"], kw["scaling"])
+    assert tuple(g.linear_lora(q, x[:0], A, B, ids[:0], s).shape) == (0, d_row)

@@ -22,6 +22,9 @@ SIG = {
     "gptqs_rmsnorm_int8": (dt, [vp, dt, i64, vp, i64, vp, dt, ctypes.c_float, i64, i64, vp, i64, vp, i64, vp, i64, vp,
                                 vp]),
     "gptqs_linear_int8": (dt, [vp, vp, vp, i64, i64, i32, i32, vp, i64, vp, i64, vp, dt, vp]),
+    "gptqs_linear_lora_workspace_size": (sz, [i64, i64, i32]),
+    "gptqs_linear_lora": (dt, [vp, vp, vp, i64, i64, i32, i32, vp, dt, i64, i64, vp, vp, i32, i32, vp, vp, vp, dt, vp, sz,
+                               vp]),
 }
 
 
@@ -103,3 +106,28 @@ def test_int8_argument_errors(lib):
     assert call(d_row=2 ** 31 // 64) == UNSUPPORTED
     assert call(n=0, codes=None, x=None, y=None) == OK
     assert call(d_row=0, codes=None, x=None, y=None) == OK
+
+
+def test_lora_argument_errors(lib):
+    size = lib.gptqs_linear_lora_workspace_size
+    assert size(0, 256, 16) == 0 and size(4, 0, 16) == 0 and size(4, 256, 0) == 0 and size(4, 256, 257) == 0
+    assert size(1, 256, 16) == 16 * 4                      # one share of the columns
+    assert size(4, 4096, 16) >= 4 * 16 * 4 and size(4, 4096, 16) % (4 * 16 * 4) == 0
+    need = size(2, 256, 16)
+
+    def call(codes=FAKE, S=FAKE, Z=FAKE, d_row=4, d_col=256, bits=4, G=128, x=FAKE, xt=BF16, n=2, ldx=512, A=FAKE, B=FAKE,
+             m=3, rank=16, ids=FAKE, y=FAKE, yt=F32, ws=FAKE, wsb=1 << 30):
+        return lib.gptqs_linear_lora(codes, S, Z, d_row, d_col, bits, G, x, xt, n, ldx, A, B, m, rank, ids, None, y, yt,
+                                     ws, wsb, None)
+
+    stored_errors(call)
+    assert call(yt=7) == INVALID_ARG and call(xt=7) == INVALID_ARG and call(xt=F32) == UNSUPPORTED
+    assert call(n=-1) == INVALID_ARG and call(m=-1) == INVALID_ARG
+    assert call(rank=0) == INVALID_ARG and call(rank=257) == INVALID_ARG
+    assert call(ldx=255) == INVALID_ARG
+    for name in ("codes", "S", "Z", "x", "A", "B", "ids", "y"):
+        assert call(**{name: None}) == INVALID_ARG, name
+    assert call(n=65535 * 64 + 1) == UNSUPPORTED
+    assert call(ws=None) == WORKSPACE and call(wsb=need - 1) == WORKSPACE
+    assert call(ws=ctypes.c_void_p(0x1002)) == WORKSPACE   # not 4-byte aligned
+    assert call(n=0, codes=None, x=None, y=None, ws=None) == OK
