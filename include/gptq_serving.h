@@ -109,6 +109,43 @@ gptq_status gptqs_linear_lora(const uint8_t* codes, const uint16_t* scales_f16, 
                               const int32_t* adapter_ids, const float* scaling,
                               void* y, gptq_dtype y_dtype, void* ws, size_t ws_bytes, void* stream);
 
+/*
+ * A mixture-of-experts layer for a few tokens, the experts held as stored layers:
+ *   l = router x[t];  the top_k experts of largest l (equal ones: the lower index first;
+ *   a NaN counts as -infinity), in falling order;
+ *   w = softmax of l over all experts at the chosen ones, or with renormalize over the
+ *   chosen ones alone;
+ *   h_j = silu(G_e x[t]) * (U_e x[t]),  e = the j-th chosen expert;
+ *   y[t] = sum_j w_j D_e h_j.
+ * Logits, softmax and sums in fp32; w_j h_j enters the last product as two
+ * bfloat16 parts.
+ *
+ *  x            n_tokens x d, pitch ldx >= d, dtype x_dtype: GPTQ_BF16 or GPTQ_F16
+ *  router       n_experts x d, dtype x_dtype
+ *  up_*         the gate and up projections as one stored matrix of n_experts * 2 f rows
+ *               and d columns: expert e's gate rows 2 f e .. 2 f e + f - 1, then its up rows
+ *  down_*       the down projections as one of n_experts * d rows and f columns
+ *  bits, group_size   of both, as gptqs_linear_int8 (the group divides d and f)
+ *  y            n_tokens x d, pitch d, dtype y_dtype
+ *  topk_ids     n_tokens x top_k int32: the chosen experts, in falling order of l
+ *  topk_weights n_tokens x top_k fp32: w
+ *  ws           at least gptqs_moe_workspace_size(...) bytes, 16-byte aligned; contents on
+ *               entry are ignored
+ * Errors: negative sizes, top_k outside 1 .. n_experts, a pitch below d, a group that
+ * divides d or f not, odd d or f with 4-bit codes (3-bit: not multiples of 8), a bad
+ * dtype, a NULL pointer -> GPTQ_ERR_INVALID_ARG; x_dtype GPTQ_F32, bits or group_size not
+ * listed, n_tokens > 256, n_experts > 512, top_k > 32, d or f > 2^20 ->
+ * GPTQ_ERR_UNSUPPORTED; a missing, misaligned or short workspace -> GPTQ_ERR_WORKSPACE.
+ * n_tokens == 0 is a no-op.
+ */
+size_t gptqs_moe_workspace_size(int64_t n_tokens, int64_t d, int64_t f, int32_t n_experts, int32_t top_k);
+gptq_status gptqs_moe(const void* x, gptq_dtype x_dtype, int64_t n_tokens, int64_t d, int64_t ldx,
+                      const void* router, int32_t n_experts, int32_t top_k, int32_t renormalize, int64_t f,
+                      const uint8_t* up_codes, const uint16_t* up_scales_f16, const uint16_t* up_zeros_f16,
+                      const uint8_t* down_codes, const uint16_t* down_scales_f16, const uint16_t* down_zeros_f16,
+                      int32_t bits, int32_t group_size, void* y, gptq_dtype y_dtype,
+                      int32_t* topk_ids, float* topk_weights, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -81,6 +81,9 @@ def _load():
         "gptqs_linear_lora_workspace_size": (sz, [i64, i64, i32]),
         "gptqs_linear_lora": (ctypes.c_int, [vp, vp, vp, i64, i64, i32, i32, vp, ctypes.c_int, i64, i64, vp, vp, i32, i32,
                                              vp, vp, vp, ctypes.c_int, vp, sz, vp]),
+        "gptqs_moe_workspace_size": (sz, [i64, i64, i64, i32, i32]),
+        "gptqs_moe": (ctypes.c_int, [vp, ctypes.c_int, i64, i64, i64, vp, i32, i32, i32, i64, vp, vp, vp, vp, vp, vp, i32,
+                                     i32, vp, ctypes.c_int, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -495,4 +498,5 @@ def check_info(info: torch.Tensor, what: str = "gptq"):
         raise GptqError(ERR_NONFINITE, f"{what}: {status_string(ERR_NONFINITE)}")
 
 
-from .serving import Int8Rows, linear_int8, linear_lora, linear_lora_workspace_size, rmsnorm_int8  # noqa: E402,F401  (uses the names above)
+from .serving import (Int8Rows, linear_int8, linear_lora, linear_lora_workspace_size, moe,  # noqa: E402,F401
+                      moe_workspace_size, rmsnorm_int8)  # (the module uses the names above)

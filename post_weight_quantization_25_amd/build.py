@@ -12,7 +12,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgptq.so")
 SOURCES = ["api.hip", "hessian.hip", "prep.hip", "quant.hip", "sweep.hip", "linear.hip", "layers.hip", "obq.hip",
-           "serving.hip", "norm.hip", "linear_int8.hip", "linear_lora.hip"]
+           "serving.hip", "norm.hip", "linear_int8.hip", "linear_lora.hip",
+           "moe.hip"]
 ARCH = "gfx950"
 
 

@@ -35,4 +35,17 @@ gptq_status linear_lora_launch(const uint8_t* codes, const uint16_t* scales, con
                                const void* A, const void* B, int n_adapters, int rank, const int32_t* ids,
                                const float* scaling, void* y, gptq_dtype yt, void* ws, hipStream_t s);
 
+struct MoeCall {
+    const void* x; gptq_dtype xt; int64_t n, d, ldx, f;
+    const void* router; int E, k, renormalize;
+    const uint8_t* up_codes; const uint16_t* up_scales; const uint16_t* up_zeros;
+    const uint8_t* down_codes; const uint16_t* down_scales; const uint16_t* down_zeros;
+    int bits, group;
+    void* y; gptq_dtype yt; int32_t* ids; float* weights; void* ws;
+};
+constexpr int MOE_MAX_TOKENS = 256, MOE_MAX_EXPERTS = 512, MOE_MAX_TOPK = 32;
+constexpr int64_t MOE_MAX_WIDTH = (int64_t)1 << 20;   // d and f
+size_t moe_ws_bytes(int64_t n, int64_t f, int E, int k);
+gptq_status moe_launch(const MoeCall& c, hipStream_t s);
+
 }  // namespace gptq

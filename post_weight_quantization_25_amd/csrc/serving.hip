@@ -84,5 +84,43 @@ gptq_status gptqs_linear_lora(const uint8_t* codes, const uint16_t* scales_f16, 
                               A, B, n_adapters, rank, adapter_ids, scaling, y, y_dtype, ws, (hipStream_t)stream);
 }
 
+size_t gptqs_moe_workspace_size(int64_t n_tokens, int64_t d, int64_t f, int32_t n_experts, int32_t top_k) {
+    if (n_tokens <= 0 || d <= 0 || f <= 0 || n_experts < 1 || top_k < 1 || top_k > n_experts) return 0;
+    if (n_tokens > MOE_MAX_TOKENS || n_experts > MOE_MAX_EXPERTS || top_k > MOE_MAX_TOPK || d > MOE_MAX_WIDTH ||
+        f > MOE_MAX_WIDTH)
+        return 0;
+    return moe_ws_bytes(n_tokens, f, n_experts, top_k);
+}
+
+gptq_status gptqs_moe(const void* x, gptq_dtype x_dtype, int64_t n_tokens, int64_t d, int64_t ldx, const void* router,
+                      int32_t n_experts, int32_t top_k, int32_t renormalize, int64_t f, const uint8_t* up_codes,
+                      const uint16_t* up_scales_f16, const uint16_t* up_zeros_f16, const uint8_t* down_codes,
+                      const uint16_t* down_scales_f16, const uint16_t* down_zeros_f16, int32_t bits,
+                      int32_t group_size, void* y, gptq_dtype y_dtype, int32_t* topk_ids, float* topk_weights, void* ws,
+                      size_t ws_bytes, void* stream) {
+    if (n_tokens < 0 || d < 1 || f < 1 || !valid_dtype(x_dtype) || !valid_dtype(y_dtype)) return GPTQ_ERR_INVALID_ARG;
+    if (n_experts < 1 || top_k < 1 || top_k > n_experts || ldx < d) return GPTQ_ERR_INVALID_ARG;
+    int32_t group = group_size;
+    gptq_status st = check_stored(d, bits, group);
+    if (st == GPTQ_OK) st = check_stored(f, bits, group);
+    if (st != GPTQ_OK) return st;
+    if (x_dtype == GPTQ_F32 || n_tokens > MOE_MAX_TOKENS || n_experts > MOE_MAX_EXPERTS || top_k > MOE_MAX_TOPK ||
+        d > MOE_MAX_WIDTH || f > MOE_MAX_WIDTH)
+        return GPTQ_ERR_UNSUPPORTED;
+    if (n_tokens == 0) return GPTQ_OK;
+    if (!x || !router || !up_codes || !up_scales_f16 || !up_zeros_f16 || !down_codes || !down_scales_f16 ||
+        !down_zeros_f16 || !y || !topk_ids || !topk_weights)
+        return GPTQ_ERR_INVALID_ARG;
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 15) || ws_bytes < moe_ws_bytes(n_tokens, f, n_experts, top_k))
+        return GPTQ_ERR_WORKSPACE;
+    MoeCall c;
+    c.x = x; c.xt = x_dtype; c.n = n_tokens; c.d = d; c.ldx = ldx; c.f = f;
+    c.router = router; c.E = n_experts; c.k = top_k; c.renormalize = renormalize;
+    c.up_codes = up_codes; c.up_scales = up_scales_f16; c.up_zeros = up_zeros_f16;
+    c.down_codes = down_codes; c.down_scales = down_scales_f16; c.down_zeros = down_zeros_f16;
+    c.bits = bits; c.group = group; c.y = y; c.yt = y_dtype; c.ids = topk_ids; c.weights = topk_weights; c.ws = ws;
+    return moe_launch(c, (hipStream_t)stream);
+}
+
 }  // extern "C"
 #pragma GCC visibility pop

@@ -179,3 +179,50 @@ def linear_lora(q: Quantized, x: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
                                      _DT[out.dtype], None if ws is None else ws.data_ptr(),
                                      0 if ws is None else ws.numel(), s), "gptqs_linear_lora")
     return out
+
+
+def moe_workspace_size(n_tokens: int, d: int, f: int, n_experts: int, top_k: int) -> int:
+    return lib.gptqs_moe_workspace_size(n_tokens, d, f, n_experts, top_k)
+
+
+def moe(x: torch.Tensor, router: torch.Tensor, up: Quantized, down: Quantized, top_k: int, renormalize: bool = True,
+        out_dtype=torch.float32, out: torch.Tensor | None = None, ids: torch.Tensor | None = None,
+        weights: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+    """A mixture-of-experts layer for a few tokens on stored experts (gptqs_moe): router
+    (n_experts x d, x's dtype), softmax and top-k, silu(gate) * up, down, weighted sum.
+    ``up`` holds every expert's gate rows, then its up rows, as one layer of n_experts * 2 f
+    rows and d columns; ``down`` one of n_experts * d rows and f columns (``torch.cat`` of
+    the experts' codes, scales and zeros).  x (bf16/f16) may be strided.  Returns (y, ids,
+    weights): the chosen experts per token in falling order of their logits, int32, and
+    their weights, fp32."""
+    dev, dt = x.device, x.dtype
+    ldx = _rows(x, "x")
+    n, d = x.shape
+    if dt not in (torch.bfloat16, torch.float16):
+        raise ValueError("x must be bf16/f16")
+    if router.dim() != 2:
+        raise ValueError("router must be n_experts x d")
+    e = router.shape[0]
+    _tensor(router, "router", dt, (e, d), dev)
+    if (up.bits, up.group_size) != (down.bits, down.group_size):
+        raise ValueError("up and down must have the same bits and group size")
+    f = down.d_col
+    up_rows, down_rows = _stored(up, "up", dev), _stored(down, "down", dev)
+    if (up_rows, up.d_col, down_rows) != (e * 2 * f, d, e * d):
+        raise ValueError(f"up must be {e * 2 * f} x {d} and down {e * d} x {f}, not {up_rows} x {up.d_col} and "
+                         f"{down_rows} x {f}")
+    with _On(dev, stream) as s:
+        out = _out(out, n, d, out_dtype, dev)
+        if ids is None:
+            ids = torch.empty((n, top_k), dtype=torch.int32, device=dev)
+        _tensor(ids, "ids", torch.int32, (n, top_k), dev)
+        if weights is None:
+            weights = torch.empty((n, top_k), dtype=torch.float32, device=dev)
+        _tensor(weights, "weights", torch.float32, (n, top_k), dev)
+        ws = _workspace(moe_workspace_size(n, d, f, e, top_k), dev, ws)
+        _check(lib.gptqs_moe(x.data_ptr(), _DT[dt], n, d, ldx, router.data_ptr(), e, top_k, int(bool(renormalize)), f,
+                             up.codes.data_ptr(), up.scales.data_ptr(), up.zeros.data_ptr(), down.codes.data_ptr(),
+                             down.scales.data_ptr(), down.zeros.data_ptr(), up.bits, up.group_size, out.data_ptr(),
+                             _DT[out.dtype], ids.data_ptr(), weights.data_ptr(),
+                             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), s), "gptqs_moe")
+    return out, ids, weights

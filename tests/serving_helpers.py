@@ -54,3 +54,9 @@ def zero_parts(q, x):
     S, Z = (np.repeat(t.cpu().numpy().astype(np.float64), rep, axis=1) for t in (q.scales, q.zeros))
     zc = np.clip(np.rint(Z), -1 if q.bits == 8 else -240, 255 if q.bits == 8 else 240)
     return x.abs() @ torch.from_numpy(S * (np.abs(u - zc) + np.abs(Z - zc))).t()
+
+
+def part(q, r0, r1):
+    """Rows r0 .. r1 - 1 of a stored layer as a layer."""
+    import post_weight_quantization_25_amd as g
+    return g.Quantized(q.codes[r0:r1], q.scales[r0:r1], q.zeros[r0:r1], None, q.bits, q.group_size, q.d_col)

@@ -25,6 +25,9 @@ SIG = {
     "gptqs_linear_lora_workspace_size": (sz, [i64, i64, i32]),
     "gptqs_linear_lora": (dt, [vp, vp, vp, i64, i64, i32, i32, vp, dt, i64, i64, vp, vp, i32, i32, vp, vp, vp, dt, vp, sz,
                                vp]),
+    "gptqs_moe_workspace_size": (sz, [i64, i64, i64, i32, i32]),
+    "gptqs_moe": (dt, [vp, dt, i64, i64, i64, vp, i32, i32, i32, i64, vp, vp, vp, vp, vp, vp, i32, i32, vp, dt, vp, vp, vp,
+                       sz, vp]),
 }
 
 
@@ -131,3 +134,31 @@ def test_lora_argument_errors(lib):
     assert call(ws=None) == WORKSPACE and call(wsb=need - 1) == WORKSPACE
     assert call(ws=ctypes.c_void_p(0x1002)) == WORKSPACE   # not 4-byte aligned
     assert call(n=0, codes=None, x=None, y=None, ws=None) == OK
+
+
+def test_moe_argument_errors(lib):
+    size = lib.gptqs_moe_workspace_size
+    need = size(2, 256, 128, 8, 2)
+    assert need == 2 * 8 * 4 + 2 * (2 * 2 * 128 * 2)       # logits; inner values in two parts
+    for bad in ((0, 256, 128, 8, 2), (2, 0, 128, 8, 2), (2, 256, 0, 8, 2), (2, 256, 128, 0, 1), (2, 256, 128, 8, 0),
+                (2, 256, 128, 8, 9), (257, 256, 128, 8, 2), (2, 256, 128, 513, 2), (2, 256, 128, 64, 33)):
+        assert size(*bad) == 0, bad
+
+    def call(x=FAKE, xt=BF16, n=2, d=256, ldx=1024, R=FAKE, E=8, k=2, f=128, uc=FAKE, us=FAKE, uz=FAKE, dc=FAKE, ds=FAKE,
+             dz=FAKE, bits=4, G=128, y=FAKE, yt=F32, ids=FAKE, w=FAKE, ws=FAKE, wsb=1 << 30):
+        return lib.gptqs_moe(x, xt, n, d, ldx, R, E, k, 1, f, uc, us, uz, dc, ds, dz, bits, G, y, yt, ids, w, ws, wsb, None)
+
+    stored_errors(lambda d_col=256, **kw: call(d=d_col, f=d_col, **kw))
+    assert call(f=100) == INVALID_ARG                      # the group divides d alone
+    assert call(f=101, G=0) == INVALID_ARG and call(f=100, G=0, bits=3) == INVALID_ARG
+    assert call(yt=7) == INVALID_ARG and call(xt=7) == INVALID_ARG and call(xt=F32) == UNSUPPORTED
+    assert call(n=-1) == INVALID_ARG and call(d=0) == INVALID_ARG and call(f=0) == INVALID_ARG
+    assert call(k=0) == INVALID_ARG and call(k=9) == INVALID_ARG and call(E=0) == INVALID_ARG
+    assert call(ldx=255) == INVALID_ARG
+    for name in ("x", "R", "uc", "us", "uz", "dc", "ds", "dz", "y", "ids", "w"):
+        assert call(**{name: None}) == INVALID_ARG, name
+    assert call(n=257) == UNSUPPORTED and call(E=513) == UNSUPPORTED and call(E=64, k=33) == UNSUPPORTED
+    assert call(d=1 << 21, ldx=1 << 21) == UNSUPPORTED and call(f=1 << 21) == UNSUPPORTED
+    assert call(ws=None) == WORKSPACE and call(wsb=need - 1) == WORKSPACE
+    assert call(ws=ctypes.c_void_p(0x1008)) == WORKSPACE   # not 16-byte aligned
+    assert call(n=0, x=None, R=None, y=None, ws=None) == OK
