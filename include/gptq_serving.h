@@ -72,7 +72,8 @@ gptq_status gptqs_rmsnorm_int8(const void* x, gptq_dtype x_dtype, int64_t ldx,
  *  xq         n_tokens x d_col int8 (values -128 .. 127), pitch ldx >= d_col.
  *  x_scale    n_tokens fp32.
  *  y          n_tokens x d_row, pitch d_row, dtype y_dtype; written, not read.
- * Errors: as gptq_quantized_linear; another group_size -> GPTQ_ERR_UNSUPPORTED.
+ * Errors: as gptq_quantized_linear; another group_size, or more than 2^36 outputs ->
+ * GPTQ_ERR_UNSUPPORTED.
  */
 gptq_status gptqs_linear_int8(const uint8_t* codes, const uint16_t* scales_f16, const uint16_t* zeros_f16,
                               int64_t d_row, int64_t d_col, int32_t bits, int32_t group_size,

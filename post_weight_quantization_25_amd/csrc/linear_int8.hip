@@ -7,7 +7,7 @@
 // take the rows' 128-column chunks in turn and meet in LDS at the end.
 
 #include "serving.h"
-#include "stored_tile.h"
+#include "stored_gemm.h"
 
 namespace gptq {
 
@@ -62,8 +62,41 @@ __global__ __launch_bounds__(64 * TW) void int8_tile_kernel(Int8Args a) {
     }
 }
 
-template <int CB, int RUN>
+// Large batches: see stored_gemm.h.
+template <int CB, int PIECE, int BM>
+__global__ __launch_bounds__(256, 2) void int8_gemm_kernel(Int8Args a, int gm, int gn) {
+    typedef StoredGemm<X_I8, CB, PIECE, BM, 128> G;
+    __shared__ __align__(16) uint8_t lds[G::LDS_BYTES];
+    int tm, tn;
+    tile_of(gm, gn, tm, tn);
+    const int64_t tok0 = (int64_t)tm * BM, row0 = (int64_t)tn * GEMM_ROWS;
+    f32x4_t acc[G::MT][G::NT];
+    G::run(acc, a.L, a.d_row, reinterpret_cast<const uint8_t*>(a.x), a.ldx, a.n, tok0, row0, lds);
+    G::each_token(a.n, tok0, [&](int mt, int i, int64_t t) {
+        const float xs = a.xs[t];
+#pragma unroll
+        for (int nt = 0; nt < G::NT; ++nt) acc[mt][nt][i] *= xs;
+    });
+    if (a.yt == GPTQ_F32) G::template write<GPTQ_F32>(acc, a.y, a.d_row, a.n, tok0, row0);
+    else if (a.yt == GPTQ_BF16) G::template write<GPTQ_BF16>(acc, a.y, a.d_row, a.n, tok0, row0);
+    else G::template write<GPTQ_F16>(acc, a.y, a.d_row, a.n, tok0, row0);
+}
+
+template <int CB, int PIECE, int BM>
+static void launch_gemm(const Int8Args& a, hipStream_t s) {
+    const int gm = (int)((a.n + BM - 1) / BM), gn = (int)((a.d_row + GEMM_ROWS - 1) / GEMM_ROWS);
+    int8_gemm_kernel<CB, PIECE, BM><<<(unsigned)(gm * gn), 256, 0, s>>>(a, gm, gn);
+}
+
+template <int CB, int RUN, int PIECE>
 static gptq_status launch(const Int8Args& a, hipStream_t s) {
+    if (a.n > 64 && gemm_fits(a.L.d_col, a.ldx)) {
+        // 128 tokens per workgroup once that leaves two workgroups per CU, else 64
+        if ((a.n + 127) / 128 * ((a.d_row + 127) / 128) >= 512) launch_gemm<CB, PIECE, 128>(a, s);
+        else launch_gemm<CB, PIECE, 64>(a, s);
+        GPTQ_LAUNCH_CHECK();
+        return GPTQ_OK;
+    }
     const unsigned g16 = (unsigned)((a.d_row + 15) / 16), g32 = (unsigned)((a.d_row + 31) / 32);
     auto tiles = [&](int per) { return (unsigned)((a.n + per - 1) / per); };
     if (a.n <= 16) int8_tile_kernel<CB, RUN, 1, 1><<<dim3(g16, 1), 64 * TW, 0, s>>>(a);
@@ -75,7 +108,8 @@ static gptq_status launch(const Int8Args& a, hipStream_t s) {
 
 template <int CB>
 static gptq_status launch_runs(const Int8Args& a, int group, hipStream_t s) {
-    return group == 32 ? launch<CB, 8>(a, s) : group == 64 ? launch<CB, 16>(a, s) : launch<CB, 32>(a, s);
+    return group == 32 ? launch<CB, 8, 32>(a, s) : group == 64 ? launch<CB, 16, 64>(a, s)
+         : group == 128 ? launch<CB, 32, 128>(a, s) : launch<CB, 32, 0>(a, s);
 }
 
 gptq_status linear_int8_launch(const uint8_t* codes, const uint16_t* scales, const uint16_t* zeros, int64_t d_row,

@@ -10,6 +10,8 @@ namespace gptq {
 // Most tokens of a call: their tiles are on the grid's y extent (at most 65535 tiles of 64),
 // and one 1024-thread workgroup per token stays below 2^32 threads.
 constexpr int64_t SERVE_MAX_TOKENS = (int64_t)65535 * 64;
+// Most outputs of a product: its 128 x 128 tiles are one launch extent (below 2^24).
+constexpr int64_t SERVE_MAX_OUTPUTS = (int64_t)1 << 36;
 
 struct NormArgs {
     const void* x; int64_t ldx;

@@ -51,7 +51,8 @@ gptq_status gptqs_linear_int8(const uint8_t* codes, const uint16_t* scales_f16, 
     if (st != GPTQ_OK) return st;
     if (d_row == 0 || d_col == 0 || n_tokens == 0) return GPTQ_OK;
     if (!codes || !scales_f16 || !zeros_f16 || !xq || !x_scale || !y || ldx < d_col) return GPTQ_ERR_INVALID_ARG;
-    if (d_row > 2147483647LL / 64 || d_col > 2147483647LL / 64 || n_tokens > SERVE_MAX_TOKENS)
+    if (d_row > 2147483647LL / 64 || d_col > 2147483647LL / 64 || n_tokens > SERVE_MAX_TOKENS ||
+        d_row > SERVE_MAX_OUTPUTS / n_tokens)
         return GPTQ_ERR_UNSUPPORTED;
     return linear_int8_launch(codes, scales_f16, zeros_f16, d_row, d_col, bits, group_size, xq, ldx, x_scale, n_tokens,
                               y, y_dtype, (hipStream_t)stream);
@@ -76,7 +77,8 @@ gptq_status gptqs_linear_lora(const uint8_t* codes, const uint16_t* scales_f16, 
     if (d_row == 0 || d_col == 0 || n_tokens == 0) return GPTQ_OK;
     if (!codes || !scales_f16 || !zeros_f16 || !x || !y || ldx < d_col) return GPTQ_ERR_INVALID_ARG;
     if (n_adapters > 0 && (!A || !B || !adapter_ids)) return GPTQ_ERR_INVALID_ARG;
-    if (d_row > 2147483647LL / 64 || d_col > 2147483647LL / 64 || n_tokens > SERVE_MAX_TOKENS)
+    if (d_row > 2147483647LL / 64 || d_col > 2147483647LL / 64 || n_tokens > SERVE_MAX_TOKENS ||
+        d_row > SERVE_MAX_OUTPUTS / n_tokens)
         return GPTQ_ERR_UNSUPPORTED;
     if (n_adapters > 0 && (!ws || (reinterpret_cast<uintptr_t>(ws) & 3) || ws_bytes < lora_ws_bytes(n_tokens, d_col, rank)))
         return GPTQ_ERR_WORKSPACE;

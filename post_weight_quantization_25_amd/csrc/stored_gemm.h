@@ -1,0 +1,425 @@
+// Large batches: tokens x d_col activations (8- or 16-bit) with a stored layer on the
+// matrix cores.
+//
+// A workgroup of four waves owns BM tokens x 128 weight rows; a wave takes all BM tokens
+// and 32 of the rows.  So every code is loaded, by the lane that needs it, from memory
+// straight into registers and decoded once per workgroup (u - zc in the operand's type, see
+// stored_tile.h), and only the activations, which all four waves need, go through LDS: in
+// slabs of a token's row, two buffers, one
+// barrier per slab.  While slab s is multiplied, slab s + 1 is on its way into registers.
+// 16-byte pieces of a slab's row are XOR-swizzled by the row, which spreads a fragment's
+// 16 rows over all banks.
+//
+// As in stored_tile.h, a piece is the columns of one scale (128, 64 or 32), of which lane
+// l holds the RUN = piece / 4 columns from RUN (l / 16) on, on both sides.  PIECE 0 is one
+// scale per row: pieces of 128 columns whose sums run on through the row.
+#pragma once
+#include "stored_tile.h"
+
+namespace gptq {
+
+constexpr int GEMM_ROWS = 128;
+
+// Workgroup -> tile: XCD k (workgroups k, k + 8, ..) takes a contiguous run of tiles, and
+// within it token tiles run fastest in stripes of 8, so that the rows and the activations
+// in flight on one XCD stay in its L2.
+GPTQ_DEV void tile_of(int gm, int gn, int& tm, int& tn) {
+    const int total = gm * gn, lin = blockIdx.x;
+    const int base = total / 8, rest = total % 8, xcd = lin % 8;
+    const int id = xcd * base + (xcd < rest ? xcd : rest) + lin / 8;
+    const int stripe = id / (8 * gn), in = id % (8 * gn);
+    const int high = gm - 8 * stripe < 8 ? gm - 8 * stripe : 8;
+    tm = 8 * stripe + in % high;
+    tn = in / high;
+}
+
+// What a tile's 32-bit offsets and a row's 32-bit integer sums take (128 x 127 x 2^17 < 2^31).
+inline bool gemm_fits(int64_t d_col, int64_t ldx_bytes) { return d_col <= (1 << 17) && ldx_bytes <= (1 << 24); }
+
+// A wave-uniform address made visible as one: loads take it from scalar registers and add a
+// lane's 32-bit offset themselves.
+template <typename T>
+GPTQ_DEV const T* uniform(const T* p) {
+    const uint64_t b = (uint64_t)(uintptr_t)p;
+    return reinterpret_cast<const T*>((uintptr_t)(((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)) << 32) |
+                                                  (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)b)));
+}
+
+template <int X, int CB, int PIECE, int BM, int SLAB>   // SLAB: bytes of a token's row in LDS
+struct StoredGemm {
+    static constexpr int XB = xbytes<X>();
+    static constexpr int KS = SLAB / XB;                       // columns per slab
+    static constexpr int MT = BM / 16, NT = 2;                 // 16 x 16 tiles per wave
+    static constexpr int PC = PIECE ? PIECE : KS < 128 ? KS : 128;             // columns per piece
+    static constexpr int PP = KS / PC;                         // pieces per slab
+    static constexpr int RUN = PC / 4;
+    static constexpr int KB = X == X_I8 && RUN == 8 ? 8 : 16;  // bytes of a lane's operand per product
+    static constexpr int STEPS = RUN * XB / KB;                // products per piece
+    static constexpr int AU = BM * (SLAB / 16) / 256;          // 16-byte activation pieces per thread
+    static constexpr int LDS_BYTES = 2 * BM * SLAB;
+    typedef typename Acc<X>::t sum_t;
+
+    // A fragment read serves 16 lanes at a time: 8 rows (4 g .. 4 g + 3 of two g) of one lane
+    // group and the other 8 rows of the next, whose pieces are RUN XB / 16 further on.  The
+    // swizzle spreads them over the 16 16-byte columns of the 64 banks.
+    static GPTQ_DEV int slab_at(int row, int piece16) {
+        int f = row & (SLAB / 16 - 1);
+        if constexpr (SLAB == 128) {
+            const int g = row >> 1;
+            f = RUN * XB == 32 ? ((g & 1) << 1) | (g & 4) | (((g >> 1) ^ (g >> 2)) & 1) : g & 7;
+        }
+        return row * SLAB + 16 * (piece16 ^ f);
+    }
+
+    struct Codes {                                             // a slab's codes of the lane's rows
+        Raw<CB, RUN> c[NT][PP];
+        uint16_t S[NT][PP], z[NT][PP];
+    };
+    struct Frag { uint32_t w[KB / 4]; };
+    struct Operand {                                           // the same, decoded
+        Frag f[PP][NT][STEPS];
+        float S[PP][NT], rz[PP][NT];
+    };
+
+    // acc[mt][nt]: lane l's value i is token 16 mt + 4 (l / 16) + i, weight row 32 wave + 16 nt
+    // + l % 16 of the tile.
+    static GPTQ_DEV void run(f32x4_t (&acc)[MT][NT], const Stored& L, int64_t d_row, const uint8_t* x, int64_t ldx_bytes,
+                             int64_t n, int64_t tok0, int64_t row0, uint8_t* lds) {
+        const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n16 = lane & 15, q = lane >> 4;
+        const int nslab = (int)((L.d_col + KS - 1) / KS), nfull = (int)(L.d_col / KS);
+
+        // tile-relative offsets fit 32 bits (gemm_fits); rows past the end re-read the last
+        const uint8_t* xt = x + tok0 * ldx_bytes;
+        const uint8_t* ct = L.codes + row0 * L.code_ld;
+        const uint16_t* st = L.scales + row0 * L.n_groups;
+        const uint16_t* zt = L.zeros + row0 * L.n_groups;
+        const int toks = (int)(n - tok0 < BM ? n - tok0 : BM);
+        const int rows = (int)(d_row - row0 < GEMM_ROWS ? d_row - row0 : GEMM_ROWS);
+        uint32_t aoff[AU];
+#pragma unroll
+        for (int j = 0; j < AU; ++j) {
+            const int u = tid + 256 * j, r = u / (SLAB / 16);
+            aoff[j] = (uint32_t)(r < toks ? r : toks - 1) * (uint32_t)ldx_bytes + 16 * (u % (SLAB / 16));
+        }
+        uint32_t boff[NT], soff[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = 32 * wave + 16 * nt + n16, rr = r < rows ? r : rows - 1;
+            boff[nt] = (uint32_t)rr * (uint32_t)L.code_ld + q * (RUN * CB / 8);
+            soff[nt] = (uint32_t)rr * (uint32_t)L.n_groups;
+        }
+
+        auto load_a = [&](u32x4_t (&a)[AU], int s) {
+            const uint8_t* xs = uniform(xt + (int64_t)s * SLAB);
+#pragma unroll
+            for (int j = 0; j < AU; ++j) __builtin_memcpy(&a[j], xs + aoff[j], 16);
+        };
+        auto store_a = [&](const u32x4_t (&a)[AU], int s) {
+            uint8_t* buf = lds + (s & 1) * BM * SLAB;
+#pragma unroll
+            for (int j = 0; j < AU; ++j) {
+                const int u = tid + 256 * j;
+                *reinterpret_cast<u32x4_t*>(buf + slab_at(u / (SLAB / 16), u % (SLAB / 16))) = a[j];
+            }
+        };
+        auto load_b = [&](Codes& b, int s) {
+            const uint8_t* cs = uniform(ct + (int64_t)s * (KS / 8 * CB));
+            const uint16_t *ss = uniform(st + (PIECE ? s * PP : 0)), *zs = uniform(zt + (PIECE ? s * PP : 0));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int p = 0; p < PP; ++p) {
+                    b.c[nt][p] = load_raw<CB, RUN>(cs + boff[nt] + p * (PC / 8 * CB));
+                    if constexpr (PIECE != 0) {
+                        b.S[nt][p] = ss[soff[nt] + p];
+                        b.z[nt][p] = zs[soff[nt] + p];
+                    }
+                }
+        };
+        // the slab in which the rows end: zeros behind them
+        const int last = (int)(L.d_col - (int64_t)nfull * KS);  // its columns
+        auto tail_a = [&]() {
+            const uint8_t* xs = xt + (int64_t)nfull * SLAB;
+            uint8_t* buf = lds + (nfull & 1) * BM * SLAB;
+#pragma unroll
+            for (int j = 0; j < AU; ++j) {
+                const int u = tid + 256 * j, c = u % (SLAB / 16), have = last * XB - 16 * c;
+                u32x4_t v = {0u, 0u, 0u, 0u};
+                if (have >= 16) __builtin_memcpy(&v, xs + aoff[j], 16);
+                uint8_t* dst = buf + slab_at(u / (SLAB / 16), c);
+                *reinterpret_cast<u32x4_t*>(dst) = v;
+                for (int e = 0; e < have && have < 16; e += XB) {   // the piece in which they end
+                    if constexpr (XB == 1) dst[e] = xs[aoff[j] + e];
+                    else __builtin_memcpy(dst + e, xs + aoff[j] + e, 2);
+                }
+            }
+        };
+        auto tail_b = [&](Codes& b) {
+            const uint8_t* cs = ct + (int64_t)nfull * (KS / 8 * CB);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int p = 0; p < PP; ++p) {
+                    const int left = last - p * PC - q * RUN;
+                    b.c[nt][p] = load_raw_tail<CB, RUN>(cs + boff[nt] + p * (PC / 8 * CB), left < RUN ? left : RUN);
+                    if constexpr (PIECE != 0) {
+                        int g = nfull * PP + p;
+                        g = g < L.n_groups ? g : L.n_groups - 1;   // pieces behind the row
+                        b.S[nt][p] = st[soff[nt] + g];
+                        b.z[nt][p] = zt[soff[nt] + g];
+                    }
+                }
+        };
+
+        float rowS[NT], rowz[NT];                              // PIECE 0: the row's scale and zero
+        bool row_rest = false;
+        if constexpr (PIECE == 0) {
+            bool r = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                rowS[nt] = f16_bits_to_f32(st[soff[nt]]);
+                rowz[nt] = f16_bits_to_f32(zt[soff[nt]]);
+                r = r || !(rowz[nt] - zero_part<X, CB>(rowz[nt]) == 0.f);
+            }
+            row_rest = __ballot(r) != 0;
+        }
+        sum_t cs[PIECE == 0 ? MT : 1][NT], xs[PIECE == 0 ? MT : 1];   // PIECE 0: the row's running sums
+        if constexpr (PIECE == 0) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                xs[mt] = sum_t{0, 0, 0, 0};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) cs[mt][nt] = sum_t{0, 0, 0, 0};
+            }
+        } else {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        }
+
+        auto decode = [&](Operand& o, const Codes& b) {
+#pragma unroll
+            for (int p = 0; p < PP; ++p)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float z = PIECE == 0 ? rowz[nt] : f16_bits_to_f32(b.z[nt][p]), zc = zero_part<X, CB>(z);
+                    o.S[p][nt] = PIECE == 0 ? 0.f : f16_bits_to_f32(b.S[nt][p]);
+                    o.rz[p][nt] = z - zc;
+#pragma unroll
+                    for (int t = 0; t < STEPS; ++t) o.f[p][nt][t] = frag_b(b.c[nt][p], t, zc);
+                }
+        };
+        auto step = [&](const Operand& o, int s) {
+            const uint8_t* buf = lds + (s & 1) * BM * SLAB;
+#pragma unroll
+            for (int p = 0; p < PP; ++p) {
+                if constexpr (PIECE == 0) {
+                    row_products(cs, o.f[p], buf, p);
+                } else {
+                    products(acc, o.f[p], buf, p, o.S[p]);
+                    bool r = false;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) r = r || !(o.rz[p][nt] == 0.f);
+                    if (__ballot(r) != 0) rests(acc, buf, p, o.S[p], o.rz[p]);
+                }
+            }
+            if (PIECE == 0 && row_rest) piece_sums(xs, buf);
+        };
+
+        // Whole slabs: slab s + 2 is on its way into the registers that slab s has left while
+        // slab s is multiplied (two slabs' time for a load); s + 1 goes to LDS behind it.
+        u32x4_t a0[AU], a1[AU];
+        Codes b0, b1;
+        Operand o;
+        if (nfull > 0) { load_a(a0, 0); load_b(b0, 0); }
+        if (nfull > 1) { load_a(a1, 1); load_b(b1, 1); }
+        if (nfull > 0) store_a(a0, 0);
+        int s = 0;
+        auto whole = [&](u32x4_t (&a)[AU], const u32x4_t (&a_next)[AU], Codes& b) {
+            __syncthreads();
+            decode(o, b);
+            if (s + 2 < nfull) { load_a(a, s + 2); load_b(b, s + 2); }
+            __builtin_amdgcn_sched_barrier(0);                 // the loads leave before the products begin
+            step(o, s);
+            if (s + 1 < nfull) store_a(a_next, s + 1);
+            ++s;
+        };
+        while (s + 1 < nfull) { whole(a0, a1, b0); whole(a1, a0, b1); }
+        if (s < nfull) whole(a0, a1, b0);
+        if (nslab > nfull) {                                   // the slab in which the rows end
+            __syncthreads();
+            tail_a();
+            tail_b(b0);
+            __syncthreads();
+            decode(o, b0);
+            step(o, s);
+        }
+        if constexpr (PIECE == 0) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float rz = rowz[nt] - zero_part<X, CB>(rowz[nt]);
+                    settle(cs[mt][nt]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[mt][nt][i] = rowS[nt] * fmaf(-rz, (float)xs[mt][i], (float)cs[mt][nt][i]);
+                }
+        }
+    }
+
+    // f(mt, i, token) for the lane's token rows; rows past the end are given the last token.
+    template <typename F>
+    static GPTQ_DEV void each_token(int64_t n, int64_t tok0, F&& f) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t t = tok0 + 16 * mt + 4 * ((threadIdx.x & 63) >> 4) + i;
+                f(mt, i, t < n ? t : n - 1);
+            }
+    }
+
+    template <gptq_dtype YT>
+    static GPTQ_DEV void write(const f32x4_t (&acc)[MT][NT], void* y, int64_t d_row, int64_t n, int64_t tok0, int64_t row0) {
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t t = tok0 + 16 * mt + 4 * (lane >> 4) + i;
+                if (t >= n) continue;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int64_t r = row0 + 32 * wave + 16 * nt + (lane & 15);
+                    if (r < d_row) store_as<YT>(y, t * d_row + r, acc[mt][nt][i]);
+                }
+            }
+    }
+
+private:
+    static GPTQ_DEV sum_t product(const Frag& a, const Frag& b, sum_t c) {
+        if constexpr (KB == 8) return mfma8_i8(a.w[0], a.w[1], b.w[0], b.w[1], c);
+        else return mfma16<X>(u32x4_t{a.w[0], a.w[1], a.w[2], a.w[3]}, u32x4_t{b.w[0], b.w[1], b.w[2], b.w[3]}, c);
+    }
+    // the lane's operand of product t of piece p, token row `row` of the tile
+    static GPTQ_DEV Frag frag_a(const uint8_t* buf, int row, int p, int t) {
+        const int q = (threadIdx.x & 63) >> 4, byte = (p * PC + q * RUN) * XB + t * KB;
+        Frag f;
+        __builtin_memcpy(f.w, __builtin_assume_aligned(buf + slab_at(row, byte >> 4) + (KB == 8 ? (byte & 8) : 0), KB), KB);
+        return f;
+    }
+    static GPTQ_DEV Frag frag_b(const Raw<CB, RUN>& c, int t, float zc) {
+        Frag f;
+        if constexpr (X == X_I8) {
+            const uint32_t zz = (uint32_t)((int)zc * 0x01010101);
+#pragma unroll
+            for (int e = 0; e < KB / 4; ++e) f.w[e] = minus_zero_i8<CB>(code_bytes4<CB, RUN>(c, KB / 4 * t + e), zz);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t o[2];
+                minus_zero_16<X>(code_bytes4<CB, RUN>(c, 2 * t + h), zc, o);
+                f.w[2 * h] = o[0];
+                f.w[2 * h + 1] = o[1];
+            }
+        }
+        return f;
+    }
+    static GPTQ_DEV Frag ones() {
+        Frag f;
+#pragma unroll
+        for (int e = 0; e < KB / 4; ++e) f.w[e] = ones_word<X>();
+        return f;
+    }
+
+    // Products of one piece, scaled into acc.  A token tile's products are issued before the
+    // last one's sums are scaled, so that the vector unit works while the matrix unit does.
+    static GPTQ_DEV void products(f32x4_t (&acc)[MT][NT], const Frag (&bf)[NT][STEPS], const uint8_t* buf, int p,
+                                  const float (&S)[NT]) {
+        const int n16 = threadIdx.x & 15;
+        sum_t cs[2][NT];
+        constexpr int AHEAD = 2;                               // token tiles whose fragments are on their way
+        Frag a[AHEAD + 1][STEPS];
+#pragma unroll
+        for (int m = 0; m < AHEAD; ++m)
+#pragma unroll
+            for (int t = 0; t < STEPS; ++t) a[m][t] = frag_a(buf, 16 * m + n16, p, t);
+#pragma unroll
+        for (int mt = 0; mt <= MT; ++mt) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (mt + AHEAD < MT) {
+#pragma unroll
+                for (int t = 0; t < STEPS; ++t) a[(mt + AHEAD) % (AHEAD + 1)][t] = frag_a(buf, 16 * (mt + AHEAD) + n16, p, t);
+            }
+            if (mt < MT) {
+#pragma unroll
+                for (int t = 0; t < STEPS; ++t)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        cs[mt & 1][nt] = product(a[mt % (AHEAD + 1)][t], bf[nt][t], t == 0 ? sum_t{0, 0, 0, 0} : cs[mt & 1][nt]);
+            }
+            if (mt > 0) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[mt - 1][nt][i] = fmaf(S[nt], (float)cs[(mt - 1) & 1][nt][i], acc[mt - 1][nt][i]);
+            }
+            // one product, then its share of the scaling, so that both units are fed
+            constexpr int V = 8 * NT / (STEPS * NT);
+#pragma unroll
+            for (int k = 0; k < STEPS * NT; ++k) {
+                if (k == 0) __builtin_amdgcn_sched_group_barrier(0x100, STEPS, 0);   // the next tile's LDS reads
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                   // MFMA
+                __builtin_amdgcn_sched_group_barrier(0x002, V, 0);                   // VALU
+            }
+        }
+    }
+
+    // What the zeros' rests take off a piece: (z - zc) sum x.
+    static GPTQ_DEV void rests(f32x4_t (&acc)[MT][NT], const uint8_t* buf, int p, const float (&S)[NT], const float (&rz)[NT]) {
+        const int n16 = threadIdx.x & 15;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            sum_t xs = {0, 0, 0, 0};
+#pragma unroll
+            for (int t = 0; t < STEPS; ++t) xs = product(frag_a(buf, 16 * mt + n16, p, t), ones(), xs);
+            settle(xs);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[mt][nt][i] = fmaf(-S[nt] * rz[nt], (float)xs[i], acc[mt][nt][i]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+
+    static GPTQ_DEV void row_products(sum_t (&cs)[PIECE == 0 ? MT : 1][NT], const Frag (&bf)[NT][STEPS], const uint8_t* buf,
+                                      int p) {
+        const int n16 = threadIdx.x & 15;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int t = 0; t < STEPS; ++t) {
+                const Frag a = frag_a(buf, 16 * mt + n16, p, t);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) cs[mt][nt] = product(a, bf[nt][t], cs[mt][nt]);
+            }
+    }
+
+    // sum x of a slab, per token
+    static GPTQ_DEV void piece_sums(sum_t (&xs)[PIECE == 0 ? MT : 1], const uint8_t* buf) {
+        const int n16 = threadIdx.x & 15;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int p = 0; p < PP; ++p)
+#pragma unroll
+                for (int t = 0; t < STEPS; ++t) xs[mt] = product(frag_a(buf, 16 * mt + n16, p, t), ones(), xs[mt]);
+            settle(xs[mt]);
+        }
+    }
+};
+
+}  // namespace gptq

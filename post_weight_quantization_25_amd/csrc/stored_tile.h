@@ -166,6 +166,7 @@ struct Stored {
     const uint16_t* scales; const uint16_t* zeros;     // fp16, rows x n_groups
     int64_t d_col;
     int n_groups, cpg;                                 // cpg: chunks per group (128-column pieces)
+    int gshift;                                        // log2 of the group's columns (groups)
 };
 
 // Sums of RB blocks of 16 weight rows with NTT tiles of 16 tokens over the chunks c0, c0 +
@@ -288,10 +289,18 @@ GPTQ_DEV void stored_accumulate(f32x4_t (&acc)[NTT][RB], const Stored& L, const 
     }
 }
 
+// One output, rounded once (to nearest even) by the hardware's conversions.
+template <gptq_dtype YT>
+GPTQ_DEV void store_as(void* y, int64_t idx, float v) {
+    if constexpr (YT == GPTQ_F32) reinterpret_cast<float*>(y)[idx] = v;
+    else if constexpr (YT == GPTQ_BF16) reinterpret_cast<__bf16*>(y)[idx] = (__bf16)v;
+    else reinterpret_cast<_Float16*>(y)[idx] = (_Float16)v;
+}
+
 GPTQ_DEV void store_out(void* y, gptq_dtype t, int64_t idx, float v) {
-    if (t == GPTQ_F32) reinterpret_cast<float*>(y)[idx] = v;
-    else if (t == GPTQ_BF16) reinterpret_cast<uint16_t*>(y)[idx] = f32_to_bf16_bits(v);
-    else reinterpret_cast<uint16_t*>(y)[idx] = f32_to_f16_bits(v);
+    if (t == GPTQ_F32) store_as<GPTQ_F32>(y, idx, v);
+    else if (t == GPTQ_BF16) store_as<GPTQ_BF16>(y, idx, v);
+    else store_as<GPTQ_F16>(y, idx, v);
 }
 
 // Host: the stored layer's layout; group 0 = one scale per row.
@@ -300,6 +309,7 @@ inline Stored stored_layer(const uint8_t* codes, const uint16_t* scales, const u
     Stored L;
     L.codes = codes; L.code_ld = bits == 3 ? d_col / 8 * 3 : bits == 4 ? d_col / 2 : d_col;
     L.scales = scales; L.zeros = zeros; L.d_col = d_col;
+    L.gshift = group == 32 ? 5 : group == 64 ? 6 : 7;
     L.n_groups = group > 0 ? (int)(d_col / group) : 1;
     const int64_t nck = (d_col + SCK - 1) / SCK;
     L.cpg = group > 0 ? 1 : (int)nck;      // of the 128-column pieces; groups are 128 or the row

@@ -46,13 +46,15 @@ def out_rounding(ref, t):
     return fi.eps / 2 * ref.abs() + fi.smallest_normal * fi.eps / 2
 
 
-def zero_parts(q, x):
-    """S sum_c |x_c| (|u - zc| + |z - zc|), zc the whole number next to z within 240 of 0 (255
-    for 8-bit codes): what the 16-bit products add up, per token and row."""
+def zero_parts(q, x, eight=False):
+    """S sum_c |x_c| (|u - zc| + |z - zc|): what the products add up, per token and row.  zc is
+    the whole number next to z within what the operand takes: 16 bits, 240 on either side
+    of 0 (8-bit codes: -1 .. 255); 8 bits (``eight``), -112 .. 127 (8-bit codes: 128)."""
     u = o.unpack(q.codes.cpu().numpy(), q.bits).astype(np.float64)
     rep = u.shape[1] // q.scales.shape[1]
     S, Z = (np.repeat(t.cpu().numpy().astype(np.float64), rep, axis=1) for t in (q.scales, q.zeros))
-    zc = np.clip(np.rint(Z), -1 if q.bits == 8 else -240, 255 if q.bits == 8 else 240)
+    low, high = ((128, 128) if q.bits == 8 else (-112, 127)) if eight else ((-1, 255) if q.bits == 8 else (-240, 240))
+    zc = np.clip(np.rint(Z), low, high)
     return x.abs() @ torch.from_numpy(S * (np.abs(u - zc) + np.abs(Z - zc))).t()
 
 

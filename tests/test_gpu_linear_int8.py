@@ -1,18 +1,19 @@
 """gptqs_linear_int8 against its definition in 64 bits.
 
 Tolerance.  Integer sums per piece (32 to 128 columns of one scale, or a whole row of one
-scale) are exact and below 2^24 or rounded once; each piece then takes two fp32 fused
-multiply-adds (the zero's rest, the scale), the 8 waves' sums are added and x_scale
-multiplies once.  Every rounding is at most 2^-24 of a magnitude bounded by M = |x_scale|
-sum |xq| |What|, so |y - exact| <= (2 pieces + 12) 2^-24 M (1 + 2^-10), with pieces counted
-as 32 columns, plus half a step of a 16-bit output."""
+scale) are exact and below 2^24 or rounded once.  Each piece then takes at most three fp32
+operations (the scaled sum; the zero's rest z - zc, multiplied with the scale, times sum
+xq), the 8 waves' sums are added and x_scale multiplies once.  Both parts of a piece are
+bounded by its share of M = |x_scale| S sum |xq| (|u - zc| + |z - zc|), and every rounding
+is at most 2^-24 of what has been added up, so |y - exact| <= (3 pieces + 12) 2^-24 M (1 +
+2^-10), with pieces counted as 32 columns, plus half a step of a 16-bit output."""
 import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 
 from gpu_helpers import log
-from serving_helpers import BF, F32, HF, out_rounding, stored
+from serving_helpers import BF, F32, HF, out_rounding, stored, zero_parts
 
 pytestmark = pytest.mark.gpu
 
@@ -23,10 +24,10 @@ def rows8(n, d, seed, low=-128):
             torch.from_numpy((rng.random(n) * 0.1 + 0.001).astype(np.float32)).cuda())
 
 
-def compare(y, xq, xs, What, yt, note=""):
+def compare(y, q, xq, xs, What, yt, note=""):
     x = xq.cpu().double() * xs.cpu().double()[:, None]
-    ref, mag = x @ What.t(), x.abs() @ What.abs().t()
-    bound = (2 * ((What.shape[1] + 31) // 32) + 12) * 2.0 ** -24 * (1 + 2.0 ** -10) * mag + out_rounding(ref, yt)
+    ref, mag = x @ What.t(), zero_parts(q, x, eight=True)
+    bound = (3 * ((What.shape[1] + 31) // 32) + 12) * 2.0 ** -24 * (1 + 2.0 ** -10) * mag + out_rounding(ref, yt)
     err = (y.cpu().double() - ref).abs()
     log(f"  max |err| / bound = {float((err / bound.clamp_min(1e-300)).max()):.3f} {note}")
     assert y.dtype == yt and bool((err <= bound).all())
@@ -43,7 +44,8 @@ CASES = [
     (96, 512, 3, 32, 50, F32, "far"), (66, 512, 8, 128, 24, F32, "far"), (66, 512, 8, 32, 12, F32, "fraction"),
     (200, 1100, 4, 0, 100, BF, "whole"), (129, 4098, 4, 0, 130, F32, "fraction"), (513, 1024, 4, 128, 257, F32, "whole"),
     (260, 896, 4, 32, 300, F32, "whole"), (255, 576, 4, 64, 333, BF, "far"), (384, 1111, 8, 0, 200, F32, "whole"),
-    (300, 1000, 3, 0, 290, F32, "symmetric"), (4001, 2048, 3, 0, 520, BF, "symmetric"), (1111, 512, 8, 128, 640, HF, "symmetric"),
+    (300, 1000, 3, 0, 290, F32, "symmetric"), (1030, 640, 4, 128, 2050, BF, "fraction"), (3000, 256, 4, 64, 2700, F32, "whole"),
+    (4100, 130, 4, 0, 2049, HF, "far"), (2100, 352, 3, 32, 4000, BF, "whole"), (4097, 300, 8, 0, 2100, F32, "whole"), (4001, 2048, 3, 0, 520, BF, "symmetric"), (1111, 512, 8, 128, 640, HF, "symmetric"),
 ]
 
 
@@ -55,7 +57,7 @@ def test_int8_parity(d_row, d_col, bits, group, n, yt, zeros):
     xq, xs = rows8(n, d_col, 2)
     y = g.linear_int8(q, g.Int8Rows(xq, xs), out_dtype=yt)
     torch.cuda.synchronize()
-    compare(y, xq, xs, What, yt)
+    compare(y, q, xq, xs, What, yt)
     assert torch.equal(g.linear_int8(q, g.Int8Rows(xq, xs), out_dtype=yt), y)
 
 
@@ -73,7 +75,7 @@ def test_int8_largest_sums(bits, group, n):
     xs = torch.ones(n, device="cuda")
     S = q.scales.cpu().double()
     What = (S * (2 ** bits - 1)).repeat_interleave(d_col // S.shape[1], 1)
-    compare(g.linear_int8(q, g.Int8Rows(xq, xs)), xq, xs, What, F32)
+    compare(g.linear_int8(q, g.Int8Rows(xq, xs)), q, xq, xs, What, F32)
 
 
 @pytest.mark.parametrize("n", [1, 20, 150])
@@ -88,7 +90,7 @@ def test_int8_strided_rows_and_tokens_apart(n):
     buf[:, 3:3 + d_col] = xq
     big = torch.full((n + 2, d_row), 7.0, device="cuda")
     y = g.linear_int8(q, g.Int8Rows(buf[:, 3:3 + d_col], xs), out=big[1:1 + n])
-    compare(y, xq, xs, What, F32)
+    compare(y, q, xq, xs, What, F32)
     assert bool((big[0] == 7).all()) and bool((big[n + 1] == 7).all())
     xs2 = xs.clone()
     xs2[n // 2] = float("nan")
@@ -127,7 +129,7 @@ def test_norm_then_product():
     w = (1 + 0.1 * torch.randn(d, generator=gen)).to(BF).cuda()
     rows, h = g.rmsnorm_int8(x, w, r)
     y = g.linear_int8(q, rows)
-    compare(y, rows.q, rows.scale, What, F32)
+    compare(y, q, rows.q, rows.scale, What, F32)
     v = h.cpu().double()
     norm = v * w.cpu().double() / torch.sqrt((v * v).mean(1, keepdim=True) + 1e-6)
     step = rows.scale.cpu().double()[:, None] * 0.5 * (1 + 2.0 ** -20)

@@ -107,6 +107,7 @@ def test_int8_argument_errors(lib):
         assert call(**{name: None}) == INVALID_ARG, name
     assert call(n=65535 * 64 + 1) == UNSUPPORTED
     assert call(d_row=2 ** 31 // 64) == UNSUPPORTED
+    assert call(d_row=1 << 20, n=(1 << 16) + 1) == UNSUPPORTED   # more than 2^36 outputs
     assert call(n=0, codes=None, x=None, y=None) == OK
     assert call(d_row=0, codes=None, x=None, y=None) == OK
 
