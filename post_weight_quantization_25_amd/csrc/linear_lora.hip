@@ -12,7 +12,7 @@
 // keeps an infinity or a NaN of one adapter away from the tokens of the others.
 
 #include "serving.h"
-#include "stored_tile.h"
+#include "stored_gemm.h"
 
 namespace gptq {
 
@@ -177,8 +177,120 @@ __global__ __launch_bounds__(64 * TW) void lora_tile_kernel(LoraArgs a) {
     }
 }
 
-template <int X, int CB, int RUN>
+// Large batches (see stored_gemm.h).  The adapters' product is added to the finished sums on
+// the matrix cores, 32 ranks at a time: s_a v as two bfloat16 parts (v is fp32; together
+// they keep it to 2^-17) with B's rows, bfloat16 as they are, fp16 as two exact bfloat16
+// parts (fp16's 11 bits and its range fit), for each distinct adapter among the wave's
+// tokens, into the rows of the tokens that have it.
+template <int X, int CB, int PIECE, int BM>
+__global__ __launch_bounds__(256, 2) void lora_gemm_kernel(LoraArgs a, int gm, int gn) {
+    typedef StoredGemm<X, CB, PIECE, BM, 128> G;
+    __shared__ __align__(16) uint8_t lds[G::LDS_BYTES];
+    int tm, tn;
+    tile_of(gm, gn, tm, tn);
+    const int64_t tok0 = (int64_t)tm * BM, row0 = (int64_t)tn * GEMM_ROWS;
+    f32x4_t acc[G::MT][G::NT];
+    G::run(acc, a.L, a.d_row, reinterpret_cast<const uint8_t*>(a.x), 2 * a.ldx, a.n, tok0, row0, lds);
+
+    if (a.rank) {
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15, q = lane >> 4;
+        // the tile's scaled v for 32 ranks, as bfloat16 hi and lo: [token][rank], in the slabs' place
+        __bf16* vh = reinterpret_cast<__bf16*>(lds);
+        __bf16* vl = vh + BM * 32;
+        int* ids = reinterpret_cast<int*>(vl + BM * 32);
+        __syncthreads();                                       // the last slab is read
+        for (int m = threadIdx.x; m < BM; m += 256) ids[m] = adapter_of(a, tok0 + m);
+        for (int k0 = 0; k0 < a.rank; k0 += 32) {
+            __syncthreads();
+            for (int e = threadIdx.x; e < BM * 32; e += 256) {
+                const int m = e >> 5, k = k0 + (e & 31), ad = ids[m];
+                float v = 0.f;
+                if (ad >= 0 && k < a.rank) {
+                    for (int p = 0; p < a.splits; ++p) v += a.v[((int64_t)p * a.n + tok0 + m) * a.rank + k];
+                    if (a.scaling) v *= a.scaling[ad];
+                }
+                const __bf16 h = (__bf16)v;
+                vh[e] = h;
+                vl[e] = (__bf16)(v - (float)h);
+            }
+            __syncthreads();
+#pragma unroll 1
+            for (int mt = 0; mt < G::MT; ++mt) {
+                const int id = ids[16 * mt + n16];
+                const u32x4_t ah = *reinterpret_cast<const u32x4_t*>(vh + (16 * mt + n16) * 32 + 8 * q);
+                const u32x4_t al = *reinterpret_cast<const u32x4_t*>(vl + (16 * mt + n16) * 32 + 8 * q);
+                f32x4_t sum[G::NT];
+#pragma unroll
+                for (int nt = 0; nt < G::NT; ++nt) sum[nt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                uint32_t todo = (uint32_t)__ballot(id >= 0) & 0xFFFFu;
+                while (todo) {                                 // wave-uniform
+                    const int ad = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
+                    const uint32_t mine = (uint32_t)__ballot(id == ad) & 0xFFFFu;
+                    todo &= ~mine;
+                    const bool all = mine == 0xFFFFu;
+#pragma unroll
+                    for (int nt = 0; nt < G::NT; ++nt) {
+                        const int64_t r = row0 + 32 * wave + 16 * nt + n16;
+                        const uint16_t* b = a.B + ((int64_t)ad * a.d_row + (r < a.d_row ? r : a.d_row - 1)) * a.rank + k0 + 8 * q;
+                        const int left = a.rank - k0 - 8 * q;
+                        uint16_t w[8];
+                        if (left >= 8) __builtin_memcpy(w, b, 16);
+                        else
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) w[e] = e < left ? b[e] : 0;
+                        f32x4_t c = {0.f, 0.f, 0.f, 0.f};
+                        if constexpr (X == X_BF16) {
+                            u32x4_t bb;
+                            __builtin_memcpy(&bb, w, 16);
+                            c = mfma16<X_BF16>(ah, bb, c);
+                            c = mfma16<X_BF16>(al, bb, c);
+                        } else {
+                            bf16x8_t bh, bl;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float f = f16_bits_to_f32(w[e]);
+                                bh[e] = (__bf16)f;
+                                bl[e] = (__bf16)(f - (float)bh[e]);
+                            }
+                            const u32x4_t b0 = __builtin_bit_cast(u32x4_t, bh), b1 = __builtin_bit_cast(u32x4_t, bl);
+                            c = mfma16<X_BF16>(ah, b0, c);
+                            c = mfma16<X_BF16>(ah, b1, c);
+                            c = mfma16<X_BF16>(al, b0, c);
+                            c = mfma16<X_BF16>(al, b1, c);
+                        }
+                        settle(c);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) sum[nt][i] = all || ((mine >> (4 * q + i)) & 1) ? c[i] : sum[nt][i];
+                    }
+                }
+                // acc is indexed by a constant in each arm
+#pragma unroll
+                for (int m = 0; m < G::MT; ++m)
+                    if (m == mt)
+#pragma unroll
+                        for (int nt = 0; nt < G::NT; ++nt) acc[m][nt] += sum[nt];
+            }
+        }
+    }
+    if (a.yt == GPTQ_F32) G::template write<GPTQ_F32>(acc, a.y, a.d_row, a.n, tok0, row0);
+    else if (a.yt == GPTQ_BF16) G::template write<GPTQ_BF16>(acc, a.y, a.d_row, a.n, tok0, row0);
+    else G::template write<GPTQ_F16>(acc, a.y, a.d_row, a.n, tok0, row0);
+}
+
+template <int X, int CB, int PIECE, int BM>
+static void launch_gemm(const LoraArgs& a, hipStream_t s) {
+    const int gm = (int)((a.n + BM - 1) / BM), gn = (int)((a.d_row + GEMM_ROWS - 1) / GEMM_ROWS);
+    lora_gemm_kernel<X, CB, PIECE, BM><<<(unsigned)(gm * gn), 256, 0, s>>>(a, gm, gn);
+}
+
+template <int X, int CB, int RUN, int PIECE>
 static gptq_status launch(const LoraArgs& a, hipStream_t s) {
+    if (a.n > 64 && gemm_fits(a.L.d_col, 2 * a.ldx)) {
+        if ((a.n + 127) / 128 * ((a.d_row + 127) / 128) >= 512) launch_gemm<X, CB, PIECE, 128>(a, s);
+        else launch_gemm<X, CB, PIECE, 64>(a, s);
+        GPTQ_LAUNCH_CHECK();
+        return GPTQ_OK;
+    }
     const unsigned g16 = (unsigned)((a.d_row + 15) / 16), g32 = (unsigned)((a.d_row + 31) / 32);
     auto tiles = [&](int per) { return (unsigned)((a.n + per - 1) / per); };
     if (a.n <= 16) lora_tile_kernel<X, CB, RUN, 1, 1><<<dim3(g16, 1), 64 * TW, 0, s>>>(a);
@@ -190,7 +302,9 @@ static gptq_status launch(const LoraArgs& a, hipStream_t s) {
 
 template <int X, int CB>
 static gptq_status launch_runs(const LoraArgs& a, int group, hipStream_t s) {
-    return group == 32 ? launch<X, CB, 8>(a, s) : group == 64 ? launch<X, CB, 16>(a, s) : launch<X, CB, 32>(a, s);
+    // (16-bit slabs hold 64 columns: a group of 128 is two pieces with one scale)
+    return group == 32 ? launch<X, CB, 8, 32>(a, s) : group == 64 ? launch<X, CB, 16, 64>(a, s)
+         : group == 128 ? launch<X, CB, 32, 64>(a, s) : launch<X, CB, 32, 0>(a, s);
 }
 
 template <int X>

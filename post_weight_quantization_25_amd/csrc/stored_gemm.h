@@ -45,7 +45,7 @@ GPTQ_DEV const T* uniform(const T* p) {
                                                   (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)b)));
 }
 
-template <int X, int CB, int PIECE, int BM, int SLAB>   // SLAB: bytes of a token's row in LDS
+template <int X, int CB, int PIECE, int BM, int SLAB>   // SLAB: bytes of a token's row in LDS (128 or 256)
 struct StoredGemm {
     static constexpr int XB = xbytes<X>();
     static constexpr int KS = SLAB / XB;                       // columns per slab
@@ -59,14 +59,17 @@ struct StoredGemm {
     static constexpr int LDS_BYTES = 2 * BM * SLAB;
     typedef typename Acc<X>::t sum_t;
 
-    // A fragment read serves 16 lanes at a time: 8 rows (4 g .. 4 g + 3 of two g) of one lane
-    // group and the other 8 rows of the next, whose pieces are RUN XB / 16 further on.  The
-    // swizzle spreads them over the 16 16-byte columns of the 64 banks.
+    // A fragment read serves 16 lanes at a time: rows 0 - 3 and 12 - 15 of one lane group and
+    // the other 8 rows of the next, whose pieces are RUN XB / 16 further on.  The swizzle
+    // spreads them over the 16 16-byte columns of the 64 banks.
     static GPTQ_DEV int slab_at(int row, int piece16) {
-        int f = row & (SLAB / 16 - 1);
+        constexpr bool EVEN = RUN * XB % 32 == 0;              // the lane groups' pieces differ in bits above the lowest
+        int f = row & 15;
         if constexpr (SLAB == 128) {
-            const int g = row >> 1;
-            f = RUN * XB == 32 ? ((g & 1) << 1) | (g & 4) | (((g >> 1) ^ (g >> 2)) & 1) : g & 7;
+            const int g = f >> 1;
+            f = EVEN ? ((g & 1) << 1) | (g & 4) | (((g >> 1) ^ (g >> 2)) & 1) : g;
+        } else if constexpr (EVEN) {
+            f = ((f & 3) << 1) | (f & 8) | (((f >> 2) ^ (f >> 3)) & 1);
         }
         return row * SLAB + 16 * (piece16 ^ f);
     }
@@ -124,7 +127,8 @@ struct StoredGemm {
         };
         auto load_b = [&](Codes& b, int s) {
             const uint8_t* cs = uniform(ct + (int64_t)s * (KS / 8 * CB));
-            const uint16_t *ss = uniform(st + (PIECE ? s * PP : 0)), *zs = uniform(zt + (PIECE ? s * PP : 0));
+            const int g0 = PIECE ? (s * KS) >> L.gshift : 0;         // pieces are groups, or one piece a part of one
+            const uint16_t *ss = uniform(st + g0), *zs = uniform(zt + g0);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -163,7 +167,7 @@ struct StoredGemm {
                     const int left = last - p * PC - q * RUN;
                     b.c[nt][p] = load_raw_tail<CB, RUN>(cs + boff[nt] + p * (PC / 8 * CB), left < RUN ? left : RUN);
                     if constexpr (PIECE != 0) {
-                        int g = nfull * PP + p;
+                        int g = (nfull * KS + p * PC) >> L.gshift;
                         g = g < L.n_groups ? g : L.n_groups - 1;   // pieces behind the row
                         b.S[nt][p] = st[soff[nt] + g];
                         b.z[nt][p] = zt[soff[nt] + g];
