@@ -65,7 +65,7 @@ __global__ __launch_bounds__(64 * TW) void int8_tile_kernel(Int8Args a) {
 // Large batches: see stored_gemm.h.
 template <int CB, int PIECE, int BM>
 __global__ __launch_bounds__(256, 2) void int8_gemm_kernel(Int8Args a, int gm, int gn) {
-    typedef StoredGemm<X_I8, CB, PIECE, BM, 128> G;
+    typedef StoredGemm<X_I8, CB, PIECE, BM, 256> G;
     __shared__ __align__(16) uint8_t lds[G::LDS_BYTES];
     int tm, tn;
     tile_of(gm, gn, tm, tn);

@@ -184,7 +184,7 @@ __global__ __launch_bounds__(64 * TW) void lora_tile_kernel(LoraArgs a) {
 // tokens, into the rows of the tokens that have it.
 template <int X, int CB, int PIECE, int BM>
 __global__ __launch_bounds__(256, 2) void lora_gemm_kernel(LoraArgs a, int gm, int gn) {
-    typedef StoredGemm<X, CB, PIECE, BM, 128> G;
+    typedef StoredGemm<X, CB, PIECE, BM, 256> G;
     __shared__ __align__(16) uint8_t lds[G::LDS_BYTES];
     int tm, tn;
     tile_of(gm, gn, tm, tn);
@@ -302,9 +302,8 @@ static gptq_status launch(const LoraArgs& a, hipStream_t s) {
 
 template <int X, int CB>
 static gptq_status launch_runs(const LoraArgs& a, int group, hipStream_t s) {
-    // (16-bit slabs hold 64 columns: a group of 128 is two pieces with one scale)
     return group == 32 ? launch<X, CB, 8, 32>(a, s) : group == 64 ? launch<X, CB, 16, 64>(a, s)
-         : group == 128 ? launch<X, CB, 32, 64>(a, s) : launch<X, CB, 32, 0>(a, s);
+         : group == 128 ? launch<X, CB, 32, 128>(a, s) : launch<X, CB, 32, 0>(a, s);
 }
 
 template <int X>

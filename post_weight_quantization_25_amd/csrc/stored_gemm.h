@@ -36,15 +36,6 @@ GPTQ_DEV void tile_of(int gm, int gn, int& tm, int& tn) {
 // What a tile's 32-bit offsets and a row's 32-bit integer sums take (128 x 127 x 2^17 < 2^31).
 inline bool gemm_fits(int64_t d_col, int64_t ldx_bytes) { return d_col <= (1 << 17) && ldx_bytes <= (1 << 24); }
 
-// A wave-uniform address made visible as one: loads take it from scalar registers and add a
-// lane's 32-bit offset themselves.
-template <typename T>
-GPTQ_DEV const T* uniform(const T* p) {
-    const uint64_t b = (uint64_t)(uintptr_t)p;
-    return reinterpret_cast<const T*>((uintptr_t)(((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)) << 32) |
-                                                  (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)b)));
-}
-
 template <int X, int CB, int PIECE, int BM, int SLAB>   // SLAB: bytes of a token's row in LDS (128 or 256)
 struct StoredGemm {
     static constexpr int XB = xbytes<X>();
@@ -56,7 +47,7 @@ struct StoredGemm {
     static constexpr int KB = X == X_I8 && RUN == 8 ? 8 : 16;  // bytes of a lane's operand per product
     static constexpr int STEPS = RUN * XB / KB;                // products per piece
     static constexpr int AU = BM * (SLAB / 16) / 256;          // 16-byte activation pieces per thread
-    static constexpr int LDS_BYTES = 2 * BM * SLAB;
+    static constexpr int LDS_BYTES = 2 * BM * SLAB + (PIECE ? 16 * GEMM_ROWS * 8 : 0);
     typedef typename Acc<X>::t sum_t;
 
     // A fragment read serves 16 lanes at a time: rows 0 - 3 and 12 - 15 of one lane group and
@@ -74,15 +65,29 @@ struct StoredGemm {
         return row * SLAB + 16 * (piece16 ^ f);
     }
 
-    struct Codes {                                             // a slab's codes of the lane's rows
-        Raw<CB, RUN> c[NT][PP];
-        uint16_t S[NT][PP], z[NT][PP];
-    };
+    struct Codes { Raw<CB, RUN> c[NT][PP]; };                  // a slab's codes of the lane's rows
     struct Frag { uint32_t w[KB / 4]; };
     struct Operand {                                           // the same, decoded
         Frag f[PP][NT][STEPS];
         float S[PP][NT], rz[PP][NT];
     };
+    // Scales and zeros of the tile's rows for TG groups, in LDS as [group][row]: read from
+    // memory slab by slab they would cost a cache line per row for every 4 bytes used.
+    static constexpr int TG = 16;
+    struct Entry { float S; uint32_t z; };                     // z: fp16 zero | its part in the operand's form << 16
+    static GPTQ_DEV Entry entry(uint16_t S, uint16_t z) {
+        const float zc = zero_part<X, CB>(f16_bits_to_f32(z));
+        uint32_t form;
+        if constexpr (X == X_I8) form = (uint32_t)(int)zc & 0xFFu;                                    // the byte
+        else if constexpr (X == X_F16) form = __builtin_bit_cast(uint16_t, (_Float16)(1024.f + zc));  // fp16(1024 + zc)
+        else form = f32_to_bf16_bits(zc);                                                             // bfloat16(zc), exact
+        return Entry{f16_bits_to_f32(S), z | (form << 16)};
+    }
+    static GPTQ_DEV float part_of(uint32_t form) {             // zc from its form
+        if constexpr (X == X_I8) return CB == 8 ? 128.f : (float)(int)(int8_t)(form & 0xFFu);
+        else if constexpr (X == X_F16) return f16_bits_to_f32((uint16_t)form) - 1024.f;
+        else return bf16_bits_to_f32((uint16_t)form);
+    }
 
     // acc[mt][nt]: lane l's value i is token 16 mt + 4 (l / 16) + i, weight row 32 wave + 16 nt
     // + l % 16 of the tile.
@@ -113,7 +118,7 @@ struct StoredGemm {
         }
 
         auto load_a = [&](u32x4_t (&a)[AU], int s) {
-            const uint8_t* xs = uniform(xt + (int64_t)s * SLAB);
+            const uint8_t* xs = xt + (int64_t)s * SLAB;
 #pragma unroll
             for (int j = 0; j < AU; ++j) __builtin_memcpy(&a[j], xs + aoff[j], 16);
         };
@@ -126,19 +131,21 @@ struct StoredGemm {
             }
         };
         auto load_b = [&](Codes& b, int s) {
-            const uint8_t* cs = uniform(ct + (int64_t)s * (KS / 8 * CB));
-            const int g0 = PIECE ? (s * KS) >> L.gshift : 0;         // pieces are groups, or one piece a part of one
-            const uint16_t *ss = uniform(st + g0), *zs = uniform(zt + g0);
+            const uint8_t* cs = ct + (int64_t)s * (KS / 8 * CB);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int p = 0; p < PP; ++p) {
                     b.c[nt][p] = load_raw<CB, RUN>(cs + boff[nt] + p * (PC / 8 * CB));
-                    if constexpr (PIECE != 0) {
-                        b.S[nt][p] = ss[soff[nt] + p];
-                        b.z[nt][p] = zs[soff[nt] + p];
-                    }
                 }
+        };
+        Entry* tab = reinterpret_cast<Entry*>(lds + 2 * BM * SLAB);
+        auto fill = [&](int g0) {                              // groups g0 .. g0 + TG - 1
+            for (int e = tid; e < GEMM_ROWS * TG; e += 256) {
+                const int r = e / TG, g = g0 + e % TG;
+                const uint32_t at = (uint32_t)(r < rows ? r : rows - 1) * (uint32_t)L.n_groups + g;
+                if (g < L.n_groups) tab[(e % TG) * GEMM_ROWS + r] = entry(st[at], zt[at]);
+            }
         };
         // the slab in which the rows end: zeros behind them
         const int last = (int)(L.d_col - (int64_t)nfull * KS);  // its columns
@@ -166,24 +173,17 @@ struct StoredGemm {
                 for (int p = 0; p < PP; ++p) {
                     const int left = last - p * PC - q * RUN;
                     b.c[nt][p] = load_raw_tail<CB, RUN>(cs + boff[nt] + p * (PC / 8 * CB), left < RUN ? left : RUN);
-                    if constexpr (PIECE != 0) {
-                        int g = (nfull * KS + p * PC) >> L.gshift;
-                        g = g < L.n_groups ? g : L.n_groups - 1;   // pieces behind the row
-                        b.S[nt][p] = st[soff[nt] + g];
-                        b.z[nt][p] = zt[soff[nt] + g];
-                    }
                 }
         };
 
-        float rowS[NT], rowz[NT];                              // PIECE 0: the row's scale and zero
+        Entry rowE[NT];                                        // PIECE 0: the row's scale and zero
         bool row_rest = false;
         if constexpr (PIECE == 0) {
             bool r = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                rowS[nt] = f16_bits_to_f32(st[soff[nt]]);
-                rowz[nt] = f16_bits_to_f32(zt[soff[nt]]);
-                r = r || !(rowz[nt] - zero_part<X, CB>(rowz[nt]) == 0.f);
+                rowE[nt] = entry(st[soff[nt]], zt[soff[nt]]);
+                r = r || !(f16_bits_to_f32((uint16_t)(rowE[nt].z & 0xFFFFu)) - part_of(rowE[nt].z >> 16) == 0.f);
             }
             row_rest = __ballot(r) != 0;
         }
@@ -202,17 +202,22 @@ struct StoredGemm {
                 for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
 
-        auto decode = [&](Operand& o, const Codes& b) {
+        auto decode = [&](Operand& o, const Codes& b, int s) {
 #pragma unroll
-            for (int p = 0; p < PP; ++p)
+            for (int p = 0; p < PP; ++p) {
+                int g = PIECE ? (s * KS + p * PC) >> L.gshift : 0;
+                g = g < L.n_groups ? g : L.n_groups - 1;       // pieces behind the row
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const float z = PIECE == 0 ? rowz[nt] : f16_bits_to_f32(b.z[nt][p]), zc = zero_part<X, CB>(z);
-                    o.S[p][nt] = PIECE == 0 ? 0.f : f16_bits_to_f32(b.S[nt][p]);
-                    o.rz[p][nt] = z - zc;
+                    Entry e;
+                    if constexpr (PIECE != 0) e = tab[(g % TG) * GEMM_ROWS + 32 * wave + 16 * nt + n16];
+                    else e = rowE[nt];
+                    o.S[p][nt] = e.S;
+                    o.rz[p][nt] = f16_bits_to_f32((uint16_t)(e.z & 0xFFFFu)) - part_of(e.z >> 16);
 #pragma unroll
-                    for (int t = 0; t < STEPS; ++t) o.f[p][nt][t] = frag_b(b.c[nt][p], t, zc);
+                    for (int t = 0; t < STEPS; ++t) o.f[p][nt][t] = frag_b(b.c[nt][p], t, e.z);
                 }
+            }
         };
         auto step = [&](const Operand& o, int s) {
             const uint8_t* buf = lds + (s & 1) * BM * SLAB;
@@ -231,32 +236,33 @@ struct StoredGemm {
             if (PIECE == 0 && row_rest) piece_sums(xs, buf);
         };
 
-        // Whole slabs: slab s + 2 is on its way into the registers that slab s has left while
-        // slab s is multiplied (two slabs' time for a load); s + 1 goes to LDS behind it.
-        u32x4_t a0[AU], a1[AU];
-        Codes b0, b1;
+        // Whole slabs: slab s + 1 is on its way into registers while slab s is multiplied.
+        u32x4_t a[AU];
+        Codes b;
         Operand o;
-        if (nfull > 0) { load_a(a0, 0); load_b(b0, 0); }
-        if (nfull > 1) { load_a(a1, 1); load_b(b1, 1); }
-        if (nfull > 0) store_a(a0, 0);
-        int s = 0;
-        auto whole = [&](u32x4_t (&a)[AU], const u32x4_t (&a_next)[AU], Codes& b) {
+        if constexpr (PIECE != 0) fill(0);
+        if (nfull > 0) { load_a(a, 0); load_b(b, 0); store_a(a, 0); }
+        auto begin = [&](int s) {
             __syncthreads();
-            decode(o, b);
-            if (s + 2 < nfull) { load_a(a, s + 2); load_b(b, s + 2); }
+            const int g = PIECE ? (s * KS) >> L.gshift : 0;
+            const int before = PIECE && s ? ((s - 1) * KS) >> L.gshift : 0;
+            if (PIECE && g / TG != before / TG) { fill(g); __syncthreads(); }
+        };
+        int s = 0;
+        for (; s < nfull; ++s) {
+            begin(s);
+            decode(o, b, s);
+            if (s + 1 < nfull) { load_a(a, s + 1); load_b(b, s + 1); }
             __builtin_amdgcn_sched_barrier(0);                 // the loads leave before the products begin
             step(o, s);
-            if (s + 1 < nfull) store_a(a_next, s + 1);
-            ++s;
-        };
-        while (s + 1 < nfull) { whole(a0, a1, b0); whole(a1, a0, b1); }
-        if (s < nfull) whole(a0, a1, b0);
+            if (s + 1 < nfull) store_a(a, s + 1);
+        }
         if (nslab > nfull) {                                   // the slab in which the rows end
-            __syncthreads();
+            begin(s);
             tail_a();
-            tail_b(b0);
+            tail_b(b);
             __syncthreads();
-            decode(o, b0);
+            decode(o, b, s);
             step(o, s);
         }
         if constexpr (PIECE == 0) {
@@ -264,11 +270,11 @@ struct StoredGemm {
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const float rz = rowz[nt] - zero_part<X, CB>(rowz[nt]);
+                    const float rz = f16_bits_to_f32((uint16_t)(rowE[nt].z & 0xFFFFu)) - part_of(rowE[nt].z >> 16);
                     settle(cs[mt][nt]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        acc[mt][nt][i] = rowS[nt] * fmaf(-rz, (float)xs[mt][i], (float)cs[mt][nt][i]);
+                        acc[mt][nt][i] = rowE[nt].S * fmaf(-rz, (float)xs[mt][i], (float)cs[mt][nt][i]);
                 }
         }
     }
@@ -314,17 +320,22 @@ private:
         __builtin_memcpy(f.w, __builtin_assume_aligned(buf + slab_at(row, byte >> 4) + (KB == 8 ? (byte & 8) : 0), KB), KB);
         return f;
     }
-    static GPTQ_DEV Frag frag_b(const Raw<CB, RUN>& c, int t, float zc) {
+    static GPTQ_DEV Frag frag_b(const Raw<CB, RUN>& c, int t, uint32_t z) {   // z: an Entry's
         Frag f;
         if constexpr (X == X_I8) {
-            const uint32_t zz = (uint32_t)((int)zc * 0x01010101);
+            const uint32_t zz = __builtin_amdgcn_perm(z, z, 0x02020202u);   // the byte four times
+            // as whole numbers zc 0x01010101 = zz less 2^8 + 2^16 + 2^24 for a negative zc; the
+            // bytes of 128 + u - zc, taken modulo 256 each, want no borrow between them
+            const uint32_t zw = zz - ((zz & 0x80u) ? 0x01010100u : 0u);
 #pragma unroll
-            for (int e = 0; e < KB / 4; ++e) f.w[e] = minus_zero_i8<CB>(code_bytes4<CB, RUN>(c, KB / 4 * t + e), zz);
+            for (int e = 0; e < KB / 4; ++e) f.w[e] = minus_zero_i8<CB>(code_bytes4<CB, RUN>(c, KB / 4 * t + e), zw);
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t o[2];
-                minus_zero_16<X>(code_bytes4<CB, RUN>(c, 2 * t + h), zc, o);
+                const uint32_t u4 = code_bytes4<CB, RUN>(c, 2 * t + h);
+                if constexpr (X == X_F16) minus_zero_f16(u4, __builtin_amdgcn_perm(z, z, 0x03020302u), o);
+                else minus_zero_bf16(u4, __uint_as_float(z & 0xFFFF0000u), o);
                 f.w[2 * h] = o[0];
                 f.w[2 * h + 1] = o[1];
             }

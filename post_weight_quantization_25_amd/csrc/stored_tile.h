@@ -87,19 +87,26 @@ GPTQ_DEV uint32_t minus_zero_i8(uint32_t u4, uint32_t zz) {
 }
 
 // u - zc of four columns in a 16-bit type, two per word.
+// fp16: 0x6400 | u is 1024 + u; zz is 1024 + zc twice; both and the difference are whole
+// numbers below 2048.
+GPTQ_DEV void minus_zero_f16(uint32_t u4, uint32_t zz, uint32_t (&o)[2]) {
+    const f16x2_t z = __builtin_bit_cast(f16x2_t, zz);
+    o[0] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, __builtin_amdgcn_perm(0x64646464u, u4, 0x04010400u)) - z);
+    o[1] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, __builtin_amdgcn_perm(0x64646464u, u4, 0x04030402u)) - z);
+}
+GPTQ_DEV void minus_zero_bf16(uint32_t u4, float zc, uint32_t (&o)[2]) {
+    const f32x2_t a = {(float)(u4 & 0xFFu) - zc, (float)((u4 >> 8) & 0xFFu) - zc};
+    const f32x2_t b = {(float)((u4 >> 16) & 0xFFu) - zc, (float)(u4 >> 24) - zc};
+    o[0] = __builtin_bit_cast(uint32_t, __builtin_convertvector(a, bf16x2_t));
+    o[1] = __builtin_bit_cast(uint32_t, __builtin_convertvector(b, bf16x2_t));
+}
 template <int X>
 GPTQ_DEV void minus_zero_16(uint32_t u4, float zc, uint32_t (&o)[2]) {
     if constexpr (X == X_F16) {
-        // 0x6400 | u is 1024 + u; 1024 + zc and the difference are whole numbers below 2048
-        const _Float16 s = (_Float16)(1024.f + zc);
-        const f16x2_t zz = {s, s};
-        o[0] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, __builtin_amdgcn_perm(0x64646464u, u4, 0x04010400u)) - zz);
-        o[1] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, __builtin_amdgcn_perm(0x64646464u, u4, 0x04030402u)) - zz);
+        const uint32_t h = __builtin_bit_cast(uint16_t, (_Float16)(1024.f + zc));
+        minus_zero_f16(u4, h | (h << 16), o);
     } else {
-        const f32x2_t a = {(float)(u4 & 0xFFu) - zc, (float)((u4 >> 8) & 0xFFu) - zc};
-        const f32x2_t b = {(float)((u4 >> 16) & 0xFFu) - zc, (float)(u4 >> 24) - zc};
-        o[0] = __builtin_bit_cast(uint32_t, __builtin_convertvector(a, bf16x2_t));
-        o[1] = __builtin_bit_cast(uint32_t, __builtin_convertvector(b, bf16x2_t));
+        minus_zero_bf16(u4, zc, o);
     }
 }
 
