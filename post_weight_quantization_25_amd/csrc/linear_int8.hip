@@ -22,7 +22,7 @@ struct Int8Args {
 
 template <int CB, int RUN, int NTT, int RB>
 __global__ __launch_bounds__(64 * TW) void int8_tile_kernel(Int8Args a) {
-    constexpr int CPW = NTT == 1 ? 2 : 1;
+    constexpr int DEEP = NTT == 4 ? 1 : 2;
     __shared__ float red[TW][NTT * RB][4][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15;
     const int64_t row0 = (int64_t)blockIdx.x * 16 * RB, tok0 = (int64_t)blockIdx.y * 16 * NTT;
@@ -44,7 +44,7 @@ __global__ __launch_bounds__(64 * TW) void int8_tile_kernel(Int8Args a) {
     for (int tt = 0; tt < NTT; ++tt)
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) acc[tt][rb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    stored_accumulate<X_I8, CB, RUN, NTT, RB, CPW>(acc, a.L, row, xrow, wave, TW, (int)((a.L.d_col + SCK - 1) / SCK));
+    stored_accumulate<X_I8, CB, RUN, NTT, RB, DEEP>(acc, a.L, row, xrow, wave, TW);
 #pragma unroll
     for (int tt = 0; tt < NTT; ++tt)
 #pragma unroll

@@ -91,7 +91,7 @@ GPTQ_DEV float elem16(uint16_t b) { return X == X_BF16 ? bf16_bits_to_f32(b) : f
 
 template <int X, int CB, int RUN, int NTT, int RB>
 __global__ __launch_bounds__(64 * TW) void lora_tile_kernel(LoraArgs a) {
-    constexpr int CPW = NTT == 1 ? 2 : 1;
+    constexpr int DEEP = NTT == 4 ? 1 : 2;
     constexpr int PER = NTT * RB * 256 / (64 * TW) > 0 ? NTT * RB * 256 / (64 * TW) : 1;   // outputs per thread
     __shared__ float red[TW][NTT * RB][4][64];
     __shared__ float vs[16 * NTT][RCH + 1];
@@ -115,7 +115,7 @@ __global__ __launch_bounds__(64 * TW) void lora_tile_kernel(LoraArgs a) {
     for (int tt = 0; tt < NTT; ++tt)
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) acc[tt][rb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    stored_accumulate<X, CB, RUN, NTT, RB, CPW>(acc, a.L, row, xrow, wave, TW, (int)((a.L.d_col + SCK - 1) / SCK));
+    stored_accumulate<X, CB, RUN, NTT, RB, DEEP>(acc, a.L, row, xrow, wave, TW);
 #pragma unroll
     for (int tt = 0; tt < NTT; ++tt)
 #pragma unroll

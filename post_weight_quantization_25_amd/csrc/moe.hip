@@ -1,13 +1,14 @@
 // A mixture-of-experts layer for a few tokens, the experts held as stored layers
-// (gptqs_moe).  Four launches:
+// (gptqs_moe):
 //   moe_logits_kernel  l = router x: 16 experts x 16 tokens per workgroup, columns over its waves
-//   moe_topk_kernel    a wave per token: the largest logits one by one, softmax, ids and weights
-//   moe_up_kernel      per chosen expert and 16 inner columns: gate and up products for the
+//   moe_plan_kernel    a wave per token takes the largest logits one by one; softmax; the pairs
+//                      (token, choice) sorted by expert
+//   moe_up_kernel      per expert in use and 16 inner columns: gate and up products for the
 //                      tokens that chose it, silu(gate) up w, written as two bfloat16 parts
-//   moe_down_kernel    per 16 output columns: every chosen expert's product with the inner
-//                      values of the tokens that chose it, summed over experts in one place
-// Bound by the codes of the chosen experts, which the last two read once each.  Sums run
-// in fixed orders without atomics.
+//   moe_down_kernel    per expert in use and 16 output columns: the pairs' outputs, fp32
+//   moe_sum_kernel     y = a token's pairs added in the order of its choices
+// Bound by the codes of the chosen experts, which up and down read once each.  Sums run in
+// fixed orders without atomics, and a token's do not depend on the other tokens' choices.
 
 #include "serving.h"
 #include "stored_tile.h"
@@ -22,6 +23,8 @@ struct MoeArgs {
     Stored up, down;          // E 2f x d, E d x f
     float* logits;            // n x E
     uint16_t* hi; uint16_t* lo;   // n k x f: w silu(gate) up as bfloat16 hi + lo
+    float* part;              // n k x d: w D h per pair
+    int32_t* plan;            // see moe_plan_kernel
     int32_t* ids; float* weights;
     void* y; gptq_dtype yt;
 };
@@ -66,51 +69,60 @@ __global__ __launch_bounds__(64 * LOGW) void moe_logits_kernel(MoeArgs a) {
 constexpr int MAXE = 512, MAXK = 32, EPL = MAXE / 64;   // experts per lane
 constexpr int MAXN = 256;                               // tokens of a call
 
-// One wave per token.  A NaN logit counts as -infinity; an expert already taken has index
-// MAXE, behind every other of the same value.
-__global__ __launch_bounds__(256) void moe_topk_kernel(MoeArgs a) {
-    const int lane = threadIdx.x & 63, t = blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (t >= a.n) return;
-    float v[EPL];
-    int at[EPL];
-    float top = -INFINITY;
+// Maximum over the wave, in every lane's copy of lane 63 (DPP, no LDS).
+GPTQ_DEV uint32_t wave_umax(uint32_t v) {
+#define GPTQ_STEP(CTRL, ROWS)                                                                                  \
+    {                                                                                                          \
+        const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, ROWS, 0xf, false);      \
+        v = o > v ? o : v;                                                                                     \
+    }
+    GPTQ_STEP(0x111, 0xf) GPTQ_STEP(0x112, 0xf) GPTQ_STEP(0x114, 0xf) GPTQ_STEP(0x118, 0xf)   // row_shr 1, 2, 4, 8
+    GPTQ_STEP(0x142, 0xa) GPTQ_STEP(0x143, 0xc)                                               // row_bcast 15, 31
+#undef GPTQ_STEP
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// The top_k largest logits of token t and their softmax, by one wave.  A logit's key orders
+// as the logits do (a NaN as -infinity, -0 as 0); 0 is no logit's key and marks what is
+// taken or absent.  Of equal keys the lowest expert is found as the largest MAXE - 1 - e.
+GPTQ_DEV void topk_of(const MoeArgs& a, int t) {
+    const int lane = threadIdx.x & 63;
+    uint32_t key[EPL];
+    float l[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
         const int e = lane + 64 * i;
-        const float l = e < a.E ? a.logits[(int64_t)t * a.E + e] : -INFINITY;
-        v[i] = l == l ? l : -INFINITY;
-        at[i] = e < a.E ? e : MAXE;
-        top = fmaxf(top, v[i]);
+        float v = e < a.E ? a.logits[(int64_t)t * a.E + e] : -INFINITY;
+        v = v == v ? v + 0.f : -INFINITY;
+        const uint32_t u = __float_as_uint(v);
+        l[i] = v;
+        key[i] = e < a.E ? u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u) : 0u;
     }
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-    float sum = 0.f;
-    if (!a.renormalize) {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) sum += lane + 64 * i < a.E ? expf(v[i] - top) : 0.f;
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
-    }
-    float mine = 0.f;           // lane j: the j-th choice's exp
+    float top = 0.f, sum = 0.f, mine = 0.f;           // mine: lane j holds the j-th choice's exp
     int id = 0;
     for (int j = 0; j < a.k; ++j) {
-        float bv = -INFINITY;
-        int bi = MAXE;
+        uint32_t best = 0;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (v[i] > bv || (v[i] == bv && at[i] < bi)) { bv = v[i]; bi = at[i]; }
+        for (int i = 0; i < EPL; ++i) best = key[i] > best ? key[i] : best;
+        best = wave_umax(best);
+        uint32_t at = 0;
 #pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) {
-            const float ov = __shfl_xor(bv, o);
-            const int oi = __shfl_xor(bi, o);
-            if (ov > bv || (ov == bv && oi < bi)) { bv = ov; bi = oi; }
-        }
+        for (int i = 0; i < EPL; ++i) at = key[i] == best && (uint32_t)(MAXE - lane - 64 * i) > at ? MAXE - lane - 64 * i : at;
+        const int e = MAXE - (int)wave_umax(at);
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (at[i] == bi) { at[i] = MAXE; v[i] = -INFINITY; }
-        const float p = expf(bv - top);
-        if (a.renormalize) sum += p;
-        if (lane == j) { mine = p; id = bi; }
+        for (int i = 0; i < EPL; ++i) key[i] = e == lane + 64 * i ? 0u : key[i];
+        const float v = __uint_as_float(best ^ ((best >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+        if (j == 0) top = v;
+        const float p = expf(v - top);
+        sum += p;
+        if (lane == j) { mine = p; id = e; }
+    }
+    if (!a.renormalize) {
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) sum += lane + 64 * i < a.E ? expf(l[i] - top) : 0.f;
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
     }
     if (lane < a.k) {
         a.ids[(int64_t)t * a.k + lane] = id;
@@ -118,66 +130,87 @@ __global__ __launch_bounds__(256) void moe_topk_kernel(MoeArgs a) {
     }
 }
 
-// The experts that the calls' pairs name, as bits in LDS (every thread of the workgroup).
-GPTQ_DEV void active_bits(const MoeArgs& a, int p0, int p1, uint32_t* bits, int threads) {
-    if (threadIdx.x < MAXE / 32) bits[threadIdx.x] = 0;
-    __syncthreads();
-    for (int p = p0 + threadIdx.x; p < p1; p += threads) {
-        const int e = a.ids[p];
-        atomicOr(&bits[e >> 5], 1u << (e & 31));
-    }
-    __syncthreads();
+__global__ __launch_bounds__(256) void moe_topk_kernel(MoeArgs a) {
+    const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (t < a.n) topk_of(a, t);
 }
 
-// The s-th expert of the bits, or -1.
-GPTQ_DEV int nth_expert(const uint32_t* bits, int s) {
-    for (int w = 0; w < MAXE / 32; ++w) {
-        uint32_t b = bits[w];
-        const int c = __popc(b);
-        if (s < c) {
-            for (; s > 0; --s) b &= b - 1;
-            return 32 * w + __builtin_ctz(b);
+// The plan: the chosen experts in rising order, and the pairs (token, choice) sorted by
+// expert, in token order within one.  plan: [0] experts in use, [1 + 2 s] the s-th of them,
+// [2 + 2 s] where its pairs begin (and one more: where they end), from PAIRS on the pairs.
+constexpr int PAIRS = 2 + 2 * MAXE;
+constexpr int PLAN_W = 16;
+
+// TOPK: the same workgroup chooses first (few tokens: one launch less).
+template <bool TOPK>
+__global__ __launch_bounds__(64 * PLAN_W) void moe_plan_kernel(MoeArgs a) {
+    __shared__ int count[MAXE], start[MAXE], slot[MAXE];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, pairs = a.n * a.k;
+    if (TOPK) {
+        for (int t = wave; t < a.n; t += PLAN_W) topk_of(a, t);
+        __threadfence_block();
+    }
+    for (int e = threadIdx.x; e < MAXE; e += 64 * PLAN_W) count[e] = 0;
+    __syncthreads();
+    for (int p = threadIdx.x; p < pairs; p += 64 * PLAN_W) atomicAdd(&count[a.ids[p]], 1);   // whole numbers: any order
+    __syncthreads();
+    if (wave == 0) {                                        // prefix sums over the experts, EPL per lane
+        int c[EPL], mine = 0, used = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) { c[i] = count[EPL * lane + i]; mine += c[i]; used += c[i] > 0; }
+        int at = mine, us = used;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int u = __shfl_up(at, o), v = __shfl_up(us, o);
+            if (lane >= o) { at += u; us += v; }
         }
-        s -= c;
+        const int total = __shfl(us, 63);
+        at -= mine;
+        us -= used;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            const int e = EPL * lane + i;
+            start[e] = at;
+            slot[e] = us;
+            if (c[i]) { a.plan[1 + 2 * us] = e; a.plan[2 + 2 * us] = at; ++us; }
+            at += c[i];
+        }
+        if (lane == 0) { a.plan[0] = total; a.plan[2 + 2 * total] = pairs; }
     }
-    return -1;
-}
-
-constexpr int UPW = 8;
-
-// Grid: 16 inner columns x the s-th chosen expert.
-template <int X, int CB, int RUN>
-__global__ __launch_bounds__(64 * UPW) void moe_up_kernel(MoeArgs a) {
-    __shared__ uint32_t bits[MAXE / 32];
-    __shared__ int list[MAXN], count;
-    __shared__ float red[UPW][2][4][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15;
-    const int pairs = a.n * a.k;
-    active_bits(a, 0, pairs, bits, 64 * UPW);
-    const int e = nth_expert(bits, blockIdx.y);
-    if (e < 0) return;                                      // the whole workgroup
-    if (wave == 0) {                                        // the pairs that chose e, in order
-        int c = 0;
+    __syncthreads();
+    // each expert's pairs, a wave per expert; experts are few, pairs at most 8192
+    for (int e = wave; e < a.E; e += PLAN_W) {
+        if (count[e] == 0) continue;
+        int c = start[e];
         for (int p0 = 0; p0 < pairs; p0 += 64) {
             const int p = p0 + lane;
-            const bool mine = p < pairs && a.ids[p] == e;
-            const uint64_t b = __ballot(mine);
-            if (mine) list[c + __popcll(b & ((1ull << lane) - 1))] = p;
+            const bool hit = p < pairs && a.ids[p] == e;
+            const uint64_t b = __ballot(hit);
+            if (hit) a.plan[PAIRS + c + __popcll(b & ((1ull << lane) - 1))] = p;
             c += __popcll(b);
         }
-        if (lane == 0) count = c;
     }
-    __syncthreads();
-    const int cnt = count;
+}
+
+constexpr int MW = 8;         // waves per workgroup of the experts' products
+
+// Grid: 16 inner columns x the s-th expert in use.
+template <int X, int CB, int RUN>
+__global__ __launch_bounds__(64 * MW, 4) void moe_up_kernel(MoeArgs a) {
+    __shared__ float red[MW][2][4][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15;
+    const int s = blockIdx.y;
+    if (s >= a.plan[0]) return;                             // the whole workgroup
+    const int e = a.plan[1 + 2 * s], p0 = a.plan[2 + 2 * s];
+    const int cnt = (s + 1 < a.plan[0] ? a.plan[4 + 2 * s] : a.n * a.k) - p0;
     const int64_t f0 = (int64_t)blockIdx.x * 16;
     const int64_t fr = f0 + n16 < a.f ? f0 + n16 : a.f - 1;
     const int64_t row[2] = {(int64_t)e * 2 * a.f + fr, (int64_t)e * 2 * a.f + a.f + fr};
-    const int nck = (int)((a.d + SCK - 1) / SCK);
     for (int m0 = 0; m0 < cnt; m0 += MOE_T) {
-        const int p = list[m0 + n16 < cnt ? m0 + n16 : cnt - 1];
+        const int p = a.plan[PAIRS + p0 + (m0 + n16 < cnt ? m0 + n16 : cnt - 1)];
         const uint8_t* const xrow[1] = {reinterpret_cast<const uint8_t*>(a.x + (int64_t)(p / a.k) * a.ldx)};
         f32x4_t acc[1][2] = {{f32x4_t{0.f, 0.f, 0.f, 0.f}, f32x4_t{0.f, 0.f, 0.f, 0.f}}};
-        stored_accumulate<X, CB, RUN, 1, 2, RUN == 32 ? 2 : 1>(acc, a.up, row, xrow, wave, UPW, nck);
+        stored_accumulate<X, CB, RUN, 1, 2, 1>(acc, a.up, row, xrow, wave, MW);
         __syncthreads();                                    // the last tile's sums are read
 #pragma unroll
         for (int rb = 0; rb < 2; ++rb)
@@ -189,11 +222,11 @@ __global__ __launch_bounds__(64 * UPW) void moe_up_kernel(MoeArgs a) {
             if (m0 + m < cnt && f0 + n < a.f) {
                 float g = 0.f, u = 0.f;
 #pragma unroll
-                for (int w = 0; w < UPW; ++w) {
+                for (int w = 0; w < MW; ++w) {
                     g += red[w][0][m & 3][n + 16 * (m >> 2)];
                     u += red[w][1][m & 3][n + 16 * (m >> 2)];
                 }
-                const int pr = list[m0 + m];
+                const int pr = a.plan[PAIRS + p0 + m0 + m];
                 const float h = g / (1.f + expf(-g)) * u * a.weights[pr];
                 const uint16_t hb = f32_to_bf16_bits(h);
                 a.hi[(int64_t)pr * a.f + f0 + n] = hb;
@@ -203,150 +236,46 @@ __global__ __launch_bounds__(64 * UPW) void moe_up_kernel(MoeArgs a) {
     }
 }
 
-// Grid: 16 output columns x NTT tiles of 16 tokens.  The waves share the (expert, chunk)
-// pairs; token t of a tile keeps its place in the operand, empty where it did not choose
-// the expert, and its sums are left alone there.
-template <int CB, int RUN, int NTT, int W>
-__global__ __launch_bounds__(64 * W) void moe_down_kernel(MoeArgs a) {
-    constexpr int X = X_BF16, P = 32 / RUN;
-    __shared__ uint32_t bits[MAXE / 32];
-    __shared__ uint16_t experts[MAXE];
-    __shared__ uint8_t choice[MAXE][16 * NTT];              // [active expert][token]: its j, or 255
-    __shared__ float red[W][NTT][4][64];
-    __shared__ int n_active;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15, q = lane >> 4;
-    const int t0 = blockIdx.y * 16 * NTT, t1 = t0 + 16 * NTT < a.n ? t0 + 16 * NTT : a.n;
+// Grid: 16 output columns x the s-th expert in use.  The two bfloat16 parts of a pair's
+// inner values are two tiles of the same tokens; their sums are added at the end.
+template <int CB, int RUN>
+__global__ __launch_bounds__(64 * MW, 4) void moe_down_kernel(MoeArgs a) {
+    __shared__ float red[MW][4][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15;
+    const int s = blockIdx.y;
+    if (s >= a.plan[0]) return;
+    const int e = a.plan[1 + 2 * s], p0 = a.plan[2 + 2 * s];
+    const int cnt = (s + 1 < a.plan[0] ? a.plan[4 + 2 * s] : a.n * a.k) - p0;
     const int64_t r0 = (int64_t)blockIdx.x * 16;
-    active_bits(a, t0 * a.k, t1 * a.k, bits, 64 * W);
-    auto rank_of = [&](int e) {                             // active experts below e
-        int c = 0;
-        for (int w = 0; w < (e >> 5); ++w) c += __popc(bits[w]);
-        return c + __popc(bits[e >> 5] & ((1u << (e & 31)) - 1));
-    };
-    for (int e = threadIdx.x; e < MAXE; e += 64 * W)
-        if ((bits[e >> 5] >> (e & 31)) & 1) experts[rank_of(e)] = (uint16_t)e;
-    if (threadIdx.x == 0) {
-        int c = 0;
-        for (int w = 0; w < MAXE / 32; ++w) c += __popc(bits[w]);
-        n_active = c;
+    const int64_t row[1] = {(int64_t)e * a.d + (r0 + n16 < a.d ? r0 + n16 : a.d - 1)};
+    for (int m0 = 0; m0 < cnt; m0 += MOE_T) {
+        const int64_t at = (int64_t)a.plan[PAIRS + p0 + (m0 + n16 < cnt ? m0 + n16 : cnt - 1)] * a.f;
+        const uint8_t* const xrow[2] = {reinterpret_cast<const uint8_t*>(a.hi + at), reinterpret_cast<const uint8_t*>(a.lo + at)};
+        f32x4_t acc[2][1] = {{f32x4_t{0.f, 0.f, 0.f, 0.f}}, {f32x4_t{0.f, 0.f, 0.f, 0.f}}};
+        stored_accumulate<X_BF16, CB, RUN, 2, 1, 1>(acc, a.down, row, xrow, wave, MW);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) red[wave][i][lane] = acc[0][0][i] + acc[1][0][i];
+        __syncthreads();
+        if (threadIdx.x < 256) {
+            const int m = threadIdx.x >> 4, n = threadIdx.x & 15;
+            if (m0 + m < cnt && r0 + n < a.d) {
+                float v = 0.f;
+#pragma unroll
+                for (int w = 0; w < MW; ++w) v += red[w][m & 3][n + 16 * (m >> 2)];
+                a.part[(int64_t)a.plan[PAIRS + p0 + m0 + m] * a.d + r0 + n] = v;
+            }
+        }
     }
-    __syncthreads();
-    const int na = n_active;
-    for (int i = threadIdx.x; i < na * 16 * NTT; i += 64 * W) (&choice[0][0])[i] = 255;
-    __syncthreads();
-    for (int p = t0 * a.k + threadIdx.x; p < t1 * a.k; p += 64 * W)
-        choice[rank_of(a.ids[p])][p / a.k - t0] = (uint8_t)(p % a.k);
-    __syncthreads();
+}
 
-    const Stored& L = a.down;
-    const int64_t rr = r0 + n16 < a.d ? r0 + n16 : a.d - 1;
-    const int nck = (int)((a.f + SCK - 1) / SCK);
-    f32x4_t acc[NTT];
-#pragma unroll
-    for (int tt = 0; tt < NTT; ++tt) acc[tt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    // chunk c of expert e goes to wave (e nck + c) % W: the same one whichever other experts
-    // are active, so a token's sums do not depend on the other tokens' choices
-    int s = 0, c = -1;
-    auto next = [&]() {                                     // wave-uniform
-        if (c >= 0) { c += W; if (c < nck) return; ++s; }
-        for (; s < na; ++s) {
-            c = (int)(((int64_t)wave - (int64_t)experts[s] * nck) % W);
-            c = c < 0 ? c + W : c;
-            if (c < nck) return;
-        }
-    };
-    for (next(); s < na; next()) {
-        const int64_t row = (int64_t)experts[s] * a.d + rr;
-        const bool full = (int64_t)(c + 1) * SCK <= a.f;
-        uint32_t has[NTT];
-        int64_t hrow[NTT];
-        bool mine[NTT];
-#pragma unroll
-        for (int tt = 0; tt < NTT; ++tt) {
-            const int j = choice[s][16 * tt + n16];
-            mine[tt] = j != 255;
-            has[tt] = (uint32_t)__ballot(mine[tt]) & 0xFFFFu;
-            hrow[tt] = ((int64_t)(t0 + 16 * tt + n16) * a.k + j) * a.f;
-        }
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const int64_t col = (int64_t)c * SCK + p * 4 * RUN + q * RUN;
-            const int left = (int)(a.f - col < RUN ? a.f - col : RUN);
-            int g = RUN == 32 ? c / L.cpg : c * P + p;
-            g = g < L.n_groups ? g : L.n_groups - 1;
-            const uint8_t* src = L.codes + row * L.code_ld + col / 8 * CB;
-            const Raw<CB, RUN> cw = full ? load_raw<CB, RUN>(src) : load_raw_tail<CB, RUN>(src, left);
-            const float S = f16_bits_to_f32(L.scales[row * L.n_groups + g]);
-            const float z = f16_bits_to_f32(L.zeros[row * L.n_groups + g]);
-            XRun<X, RUN> xh[NTT], xl[NTT];
-#pragma unroll
-            for (int tt = 0; tt < NTT; ++tt) {
-                const int m = mine[tt] ? left : 0;          // nothing of a token that did not choose it
-                const uint8_t* hp = reinterpret_cast<const uint8_t*>(a.hi + hrow[tt] + col);
-                const uint8_t* lp = reinterpret_cast<const uint8_t*>(a.lo + hrow[tt] + col);
-                if (m == RUN) { xh[tt] = load_x<X, RUN>(hp); xl[tt] = load_x<X, RUN>(lp); }
-                else { xh[tt] = load_x_tail<X, RUN>(hp, m); xl[tt] = load_x_tail<X, RUN>(lp, m); }
-            }
-            const float zc = zero_part<X, CB>(z), rz = z - zc;
-            float xs[NTT][4];
-#pragma unroll
-            for (int tt = 0; tt < NTT; ++tt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) xs[tt][i] = 0.f;
-            if (__ballot(!(rz == 0.f)) != 0) {
-                const u32x4_t w1 = {ones_word<X>(), ones_word<X>(), ones_word<X>(), ones_word<X>()};
-#pragma unroll
-                for (int tt = 0; tt < NTT; ++tt) {
-                    f32x4_t sm = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int u = 0; u < RUN / 8; ++u) {
-                        const uint32_t *h = xh[tt].w + 4 * u, *l = xl[tt].w + 4 * u;
-                        sm = mfma16<X>(u32x4_t{h[0], h[1], h[2], h[3]}, w1, sm);
-                        sm = mfma16<X>(u32x4_t{l[0], l[1], l[2], l[3]}, w1, sm);
-                    }
-                    settle(sm);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) xs[tt][i] = sm[i];
-                }
-            }
-            f32x4_t cs[NTT];
-#pragma unroll
-            for (int tt = 0; tt < NTT; ++tt) cs[tt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int u = 0; u < RUN / 8; ++u) {
-                uint32_t b0[2], b1[2];
-                minus_zero_16<X>(code_bytes4<CB, RUN>(cw, 2 * u), zc, b0);
-                minus_zero_16<X>(code_bytes4<CB, RUN>(cw, 2 * u + 1), zc, b1);
-                const u32x4_t b = {b0[0], b0[1], b1[0], b1[1]};
-#pragma unroll
-                for (int tt = 0; tt < NTT; ++tt) {
-                    const uint32_t *h = xh[tt].w + 4 * u, *l = xl[tt].w + 4 * u;
-                    cs[tt] = mfma16<X>(u32x4_t{h[0], h[1], h[2], h[3]}, b, cs[tt]);
-                    cs[tt] = mfma16<X>(u32x4_t{l[0], l[1], l[2], l[3]}, b, cs[tt]);
-                }
-            }
-#pragma unroll
-            for (int tt = 0; tt < NTT; ++tt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float v = fmaf(S, fmaf(-rz, xs[tt][i], cs[tt][i]), acc[tt][i]);
-                    acc[tt][i] = (has[tt] >> (4 * q + i)) & 1 ? v : acc[tt][i];
-                }
-        }
-    }
-#pragma unroll
-    for (int tt = 0; tt < NTT; ++tt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) red[wave][tt][i][lane] = acc[tt][i];
-    __syncthreads();
-    for (int o = threadIdx.x; o < NTT * 256; o += 64 * W) {
-        const int tt = o >> 8, m = (o >> 4) & 15, n = o & 15;
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) v += red[w][tt][m & 3][n + 16 * (m >> 2)];
-        const int t = t0 + 16 * tt + m;
-        if (t < a.n && r0 + n < a.d) store_out(a.y, a.yt, (int64_t)t * a.d + r0 + n, v);
-    }
+__global__ __launch_bounds__(256) void moe_sum_kernel(MoeArgs a) {
+    const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int t = blockIdx.y;
+    if (r >= a.d) return;
+    float v = 0.f;
+    for (int j = 0; j < a.k; ++j) v += a.part[((int64_t)t * a.k + j) * a.d + r];
+    store_out(a.y, a.yt, (int64_t)t * a.d + r, v);
 }
 
 template <int X, int CB, int RUN>
@@ -355,12 +284,20 @@ static gptq_status launch(const MoeArgs& a, hipStream_t s) {
     const int slots = a.E < a.n * a.k ? a.E : a.n * a.k;
     moe_logits_kernel<X><<<dim3((unsigned)((a.E + 15) / 16), (unsigned)((a.n + 15) / 16)), 64 * LOGW, 0, s>>>(a);
     GPTQ_LAUNCH_CHECK();
-    moe_topk_kernel<<<(unsigned)((a.n + 3) / 4), 256, 0, s>>>(a);
+    // up to 64 tokens one workgroup chooses and plans (a wave takes up to 4 tokens one after
+    // another); beyond, choosing is spread over the device first
+    if (a.n <= 64) moe_plan_kernel<true><<<1, 64 * PLAN_W, 0, s>>>(a);
+    else {
+        moe_topk_kernel<<<(unsigned)((a.n + 3) / 4), 256, 0, s>>>(a);
+        GPTQ_LAUNCH_CHECK();
+        moe_plan_kernel<false><<<1, 64 * PLAN_W, 0, s>>>(a);
+    }
     GPTQ_LAUNCH_CHECK();
-    moe_up_kernel<X, CB, RUN><<<dim3(ef, (unsigned)slots), 64 * UPW, 0, s>>>(a);
+    moe_up_kernel<X, CB, RUN><<<dim3(ef, (unsigned)slots), 64 * MW, 0, s>>>(a);
     GPTQ_LAUNCH_CHECK();
-    if (a.n <= 16) moe_down_kernel<CB, RUN, 1, 16><<<dim3(dd, 1), 64 * 16, 0, s>>>(a);
-    else moe_down_kernel<CB, RUN, 4, 8><<<dim3(dd, (unsigned)((a.n + 63) / 64)), 64 * 8, 0, s>>>(a);
+    moe_down_kernel<CB, RUN><<<dim3(dd, (unsigned)slots), 64 * MW, 0, s>>>(a);
+    GPTQ_LAUNCH_CHECK();
+    moe_sum_kernel<<<dim3((unsigned)((a.d + 255) / 256), (unsigned)a.n), 256, 0, s>>>(a);
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
 }
@@ -377,9 +314,20 @@ static gptq_status launch_bits(const MoeArgs& a, int bits, int group, hipStream_
 
 static size_t up16(size_t v) { return (v + 15) & ~(size_t)15; }
 
-size_t moe_ws_bytes(int64_t n, int64_t f, int E, int k) {
-    return up16((size_t)n * E * sizeof(float)) + 2 * up16((size_t)n * k * (size_t)f * sizeof(uint16_t));
+// Offsets of the workspace's parts, in this order, each 16-byte aligned; the last is its size.
+struct MoeWs { size_t hi, lo, part, plan, end; };
+static MoeWs moe_ws(int64_t n, int64_t d, int64_t f, int E, int k) {
+    MoeWs w;
+    const size_t inner = up16((size_t)n * k * (size_t)f * sizeof(uint16_t));
+    w.hi = up16((size_t)n * E * sizeof(float));
+    w.lo = w.hi + inner;
+    w.part = w.lo + inner;
+    w.plan = w.part + up16((size_t)n * k * (size_t)d * sizeof(float));
+    w.end = w.plan + up16((size_t)(PAIRS + 1 + n * k) * sizeof(int32_t));
+    return w;
 }
+
+size_t moe_ws_bytes(int64_t n, int64_t d, int64_t f, int E, int k) { return moe_ws(n, d, f, E, k).end; }
 
 gptq_status moe_launch(const MoeCall& c, hipStream_t s) {
     MoeArgs a;
@@ -388,10 +336,12 @@ gptq_status moe_launch(const MoeCall& c, hipStream_t s) {
     a.up = stored_layer(c.up_codes, c.up_scales, c.up_zeros, c.d, c.bits, c.group);
     a.down = stored_layer(c.down_codes, c.down_scales, c.down_zeros, c.f, c.bits, c.group);
     uint8_t* w = (uint8_t*)c.ws;
+    const MoeWs o = moe_ws(c.n, c.d, c.f, c.E, c.k);
     a.logits = (float*)w;
-    w += up16((size_t)c.n * c.E * sizeof(float));
-    a.hi = (uint16_t*)w;
-    a.lo = (uint16_t*)(w + up16((size_t)c.n * c.k * (size_t)c.f * sizeof(uint16_t)));
+    a.hi = (uint16_t*)(w + o.hi);
+    a.lo = (uint16_t*)(w + o.lo);
+    a.part = (float*)(w + o.part);
+    a.plan = (int32_t*)(w + o.plan);
     a.ids = c.ids; a.weights = c.weights; a.y = c.y; a.yt = c.yt;
     return c.xt == GPTQ_BF16 ? launch_bits<X_BF16>(a, c.bits, c.group, s) : launch_bits<X_F16>(a, c.bits, c.group, s);
 }

@@ -47,7 +47,7 @@ struct MoeCall {
 };
 constexpr int MOE_MAX_TOKENS = 256, MOE_MAX_EXPERTS = 512, MOE_MAX_TOPK = 32;
 constexpr int64_t MOE_MAX_WIDTH = (int64_t)1 << 20;   // d and f
-size_t moe_ws_bytes(int64_t n, int64_t f, int E, int k);
+size_t moe_ws_bytes(int64_t n, int64_t d, int64_t f, int E, int k);
 gptq_status moe_launch(const MoeCall& c, hipStream_t s);
 
 }  // namespace gptq

@@ -91,7 +91,7 @@ size_t gptqs_moe_workspace_size(int64_t n_tokens, int64_t d, int64_t f, int32_t 
     if (n_tokens > MOE_MAX_TOKENS || n_experts > MOE_MAX_EXPERTS || top_k > MOE_MAX_TOPK || d > MOE_MAX_WIDTH ||
         f > MOE_MAX_WIDTH)
         return 0;
-    return moe_ws_bytes(n_tokens, f, n_experts, top_k);
+    return moe_ws_bytes(n_tokens, d, f, n_experts, top_k);
 }
 
 gptq_status gptqs_moe(const void* x, gptq_dtype x_dtype, int64_t n_tokens, int64_t d, int64_t ldx, const void* router,
@@ -113,7 +113,7 @@ gptq_status gptqs_moe(const void* x, gptq_dtype x_dtype, int64_t n_tokens, int64
     if (!x || !router || !up_codes || !up_scales_f16 || !up_zeros_f16 || !down_codes || !down_scales_f16 ||
         !down_zeros_f16 || !y || !topk_ids || !topk_weights)
         return GPTQ_ERR_INVALID_ARG;
-    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 15) || ws_bytes < moe_ws_bytes(n_tokens, f, n_experts, top_k))
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 15) || ws_bytes < moe_ws_bytes(n_tokens, d, f, n_experts, top_k))
         return GPTQ_ERR_WORKSPACE;
     MoeCall c;
     c.x = x; c.xt = x_dtype; c.n = n_tokens; c.d = d; c.ldx = ldx; c.f = f;

@@ -100,6 +100,21 @@ GPTQ_DEV void minus_zero_bf16(uint32_t u4, float zc, uint32_t (&o)[2]) {
     o[0] = __builtin_bit_cast(uint32_t, __builtin_convertvector(a, bf16x2_t));
     o[1] = __builtin_bit_cast(uint32_t, __builtin_convertvector(b, bf16x2_t));
 }
+// u itself of four columns of 3- or 4-bit codes in a 16-bit type.  A byte below 16 read as
+// an FP8 E4M3 number is u 2^-9 (u < 8: the subnormals; 8 to 15: 2^-6 (1 + (u - 8) / 8)),
+// and one instruction turns two of them into 16-bit numbers times a power of two: half an
+// instruction per code, where a conversion and a subtraction in fp32 take two and a half.
+template <int X>
+GPTQ_DEV void plain_16(uint32_t u4, uint32_t (&o)[2]) {
+    if constexpr (X == X_F16) {
+        o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(u4, 512.f, false));
+        o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(u4, 512.f, true));
+    } else {
+        o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(u4, 512.f, false));
+        o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(u4, 512.f, true));
+    }
+}
+
 template <int X>
 GPTQ_DEV void minus_zero_16(uint32_t u4, float zc, uint32_t (&o)[2]) {
     if constexpr (X == X_F16) {
@@ -172,127 +187,163 @@ struct Stored {
     const uint8_t* codes; int64_t code_ld;             // bytes per row
     const uint16_t* scales; const uint16_t* zeros;     // fp16, rows x n_groups
     int64_t d_col;
-    int n_groups, cpg;                                 // cpg: chunks per group (128-column pieces)
+    int n_groups;
     int gshift;                                        // log2 of the group's columns (groups)
 };
 
+// What one chunk of RB row blocks and NTT token tiles needs, in registers.
+template <int X, int CB, int RUN, int NTT, int RB>
+struct Chunk {
+    static constexpr int P = 32 / RUN;        // pieces
+    Raw<CB, RUN> c[RB][P];
+    XRun<X, RUN> x[NTT][P];
+    uint16_t S[RB][P], z[RB][P];
+
+    // row[rb]: the lane's weight row; xrow[tt]: its token's first element
+    // TAIL: the chunk in which the rows end
+    template <bool TAIL>
+    GPTQ_DEV void load(const Stored& L, const int64_t (&row)[RB], const uint8_t* const (&xrow)[NTT], int c0) {
+        const int q = (threadIdx.x & 63) >> 4;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int64_t col = (int64_t)c0 * SCK + p * 4 * RUN + q * RUN;
+            const int left = (int)(L.d_col - col < RUN ? L.d_col - col : RUN);
+            int g = RUN == 32 && L.n_groups == 1 ? 0 : c0 * P + p;
+            if (TAIL) g = g < L.n_groups ? g : L.n_groups - 1;
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb) {
+                const uint8_t* src = L.codes + row[rb] * L.code_ld + col / 8 * CB;
+                c[rb][p] = !TAIL ? load_raw<CB, RUN>(src) : load_raw_tail<CB, RUN>(src, left);
+                S[rb][p] = L.scales[row[rb] * L.n_groups + g];
+                z[rb][p] = L.zeros[row[rb] * L.n_groups + g];
+            }
+#pragma unroll
+            for (int tt = 0; tt < NTT; ++tt) {
+                const uint8_t* src = xrow[tt] + col * xbytes<X>();
+                x[tt][p] = !TAIL ? load_x<X, RUN>(src) : load_x_tail<X, RUN>(src, left);
+            }
+        }
+    }
+
+    // 3- and 4-bit codes with 16-bit activations enter as they are (see plain_16); the whole
+    // zero is then a rest, taken off with sum x, which all the row blocks share
+    static constexpr bool PLAIN = X != X_I8 && CB != 8;
+    typedef typename Acc<X>::t sum_t;
+
+    // sum x of piece p, per token
+    GPTQ_DEV void x_sums(float (&xs)[NTT][4], int p) const {
+        const uint32_t w1 = ones_word<X>();
+#pragma unroll
+        for (int tt = 0; tt < NTT; ++tt) {
+            sum_t s = {0, 0, 0, 0};
+            const uint32_t* a = x[tt][p].w;
+            if constexpr (X == X_I8 && RUN == 8) {
+                s = mfma8_i8(a[0], a[1], w1, w1, s);
+            } else {
+#pragma unroll
+                for (int t = 0; t < RUN * xbytes<X>() / 16; ++t)
+                    s = mfma16<X>(u32x4_t{a[4 * t], a[4 * t + 1], a[4 * t + 2], a[4 * t + 3]}, u32x4_t{w1, w1, w1, w1}, s);
+            }
+            if constexpr (!PLAIN) settle(s);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) xs[tt][i] = (float)s[i];
+        }
+    }
+
+    // acc[tt][rb] += the chunk's sums: lane l's value i the output of weight row l % 16 and
+    // token 4 (l / 16) + i
+    GPTQ_DEV void multiply(f32x4_t (&acc)[NTT][RB]) const {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            float xs[NTT][4];
+            if constexpr (PLAIN) x_sums(xs, p);
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb) {
+                const float S = f16_bits_to_f32(this->S[rb][p]), z = f16_bits_to_f32(this->z[rb][p]);
+                const float zc = PLAIN ? 0.f : zero_part<X, CB>(z), rz = z - zc;
+                sum_t cs[NTT];
+#pragma unroll
+                for (int tt = 0; tt < NTT; ++tt) cs[tt] = sum_t{0, 0, 0, 0};
+                if constexpr (X == X_I8 && RUN == 8) {
+                    const uint32_t zz = (uint32_t)((int)zc * 0x01010101);
+                    const uint32_t b0 = minus_zero_i8<CB>(code_bytes4<CB, RUN>(c[rb][p], 0), zz);
+                    const uint32_t b1 = minus_zero_i8<CB>(code_bytes4<CB, RUN>(c[rb][p], 1), zz);
+#pragma unroll
+                    for (int tt = 0; tt < NTT; ++tt) cs[tt] = mfma8_i8(x[tt][p].w[0], x[tt][p].w[1], b0, b1, cs[tt]);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < RUN * xbytes<X>() / 16; ++t) {
+                        u32x4_t b;
+                        if constexpr (X == X_I8) {
+                            const uint32_t zz = (uint32_t)((int)zc * 0x01010101);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                b[e] = minus_zero_i8<CB>(code_bytes4<CB, RUN>(c[rb][p], 4 * t + e), zz);
+                        } else {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                uint32_t o[2];
+                                const uint32_t u4 = code_bytes4<CB, RUN>(c[rb][p], 2 * t + h);
+                                if constexpr (PLAIN) plain_16<X>(u4, o);
+                                else minus_zero_16<X>(u4, zc, o);
+                                b[2 * h] = o[0];
+                                b[2 * h + 1] = o[1];
+                            }
+                        }
+#pragma unroll
+                        for (int tt = 0; tt < NTT; ++tt) {
+                            const uint32_t* a = x[tt][p].w + 4 * t;
+                            cs[tt] = mfma16<X>(u32x4_t{a[0], a[1], a[2], a[3]}, b, cs[tt]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int tt = 0; tt < NTT; ++tt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        acc[tt][rb][i] = fmaf(S, (float)cs[tt][i], acc[tt][rb][i]);
+                        if constexpr (PLAIN) acc[tt][rb][i] = fmaf(-S * rz, xs[tt][i], acc[tt][rb][i]);
+                    }
+                if constexpr (!PLAIN) {
+                    if (__ballot(!(rz == 0.f)) != 0) {         // some zero leaves a rest: rz sum x off the piece
+                        x_sums(xs, p);
+#pragma unroll
+                        for (int tt = 0; tt < NTT; ++tt)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) acc[tt][rb][i] = fmaf(-S * rz, xs[tt][i], acc[tt][rb][i]);
+                    }
+                }
+            }
+        }
+    }
+};
+
 // Sums of RB blocks of 16 weight rows with NTT tiles of 16 tokens over the chunks c0, c0 +
-// step, .. below nck: acc[tt][rb], lane l's value i the output of weight row l % 16 and
-// token 4 (l / 16) + i.  row[rb]: the lane's weight row; xrow[tt]: the lane's token's
-// first element.  CPW chunks are loaded before their arithmetic begins.
-template <int X, int CB, int RUN, int NTT, int RB, int CPW>
+// step, .. of a row.  DEEP chunks are in registers at a time: one is multiplied while the
+// others are on their way.
+template <int X, int CB, int RUN, int NTT, int RB, int DEEP>
 GPTQ_DEV void stored_accumulate(f32x4_t (&acc)[NTT][RB], const Stored& L, const int64_t (&row)[RB],
-                                const uint8_t* const (&xrow)[NTT], int c0, int step, int nck) {
-    constexpr int P = 32 / RUN;               // pieces per chunk
-    constexpr int XB = xbytes<X>();
-    const int q = (threadIdx.x & 63) >> 4;
-    for (int cb = c0; cb < nck; cb += step * CPW) {
-        Raw<CB, RUN> cw[CPW][RB][P];
-        XRun<X, RUN> xw[CPW][NTT][P];
-        uint16_t S16[CPW][RB][P], Z16[CPW][RB][P];
+                                const uint8_t* const (&xrow)[NTT], int c0, int step) {
+    const int nfull = (int)(L.d_col / SCK);
+    Chunk<X, CB, RUN, NTT, RB> ch[DEEP];
 #pragma unroll
-        for (int j = 0; j < CPW; ++j) {
-            const int c = cb + step * j < nck ? cb + step * j : cb;   // chunks past the end re-read the first
-            const bool full = (int64_t)(c + 1) * SCK <= L.d_col;
+    for (int j = 0; j < DEEP; ++j)
+        if (c0 + j * step < nfull) ch[j].template load<false>(L, row, xrow, c0 + j * step);
+    __builtin_amdgcn_sched_barrier(0);         // every load above the arithmetic
+    for (int c = c0; c < nfull; c += DEEP * step) {
 #pragma unroll
-            for (int p = 0; p < P; ++p) {
-                const int64_t col = (int64_t)c * SCK + p * 4 * RUN + q * RUN;
-                const int64_t left = L.d_col - col;
-                int g = RUN == 32 ? c / L.cpg : c * P + p;
-                g = g < L.n_groups ? g : L.n_groups - 1;
-#pragma unroll
-                for (int rb = 0; rb < RB; ++rb) {
-                    const uint8_t* src = L.codes + row[rb] * L.code_ld + col / 8 * CB;
-                    cw[j][rb][p] = full ? load_raw<CB, RUN>(src) : load_raw_tail<CB, RUN>(src, (int)(left < RUN ? left : RUN));
-                    S16[j][rb][p] = L.scales[row[rb] * L.n_groups + g];
-                    Z16[j][rb][p] = L.zeros[row[rb] * L.n_groups + g];
-                }
-#pragma unroll
-                for (int tt = 0; tt < NTT; ++tt) {
-                    const uint8_t* src = xrow[tt] + col * XB;
-                    xw[j][tt][p] = full ? load_x<X, RUN>(src) : load_x_tail<X, RUN>(src, (int)(left < RUN ? left : RUN));
-                }
+        for (int j = 0; j < DEEP; ++j) {
+            const int at = c + j * step, next = at + DEEP * step;
+            if (at < nfull) {                  // wave-uniform
+                ch[j].multiply(acc);
+                if (next < nfull) ch[j].template load<false>(L, row, xrow, next);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
-        __builtin_amdgcn_sched_barrier(0);    // keep every load above the arithmetic
-#pragma unroll
-        for (int j = 0; j < CPW; ++j) {
-            if (cb + step * j >= nck) break;  // wave-uniform
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-#pragma unroll
-                for (int rb = 0; rb < RB; ++rb) {
-                    const float S = f16_bits_to_f32(S16[j][rb][p]), z = f16_bits_to_f32(Z16[j][rb][p]);
-                    const float zc = zero_part<X, CB>(z), rz = z - zc;
-                    typedef typename Acc<X>::t sum_t;
-                    // sum x where some zero has a rest, as fp32
-                    float xs[NTT][4];
-#pragma unroll
-                    for (int tt = 0; tt < NTT; ++tt)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) xs[tt][i] = 0.f;
-                    if (__ballot(!(rz == 0.f)) != 0) {
-                        const uint32_t w1 = ones_word<X>();
-                        sum_t s[NTT];
-#pragma unroll
-                        for (int tt = 0; tt < NTT; ++tt) {
-                            s[tt] = sum_t{0, 0, 0, 0};
-                            const uint32_t* a = xw[j][tt][p].w;
-                            if constexpr (X == X_I8 && RUN == 8) {
-                                s[tt] = mfma8_i8(a[0], a[1], w1, w1, s[tt]);
-                            } else {
-#pragma unroll
-                                for (int t = 0; t < RUN * xbytes<X>() / 16; ++t)
-                                    s[tt] = mfma16<X>(u32x4_t{a[4 * t], a[4 * t + 1], a[4 * t + 2], a[4 * t + 3]},
-                                                      u32x4_t{w1, w1, w1, w1}, s[tt]);
-                            }
-                        }
-#pragma unroll
-                        for (int tt = 0; tt < NTT; ++tt) {
-                            settle(s[tt]);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) xs[tt][i] = (float)s[tt][i];
-                        }
-                    }
-                    sum_t cs[NTT];
-#pragma unroll
-                    for (int tt = 0; tt < NTT; ++tt) cs[tt] = sum_t{0, 0, 0, 0};
-                    if constexpr (X == X_I8 && RUN == 8) {
-                        const uint32_t zz = (uint32_t)((int)zc * 0x01010101);
-                        const uint32_t b0 = minus_zero_i8<CB>(code_bytes4<CB, RUN>(cw[j][rb][p], 0), zz);
-                        const uint32_t b1 = minus_zero_i8<CB>(code_bytes4<CB, RUN>(cw[j][rb][p], 1), zz);
-#pragma unroll
-                        for (int tt = 0; tt < NTT; ++tt) cs[tt] = mfma8_i8(xw[j][tt][p].w[0], xw[j][tt][p].w[1], b0, b1, cs[tt]);
-                    } else {
-#pragma unroll
-                        for (int t = 0; t < RUN * xbytes<X>() / 16; ++t) {
-                            u32x4_t b;
-                            if constexpr (X == X_I8) {
-                                const uint32_t zz = (uint32_t)((int)zc * 0x01010101);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    b[e] = minus_zero_i8<CB>(code_bytes4<CB, RUN>(cw[j][rb][p], 4 * t + e), zz);
-                            } else {
-                                uint32_t lo[2], hi[2];
-                                minus_zero_16<X>(code_bytes4<CB, RUN>(cw[j][rb][p], 2 * t), zc, lo);
-                                minus_zero_16<X>(code_bytes4<CB, RUN>(cw[j][rb][p], 2 * t + 1), zc, hi);
-                                b = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
-                            }
-#pragma unroll
-                            for (int tt = 0; tt < NTT; ++tt) {
-                                const uint32_t* a = xw[j][tt][p].w + 4 * t;
-                                cs[tt] = mfma16<X>(u32x4_t{a[0], a[1], a[2], a[3]}, b, cs[tt]);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int tt = 0; tt < NTT; ++tt)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            acc[tt][rb][i] = fmaf(S, fmaf(-rz, xs[tt][i], (float)cs[tt][i]), acc[tt][rb][i]);
-                }
-            }
-        }
+    }
+    if (L.d_col % SCK && nfull >= c0 && (nfull - c0) % step == 0) {
+        ch[0].template load<true>(L, row, xrow, nfull);
+        ch[0].multiply(acc);
     }
 }
 
@@ -318,8 +369,6 @@ inline Stored stored_layer(const uint8_t* codes, const uint16_t* scales, const u
     L.scales = scales; L.zeros = zeros; L.d_col = d_col;
     L.gshift = group == 32 ? 5 : group == 64 ? 6 : 7;
     L.n_groups = group > 0 ? (int)(d_col / group) : 1;
-    const int64_t nck = (d_col + SCK - 1) / SCK;
-    L.cpg = group > 0 ? 1 : (int)nck;      // of the 128-column pieces; groups are 128 or the row
     return L;
 }
 

@@ -47,13 +47,15 @@ def out_rounding(ref, t):
 
 
 def zero_parts(q, x, eight=False):
-    """S sum_c |x_c| (|u - zc| + |z - zc|): what the products add up, per token and row.  zc is
-    the whole number next to z within what the operand takes: 16 bits, 240 on either side
-    of 0 (8-bit codes: -1 .. 255); 8 bits (``eight``), -112 .. 127 (8-bit codes: 128)."""
+    """S sum_c |x_c| (|u - zc| + |z - zc|): what the products add up, per token and row, with
+    zc the part of the zero that the operand takes.  8 bits (``eight``): the whole number
+    next to z in -112 .. 127 (8-bit codes: 128).  16 bits: for 8-bit codes the one in -1 ..
+    255; for narrower ones 0, small batches taking the codes as they are (large ones take
+    a zc between 0 and z, for which the sum is no larger: |u - zc| <= |u| + |zc|)."""
     u = o.unpack(q.codes.cpu().numpy(), q.bits).astype(np.float64)
     rep = u.shape[1] // q.scales.shape[1]
     S, Z = (np.repeat(t.cpu().numpy().astype(np.float64), rep, axis=1) for t in (q.scales, q.zeros))
-    low, high = ((128, 128) if q.bits == 8 else (-112, 127)) if eight else ((-1, 255) if q.bits == 8 else (-240, 240))
+    low, high = ((128, 128) if q.bits == 8 else (-112, 127)) if eight else ((-1, 255) if q.bits == 8 else (0, 0))
     zc = np.clip(np.rint(Z), low, high)
     return x.abs() @ torch.from_numpy(S * (np.abs(u - zc) + np.abs(Z - zc))).t()
 
