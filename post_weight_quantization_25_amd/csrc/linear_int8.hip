@@ -35,9 +35,8 @@ __global__ __launch_bounds__(64 * TW) void int8_tile_kernel(Int8Args a) {
     }
 #pragma unroll
     for (int tt = 0; tt < NTT; ++tt) {
-        int64_t t = tok0 + 16 * tt + n16;
-        t = t < a.n ? t : a.n - 1;                               // a repeated token past the end
-        xrow[tt] = reinterpret_cast<const uint8_t*>(a.x) + t * a.ldx;
+        const int64_t t = tok0 + 16 * tt + n16;
+        xrow[tt] = t < a.n ? reinterpret_cast<const uint8_t*>(a.x) + t * a.ldx : nullptr;
     }
     f32x4_t acc[NTT][RB];
 #pragma unroll

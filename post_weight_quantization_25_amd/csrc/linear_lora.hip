@@ -106,9 +106,8 @@ __global__ __launch_bounds__(64 * TW) void lora_tile_kernel(LoraArgs a) {
     }
 #pragma unroll
     for (int tt = 0; tt < NTT; ++tt) {
-        int64_t t = tok0 + 16 * tt + n16;
-        t = t < a.n ? t : a.n - 1;
-        xrow[tt] = reinterpret_cast<const uint8_t*>(a.x + t * a.ldx);
+        const int64_t t = tok0 + 16 * tt + n16;
+        xrow[tt] = t < a.n ? reinterpret_cast<const uint8_t*>(a.x + t * a.ldx) : nullptr;
     }
     f32x4_t acc[NTT][RB];
 #pragma unroll

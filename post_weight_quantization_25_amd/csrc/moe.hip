@@ -207,8 +207,9 @@ __global__ __launch_bounds__(64 * MW, 4) void moe_up_kernel(MoeArgs a) {
     const int64_t fr = f0 + n16 < a.f ? f0 + n16 : a.f - 1;
     const int64_t row[2] = {(int64_t)e * 2 * a.f + fr, (int64_t)e * 2 * a.f + a.f + fr};
     for (int m0 = 0; m0 < cnt; m0 += MOE_T) {
-        const int p = a.plan[PAIRS + p0 + (m0 + n16 < cnt ? m0 + n16 : cnt - 1)];
-        const uint8_t* const xrow[1] = {reinterpret_cast<const uint8_t*>(a.x + (int64_t)(p / a.k) * a.ldx)};
+        const bool live = m0 + n16 < cnt;
+        const int p = live ? a.plan[PAIRS + p0 + m0 + n16] : 0;
+        const uint8_t* const xrow[1] = {live ? reinterpret_cast<const uint8_t*>(a.x + (int64_t)(p / a.k) * a.ldx) : nullptr};
         f32x4_t acc[1][2] = {{f32x4_t{0.f, 0.f, 0.f, 0.f}, f32x4_t{0.f, 0.f, 0.f, 0.f}}};
         stored_accumulate<X, CB, RUN, 1, 2, 1>(acc, a.up, row, xrow, wave, MW);
         __syncthreads();                                    // the last tile's sums are read
@@ -249,8 +250,10 @@ __global__ __launch_bounds__(64 * MW, 4) void moe_down_kernel(MoeArgs a) {
     const int64_t r0 = (int64_t)blockIdx.x * 16;
     const int64_t row[1] = {(int64_t)e * a.d + (r0 + n16 < a.d ? r0 + n16 : a.d - 1)};
     for (int m0 = 0; m0 < cnt; m0 += MOE_T) {
-        const int64_t at = (int64_t)a.plan[PAIRS + p0 + (m0 + n16 < cnt ? m0 + n16 : cnt - 1)] * a.f;
-        const uint8_t* const xrow[2] = {reinterpret_cast<const uint8_t*>(a.hi + at), reinterpret_cast<const uint8_t*>(a.lo + at)};
+        const bool live = m0 + n16 < cnt;
+        const int64_t at = live ? (int64_t)a.plan[PAIRS + p0 + m0 + n16] * a.f : 0;
+        const uint8_t* const xrow[2] = {live ? reinterpret_cast<const uint8_t*>(a.hi + at) : nullptr,
+                                        live ? reinterpret_cast<const uint8_t*>(a.lo + at) : nullptr};
         f32x4_t acc[2][1] = {{f32x4_t{0.f, 0.f, 0.f, 0.f}}, {f32x4_t{0.f, 0.f, 0.f, 0.f}}};
         stored_accumulate<X_BF16, CB, RUN, 2, 1, 1>(acc, a.down, row, xrow, wave, MW);
         __syncthreads();

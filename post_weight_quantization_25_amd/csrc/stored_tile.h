@@ -195,15 +195,23 @@ struct Stored {
 template <int X, int CB, int RUN, int NTT, int RB>
 struct Chunk {
     static constexpr int P = 32 / RUN;        // pieces
+    static constexpr int SZ = (RB + 1) / 2;
     Raw<CB, RUN> c[RB][P];
     XRun<X, RUN> x[NTT][P];
-    uint16_t S[RB][P], z[RB][P];
+    // one load fetches the scales and zeros of two row blocks: lane group q holds the scale (q
+    // even) or the zero (odd) of block 2 k + q / 2
+    uint16_t sz[SZ][P];
 
-    // row[rb]: the lane's weight row; xrow[tt]: its token's first element
-    // TAIL: the chunk in which the rows end
+    // row[rb]: the lane's weight row; xrow[tt]: its token's first element, or nullptr for a row
+    // of the tile without a token (zeros, and nothing is read).  TAIL: the chunk in which the
+    // rows end
     template <bool TAIL>
     GPTQ_DEV void load(const Stored& L, const int64_t (&row)[RB], const uint8_t* const (&xrow)[NTT], int c0) {
         const int q = (threadIdx.x & 63) >> 4;
+        const uint16_t* tab = (q & 1) ? L.zeros : L.scales;
+        int64_t szrow[SZ];
+#pragma unroll
+        for (int k = 0; k < SZ; ++k) szrow[k] = row[2 * k + 1 < RB && q >= 2 ? 2 * k + 1 : 2 * k] * L.n_groups;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             const int64_t col = (int64_t)c0 * SCK + p * 4 * RUN + q * RUN;
@@ -214,15 +222,32 @@ struct Chunk {
             for (int rb = 0; rb < RB; ++rb) {
                 const uint8_t* src = L.codes + row[rb] * L.code_ld + col / 8 * CB;
                 c[rb][p] = !TAIL ? load_raw<CB, RUN>(src) : load_raw_tail<CB, RUN>(src, left);
-                S[rb][p] = L.scales[row[rb] * L.n_groups + g];
-                z[rb][p] = L.zeros[row[rb] * L.n_groups + g];
             }
 #pragma unroll
-            for (int tt = 0; tt < NTT; ++tt) {
-                const uint8_t* src = xrow[tt] + col * xbytes<X>();
-                x[tt][p] = !TAIL ? load_x<X, RUN>(src) : load_x_tail<X, RUN>(src, left);
+            for (int k = 0; k < SZ; ++k) sz[k][p] = tab[szrow[k] + g];
+        }
+#pragma unroll
+        for (int tt = 0; tt < NTT; ++tt) {
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+#pragma unroll
+                for (int e = 0; e < RUN * xbytes<X>() / 4; ++e) x[tt][p].w[e] = 0;
+            if (xrow[tt] != nullptr) {
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    const int64_t col = (int64_t)c0 * SCK + p * 4 * RUN + q * RUN;
+                    const int left = (int)(L.d_col - col < RUN ? L.d_col - col : RUN);
+                    const uint8_t* src = xrow[tt] + col * xbytes<X>();
+                    x[tt][p] = !TAIL ? load_x<X, RUN>(src) : load_x_tail<X, RUN>(src, left);
+                }
             }
         }
+    }
+
+    // scale (which 0) or zero (1) of the lane's row in block rb
+    GPTQ_DEV float scale_of(int rb, int p, int which) const {
+        const int v = __shfl((int)sz[rb / 2][p], (int)(threadIdx.x & 15) + 16 * (2 * (rb & 1) + which));
+        return f16_bits_to_f32((uint16_t)v);
     }
 
     // 3- and 4-bit codes with 16-bit activations enter as they are (see plain_16); the whole
@@ -259,7 +284,7 @@ struct Chunk {
             if constexpr (PLAIN) x_sums(xs, p);
 #pragma unroll
             for (int rb = 0; rb < RB; ++rb) {
-                const float S = f16_bits_to_f32(this->S[rb][p]), z = f16_bits_to_f32(this->z[rb][p]);
+                const float S = scale_of(rb, p, 0), z = scale_of(rb, p, 1);
                 const float zc = PLAIN ? 0.f : zero_part<X, CB>(z), rz = z - zc;
                 sum_t cs[NTT];
 #pragma unroll
