@@ -24,8 +24,8 @@ typedef unsigned long long u64;
 template <gptq_dtype T>
 GPTQ_DEV float round_to(float v) {
     if constexpr (T == GPTQ_F32) return v;
-    else if constexpr (T == GPTQ_BF16) return bf16_bits_to_f32(f32_to_bf16_bits(v));
-    else return f16_bits_to_f32(f32_to_f16_bits(v));
+    else if constexpr (T == GPTQ_BF16) return (float)(__bf16)v;
+    else return (float)(_Float16)v;
 }
 
 // Eight consecutive elements from idx on, of which the first m exist (0 for the others).
@@ -63,7 +63,8 @@ GPTQ_DEV void store8(void* base, int64_t idx, int m, const float (&v)[8]) {
     } else {
         uint16_t b[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) b[e] = T == GPTQ_BF16 ? f32_to_bf16_bits(v[e]) : f32_to_f16_bits(v[e]);
+        for (int e = 0; e < 8; ++e)
+            b[e] = T == GPTQ_BF16 ? __builtin_bit_cast(uint16_t, (__bf16)v[e]) : __builtin_bit_cast(uint16_t, (_Float16)v[e]);
         if (m >= 8) __builtin_memcpy(reinterpret_cast<uint16_t*>(base) + idx, b, 16);
         else
 #pragma unroll
@@ -81,16 +82,27 @@ GPTQ_DEV void store_codes(int8_t* q, int64_t idx, int m, const int (&k)[8]) {
         for (int e = 0; e < 8; ++e) if (e < m) q[idx + e] = b[e];
 }
 
-// Code of p in a row with maximum am (both exact): see the head of the file.
-GPTQ_DEV int code_exact32(float p, float inv, float am) {
-    const float t = p * inv, a = fabsf(t);
-    float k = rintf(a);
-    if (fabsf(fabsf(a - k) - 0.5f) < 0x1p-13f) {
-        const float m = floorf(a);
-        const double l = 254.0 * (double)fabsf(p), r = (2.0 * (double)m + 1.0) * (double)am;
-        k = l > r ? m + 1.f : l < r ? m : (((int)m & 1) ? m + 1.f : m);
+// Codes of eight products p in a row with maximum am (all exact, inv = 127 / am): see the
+// head of the file.
+GPTQ_DEV void codes_exact32(const float (&p)[8], float inv, float am, int (&k)[8]) {
+    float near = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float t = p[e] * inv, r = rintf(t);
+        near = fmaxf(near, fabsf(t - r));
+        k[e] = (int)r;
     }
-    return p < 0.f ? -(int)k : (int)k;
+    if (near > 0.5f - 0x1p-13f) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float a = fabsf(p[e] * inv), m = floorf(a);
+            if (fabsf(a - m - 0.5f) < 0x1p-13f) {
+                const double l = 254.0 * (double)fabsf(p[e]), r = (2.0 * (double)m + 1.0) * (double)am;
+                const int up = (int)m + 1, c = l > r ? up : l < r ? (int)m : (((int)m & 1) ? up : (int)m);
+                k[e] = p[e] < 0.f ? -c : c;
+            }
+        }
+    }
 }
 
 GPTQ_DEV double wave_add(double v) {
@@ -118,143 +130,32 @@ constexpr u64 INF64 = 0x7ff0000000000000ull;
 // been rounded by underflow or overflow.
 GPTQ_DEV bool plain_max(uint32_t b) { return b >= 0x0f800000u && b < 0x7b800000u; }   // 2^-96 .. 2^120
 
-// TPR threads per row (a wave, or a workgroup), NV vectors of 8 elements per thread; rows
-// of up to 8 TPR NV elements.
-template <gptq_dtype XT, gptq_dtype WT, int TPR, int NV>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a) {
-    constexpr int ROWS = TPR < 256 ? 256 / TPR : 1;       // rows per workgroup
-    constexpr int WAVES = TPR / 64;                       // waves per row
-    constexpr bool WIDE = XT == GPTQ_F32 || WT == GPTQ_F32;   // p is not exact in fp32
-    __shared__ double s_sum[WAVES];
-    __shared__ u64 s_max[WAVES];
-    const int tid = threadIdx.x % TPR, wave = tid >> 6;
-    const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
-    if (WAVES == 1 && row >= a.n) return;                 // whole waves: no barrier below
-
-    float h[NV][8];
-    double ss = 0.0;
-    uint32_t mb = 0;
-    u64 mb64 = 0;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int64_t c = 8 * ((int64_t)tid + (int64_t)TPR * j);
-        const int m = c + 8 <= a.d ? 8 : c < a.d ? (int)(a.d - c) : 0;
-        load8<XT>(a.x, row * a.ldx + c, m, h[j]);
-        if (a.r) {
-            float r[8];
-            load8<XT>(a.r, row * a.ldr + c, m, r);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) h[j][e] = round_to<XT>(h[j][e] + r[e]);
-        }
-    }
-    float w[NV][8];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int64_t c = 8 * ((int64_t)tid + (int64_t)TPR * j);
-        const int m = c + 8 <= a.d ? 8 : c < a.d ? (int)(a.d - c) : 0;
-        load8<WT>(a.w, c, m, w[j]);
-        if (a.h) store8<XT>(a.h, row * a.ldh + c, m, h[j]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            ss = fma((double)h[j][e], (double)h[j][e], ss);
-            if constexpr (WIDE) {
-                const u64 b = mag_bits((double)h[j][e] * (double)w[j][e]);
-                mb64 = b > mb64 ? b : mb64;
-            } else {
-                const uint32_t b = mag_bits(h[j][e] * w[j][e]);
-                mb = b > mb ? b : mb;
-            }
-        }
-    }
-    ss = wave_add(ss);
-    if constexpr (WIDE) mb64 = wave_max(mb64); else mb = wave_max(mb);
-    if constexpr (WAVES > 1) {
-        if ((threadIdx.x & 63) == 0) { s_sum[wave] = ss; s_max[wave] = WIDE ? mb64 : (u64)mb; }
-        __syncthreads();
-        ss = 0.0;
-#pragma unroll
-        for (int k = 0; k < WAVES; ++k) {
-            ss += s_sum[k];
-            if constexpr (WIDE) mb64 = s_max[k] > mb64 ? s_max[k] : mb64;
-            else mb = (uint32_t)s_max[k] > mb ? (uint32_t)s_max[k] : mb;
-        }
-    }
-    const double rstd = 1.0 / sqrt(ss / (double)a.d + (double)a.eps);
-    bool narrow = false;
-    if constexpr (!WIDE) narrow = plain_max(mb);
-    double am = 0.0;
-    if (!narrow) {
-        // the maximum in 64 bits (a row-uniform branch: 16-bit rows come here only when
-        // all their products are tiny or zero, or one is huge or not finite)
-        if constexpr (!WIDE) {
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const u64 b = mag_bits((double)h[j][e] * (double)w[j][e]);
-                    mb64 = b > mb64 ? b : mb64;
-                }
-            mb64 = wave_max(mb64);
-            if constexpr (WAVES > 1) {
-                __syncthreads();                          // the first use of s_max is read
-                if ((threadIdx.x & 63) == 0) s_max[wave] = mb64;
-                __syncthreads();
-#pragma unroll
-                for (int k = 0; k < WAVES; ++k) mb64 = s_max[k] > mb64 ? s_max[k] : mb64;
-            }
-        }
-        am = __longlong_as_double((long long)mb64);
-    } else {
-        am = (double)__uint_as_float(mb);
-    }
-    const bool bad = !narrow && mb64 >= INF64;
-    const float amf = __uint_as_float(mb), inv = narrow ? 127.f / amf : 0.f;
-    const float rstdf = (float)rstd;
-    if (tid == 0) a.scale[row] = bad ? __uint_as_float(0x7fc00000u) : am == 0.0 ? 1.f : (float)(am * rstd / 127.0);
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int64_t c = 8 * ((int64_t)tid + (int64_t)TPR * j);
-        const int m = c + 8 <= a.d ? 8 : c < a.d ? (int)(a.d - c) : 0;
-        int k[8];
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (narrow) {
-                const float p = h[j][e] * w[j][e];
-                k[e] = code_exact32(p, inv, amf);
-                y[e] = p * rstdf;
-            } else {
-                const double p = (double)h[j][e] * (double)w[j][e];
-                k[e] = bad || am == 0.0 ? 0 : (int)rint(p * 127.0 / am);
-                y[e] = (float)(p * rstd);
-            }
-        }
-        store_codes(a.q, row * a.ldq + c, m, k);
-        if (a.y) store8<XT>(a.y, row * a.ldy + c, m, y);
-    }
-}
-
-// Rows of any length: two passes over the row; the second reads h where it was written
-// (each thread its own elements), else x and the residual again.
-template <gptq_dtype XT, gptq_dtype WT>
-__global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
-    __shared__ double s_sum[16];
-    __shared__ u64 s_max[16];
-    const int tid = threadIdx.x;
-    const int64_t row = blockIdx.x;
+// A row by TPR threads in two passes over memory, products in 64 bits: rows too long for
+// registers, fp32 rows or weights (their products are not exact in fp32), and 16-bit rows
+// whose products are all tiny or zero, or of which one is huge or not finite.  FIRST: h is
+// formed, and written where it is wanted; else it has been.  The second pass reads h where
+// it was written (each thread its own elements), else x and the residual again.
+template <gptq_dtype XT, gptq_dtype WT, int TPR, bool FIRST>
+GPTQ_DEV void row_in_64(const NormArgs& a, int64_t row, int tid, double* s_sum, u64* s_max) {
+    constexpr int WAVES = TPR / 64;
     double ss = 0.0;
     u64 mb = 0;
-    for (int64_t c = 8 * (int64_t)tid; c < a.d; c += 8 * 1024) {
+#pragma unroll 1
+    for (int64_t c = 8 * (int64_t)tid; c < a.d; c += 8 * TPR) {
         const int m = c + 8 <= a.d ? 8 : (int)(a.d - c);
         float h[8], r[8], w[8];
-        load8<XT>(a.x, row * a.ldx + c, m, h);
-        if (a.r) {
-            load8<XT>(a.r, row * a.ldr + c, m, r);
+        if (!FIRST && a.h) {
+            load8<XT>(a.h, row * a.ldh + c, m, h);
+        } else {
+            load8<XT>(a.x, row * a.ldx + c, m, h);
+            if (a.r) {
+                load8<XT>(a.r, row * a.ldr + c, m, r);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[e] = round_to<XT>(h[e] + r[e]);
+                for (int e = 0; e < 8; ++e) h[e] = round_to<XT>(h[e] + r[e]);
+            }
         }
         load8<WT>(a.w, c, m, w);
-        if (a.h) store8<XT>(a.h, row * a.ldh + c, m, h);
+        if (FIRST && a.h) store8<XT>(a.h, row * a.ldh + c, m, h);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             ss = fma((double)h[e], (double)h[e], ss);
@@ -264,15 +165,19 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
     }
     ss = wave_add(ss);
     mb = wave_max(mb);
-    if ((tid & 63) == 0) { s_sum[tid >> 6] = ss; s_max[tid >> 6] = mb; }
-    __syncthreads();
-    ss = 0.0;
-    for (int k = 0; k < 16; ++k) { ss += s_sum[k]; mb = s_max[k] > mb ? s_max[k] : mb; }
+    if constexpr (WAVES > 1) {
+        __syncthreads();                                  // earlier uses of the arrays are read
+        if ((tid & 63) == 0) { s_sum[tid >> 6] = ss; s_max[tid >> 6] = mb; }
+        __syncthreads();
+        ss = 0.0;
+        for (int k = 0; k < WAVES; ++k) { ss += s_sum[k]; mb = s_max[k] > mb ? s_max[k] : mb; }
+    }
     const double rstd = 1.0 / sqrt(ss / (double)a.d + (double)a.eps);
     const bool bad = mb >= INF64;
     const double am = __longlong_as_double((long long)mb);
     if (tid == 0) a.scale[row] = bad ? __uint_as_float(0x7fc00000u) : am == 0.0 ? 1.f : (float)(am * rstd / 127.0);
-    for (int64_t c = 8 * (int64_t)tid; c < a.d; c += 8 * 1024) {
+#pragma unroll 1
+    for (int64_t c = 8 * (int64_t)tid; c < a.d; c += 8 * TPR) {
         const int m = c + 8 <= a.d ? 8 : (int)(a.d - c);
         float h[8], r[8], w[8], y[8];
         int k[8];
@@ -298,15 +203,105 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormArgs a) {
     }
 }
 
+// 16-bit rows and weights.  TPR threads per row (a wave, or a workgroup), NV vectors of 8
+// elements per thread; rows of up to 8 TPR NV elements.
+template <gptq_dtype XT, int TPR, int NV>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a) {
+    constexpr int ROWS = TPR < 256 ? 256 / TPR : 1;       // rows per workgroup
+    constexpr int WAVES = TPR / 64;                       // waves per row
+    __shared__ double s_sum[WAVES];
+    __shared__ u64 s_max[WAVES];
+    const int tid = threadIdx.x % TPR, wave = tid >> 6;
+    const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
+    if (WAVES == 1 && row >= a.n) return;                 // whole waves: no barrier below
+
+    float p[NV][8];                                       // first h, then the products
+    double ss = 0.0;
+    uint32_t mb = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int64_t c = 8 * ((int64_t)tid + (int64_t)TPR * j);
+        const int m = c + 8 <= a.d ? 8 : c < a.d ? (int)(a.d - c) : 0;
+        load8<XT>(a.x, row * a.ldx + c, m, p[j]);
+        if (a.r) {
+            float r[8];
+            load8<XT>(a.r, row * a.ldr + c, m, r);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[j][e] = round_to<XT>(p[j][e] + r[e]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int64_t c = 8 * ((int64_t)tid + (int64_t)TPR * j);
+        const int m = c + 8 <= a.d ? 8 : c < a.d ? (int)(a.d - c) : 0;
+        float w[8];
+        load8<XT>(a.w, c, m, w);
+        if (a.h) store8<XT>(a.h, row * a.ldh + c, m, p[j]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            ss = fma((double)p[j][e], (double)p[j][e], ss);
+            p[j][e] *= w[e];
+            const uint32_t b = mag_bits(p[j][e]);
+            mb = b > mb ? b : mb;
+        }
+    }
+    ss = wave_add(ss);
+    mb = wave_max(mb);
+    if constexpr (WAVES > 1) {
+        if ((threadIdx.x & 63) == 0) { s_sum[wave] = ss; s_max[wave] = mb; }
+        __syncthreads();
+        ss = 0.0;
+#pragma unroll
+        for (int k = 0; k < WAVES; ++k) {
+            ss += s_sum[k];
+            mb = (uint32_t)s_max[k] > mb ? (uint32_t)s_max[k] : mb;
+        }
+    }
+    if (!plain_max(mb)) {                                 // row-uniform, rare
+        row_in_64<XT, XT, TPR, false>(a, row, tid, s_sum, s_max);
+        return;
+    }
+    const double rstd = 1.0 / sqrt(ss / (double)a.d + (double)a.eps);
+    const float am = __uint_as_float(mb), inv = 127.f / am, rstdf = (float)rstd;
+    if (tid == 0) a.scale[row] = (float)((double)am * rstd / 127.0);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int64_t c = 8 * ((int64_t)tid + (int64_t)TPR * j);
+        const int m = c + 8 <= a.d ? 8 : c < a.d ? (int)(a.d - c) : 0;
+        int k[8];
+        codes_exact32(p[j], inv, am, k);
+        store_codes(a.q, row * a.ldq + c, m, k);
+        if (a.y) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[j][e] *= rstdf;
+            store8<XT>(a.y, row * a.ldy + c, m, p[j]);
+        }
+    }
+}
+
+template <gptq_dtype XT, gptq_dtype WT, int TPR>
+__global__ __launch_bounds__(TPR) void norm_64_kernel(NormArgs a) {
+    __shared__ double s_sum[TPR / 64];
+    __shared__ u64 s_max[TPR / 64];
+    row_in_64<XT, WT, TPR, true>(a, blockIdx.x, threadIdx.x, s_sum, s_max);
+}
+
 template <gptq_dtype XT, gptq_dtype WT>
 static gptq_status launch(const NormArgs& a, hipStream_t s) {
     const unsigned n = (unsigned)a.n;
-    if (a.d <= 512) norm_kernel<XT, WT, 64, 1><<<(unsigned)((a.n + 3) / 4), 256, 0, s>>>(a);
-    else if (a.d <= 2048) norm_kernel<XT, WT, 256, 1><<<n, 256, 0, s>>>(a);
-    else if (a.d <= 4096) norm_kernel<XT, WT, 256, 2><<<n, 256, 0, s>>>(a);
-    else if (a.d <= 8192) norm_kernel<XT, WT, 512, 2><<<n, 512, 0, s>>>(a);
-    else if (a.d <= 16384) norm_kernel<XT, WT, 1024, 2><<<n, 1024, 0, s>>>(a);
-    else norm_long_kernel<XT, WT><<<n, 1024, 0, s>>>(a);
+    if constexpr (XT != GPTQ_F32 && WT == XT) {
+        if (a.d <= 16384) {
+            if (a.d <= 512) norm_kernel<XT, 64, 1><<<(unsigned)((a.n + 3) / 4), 256, 0, s>>>(a);
+            else if (a.d <= 2048) norm_kernel<XT, 256, 1><<<n, 256, 0, s>>>(a);
+            else if (a.d <= 4096) norm_kernel<XT, 256, 2><<<n, 256, 0, s>>>(a);
+            else if (a.d <= 8192) norm_kernel<XT, 512, 2><<<n, 512, 0, s>>>(a);
+            else norm_kernel<XT, 1024, 2><<<n, 1024, 0, s>>>(a);
+            GPTQ_LAUNCH_CHECK();
+            return GPTQ_OK;
+        }
+    }
+    if (a.d <= 4096) norm_64_kernel<XT, WT, 256><<<n, 256, 0, s>>>(a);
+    else norm_64_kernel<XT, WT, 1024><<<n, 1024, 0, s>>>(a);
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
 }
