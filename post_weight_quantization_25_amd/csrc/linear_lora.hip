@@ -4,8 +4,9 @@
 //
 // Two launches.  lora_shrink_kernel forms v[t] = A_a x[t] on the matrix cores: a workgroup
 // takes 16 tokens and a share of the columns, and for each distinct adapter among its
-// tokens multiplies all 16 by that adapter's rows and keeps the rows of the tokens that
-// have it (a run of tokens with one adapter costs one product).  The shares' sums go to
+// tokens (few tokens: its share of them) multiplies all 16 by that adapter's rows and
+// keeps the rows of the tokens that have it (a run of tokens with one adapter costs one
+// product).  v of a token without an adapter is not written, and not used.  The shares' sums go to
 // the workspace, fp32, and are added in a fixed order by the readers.  Then the
 // projection's kernel adds s_a B_a v to its own sums before its one rounding, so the
 // adapters cost no extra pass over y.  Selecting rows, rather than multiplying by zero,
@@ -27,6 +28,7 @@ struct LoraArgs {
     const uint16_t* A; const uint16_t* B; int n_adapters; int rank;   // rank 0: no adapters
     const int32_t* ids; const float* scaling;
     float* v; int splits; int64_t share;   // v: splits x n x rank; share: columns per split
+    int slots;                             // workgroups among which a tile's adapters are dealt
     void* y; gptq_dtype yt;
 };
 
@@ -46,14 +48,16 @@ __global__ __launch_bounds__(64 * SW) void lora_shrink_kernel(LoraArgs a) {
     const uint8_t* xrow = reinterpret_cast<const uint8_t*>(a.x + t * a.ldx);
     const int64_t col_a = (int64_t)blockIdx.y * a.share;
     const int64_t col_b = col_a + a.share < a.L.d_col ? col_a + a.share : a.L.d_col;
-    const int rt = blockIdx.z;                                   // 16 ranks
+    const int rt = blockIdx.z / a.slots, slot = blockIdx.z % a.slots;   // 16 ranks; a share of the tile's adapters
     const int k = 16 * rt + n16 < a.rank ? 16 * rt + n16 : a.rank - 1;
     f32x4_t out = {0.f, 0.f, 0.f, 0.f};
-    uint32_t todo = (uint32_t)__ballot(id >= 0) & 0xFFFFu;
-    while (todo) {                                               // wave-uniform
+    uint32_t todo = (uint32_t)__ballot(id >= 0) & 0xFFFFu, done = 0;
+    for (int j = 0; todo; ++j) {                                 // wave-uniform
         const int ad = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
         const uint32_t mine = (uint32_t)__ballot(id == ad) & 0xFFFFu;
         todo &= ~mine;
+        if (j % a.slots != slot) continue;
+        done |= mine;
         const uint8_t* arow = reinterpret_cast<const uint8_t*>(a.A + ((int64_t)ad * a.rank + k) * a.L.d_col);
         f32x4_t cs = {0.f, 0.f, 0.f, 0.f};
         for (int64_t c0 = col_a + 128 * wave; c0 < col_b; c0 += SHARE) {
@@ -75,6 +79,7 @@ __global__ __launch_bounds__(64 * SW) void lora_shrink_kernel(LoraArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) out[i] = (mine >> (4 * q + i)) & 1 ? cs[i] : out[i];
     }
+    if (done == 0) return;                                       // the whole workgroup: every wave sees the same ids
 #pragma unroll
     for (int i = 0; i < 4; ++i) red[wave][i][lane] = out[i];
     __syncthreads();
@@ -82,7 +87,7 @@ __global__ __launch_bounds__(64 * SW) void lora_shrink_kernel(LoraArgs a) {
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < SW; ++w) v += red[w][m & 3][n + 16 * (m >> 2)];
-    if (tok0 + m < a.n && 16 * rt + n < a.rank)
+    if (((done >> m) & 1) && 16 * rt + n < a.rank)
         a.v[((int64_t)blockIdx.y * a.n + tok0 + m) * a.rank + 16 * rt + n] = v;
 }
 
@@ -308,7 +313,7 @@ static gptq_status launch_runs(const LoraArgs& a, int group, hipStream_t s) {
 template <int X>
 static gptq_status launch_bits(const LoraArgs& a, int bits, int group, hipStream_t s) {
     if (a.rank) {
-        const dim3 grid((unsigned)((a.n + 15) / 16), (unsigned)a.splits, (unsigned)((a.rank + 15) / 16));
+        const dim3 grid((unsigned)((a.n + 15) / 16), (unsigned)a.splits, (unsigned)((a.rank + 15) / 16 * a.slots));
         lora_shrink_kernel<X><<<grid, 64 * SW, 0, s>>>(a);
         GPTQ_LAUNCH_CHECK();
     }
@@ -339,6 +344,8 @@ gptq_status linear_lora_launch(const uint8_t* codes, const uint16_t* scales, con
     a.ids = ids; a.scaling = scaling; a.v = (float*)ws;
     a.splits = a.rank ? lora_splits(n, d_col, rank) : 0;
     a.share = a.rank ? ((d_col + SHARE - 1) / SHARE + a.splits - 1) / a.splits * SHARE : 0;
+    // few tokens: each adapter of a tile in a workgroup of its own; many: one after another
+    a.slots = n <= 64 ? (n < 16 ? (int)n : 16) : 1;
     a.y = y; a.yt = yt;
     return xt == GPTQ_BF16 ? launch_bits<X_BF16>(a, bits, group, s) : launch_bits<X_F16>(a, bits, group, s);
 }

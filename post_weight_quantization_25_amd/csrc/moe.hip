@@ -283,7 +283,7 @@ __global__ __launch_bounds__(256) void moe_sum_kernel(MoeArgs a) {
 
 template <int X, int CB, int RUN>
 static gptq_status launch(const MoeArgs& a, hipStream_t s) {
-    const unsigned ef = (unsigned)((a.f + 15) / 16), dd = (unsigned)((a.d + 15) / 16);
+    const unsigned ef = (unsigned)((a.f + 15) / 16);
     const int slots = a.E < a.n * a.k ? a.E : a.n * a.k;
     moe_logits_kernel<X><<<dim3((unsigned)((a.E + 15) / 16), (unsigned)((a.n + 15) / 16)), 64 * LOGW, 0, s>>>(a);
     GPTQ_LAUNCH_CHECK();
@@ -298,7 +298,7 @@ static gptq_status launch(const MoeArgs& a, hipStream_t s) {
     GPTQ_LAUNCH_CHECK();
     moe_up_kernel<X, CB, RUN><<<dim3(ef, (unsigned)slots), 64 * MW, 0, s>>>(a);
     GPTQ_LAUNCH_CHECK();
-    moe_down_kernel<CB, RUN><<<dim3(dd, (unsigned)slots), 64 * MW, 0, s>>>(a);
+    moe_down_kernel<CB, RUN><<<dim3((unsigned)((a.d + 15) / 16), (unsigned)slots), 64 * MW, 0, s>>>(a);
     GPTQ_LAUNCH_CHECK();
     moe_sum_kernel<<<dim3((unsigned)((a.d + 255) / 256), (unsigned)a.n), 256, 0, s>>>(a);
     GPTQ_LAUNCH_CHECK();

@@ -12,30 +12,34 @@ from dataclasses import dataclass
 
 import torch
 
-from . import _DT, Quantized, _check, _check_quantized, _dev, _tensor, _workspace, lib
+from . import _DT, Quantized, _check, _check_quantized, _dev, _n_groups, _tensor, _workspace, code_bytes, lib
+
+
+_current_device = torch.cuda.current_device
+_raw_stream = torch._C._cuda_getCurrentRawStream   # current_stream(i).cuda_stream without the object
 
 
 class _On:
     """The operands' device made current and ``stream`` made the current stream, where they
     are not already; gives the stream's handle."""
+    __slots__ = ("index", "inner")
 
     def __init__(self, device, stream):
-        self._inner = []
-        if device.index != torch.cuda.current_device():
-            self._inner.append(torch.cuda.device(device))
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, the operands on {device}")
-            self._inner.append(torch.cuda.stream(stream))
-        self._device = device
+        self.index, self.inner = device.index, ()
+        if stream is not None or self.index != _current_device():
+            self.inner = (torch.cuda.device(device),)
+            if stream is not None:
+                if stream.device != device:
+                    raise ValueError(f"stream is on {stream.device}, the operands on {device}")
+                self.inner += (torch.cuda.stream(stream),)
 
     def __enter__(self):
-        for c in self._inner:
+        for c in self.inner:
             c.__enter__()
-        return torch.cuda.current_stream(self._device).cuda_stream
+        return _raw_stream(self.index)
 
     def __exit__(self, *exc):
-        for c in reversed(self._inner):
+        for c in reversed(self.inner):
             c.__exit__(*exc)
 
 
@@ -45,14 +49,14 @@ def _rows(t: torch.Tensor, name: str, dtype=None, shape=None, device=None) -> in
         raise ValueError(f"{name} must be a 2-D device tensor")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must have dtype {dtype}, not {t.dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, the other operands on {device}")
     n, d = t.shape
-    s0, s1 = t.stride()
     if n == 0 or d == 0:
         return d
+    s0, s1 = t.stride()
     if (s1 != 1 and d > 1) or (s0 < d and n > 1):
         raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
     return max(s0, d)
@@ -63,6 +67,15 @@ class Int8Rows:
     """Rows of 8-bit codes with one scale each: row t stands for q[t] * scale[t]."""
     q: torch.Tensor          # int8, n_tokens x d (rows may be strided)
     scale: torch.Tensor      # float32, n_tokens
+
+
+def _shared(o, ldo: int, name: str, x, ldx: int, r, ldr: int):
+    """An output that is an input's buffer must have its row pitch."""
+    if o.shape[0] < 2:
+        return
+    at = o.data_ptr()
+    if (at == x.data_ptr() and ldo != ldx) or (r is not None and at == r.data_ptr() and ldo != ldr):
+        raise ValueError(f"{name} shares a buffer with an input of another row pitch")
 
 
 def rmsnorm_int8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
@@ -77,32 +90,35 @@ def rmsnorm_int8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor |
         raise ValueError("x must be f32/bf16/f16")
     dev, dt = x.device, x.dtype
     ldx = _rows(x, "x")
-    shape = n, d = tuple(x.shape)
+    shape = n, d = x.shape
     _tensor(weight, "weight", (dt, torch.float32), (d,), dev)
     ldr = 0 if residual is None else _rows(residual, "residual", dt, shape, dev)
     if residual is None and residual_out is not None:
         raise ValueError("residual_out without a residual")
+    ldn = 0
     if normed is not None:
         ldn = _rows(normed, "normed", dt, shape, dev)
         if residual_out is not None and normed.data_ptr() == residual_out.data_ptr() and n and d:
             raise ValueError("normed and residual_out must be different buffers")
     with _On(dev, stream) as s:
-        if residual is not None and residual_out is None:
-            residual_out = torch.empty(shape, dtype=dt, device=dev)
-        ldo = 0 if residual_out is None else _rows(residual_out, "residual_out", dt, shape, dev)
-        for o, ldo_, name in ((residual_out, ldo, "residual_out"), (normed, 0 if normed is None else ldn, "normed")):
-            for i, ldi in ((x, ldx), (residual, ldr)):
-                if o is not None and i is not None and o.data_ptr() == i.data_ptr() and ldo_ != ldi and n > 1:
-                    raise ValueError(f"{name} shares a buffer with an input of another row pitch")
+        ldo = 0
+        if residual_out is not None:
+            ldo = _rows(residual_out, "residual_out", dt, shape, dev)
+            _shared(residual_out, ldo, "residual_out", x, ldx, residual, ldr)
+        elif residual is not None:
+            residual_out, ldo = torch.empty(shape, dtype=dt, device=dev), d
+        if normed is not None:
+            _shared(normed, ldn, "normed", x, ldx, residual, ldr)
         if out is None:
-            out = Int8Rows(torch.empty(shape, dtype=torch.int8, device=dev),
-                           torch.empty(n, dtype=torch.float32, device=dev))
-        ldq = _rows(out.q, "out.q", torch.int8, shape, dev)
-        _tensor(out.scale, "out.scale", torch.float32, (n,), dev)
+            out, ldq = Int8Rows(torch.empty(shape, dtype=torch.int8, device=dev),
+                                torch.empty(n, dtype=torch.float32, device=dev)), d
+        else:
+            ldq = _rows(out.q, "out.q", torch.int8, shape, dev)
+            _tensor(out.scale, "out.scale", torch.float32, (n,), dev)
         _check(lib.gptqs_rmsnorm_int8(
             x.data_ptr(), _DT[dt], ldx, None if residual is None else residual.data_ptr(), ldr, weight.data_ptr(),
             _DT[weight.dtype], eps, n, d, None if residual_out is None else residual_out.data_ptr(), ldo,
-            None if normed is None else normed.data_ptr(), 0 if normed is None else ldn, out.q.data_ptr(), ldq,
+            None if normed is None else normed.data_ptr(), ldn, out.q.data_ptr(), ldq,
             out.scale.data_ptr(), s), "gptqs_rmsnorm_int8")
     return out, (x if residual is None else residual_out)
 
@@ -111,9 +127,14 @@ def _stored(q: Quantized, name: str, device) -> int:
     """q is a layer on an integer grid with whole arrays on ``device``; its rows."""
     if q.fp4:
         raise ValueError(f"{name} is on the E2M1 grid; the products read integer-grid codes")
-    _dev(q.codes, f"{name}.codes")
-    d_row = q.codes.shape[0]
-    _check_quantized(q, name, d_row, device)
+    c, S, Z = q.codes, q.scales, q.zeros
+    d_row = c.shape[0]
+    groups = (d_row, _n_groups(q.group_size, q.d_col))
+    if not (c.dtype is torch.uint8 and S.dtype is Z.dtype is torch.float16 and c.device == S.device == Z.device == device
+            and c.shape == (d_row, code_bytes(q.bits, q.d_col)) and S.shape == Z.shape == groups
+            and c.is_contiguous() and S.is_contiguous() and Z.is_contiguous()):
+        _dev(c, f"{name}.codes")
+        _check_quantized(q, name, d_row, device)   # says which
     return d_row
 
 
