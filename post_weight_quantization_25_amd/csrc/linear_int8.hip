@@ -21,8 +21,8 @@ struct Int8Args {
 };
 
 template <int CB, int RUN, int NTT, int RB>
-__global__ __launch_bounds__(64 * TW) void int8_tile_kernel(Int8Args a) {
-    constexpr int DEEP = NTT == 4 ? 1 : 2;
+__global__ __launch_bounds__(64 * TW, 4) void int8_tile_kernel(Int8Args a) {
+    constexpr int DEEP = NTT >= 3 ? 1 : 2;
     __shared__ float red[TW][NTT * RB][4][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15;
     const int64_t row0 = (int64_t)blockIdx.x * 16 * RB, tok0 = (int64_t)blockIdx.y * 16 * NTT;
@@ -87,6 +87,13 @@ static void launch_gemm(const Int8Args& a, hipStream_t s) {
     int8_gemm_kernel<CB, PIECE, BM><<<(unsigned)(gm * gn), 256, 0, s>>>(a, gm, gn);
 }
 
+template <int CB, int RUN, int NTT>
+static void launch_tiles(const Int8Args& a, hipStream_t s) {
+    constexpr int RB = RUN == 8 ? 1 : 2;
+    const dim3 grid((unsigned)((a.d_row + 16 * RB - 1) / (16 * RB)), (unsigned)((a.n + 16 * NTT - 1) / (16 * NTT)));
+    int8_tile_kernel<CB, RUN, NTT, RB><<<grid, 64 * TW, 0, s>>>(a);
+}
+
 template <int CB, int RUN, int PIECE>
 static gptq_status launch(const Int8Args& a, hipStream_t s) {
     if (a.n > 64 && gemm_fits(a.L.d_col, a.ldx)) {
@@ -96,11 +103,11 @@ static gptq_status launch(const Int8Args& a, hipStream_t s) {
         GPTQ_LAUNCH_CHECK();
         return GPTQ_OK;
     }
-    const unsigned g16 = (unsigned)((a.d_row + 15) / 16), g32 = (unsigned)((a.d_row + 31) / 32);
-    auto tiles = [&](int per) { return (unsigned)((a.n + per - 1) / per); };
+    const unsigned g16 = (unsigned)((a.d_row + 15) / 16);
     if (a.n <= 16) int8_tile_kernel<CB, RUN, 1, 1><<<dim3(g16, 1), 64 * TW, 0, s>>>(a);
     else if (a.n <= 32) int8_tile_kernel<CB, RUN, 2, 1><<<dim3(g16, 1), 64 * TW, 0, s>>>(a);
-    else int8_tile_kernel<CB, RUN, 4, RUN == 8 ? 1 : 2><<<dim3(RUN == 8 ? g16 : g32, tiles(64)), 64 * TW, 0, s>>>(a);
+    else if (a.n <= 48) launch_tiles<CB, RUN, 3>(a, s);
+    else launch_tiles<CB, RUN, 4>(a, s);
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
 }

@@ -96,8 +96,8 @@ GPTQ_DEV float elem16(uint16_t b) { return X == X_BF16 ? bf16_bits_to_f32(b) : f
 
 template <int X, int CB, int RUN, int NTT, int RB>
 __global__ __launch_bounds__(64 * TW) void lora_tile_kernel(LoraArgs a) {
-    constexpr int DEEP = NTT == 4 ? 1 : 2;
-    constexpr int PER = NTT * RB * 256 / (64 * TW) > 0 ? NTT * RB * 256 / (64 * TW) : 1;   // outputs per thread
+    constexpr int DEEP = NTT >= 3 ? 1 : 2;
+    constexpr int PER = (NTT * RB * 256 + 64 * TW - 1) / (64 * TW);   // outputs per thread
     __shared__ float red[TW][NTT * RB][4][64];
     __shared__ float vs[16 * NTT][RCH + 1];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15;
@@ -295,11 +295,12 @@ static gptq_status launch(const LoraArgs& a, hipStream_t s) {
         GPTQ_LAUNCH_CHECK();
         return GPTQ_OK;
     }
-    const unsigned g16 = (unsigned)((a.d_row + 15) / 16), g32 = (unsigned)((a.d_row + 31) / 32);
+    const unsigned g16 = (unsigned)((a.d_row + 15) / 16);
     auto tiles = [&](int per) { return (unsigned)((a.n + per - 1) / per); };
     if (a.n <= 16) lora_tile_kernel<X, CB, RUN, 1, 1><<<dim3(g16, 1), 64 * TW, 0, s>>>(a);
     else if (a.n <= 32) lora_tile_kernel<X, CB, RUN, 2, 1><<<dim3(g16, 1), 64 * TW, 0, s>>>(a);
-    else lora_tile_kernel<X, CB, RUN, 4, RUN == 8 ? 1 : 2><<<dim3(RUN == 8 ? g16 : g32, tiles(64)), 64 * TW, 0, s>>>(a);
+    else if (a.n <= 48) lora_tile_kernel<X, CB, RUN, 3, 1><<<dim3(g16, tiles(48)), 64 * TW, 0, s>>>(a);
+    else lora_tile_kernel<X, CB, RUN, 4, 1><<<dim3(g16, tiles(64)), 64 * TW, 0, s>>>(a);
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
 }
