@@ -202,25 +202,30 @@ struct Chunk {
     // even) or the zero (odd) of block 2 k + q / 2
     uint16_t sz[SZ][P];
 
-    // row[rb]: the lane's weight row; xrow[tt]: its token's first element, or nullptr for a row
-    // of the tile without a token (zeros, and nothing is read).  TAIL: the chunk in which the
-    // rows end
+    // Codes are loaded by lane l for row l / 4 and lane group l % 4, so that four neighbouring
+    // lanes read one contiguous piece of a row (a cache access each 64 bytes instead of one
+    // per lane), and handed to the lane that multiplies them (arrange).
+    //
+    // row[rb]: the row that the lane multiplies; crow[rb]: the row whose codes it loads;
+    // xrow[tt]: its token's first element, or nullptr for a row of the tile without a token
+    // (zeros, and nothing is read).  TAIL: the chunk in which the rows end
     template <bool TAIL>
-    GPTQ_DEV void load(const Stored& L, const int64_t (&row)[RB], const uint8_t* const (&xrow)[NTT], int c0) {
-        const int q = (threadIdx.x & 63) >> 4;
+    GPTQ_DEV void load(const Stored& L, const int64_t (&row)[RB], const int64_t (&crow)[RB],
+                       const uint8_t* const (&xrow)[NTT], int c0) {
+        const int q = (threadIdx.x & 63) >> 4, cq = threadIdx.x & 3;
         const uint16_t* tab = (q & 1) ? L.zeros : L.scales;
         int64_t szrow[SZ];
 #pragma unroll
         for (int k = 0; k < SZ; ++k) szrow[k] = row[2 * k + 1 < RB && q >= 2 ? 2 * k + 1 : 2 * k] * L.n_groups;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            const int64_t col = (int64_t)c0 * SCK + p * 4 * RUN + q * RUN;
+            const int64_t col = (int64_t)c0 * SCK + p * 4 * RUN + cq * RUN;
             const int left = (int)(L.d_col - col < RUN ? L.d_col - col : RUN);
             int g = RUN == 32 && L.n_groups == 1 ? 0 : c0 * P + p;
             if (TAIL) g = g < L.n_groups ? g : L.n_groups - 1;
 #pragma unroll
             for (int rb = 0; rb < RB; ++rb) {
-                const uint8_t* src = L.codes + row[rb] * L.code_ld + col / 8 * CB;
+                const uint8_t* src = L.codes + crow[rb] * L.code_ld + col / 8 * CB;
                 c[rb][p] = !TAIL ? load_raw<CB, RUN>(src) : load_raw_tail<CB, RUN>(src, left);
             }
 #pragma unroll
@@ -242,6 +247,18 @@ struct Chunk {
                 }
             }
         }
+    }
+
+    // lane (row n, group q) takes the codes that lane 4 n + q loaded
+    GPTQ_DEV void arrange() {
+        const int from = 4 * (4 * (int)(threadIdx.x & 15) + (int)((threadIdx.x & 63) >> 4));
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+#pragma unroll
+                for (int e = 0; e < (CB * RUN + 31) / 32; ++e)
+                    c[rb][p].w[e] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)c[rb][p].w[e]);
     }
 
     // scale (which 0) or zero (1) of the lane's row in block rb
@@ -350,24 +367,30 @@ template <int X, int CB, int RUN, int NTT, int RB, int DEEP>
 GPTQ_DEV void stored_accumulate(f32x4_t (&acc)[NTT][RB], const Stored& L, const int64_t (&row)[RB],
                                 const uint8_t* const (&xrow)[NTT], int c0, int step) {
     const int nfull = (int)(L.d_col / SCK);
+    // the rows whose codes the lane loads: those that lane l / 4 of the wave multiplies
+    int64_t crow[RB];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) crow[rb] = __shfl(row[rb], (int)(threadIdx.x & 63) >> 2);
     Chunk<X, CB, RUN, NTT, RB> ch[DEEP];
 #pragma unroll
     for (int j = 0; j < DEEP; ++j)
-        if (c0 + j * step < nfull) ch[j].template load<false>(L, row, xrow, c0 + j * step);
+        if (c0 + j * step < nfull) ch[j].template load<false>(L, row, crow, xrow, c0 + j * step);
     __builtin_amdgcn_sched_barrier(0);         // every load above the arithmetic
     for (int c = c0; c < nfull; c += DEEP * step) {
 #pragma unroll
         for (int j = 0; j < DEEP; ++j) {
             const int at = c + j * step, next = at + DEEP * step;
             if (at < nfull) {                  // wave-uniform
+                ch[j].arrange();
                 ch[j].multiply(acc);
-                if (next < nfull) ch[j].template load<false>(L, row, xrow, next);
+                if (next < nfull) ch[j].template load<false>(L, row, crow, xrow, next);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
     }
     if (L.d_col % SCK && nfull >= c0 && (nfull - c0) % step == 0) {
-        ch[0].template load<true>(L, row, xrow, nfull);
+        ch[0].template load<true>(L, row, crow, xrow, nfull);
+        ch[0].arrange();
         ch[0].multiply(acc);
     }
 }
