@@ -98,28 +98,35 @@ template <int X, int CB, int RUN, int NTT, int RB>
 __global__ __launch_bounds__(64 * TW) void lora_tile_kernel(LoraArgs a) {
     constexpr int DEEP = NTT >= 3 ? 1 : 2;
     constexpr int PER = (NTT * RB * 256 + 64 * TW - 1) / (64 * TW);   // outputs per thread
-    __shared__ float red[TW][NTT * RB][4][64];
+    constexpr int STAGE = 16 * SCK * xbytes<X>();                   // one tile's chunk
+    constexpr int RED = TW * NTT * RB * 1024, LDS = NTT > 1 && TW * STAGE > RED ? TW * STAGE : RED;
+    __shared__ __align__(16) uint8_t stage[LDS];
+    float (*red)[NTT * RB][4][64] = reinterpret_cast<float (*)[NTT * RB][4][64]>(stage);
     __shared__ float vs[16 * NTT][RCH + 1];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15;
     const int64_t row0 = (int64_t)blockIdx.x * 16 * RB, tok0 = (int64_t)blockIdx.y * 16 * NTT;
     int64_t row[RB];
-    const uint8_t* xrow[NTT];
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
         const int64_t r = row0 + 16 * rb + n16;
         row[rb] = r < a.d_row ? r : a.d_row - 1;
-    }
-#pragma unroll
-    for (int tt = 0; tt < NTT; ++tt) {
-        const int64_t t = tok0 + 16 * tt + n16;
-        xrow[tt] = t < a.n ? reinterpret_cast<const uint8_t*>(a.x + t * a.ldx) : nullptr;
     }
     f32x4_t acc[NTT][RB];
 #pragma unroll
     for (int tt = 0; tt < NTT; ++tt)
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) acc[tt][rb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    stored_accumulate<X, CB, RUN, NTT, RB, DEEP>(acc, a.L, row, xrow, wave, TW);
+    // one tile of few tokens is read in place, its empty rows costing nothing; more tiles in
+    // contiguous pieces
+    if constexpr (NTT == 1) {
+        const int64_t t = tok0 + n16;
+        const XScattered<1> xr = {{t < a.n ? reinterpret_cast<const uint8_t*>(a.x + tok0 * a.ldx) + n16 * 2 * a.ldx : nullptr}};
+        stored_accumulate<X, CB, RUN, NTT, RB, DEEP>(acc, a.L, row, xr, wave, TW);
+    } else {
+        const XConsecutive xr = {reinterpret_cast<const uint8_t*>(a.x + tok0 * a.ldx), 2 * a.ldx, (int)(a.n - tok0 < 16 * NTT ? a.n - tok0 : 16 * NTT), stage + STAGE * wave};
+        stored_accumulate<X, CB, RUN, NTT, RB, DEEP>(acc, a.L, row, xr, wave, TW);
+        __syncthreads();                       // the stages give way to the sums
+    }
 #pragma unroll
     for (int tt = 0; tt < NTT; ++tt)
 #pragma unroll

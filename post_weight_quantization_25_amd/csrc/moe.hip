@@ -209,9 +209,9 @@ __global__ __launch_bounds__(64 * MW, 4) void moe_up_kernel(MoeArgs a) {
     for (int m0 = 0; m0 < cnt; m0 += MOE_T) {
         const bool live = m0 + n16 < cnt;
         const int p = live ? a.plan[PAIRS + p0 + m0 + n16] : 0;
-        const uint8_t* const xrow[1] = {live ? reinterpret_cast<const uint8_t*>(a.x + (int64_t)(p / a.k) * a.ldx) : nullptr};
+        const XScattered<1> xr = {{live ? reinterpret_cast<const uint8_t*>(a.x + (int64_t)(p / a.k) * a.ldx) : nullptr}};
         f32x4_t acc[1][2] = {{f32x4_t{0.f, 0.f, 0.f, 0.f}, f32x4_t{0.f, 0.f, 0.f, 0.f}}};
-        stored_accumulate<X, CB, RUN, 1, 2, 1>(acc, a.up, row, xrow, wave, MW);
+        stored_accumulate<X, CB, RUN, 1, 2, 1>(acc, a.up, row, xr, wave, MW);
         __syncthreads();                                    // the last tile's sums are read
 #pragma unroll
         for (int rb = 0; rb < 2; ++rb)
@@ -252,10 +252,10 @@ __global__ __launch_bounds__(64 * MW, 4) void moe_down_kernel(MoeArgs a) {
     for (int m0 = 0; m0 < cnt; m0 += MOE_T) {
         const bool live = m0 + n16 < cnt;
         const int64_t at = live ? (int64_t)a.plan[PAIRS + p0 + m0 + n16] * a.f : 0;
-        const uint8_t* const xrow[2] = {live ? reinterpret_cast<const uint8_t*>(a.hi + at) : nullptr,
-                                        live ? reinterpret_cast<const uint8_t*>(a.lo + at) : nullptr};
+        const XScattered<2> xr = {{live ? reinterpret_cast<const uint8_t*>(a.hi + at) : nullptr,
+                                   live ? reinterpret_cast<const uint8_t*>(a.lo + at) : nullptr}};
         f32x4_t acc[2][1] = {{f32x4_t{0.f, 0.f, 0.f, 0.f}}, {f32x4_t{0.f, 0.f, 0.f, 0.f}}};
-        stored_accumulate<X_BF16, CB, RUN, 2, 1, 1>(acc, a.down, row, xrow, wave, MW);
+        stored_accumulate<X_BF16, CB, RUN, 2, 1, 1>(acc, a.down, row, xr, wave, MW);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 4; ++i) red[wave][i][lane] = acc[0][0][i] + acc[1][0][i];

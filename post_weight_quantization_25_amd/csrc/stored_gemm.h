@@ -65,6 +65,12 @@ struct StoredGemm {
         return row * SLAB + 16 * (piece16 ^ f);
     }
 
+    // With 64 tokens per workgroup codes are half the cache accesses: lane l then loads row l /
+    // 4's piece l % 4 (contiguous over four lanes, an access per 64 bytes instead of one per
+    // lane) and decode hands it to the lane that multiplies it (777 tokens x 4001 x 11008 int3:
+    // 61.8 us against 65.9).  With 128 the lanes' own loads are as good (4096 tokens x 4096 x
+    // 4096 int4: 114 us against 116).
+    static constexpr bool SPREAD = BM == 64;
     struct Codes { Raw<CB, RUN> c[NT][PP]; };                  // a slab's codes of the lane's rows
     struct Frag { uint32_t w[KB / 4]; };
     struct Operand {                                           // the same, decoded
@@ -109,12 +115,13 @@ struct StoredGemm {
             const int u = tid + 256 * j, r = u / (SLAB / 16);
             aoff[j] = (uint32_t)(r < toks ? r : toks - 1) * (uint32_t)ldx_bytes + 16 * (u % (SLAB / 16));
         }
+        const int crow = SPREAD ? lane >> 2 : n16, cpart = SPREAD ? lane & 3 : q;
         uint32_t boff[NT], soff[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int r = 32 * wave + 16 * nt + n16, rr = r < rows ? r : rows - 1;
-            boff[nt] = (uint32_t)rr * (uint32_t)L.code_ld + q * (RUN * CB / 8);
-            soff[nt] = (uint32_t)rr * (uint32_t)L.n_groups;
+            const int r = 32 * wave + 16 * nt + n16, c = 32 * wave + 16 * nt + crow;
+            boff[nt] = (uint32_t)(c < rows ? c : rows - 1) * (uint32_t)L.code_ld + cpart * (RUN * CB / 8);
+            soff[nt] = (uint32_t)(r < rows ? r : rows - 1) * (uint32_t)L.n_groups;
         }
 
         auto load_a = [&](u32x4_t (&a)[AU], int s) {
@@ -171,7 +178,7 @@ struct StoredGemm {
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int p = 0; p < PP; ++p) {
-                    const int left = last - p * PC - q * RUN;
+                    const int left = last - p * PC - cpart * RUN;
                     b.c[nt][p] = load_raw_tail<CB, RUN>(cs + boff[nt] + p * (PC / 8 * CB), left < RUN ? left : RUN);
                 }
         };
@@ -213,9 +220,13 @@ struct StoredGemm {
                     if constexpr (PIECE != 0) e = tab[(g % TG) * GEMM_ROWS + 32 * wave + 16 * nt + n16];
                     else e = rowE[nt];
                     o.S[p][nt] = e.S;
+                    Raw<CB, RUN> codes = b.c[nt][p];
+#pragma unroll
+                    for (int w = 0; w < (SPREAD ? (CB * RUN + 31) / 32 : 0); ++w)
+                        codes.w[w] = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (4 * n16 + q), (int)codes.w[w]);
                     o.rz[p][nt] = f16_bits_to_f32((uint16_t)(e.z & 0xFFFFu)) - part_of(e.z >> 16);
 #pragma unroll
-                    for (int t = 0; t < STEPS; ++t) o.f[p][nt][t] = frag_b(b.c[nt][p], t, e.z);
+                    for (int t = 0; t < STEPS; ++t) o.f[p][nt][t] = frag_b(codes, t, e.z);
                 }
             }
         };

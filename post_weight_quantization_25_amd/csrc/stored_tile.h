@@ -191,6 +191,20 @@ struct Stored {
     int gshift;                                        // log2 of the group's columns (groups)
 };
 
+// The activation rows of NTT tiles of 16 tokens.  Scattered: a pointer per lane to the token
+// of row l % 16 of each tile, nullptr for a row without one.
+template <int NTT>
+struct XScattered {
+    const uint8_t* row[NTT];
+};
+// Consecutive: `live` rows from base on, pitch bytes apart, loaded in contiguous pieces (64
+// lanes read 4 or 8 whole rows of a chunk) and put in order through the wave's own `stage`
+// in LDS (a tile's chunk: 16 rows x 128 columns).
+struct XConsecutive {
+    const uint8_t* base; int64_t pitch; int live;
+    uint8_t* stage;
+};
+
 // What one chunk of RB row blocks and NTT token tiles needs, in registers.
 template <int X, int CB, int RUN, int NTT, int RB>
 struct Chunk {
@@ -206,12 +220,11 @@ struct Chunk {
     // lanes read one contiguous piece of a row (a cache access each 64 bytes instead of one
     // per lane), and handed to the lane that multiplies them (arrange).
     //
-    // row[rb]: the row that the lane multiplies; crow[rb]: the row whose codes it loads;
-    // xrow[tt]: its token's first element, or nullptr for a row of the tile without a token
-    // (zeros, and nothing is read).  TAIL: the chunk in which the rows end
-    template <bool TAIL>
-    GPTQ_DEV void load(const Stored& L, const int64_t (&row)[RB], const int64_t (&crow)[RB],
-                       const uint8_t* const (&xrow)[NTT], int c0) {
+    // row[rb]: the row that the lane multiplies; crow[rb]: the row whose codes it loads.  A
+    // row of a tile without a token is zeros, and nothing is read for it.  TAIL: the chunk in
+    // which the rows end
+    template <bool TAIL, typename XR>
+    GPTQ_DEV void load(const Stored& L, const int64_t (&row)[RB], const int64_t (&crow)[RB], const XR& xr, int c0) {
         const int q = (threadIdx.x & 63) >> 4, cq = threadIdx.x & 3;
         const uint16_t* tab = (q & 1) ? L.zeros : L.scales;
         int64_t szrow[SZ];
@@ -231,22 +244,91 @@ struct Chunk {
 #pragma unroll
             for (int k = 0; k < SZ; ++k) sz[k][p] = tab[szrow[k] + g];
         }
+        load_x_rows<TAIL>(L, xr, c0);
+    }
+
+    template <bool TAIL>
+    GPTQ_DEV void load_x_rows(const Stored& L, const XScattered<NTT>& xr, int c0) {
+        const int q = (threadIdx.x & 63) >> 4;
 #pragma unroll
         for (int tt = 0; tt < NTT; ++tt) {
 #pragma unroll
             for (int p = 0; p < P; ++p)
 #pragma unroll
                 for (int e = 0; e < RUN * xbytes<X>() / 4; ++e) x[tt][p].w[e] = 0;
-            if (xrow[tt] != nullptr) {
+            if (xr.row[tt] != nullptr) {
 #pragma unroll
                 for (int p = 0; p < P; ++p) {
                     const int64_t col = (int64_t)c0 * SCK + p * 4 * RUN + q * RUN;
                     const int left = (int)(L.d_col - col < RUN ? L.d_col - col : RUN);
-                    const uint8_t* src = xrow[tt] + col * xbytes<X>();
+                    const uint8_t* src = xr.row[tt] + col * xbytes<X>();
                     x[tt][p] = !TAIL ? load_x<X, RUN>(src) : load_x_tail<X, RUN>(src, left);
                 }
             }
         }
+    }
+
+    static constexpr int PPR = SCK * xbytes<X>() / 16;      // 16-byte pieces of a row's chunk
+    static constexpr int XL = 16 * PPR / 64;                // loads per tile
+
+    // piece k of the wave's XL loads of a tile, kept where x is until it is put in order
+    GPTQ_DEV uint32_t& x_word(int tt, int w) { return x[tt][w / (RUN * xbytes<X>() / 4)].w[w % (RUN * xbytes<X>() / 4)]; }
+
+    template <bool TAIL>
+    GPTQ_DEV void load_x_rows(const Stored& L, const XConsecutive& xr, int c0) {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int tt = 0; tt < NTT; ++tt)
+#pragma unroll
+            for (int k = 0; k < XL; ++k) {
+                const int r = 16 * tt + (64 * k + lane) / PPR, piece = (64 * k + lane) % PPR;
+                uint32_t v[4] = {0u, 0u, 0u, 0u};
+                if (r < xr.live) {
+                    const uint8_t* src = xr.base + r * xr.pitch + (int64_t)c0 * SCK * xbytes<X>() + 16 * piece;
+                    if constexpr (!TAIL) {
+                        __builtin_memcpy(v, src, 16);
+                    } else {
+                        const int64_t left = L.d_col - (int64_t)c0 * SCK - piece * (16 / xbytes<X>());
+                        const XRun<X, 16 / xbytes<X>()> t = load_x_tail<X, 16 / xbytes<X>()>(src, (int)(left < 16 ? left : 16));
+                        __builtin_memcpy(v, t.w, 16);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x_word(tt, 4 * k + e) = v[e];
+            }
+    }
+
+    GPTQ_DEV void arrange_x(const XScattered<NTT>&) {}
+    GPTQ_DEV void arrange_x(const XConsecutive& xr) {
+        const int lane = threadIdx.x & 63, n16 = lane & 15, q = lane >> 4;
+        constexpr int B = RUN * xbytes<X>();                // bytes of a lane's run
+        auto at = [&](int r, int piece) { return xr.stage + (r * PPR + (piece ^ (r & (PPR - 1)))) * 16; };
+#pragma unroll
+        for (int tt = 0; tt < NTT; ++tt) {
+            // the wave's own memory, and its LDS operations keep their order: only the compiler
+            // is held back
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int k = 0; k < XL; ++k)
+                *reinterpret_cast<u32x4_t*>(at((64 * k + lane) / PPR, (64 * k + lane) % PPR)) =
+                    u32x4_t{x_word(tt, 4 * k), x_word(tt, 4 * k + 1), x_word(tt, 4 * k + 2), x_word(tt, 4 * k + 3)};
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const int byte = p * 4 * B + q * B;
+                if constexpr (B >= 16) {
+#pragma unroll
+                    for (int e = 0; e < B / 16; ++e) {
+                        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(at(n16, byte / 16 + e));
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) x[tt][p].w[4 * e + w] = v[w];
+                    }
+                } else {
+                    __builtin_memcpy(x[tt][p].w, __builtin_assume_aligned(at(n16, byte / 16) + byte % 16, 8), 8);
+                }
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
     }
 
     // lane (row n, group q) takes the codes that lane 4 n + q loaded
@@ -363,9 +445,9 @@ struct Chunk {
 // Sums of RB blocks of 16 weight rows with NTT tiles of 16 tokens over the chunks c0, c0 +
 // step, .. of a row.  DEEP chunks are in registers at a time: one is multiplied while the
 // others are on their way.
-template <int X, int CB, int RUN, int NTT, int RB, int DEEP>
-GPTQ_DEV void stored_accumulate(f32x4_t (&acc)[NTT][RB], const Stored& L, const int64_t (&row)[RB],
-                                const uint8_t* const (&xrow)[NTT], int c0, int step) {
+template <int X, int CB, int RUN, int NTT, int RB, int DEEP, typename XR>
+GPTQ_DEV void stored_accumulate(f32x4_t (&acc)[NTT][RB], const Stored& L, const int64_t (&row)[RB], const XR& xr, int c0,
+                                int step) {
     const int nfull = (int)(L.d_col / SCK);
     // the rows whose codes the lane loads: those that lane l / 4 of the wave multiplies
     int64_t crow[RB];
@@ -374,7 +456,7 @@ GPTQ_DEV void stored_accumulate(f32x4_t (&acc)[NTT][RB], const Stored& L, const 
     Chunk<X, CB, RUN, NTT, RB> ch[DEEP];
 #pragma unroll
     for (int j = 0; j < DEEP; ++j)
-        if (c0 + j * step < nfull) ch[j].template load<false>(L, row, crow, xrow, c0 + j * step);
+        if (c0 + j * step < nfull) ch[j].template load<false>(L, row, crow, xr, c0 + j * step);
     __builtin_amdgcn_sched_barrier(0);         // every load above the arithmetic
     for (int c = c0; c < nfull; c += DEEP * step) {
 #pragma unroll
@@ -382,15 +464,17 @@ GPTQ_DEV void stored_accumulate(f32x4_t (&acc)[NTT][RB], const Stored& L, const 
             const int at = c + j * step, next = at + DEEP * step;
             if (at < nfull) {                  // wave-uniform
                 ch[j].arrange();
+                ch[j].arrange_x(xr);
                 ch[j].multiply(acc);
-                if (next < nfull) ch[j].template load<false>(L, row, crow, xrow, next);
+                if (next < nfull) ch[j].template load<false>(L, row, crow, xr, next);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
     }
     if (L.d_col % SCK && nfull >= c0 && (nfull - c0) % step == 0) {
-        ch[0].template load<true>(L, row, crow, xrow, nfull);
+        ch[0].template load<true>(L, row, crow, xr, nfull);
         ch[0].arrange();
+        ch[0].arrange_x(xr);
         ch[0].multiply(acc);
     }
 }
