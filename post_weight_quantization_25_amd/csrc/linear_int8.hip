@@ -2,9 +2,15 @@
 //   y[t][r] = xs[t] sum_g S[r][g] sum_{c in g} xq[t][c] (u[r][c] - z[r][g]),
 // integer products on v_mfma_i32_16x16x64_i8 (exact), groups added in fp32.
 //
-// Small batches (tile_kernel): bound by the codes' bytes and, at one token, by the latency
-// of one round trip.  A workgroup of 8 waves owns 16 RB rows and 16 NTT tokens; its waves
-// take the rows' 128-column chunks in turn and meet in LDS at the end.
+// Small batches (int8_tile_kernel): bound by the codes' bytes and, at one token, by the
+// latency of one round trip.  A workgroup of 8 waves owns 16 RB rows and 16 NTT tokens; its
+// waves take the rows' 128-column chunks in turn and meet in LDS at the end.  One token,
+// 4096 x 4096 int4 g128: 5.0 us; 48 tokens x 11008 x 4096 g64: 17 us (see stored_tile.h).
+//
+// Large ones (int8_gemm_kernel, stored_gemm.h): bound by the vector unit's issue, two
+// instructions per four sums and 128 columns to scale them beside two products of the
+// matrix unit, plus the decoding.  4096 tokens x 4096 x 4096 int4 g128: 114 us, 1.2 Pop/s,
+// where the library's plain int8 product reaches 2.05.
 
 #include "serving.h"
 #include "stored_gemm.h"
@@ -103,9 +109,16 @@ static void launch_tiles(const Int8Args& a, hipStream_t s) {
 
 template <int CB, int RUN, int PIECE>
 static gptq_status launch(const Int8Args& a, hipStream_t s) {
-    if (a.n > 64 && gemm_fits(a.L.d_col, a.ldx)) {
-        // 128 tokens per workgroup once that leaves two workgroups per CU, else 64
-        if ((a.n + 127) / 128 * ((a.d_row + 127) / 128) >= 512) launch_gemm<CB, PIECE, 128>(a, s);
+    // Rules by size, both sides measured (int4 g128, us, replayed):
+    //  - the two kernels meet at about 2^21 outputs.  Rows x columns, tokens: tiles / LDS kernel:
+    //    4096 x 4096, 384: 26.3 / 29.4, 512: 33.9 / 30.1; 11008 x 4096, 128: 27.0 / 29.7, 192:
+    //    42.4 / 40.2; 4096 x 11008, 384: 60.7 / 72.2, 512: 78.7 / 73.9; 2048 x 1408, 768: 15.5 /
+    //    17.5, 1024: 19.5 / 17.6.
+    //  - 128 tokens per workgroup once that leaves more than 320 of them; 4096 columns, rows and
+    //    tokens (workgroups): 64 / 128: 4096, 1024 (256): 42.1 / 43.1, 1536 (384): 63.8 / 60.5,
+    //    2048 (512): 80.5 / 62.9; 11008, 320 (258): 41.7 / 57.5, 512 (344): 63.1 / 60.2.
+    if (a.n * a.d_row >= ((int64_t)1 << 21) && gemm_fits(a.L.d_col, a.ldx)) {
+        if ((a.n + 127) / 128 * ((a.d_row + 127) / 128) > 320) launch_gemm<CB, PIECE, 128>(a, s);
         else launch_gemm<CB, PIECE, 64>(a, s);
         GPTQ_LAUNCH_CHECK();
         return GPTQ_OK;

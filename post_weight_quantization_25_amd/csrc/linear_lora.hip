@@ -11,6 +11,13 @@
 // projection's kernel adds s_a B_a v to its own sums before its one rounding, so the
 // adapters cost no extra pass over y.  Selecting rows, rather than multiplying by zero,
 // keeps an infinity or a NaN of one adapter away from the tokens of the others.
+//
+// One token, 4096 x 4096 int4 g128, rank 16: 3.3 + 6.8 us; 40 tokens with up to 32 adapters
+// of rank 32: 6.2 + 19 us; 2048 tokens x 11008 x 4096, rank 16, runs of 450 tokens: 300 us
+// together (10 the first), 620 Tflop/s of the 1286 that the library's bf16 product on plain
+// weights reaches:
+// there the decoding to bfloat16 (a conversion, a subtraction and half a packing per code)
+// shares the vector unit with the scaling.
 
 #include "serving.h"
 #include "stored_gemm.h"
@@ -296,8 +303,17 @@ static void launch_gemm(const LoraArgs& a, hipStream_t s) {
 
 template <int X, int CB, int RUN, int PIECE>
 static gptq_status launch(const LoraArgs& a, hipStream_t s) {
-    if (a.n > 64 && gemm_fits(a.L.d_col, 2 * a.ldx)) {
-        if ((a.n + 127) / 128 * ((a.d_row + 127) / 128) >= 512) launch_gemm<X, CB, PIECE, 128>(a, s);
+    // Rules by size, both sides measured (int4 g128, bf16, rank 16, us, replayed):
+    //  - the two kernels meet at about 2^20 outputs.  Rows x columns, tokens: tiles / LDS kernel:
+    //    4096 x 4096, 256: 61.5 / 67.2, 320: 78.0 / 63.4; 11008 x 4096, 64: 44.5 / 63, 96: 77.3 /
+    //    62.9; 4096 x 11008, 256: 137 / 165, 320: 170 / 157; 2048 x 1408, 384: 27.6 / 31.0, 512:
+    //    35.0 / 32.2.
+    //  - 128 tokens per workgroup once that leaves more than 320 of them; 4096 columns, rows and
+    //    tokens (workgroups): 64 / 128: 4096, 1024 (256): 78 / 112, 1536 (384): 130 / 114, 2048
+    //    (512): 135 / 111; 11008, 512 (344): 136 / 117, 2048 (1376): 356 / 307.  Where the last
+    //    round of workgroups is nearly empty it can lose 5% (11008, 1024 (688): 213 / 222).
+    if (a.n * a.d_row > ((int64_t)1 << 20) && gemm_fits(a.L.d_col, 2 * a.ldx)) {
+        if ((a.n + 127) / 128 * ((a.d_row + 127) / 128) > 320) launch_gemm<X, CB, PIECE, 128>(a, s);
         else launch_gemm<X, CB, PIECE, 64>(a, s);
         GPTQ_LAUNCH_CHECK();
         return GPTQ_OK;

@@ -7,8 +7,14 @@
 //                      tokens that chose it, silu(gate) up w, written as two bfloat16 parts
 //   moe_down_kernel    per expert in use and 16 output columns: the pairs' outputs, fp32
 //   moe_sum_kernel     y = a token's pairs added in the order of its choices
-// Bound by the codes of the chosen experts, which up and down read once each.  Sums run in
-// fixed orders without atomics, and a token's do not depend on the other tokens' choices.
+// Bound by the codes of the chosen experts, which up and down read once each.  One token,
+// 8 of 64 experts of 2048 x 1408 int4: 4.2 + 5.8 + 13 + 9.4 + 3.8 us for 35 MB of codes,
+// latency of five dependent launches; 32 tokens, 2 of 16 experts of 4096 x 5504: 8.7 + 4.6
+// + 4.8 + 118 + 88 + 4.7 us (choice and plan in two launches), up at 3.1 TB/s and down at
+// 2.1 (its two-part inner values are most of its loads; 32 rows per workgroup, gathered
+// loads of them through LDS, and two chunks ahead all measured slower).  A first form in
+// which a workgroup of down walked all experts took 494 us.  Sums run in fixed orders
+// without atomics, and a token's do not depend on the other tokens' choices.
 
 #include "serving.h"
 #include "stored_tile.h"
@@ -66,8 +72,7 @@ __global__ __launch_bounds__(64 * LOGW) void moe_logits_kernel(MoeArgs a) {
     }
 }
 
-constexpr int MAXE = 512, MAXK = 32, EPL = MAXE / 64;   // experts per lane
-constexpr int MAXN = 256;                               // tokens of a call
+constexpr int MAXE = 512, EPL = MAXE / 64;   // experts per lane
 
 // Maximum over the wave, in every lane's copy of lane 63 (DPP, no LDS).
 GPTQ_DEV uint32_t wave_umax(uint32_t v) {
@@ -287,9 +292,11 @@ static gptq_status launch(const MoeArgs& a, hipStream_t s) {
     const int slots = a.E < a.n * a.k ? a.E : a.n * a.k;
     moe_logits_kernel<X><<<dim3((unsigned)((a.E + 15) / 16), (unsigned)((a.n + 15) / 16)), 64 * LOGW, 0, s>>>(a);
     GPTQ_LAUNCH_CHECK();
-    // up to 64 tokens one workgroup chooses and plans (a wave takes up to 4 tokens one after
-    // another); beyond, choosing is spread over the device first
-    if (a.n <= 64) moe_plan_kernel<true><<<1, 64 * PLAN_W, 0, s>>>(a);
+    // While each of its waves has one token at most, one workgroup chooses and plans; beyond,
+    // choosing is spread over the device first.  Whole calls, one workgroup / two launches, us:
+    // 1 token, 8, 64 and 256 experts: 28.4 / 29.5, 31.9 / 32.9, 34.2 / 35.1; 16 tokens: 30.5 /
+    // 31.3, 40.7 / 39.1, 58.5 / 57.3; 32 tokens: 32.9 / 31.8, 52.2 / 45.2, 91.6 / 84.5.
+    if (a.n <= PLAN_W) moe_plan_kernel<true><<<1, 64 * PLAN_W, 0, s>>>(a);
     else {
         moe_topk_kernel<<<(unsigned)((a.n + 3) / 4), 256, 0, s>>>(a);
         GPTQ_LAUNCH_CHECK();

@@ -12,7 +12,13 @@
 // One pass: a row's x and residual are read once into registers (16 bytes per load), h
 // and the codes are written from there.  Bound by HBM: 2 (x) + 2 (residual) + 2 (h) + 1
 // (q) bytes per element of a 16-bit row; the squares' sum is kept in 64 bits (one
-// conversion and one fp64 multiply-add per element, hidden behind the loads).
+// conversion and one fp64 multiply-add per element, hidden behind the loads).  8192 x 4096
+// bf16 with a residual: 52 us, 4.5 TB/s of 5.4 a copy reaches; one row of 4096: 3.8 us, a
+// launch and one round trip.  With the 64-bit path's operands kept in registers beside the
+// others (138 registers against 68) the same rows took 89 us.
+//
+// Threads per row by width: a wave to 512, then 256 threads with one or two vectors of 8,
+// 512 and 1024 with two, so that a row is read in one or two loads per thread.
 
 #include "common.h"
 #include "serving.h"

@@ -10,6 +10,12 @@
 // 16-byte pieces of a slab's row are XOR-swizzled by the row, which spreads a fragment's
 // 16 rows over all banks.
 //
+// Measured on the way (8-bit, 4096 tokens x 4096 x 4096 int4 g128, under the profiler): both
+// operands through LDS 200 us, codes straight to registers 145, scales through LDS too (a
+// cache line per row for 4 bytes otherwise) 137; 114 replayed without the profiler.  256
+// registers and 80 KB of LDS leave two waves per SIMD, whose issue slots and waits are what
+// is left; the matrix unit is busy a fifth of the time.
+//
 // As in stored_tile.h, a piece is the columns of one scale (128, 64 or 32), of which lane
 // l holds the RUN = piece / 4 columns from RUN (l / 16) on, on both sides.  PIECE 0 is one
 // scale per row: pieces of 128 columns whose sums run on through the row.

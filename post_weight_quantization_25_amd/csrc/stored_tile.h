@@ -11,9 +11,19 @@
 //
 // Zeros: the operand is u - zc with zc = z rounded to a whole number and clamped so that
 // u - zc is exact in the operand's type (8 bits: u - 128 for 8-bit codes, zc in -112 ..
-// 127 for narrower ones; 16 bits: |u - zc| <= 256).  z - zc is 0 for the quantizer's usual
-// zeros; where it is not, (z - zc) sum x is taken off the piece, with sum x from a product
-// of the same activations with ones, so every zero is served with exact operands.
+// 127 for narrower ones; 16 bits: |u - zc| <= 256, or zc = 0 for 3- and 4-bit codes, see
+// plain_16).  What that leaves of z is taken off the piece as (z - zc) sum x, with sum x
+// from a product of the same activations with ones, so every zero is served with exact
+// operands.
+//
+// What bounds these kernels is the L1's accesses rather than bytes: a lane's 16-byte load
+// of a row of its own is one access, four neighbouring lanes reading one row are a quarter
+// each.  So codes and the activations of several tiles are loaded contiguously and handed
+// to their lanes across the wave or through LDS (48 tokens x 11008 x 4096 int4 g64, 8-bit
+// rows: 25 us with every lane loading its own, 21 with codes contiguous, 17 with both); the
+// scales and zeros of two row blocks come in one load (33 -> 26 us with the rows without
+// tokens skipped).  Loading two chunks ahead costs registers, hence workgroups, and measured
+// the same or slower.
 #pragma once
 #include "common.h"
 

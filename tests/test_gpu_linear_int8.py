@@ -45,7 +45,8 @@ CASES = [
     (200, 1100, 4, 0, 100, BF, "whole"), (129, 4098, 4, 0, 130, F32, "fraction"), (513, 1024, 4, 128, 257, F32, "whole"),
     (260, 896, 4, 32, 300, F32, "whole"), (255, 576, 4, 64, 333, BF, "far"), (384, 1111, 8, 0, 200, F32, "whole"),
     (300, 1000, 3, 0, 290, F32, "symmetric"), (1030, 640, 4, 128, 2050, BF, "fraction"), (3000, 256, 4, 64, 2700, F32, "whole"),
-    (4100, 130, 4, 0, 2049, HF, "far"), (2100, 352, 3, 32, 4000, BF, "whole"), (4097, 300, 8, 0, 2100, F32, "whole"), (4001, 2048, 3, 0, 520, BF, "symmetric"), (1111, 512, 8, 128, 640, HF, "symmetric"),
+    (2100, 224, 3, 32, 1030, F32, "whole"), (1500, 320, 4, 64, 1500, F32, "fraction"), (2200, 1000, 3, 0, 1000, BF, "symmetric"),
+    (2050, 512, 8, 128, 1100, F32, "far"), (1600, 800, 4, 32, 1400, BF, "far"), (4100, 130, 4, 0, 2049, HF, "far"), (2100, 352, 3, 32, 4000, BF, "whole"), (4097, 300, 8, 0, 2100, F32, "whole"), (4001, 2048, 3, 0, 520, BF, "symmetric"), (1111, 512, 8, 128, 640, HF, "symmetric"),
 ]
 
 
@@ -62,7 +63,7 @@ def test_int8_parity(d_row, d_col, bits, group, n, yt, zeros):
 
 
 @pytest.mark.parametrize("bits,group", [(4, 128), (4, -1), (8, 0), (3, 64), (8, 32)])
-@pytest.mark.parametrize("n", [1, 40, 300])
+@pytest.mark.parametrize("n", [1, 40, 300, 30000])
 def test_int8_largest_sums(bits, group, n):
     """Every activation -128 and every code at one end: the largest sums a piece and a row
     can hold, all of one sign."""
@@ -78,7 +79,7 @@ def test_int8_largest_sums(bits, group, n):
     compare(g.linear_int8(q, g.Int8Rows(xq, xs)), q, xq, xs, What, F32)
 
 
-@pytest.mark.parametrize("n", [1, 20, 150])
+@pytest.mark.parametrize("n", [1, 20, 150, 14100])
 def test_int8_strided_rows_and_tokens_apart(n):
     """An odd row pitch and an unaligned first row; a NaN scale of one token and of one weight
     row stay there; rows past the outputs keep what they held."""

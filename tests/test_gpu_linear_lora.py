@@ -76,7 +76,9 @@ CASES = [
     (255, 576, 4, 64, 333, BF, BF, 4, 13, "runs", "far"), (384, 1111, 8, 0, 200, BF, F32, 2, 128, "one", "whole"),
     (300, 1000, 3, 0, 290, HF, F32, 5, 16, "runs", "symmetric"), (1001, 2048, 3, 128, 520, BF, BF, 7, 16, "runs", "whole"),
     (640, 512, 8, 32, 700, HF, F32, 3, 200, "mixed", "fraction"), (1111, 1024, 4, 128, 1030, BF, BF, 64, 32, "mixed", "whole"),
-    (3000, 192, 4, 64, 2700, BF, F32, 5, 16, "runs", "whole"), (4100, 130, 4, 0, 2049, HF, F32, 5, 40, "mixed", "far"),
+    (1300, 896, 4, 32, 900, HF, F32, 30, 48, "mixed", "whole"), (1200, 576, 4, 64, 1000, BF, BF, 4, 13, "runs", "far"),
+    (2048, 1000, 3, 0, 600, HF, F32, 5, 16, "runs", "symmetric"), (1100, 320, 8, 32, 1000, HF, F32, 3, 200, "mixed", "fraction"),
+    (1100, 1111, 8, 0, 1000, BF, F32, 2, 128, "one", "whole"), (3000, 192, 4, 64, 2700, BF, F32, 5, 16, "runs", "whole"), (4100, 130, 4, 0, 2049, HF, F32, 5, 40, "mixed", "far"),
     (2100, 352, 3, 32, 4000, BF, F32, 300, 16, "mixed", "whole"), (4097, 300, 8, 0, 2100, HF, HF, 2, 8, "runs", "fraction"),
     (4100, 384, 4, 128, 2050, HF, F32, 2, 256, "outside", "fraction"),
 ]
@@ -97,7 +99,7 @@ def test_lora_parity(d_row, d_col, bits, group, n, dt, yt, m, rank, kind, zeros)
     assert torch.equal(g.linear_lora(q, x, A, B, ids, s, out_dtype=yt), y)
 
 
-@pytest.mark.parametrize("n", [1, 30, 60, 200])
+@pytest.mark.parametrize("n", [1, 30, 60, 200, 7100])
 def test_lora_without_adapters_is_the_projection(n):
     """No adapters at all, or no token with one: the shared projection, bit for bit the same."""
     import post_weight_quantization_25_amd as g
@@ -110,7 +112,7 @@ def test_lora_without_adapters_is_the_projection(n):
     compare(y0, q, What, x, A, B, some_ids(n, 3, "none"), s, F32)
 
 
-@pytest.mark.parametrize("n", [5, 40, 300])
+@pytest.mark.parametrize("n", [5, 40, 300, 7100])
 @pytest.mark.parametrize("dt", [BF, HF])
 def test_lora_bad_adapters_stay_with_their_tokens(n, dt):
     """NaNs and infinities in one adapter, one token and one weight row change nothing else."""
@@ -135,7 +137,7 @@ def test_lora_bad_adapters_stay_with_their_tokens(n, dt):
     assert torch.equal(y2[~bad], y[~bad]) and not bool(torch.isfinite(y2[bad]).any())
 
 
-@pytest.mark.parametrize("n", [2, 40, 300])
+@pytest.mark.parametrize("n", [2, 40, 300, 16500])
 def test_lora_large_and_small_intermediates(n):
     """A x beyond fp16's range, and far below its smallest normal number: v is not an fp16 value."""
     import post_weight_quantization_25_amd as g
@@ -149,7 +151,7 @@ def test_lora_large_and_small_intermediates(n):
         compare(g.linear_lora(q, x, A2, B2, ids, s), q, What, x, A2, B2, ids, s, F32)
 
 
-@pytest.mark.parametrize("n", [2, 70])
+@pytest.mark.parametrize("n", [2, 70, 7100])
 def test_lora_strides_workspace_and_refusals(n):
     import post_weight_quantization_25_amd as g
     d_row, d_col, m, rank = 150, 384, 4, 12
