@@ -20,6 +20,7 @@
 // l holds the RUN = piece / 4 columns from RUN (l / 16) on, on both sides.  PIECE 0 is one
 // scale per row: pieces of 128 columns whose sums run on through the row.
 #pragma once
+#include "serving_rules.h"
 #include "stored_tile.h"
 
 namespace gptq {
@@ -38,9 +39,6 @@ GPTQ_DEV void tile_of(int gm, int gn, int& tm, int& tn) {
     tm = 8 * stripe + in % high;
     tn = in / high;
 }
-
-// What a tile's 32-bit offsets and a row's 32-bit integer sums take (128 x 127 x 2^17 < 2^31).
-inline bool gemm_fits(int64_t d_col, int64_t ldx_bytes) { return d_col <= (1 << 17) && ldx_bytes <= (1 << 24); }
 
 template <int X, int CB, int PIECE, int BM, int SLAB>   // SLAB: bytes of a token's row in LDS (128 or 256)
 struct StoredGemm {

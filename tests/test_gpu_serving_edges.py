@@ -1,0 +1,46 @@
+"""The serving operators where a sum, a split or a conversion reaches the end of its type's
+range: the longest rows of the lowest values, intermediates above bfloat16's largest value,
+infinities, rows of subnormals, rows of no columns."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from gpu_helpers import log
+from oracle import gptq_oracle as o
+from serving_helpers import BF, F32, HF, stored
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+@pytest.mark.parametrize("d_col", [131072, 131071])
+def test_int8_longest_rows_of_the_lowest_values(d_col):
+    """Activations of -128 against codes of 0 and a zero of 128: a row's integer sum is 128 *
+    128 * d_col, which for 2^17 columns is 2^31.  S = 2^-6 and x_scale = 1: every output is
+    2^8 d_col, to be had within 3 roundings per 128 columns and 12 at the end."""
+    import post_weight_quantization_25_amd as g
+    d_row, n = 128, 16384
+    log(f"int8 {d_row}x{d_col}, {n} tokens")
+    q = g.Quantized(torch.zeros(d_row, d_col, dtype=torch.uint8, device="cuda"),
+                    torch.full((d_row, 1), 2.0 ** -6, dtype=HF, device="cuda"),
+                    torch.full((d_row, 1), 128.0, dtype=HF, device="cuda"), None, 8, 0, d_col)
+    xq = torch.full((n, d_col), -128, dtype=torch.int8, device="cuda")
+    y = g.linear_int8(q, g.Int8Rows(xq, torch.ones(n, device="cuda")))
+    ref = 2.0 ** 8 * d_col
+    assert float((y.double() - ref).abs().max()) <= (3 * 1024 + 12) * 2.0 ** -24 * ref
+
+
+def test_int8_codes_of_zero_against_the_lowest_activations():
+    """8-bit codes of 0 enter as -128: the other end of what a piece and a row can hold."""
+    import post_weight_quantization_25_amd as g
+    for group in (0, 32, 128):
+        for n in (1, 40, 30000):
+            q, _ = stored(70, 2048, 8, group, 3)
+            q.codes.zero_()
+            q.zeros.fill_(128)
+            q.scales.fill_(2.0 ** -6)
+            xq = torch.full((n, 2048), -128, dtype=torch.int8, device="cuda")
+            y = g.linear_int8(q, g.Int8Rows(xq, torch.ones(n, device="cuda")))
+            assert bool((y == 2.0 ** 8 * 2048).all())      # multiples of 2^15 below 2^20: exact
