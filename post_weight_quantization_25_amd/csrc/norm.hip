@@ -268,7 +268,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
         return;
     }
     const double rstd = 1.0 / sqrt(ss / (double)a.d + (double)a.eps);
-    const float am = __uint_as_float(mb), inv = 127.f / am, rstdf = (float)rstd;
+    const float am = __uint_as_float(mb), inv = 127.f / am;
+    // rstd = rm 2^re: with eps = 0 a row of subnormals, or near the type's largest value, has one
+    // that is no normal fp32 number
+    int re;
+    const float rm = (float)frexp(rstd, &re);
     if (tid == 0) a.scale[row] = (float)((double)am * rstd / 127.0);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -279,7 +283,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(NormArgs a)
         store_codes(a.q, row * a.ldq + c, m, k);
         if (a.y) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) p[j][e] *= rstdf;
+            for (int e = 0; e < 8; ++e) p[j][e] = ldexpf(p[j][e] * rm, re);
             store8<XT>(a.y, row * a.ldy + c, m, p[j]);
         }
     }

@@ -15,6 +15,10 @@ pytestmark = pytest.mark.gpu
 INF = float("inf")
 
 
+def codes_of(q):
+    return torch.from_numpy(o.unpack(q.codes.cpu().numpy(), q.bits).astype(np.float64))
+
+
 @pytest.mark.parametrize("d_col", [131072, 131071])
 def test_int8_longest_rows_of_the_lowest_values(d_col):
     """Activations of -128 against codes of 0 and a zero of 128: a row's integer sum is 128 *
@@ -44,3 +48,25 @@ def test_int8_codes_of_zero_against_the_lowest_activations():
             xq = torch.full((n, 2048), -128, dtype=torch.int8, device="cuda")
             y = g.linear_int8(q, g.Int8Rows(xq, torch.ones(n, device="cuda")))
             assert bool((y == 2.0 ** 8 * 2048).all())      # multiples of 2^15 below 2^20: exact
+
+
+@pytest.mark.parametrize("d", [40, 2000, 4096, 9000, 16384])
+@pytest.mark.parametrize("size,wsize", [(2.0 ** -131, 2.0 ** 45), (2.0 ** 127, 2.0 ** -24)])
+def test_norm_rows_whose_rstd_is_no_normal_fp32_number(d, size, wsize):
+    """eps = 0: rows of subnormals have 1 / rms above fp32's largest value, rows near the
+    largest have it below the smallest normal one.  p rstd itself is about 2^45 or 2^-24: one
+    rounding of it to fp32 and one to bfloat16."""
+    import post_weight_quantization_25_amd as g
+    gen = torch.Generator().manual_seed(d)
+    x = ((0.5 + 0.5 * torch.rand(3, d, generator=gen)) * size).to(BF).cuda()
+    w = (wsize * (1 + 0.1 * torch.randn(d, generator=gen))).to(BF).cuda()
+    normed = torch.empty_like(x)
+    rows, _ = g.rmsnorm_int8(x, w, eps=0.0, normed=normed)
+    v = x.double()
+    ref = v * w.double() / torch.sqrt((v * v).mean(1, keepdim=True))
+    err = (normed.double() - ref).abs()
+    log(f"  normed max rel {float((err / ref.abs()).max()):.2e}")
+    assert bool((err <= (2.0 ** -8 + 2.0 ** -22) * ref.abs()).all())
+    am = (v * w.double()).abs().amax(1)
+    scale = am / torch.sqrt((v * v).mean(1)) / 127
+    assert bool(((rows.scale.double() - scale).abs() <= 2.0 ** -23 * scale).all())
