@@ -118,8 +118,9 @@ gptq_status gptqs_linear_lora(const uint8_t* codes, const uint16_t* scales_f16, 
  *   chosen ones alone;
  *   h_j = silu(G_e x[t]) * (U_e x[t]),  e = the j-th chosen expert;
  *   y[t] = sum_j w_j D_e h_j.
- * Logits, softmax and sums in fp32; w_j h_j enters the last product as two
- * bfloat16 parts.
+ * Logits, softmax and sums in fp32; w_j h_j enters the last product as it is (fp32, in
+ * three bfloat16 parts) where y is fp32, and to 2^-17 of each value (two parts) where y has
+ * 16 bits.
  *
  *  x            n_tokens x d, pitch ldx >= d, dtype x_dtype: GPTQ_BF16 or GPTQ_F16
  *  router       n_experts x d, dtype x_dtype

@@ -4,7 +4,8 @@
 //   moe_plan_kernel    a wave per token takes the largest logits one by one; softmax; the pairs
 //                      (token, choice) sorted by expert
 //   moe_up_kernel      per expert in use and 16 inner columns: gate and up products for the
-//                      tokens that chose it, silu(gate) up w, written as two bfloat16 parts
+//                      tokens that chose it, silu(gate) up w, written as bfloat16 parts (two
+//                      for 16-bit outputs, three for fp32)
 //   moe_down_kernel    per expert in use and 16 output columns: the pairs' outputs, fp32
 //   moe_sum_kernel     y = a token's pairs added in the order of its choices
 // Bound by the codes of the chosen experts, which up and down read once each.  One token,
@@ -28,12 +29,15 @@ struct MoeArgs {
     const uint16_t* router; int E, k; int renormalize;
     Stored up, down;          // E 2f x d, E d x f
     float* logits;            // n x E
-    uint16_t* hi; uint16_t* lo;   // n k x f: w silu(gate) up as bfloat16 hi + lo
+    uint16_t* inner;          // n k x f, for each part of w silu(gate) up in bfloat16
     float* part;              // n k x d: w D h per pair
     int32_t* plan;            // see moe_plan_kernel
     int32_t* ids; float* weights;
     void* y; gptq_dtype yt;
 };
+
+// Elements from one part of the inner values to the next: whole 16 bytes.
+GPTQ_DEV int64_t part_elems(const MoeArgs& a) { return ((int64_t)a.n * a.k * a.f + 7) & ~(int64_t)7; }
 
 constexpr int LOGW = 8;
 
@@ -197,7 +201,7 @@ __global__ __launch_bounds__(64 * PLAN_W) void moe_plan_kernel(MoeArgs a) {
     }
 }
 
-constexpr int MW = 8;         // waves per workgroup of the experts' products
+constexpr int MW = 8;         // waves per workgroup of the gate and up products
 
 // Grid: 16 inner columns x the s-th expert in use.
 template <int X, int CB, int RUN>
@@ -234,19 +238,32 @@ __global__ __launch_bounds__(64 * MW, 4) void moe_up_kernel(MoeArgs a) {
                 }
                 const int pr = a.plan[PAIRS + p0 + m0 + m];
                 const float h = g / (1.f + expf(-g)) * u * a.weights[pr];
-                const uint16_t hb = f32_to_bf16_bits(h);
-                a.hi[(int64_t)pr * a.f + f0 + n] = hb;
-                a.lo[(int64_t)pr * a.f + f0 + n] = f32_to_bf16_bits(h - bf16_bits_to_f32(hb));
+                uint16_t part[3];
+                bf16_parts(h, part);
+                uint16_t* to = a.inner + (int64_t)pr * a.f + f0 + n;
+                const int64_t plane = part_elems(a);
+                to[0] = part[0];
+                to[plane] = part[1];
+                if (a.yt == GPTQ_F32) to[2 * plane] = part[2];
             }
         }
     }
 }
 
-// Grid: 16 output columns x the s-th expert in use.  The two bfloat16 parts of a pair's
-// inner values are two tiles of the same tokens; their sums are added at the end.
-template <int CB, int RUN>
-__global__ __launch_bounds__(64 * MW, 4) void moe_down_kernel(MoeArgs a) {
-    __shared__ float red[MW][4][64];
+// Grid: 16 output columns x the s-th expert in use.  The bfloat16 parts of a pair's inner
+// values are tiles of the same tokens; their sums are added at the end.
+//
+// Three parts take 157 registers, which eight waves per workgroup would leave one workgroup
+// per compute unit, four waves three of them: fp32 outputs, eight / four: 32 tokens, 2 of 16
+// experts of 4096 x 5504, 291 / 257 us a call; one, 8 of 64 of 2048 x 1408, 42.0 / 37.4 (with
+// two parts for 16-bit outputs 226 and 36.2).
+template <int PARTS> constexpr int down_waves() { return PARTS == 2 ? 8 : 4; }
+
+template <int CB, int RUN, int PARTS>
+__global__ __launch_bounds__(64 * down_waves<PARTS>(), PARTS == 2 ? 4 : RUN == 32 ? 3 : 2)
+void moe_down_kernel(MoeArgs a) {
+    constexpr int W = down_waves<PARTS>();
+    __shared__ float red[W][4][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15;
     const int s = blockIdx.y;
     if (s >= a.plan[0]) return;
@@ -257,20 +274,29 @@ __global__ __launch_bounds__(64 * MW, 4) void moe_down_kernel(MoeArgs a) {
     for (int m0 = 0; m0 < cnt; m0 += MOE_T) {
         const bool live = m0 + n16 < cnt;
         const int64_t at = live ? (int64_t)a.plan[PAIRS + p0 + m0 + n16] * a.f : 0;
-        const XScattered<2> xr = {{live ? reinterpret_cast<const uint8_t*>(a.hi + at) : nullptr,
-                                   live ? reinterpret_cast<const uint8_t*>(a.lo + at) : nullptr}};
-        f32x4_t acc[2][1] = {{f32x4_t{0.f, 0.f, 0.f, 0.f}}, {f32x4_t{0.f, 0.f, 0.f, 0.f}}};
-        stored_accumulate<X_BF16, CB, RUN, 2, 1, 1>(acc, a.down, row, xr, wave, MW);
+        XScattered<PARTS> xr;
+        f32x4_t acc[PARTS][1];
+#pragma unroll
+        for (int j = 0; j < PARTS; ++j) {
+            xr.row[j] = live ? reinterpret_cast<const uint8_t*>(a.inner + j * part_elems(a) + at) : nullptr;
+            acc[j][0] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        }
+        stored_accumulate<X_BF16, CB, RUN, PARTS, 1, 1>(acc, a.down, row, xr, wave, W);
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) red[wave][i][lane] = acc[0][0][i] + acc[1][0][i];
+        for (int i = 0; i < 4; ++i) {
+            float v = acc[PARTS - 1][0][i];                 // the smallest first
+#pragma unroll
+            for (int j = PARTS - 2; j >= 0; --j) v += acc[j][0][i];
+            red[wave][i][lane] = v;
+        }
         __syncthreads();
         if (threadIdx.x < 256) {
             const int m = threadIdx.x >> 4, n = threadIdx.x & 15;
             if (m0 + m < cnt && r0 + n < a.d) {
                 float v = 0.f;
 #pragma unroll
-                for (int w = 0; w < MW; ++w) v += red[w][m & 3][n + 16 * (m >> 2)];
+                for (int w = 0; w < W; ++w) v += red[w][m & 3][n + 16 * (m >> 2)];
                 a.part[(int64_t)a.plan[PAIRS + p0 + m0 + m] * a.d + r0 + n] = v;
             }
         }
@@ -305,7 +331,11 @@ static gptq_status launch(const MoeArgs& a, hipStream_t s) {
     GPTQ_LAUNCH_CHECK();
     moe_up_kernel<X, CB, RUN><<<dim3(ef, (unsigned)slots), 64 * MW, 0, s>>>(a);
     GPTQ_LAUNCH_CHECK();
-    moe_down_kernel<CB, RUN><<<dim3((unsigned)((a.d + 15) / 16), (unsigned)slots), 64 * MW, 0, s>>>(a);
+    const dim3 down((unsigned)((a.d + 15) / 16), (unsigned)slots);
+    // Parts of the inner values: two, 2^-17 of each, are far below a 16-bit output's rounding
+    // (2^-9, 2^-12); fp32 outputs take three, which are the values themselves.
+    if (a.yt == GPTQ_F32) moe_down_kernel<CB, RUN, 3><<<down, 64 * down_waves<3>(), 0, s>>>(a);
+    else moe_down_kernel<CB, RUN, 2><<<down, 64 * down_waves<2>(), 0, s>>>(a);
     GPTQ_LAUNCH_CHECK();
     moe_sum_kernel<<<dim3((unsigned)((a.d + 255) / 256), (unsigned)a.n), 256, 0, s>>>(a);
     GPTQ_LAUNCH_CHECK();
@@ -325,13 +355,12 @@ static gptq_status launch_bits(const MoeArgs& a, int bits, int group, hipStream_
 static size_t up16(size_t v) { return (v + 15) & ~(size_t)15; }
 
 // Offsets of the workspace's parts, in this order, each 16-byte aligned; the last is its size.
-struct MoeWs { size_t hi, lo, part, plan, end; };
+struct MoeWs { size_t inner, part, plan, end; };
 static MoeWs moe_ws(int64_t n, int64_t d, int64_t f, int E, int k) {
     MoeWs w;
-    const size_t inner = up16((size_t)n * k * (size_t)f * sizeof(uint16_t));
-    w.hi = up16((size_t)n * E * sizeof(float));
-    w.lo = w.hi + inner;
-    w.part = w.lo + inner;
+    const size_t inner = up16((size_t)n * k * (size_t)f * sizeof(uint16_t));   // one part (part_elems)
+    w.inner = up16((size_t)n * E * sizeof(float));
+    w.part = w.inner + 3 * inner;
     w.plan = w.part + up16((size_t)n * k * (size_t)d * sizeof(float));
     w.end = w.plan + up16((size_t)(PAIRS + 1 + n * k) * sizeof(int32_t));
     return w;
@@ -348,8 +377,7 @@ gptq_status moe_launch(const MoeCall& c, hipStream_t s) {
     uint8_t* w = (uint8_t*)c.ws;
     const MoeWs o = moe_ws(c.n, c.d, c.f, c.E, c.k);
     a.logits = (float*)w;
-    a.hi = (uint16_t*)(w + o.hi);
-    a.lo = (uint16_t*)(w + o.lo);
+    a.inner = (uint16_t*)(w + o.inner);
     a.part = (float*)(w + o.part);
     a.plan = (int32_t*)(w + o.plan);
     a.ids = c.ids; a.weights = c.weights; a.y = c.y; a.yt = c.yt;

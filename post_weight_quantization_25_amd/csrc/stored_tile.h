@@ -489,6 +489,21 @@ GPTQ_DEV void stored_accumulate(f32x4_t (&acc)[NTT][RB], const Stored& L, const 
     }
 }
 
+// An fp32 number as bfloat16 parts: each the nearest to what the ones before leave (toward
+// zero where the nearest is infinite).  The first two leave at most 2^-17 of it (it is in 2^e
+// .. 2^(e+1), the first leaves at most 2^(e-8), and the second half a step of that at most,
+// 2^(e-17)); with the third they are the number itself (what the second leaves is a multiple
+// of 2^(e-23) of at most 2^(e-16): 8 bits).  An infinity or a NaN is its first part alone.
+GPTQ_DEV void bf16_parts(float v, uint16_t (&p)[3]) {
+    const uint32_t u = __float_as_uint(v);
+    const bool fin = (u & 0x7f800000u) != 0x7f800000u;
+    p[0] = f32_to_bf16_bits(v);
+    if (fin && (p[0] & 0x7fffu) == 0x7f80u) p[0] = (uint16_t)(u >> 16);
+    const float r = fin ? v - bf16_bits_to_f32(p[0]) : 0.f;
+    p[1] = f32_to_bf16_bits(r);
+    p[2] = f32_to_bf16_bits(r - bf16_bits_to_f32(p[1]));
+}
+
 // One output, rounded once (to nearest even) by the hardware's conversions.
 template <gptq_dtype YT>
 GPTQ_DEV void store_as(void* y, int64_t idx, float v) {
