@@ -87,7 +87,9 @@ gptq_status gptqs_linear_int8(const uint8_t* codes, const uint16_t* scales_f16, 
  * a token whose id is outside 0 .. n_adapters - 1 (by convention -1) takes What x[t]
  * alone.  Tokens may come in any order; runs of tokens with one adapter are cheapest.
  * A x is summed in fp32; scaling A x enters the second product in fp32 (small batches) or
- * as two bfloat16 parts.
+ * as two bfloat16 parts.  An infinite x gives infinities with the weights' signs (NaN where
+ * a code is its zero), for every token count where zeros are whole numbers in -240 .. 240;
+ * no other token's outputs change.
  *
  *  codes, scales_f16, zeros_f16, d_row, d_col, bits, group_size   as gptqs_linear_int8.
  *  x            n_tokens x d_col, pitch ldx >= d_col, dtype x_dtype: GPTQ_BF16 or GPTQ_F16

@@ -102,7 +102,7 @@ template <int X>
 GPTQ_DEV float elem16(uint16_t b) { return X == X_BF16 ? bf16_bits_to_f32(b) : f16_bits_to_f32(b); }
 
 template <int X, int CB, int RUN, int NTT, int RB>
-__global__ __launch_bounds__(64 * TW) void lora_tile_kernel(LoraArgs a) {
+__global__ __launch_bounds__(64 * TW, NTT == 1 ? 4 : 2) void lora_tile_kernel(LoraArgs a) {
     constexpr int DEEP = NTT >= 3 ? 1 : 2;
     constexpr int PER = (NTT * RB * 256 + 64 * TW - 1) / (64 * TW);   // outputs per thread
     constexpr int STAGE = 16 * SCK * xbytes<X>();                   // one tile's chunk
@@ -185,11 +185,17 @@ __global__ __launch_bounds__(64 * TW) void lora_tile_kernel(LoraArgs a) {
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
         const int o = threadIdx.x + 64 * TW * k, tr = o >> 8, m = (o >> 4) & 15, n = o & 15;
-        if (tr >= NTT * RB) continue;
+        if (tr >= NTT * RB) continue;                              // whole waves
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < TW; ++w) v += red[w][tr][m & 3][n + 16 * (m >> 2)];
         const int64_t t = tok0 + 16 * (tr / RB) + m, r = row0 + 16 * (tr % RB) + n;
+        v = finite_sum<CB>(
+            v, t < a.n && r < a.d_row, a.L,
+            [&](int i) { return row0 + 16 * (((i + 64 * TW * k) >> 8) % RB) + (i & 15); },
+            [&](int i, int64_t c, int m8, float (&x)[8]) {
+                load_x8<X>(a.x + (tok0 + 16 * (((i + 64 * TW * k) >> 8) / RB) + ((i >> 4) & 15)) * a.ldx + c, m8, x);
+            });
         if (id[k] >= 0) v += delta[k];
         if (t < a.n && r < a.d_row) store_out(a.y, a.yt, t * a.d_row + r, v);
     }

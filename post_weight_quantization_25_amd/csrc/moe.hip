@@ -8,6 +8,8 @@
 //                      for 16-bit outputs, three for fp32)
 //   moe_down_kernel    per expert in use and 16 output columns: the pairs' outputs, fp32
 //   moe_sum_kernel     y = a token's pairs added in the order of its choices
+// Sums that are not finite are taken once more as sum S (u - z) x (finite_sum in
+// stored_tile.h), in up behind its tiles and for down in moe_sum_kernel.
 // Bound by the codes of the chosen experts, which up and down read once each.  One token,
 // 8 of 64 experts of 2048 x 1408 int4: 4.2 + 5.8 + 13 + 9.4 + 3.8 us for 35 MB of codes,
 // latency of five dependent launches; 32 tokens, 2 of 16 experts of 4096 x 5504: 8.7 + 4.6
@@ -203,6 +205,19 @@ __global__ __launch_bounds__(64 * PLAN_W) void moe_plan_kernel(MoeArgs a) {
 
 constexpr int MW = 8;         // waves per workgroup of the gate and up products
 
+// Pair pr's inner value at column c from its gate and up sums; whether it is finite.
+GPTQ_DEV bool inner_value(const MoeArgs& a, int pr, int64_t c, float g, float u) {
+    const float h = g / (1.f + expf(-g)) * u * a.weights[pr];
+    uint16_t part[3];
+    bf16_parts(h, part);
+    uint16_t* to = a.inner + (int64_t)pr * a.f + c;
+    const int64_t plane = part_elems(a);
+    to[0] = part[0];
+    to[plane] = part[1];
+    if (a.yt == GPTQ_F32) to[2 * plane] = part[2];
+    return fabsf(h) < INFINITY;
+}
+
 // Grid: 16 inner columns x the s-th expert in use.
 template <int X, int CB, int RUN>
 __global__ __launch_bounds__(64 * MW, 4) void moe_up_kernel(MoeArgs a) {
@@ -215,6 +230,7 @@ __global__ __launch_bounds__(64 * MW, 4) void moe_up_kernel(MoeArgs a) {
     const int64_t f0 = (int64_t)blockIdx.x * 16;
     const int64_t fr = f0 + n16 < a.f ? f0 + n16 : a.f - 1;
     const int64_t row[2] = {(int64_t)e * 2 * a.f + fr, (int64_t)e * 2 * a.f + a.f + fr};
+    uint64_t lost = 0;
     for (int m0 = 0; m0 < cnt; m0 += MOE_T) {
         const bool live = m0 + n16 < cnt;
         const int p = live ? a.plan[PAIRS + p0 + m0 + n16] : 0;
@@ -229,6 +245,7 @@ __global__ __launch_bounds__(64 * MW, 4) void moe_up_kernel(MoeArgs a) {
         __syncthreads();
         if (threadIdx.x < 256) {
             const int m = threadIdx.x >> 4, n = threadIdx.x & 15;
+            bool bad = false;
             if (m0 + m < cnt && f0 + n < a.f) {
                 float g = 0.f, u = 0.f;
 #pragma unroll
@@ -236,17 +253,26 @@ __global__ __launch_bounds__(64 * MW, 4) void moe_up_kernel(MoeArgs a) {
                     g += red[w][0][m & 3][n + 16 * (m >> 2)];
                     u += red[w][1][m & 3][n + 16 * (m >> 2)];
                 }
-                const int pr = a.plan[PAIRS + p0 + m0 + m];
-                const float h = g / (1.f + expf(-g)) * u * a.weights[pr];
-                uint16_t part[3];
-                bf16_parts(h, part);
-                uint16_t* to = a.inner + (int64_t)pr * a.f + f0 + n;
-                const int64_t plane = part_elems(a);
-                to[0] = part[0];
-                to[plane] = part[1];
-                if (a.yt == GPTQ_F32) to[2 * plane] = part[2];
+                bad = !inner_value(a, a.plan[PAIRS + p0 + m0 + m], f0 + n, g, u);
             }
+            lost |= __ballot(bad);
         }
+    }
+    // Values that are not finite, once more from sums by wave_sum (see finite_sum: an infinite
+    // g or u, or one that is no number, leaves no finite value).  Behind the loop, whose
+    // registers it would take.
+    if (lost == 0) return;                                  // wave-uniform; no barrier below
+    for (int m0 = 0; m0 < cnt; m0 += MOE_T) {
+        const int m = threadIdx.x >> 4, n = threadIdx.x & 15;
+        const bool mine = m0 + m < cnt && f0 + n < a.f;
+        const int pr = mine ? a.plan[PAIRS + p0 + m0 + m] : 0;
+        const float h = mine ? bf16_bits_to_f32(a.inner[(int64_t)pr * a.f + f0 + n]) : 0.f;
+        const auto x8 = [&](int i, int64_t c, int m8, float (&x)[8]) {
+            load_x8<X>(a.x + (int64_t)(a.plan[PAIRS + p0 + m0 + (i >> 4)] / a.k) * a.ldx + c, m8, x);
+        };
+        const float g = finite_sum<CB>(h, mine, a.up, [&](int i) { return (int64_t)e * 2 * a.f + f0 + (i & 15); }, x8);
+        const float u = finite_sum<CB>(h, mine, a.up, [&](int i) { return ((int64_t)e * 2 + 1) * a.f + f0 + (i & 15); }, x8);
+        if (!(fabsf(h) < INFINITY)) inner_value(a, pr, f0 + n, g, u);
     }
 }
 
@@ -303,13 +329,35 @@ void moe_down_kernel(MoeArgs a) {
     }
 }
 
+// y from the pairs' outputs; those that are not finite once more from down's rows (finite_sum:
+// here and not in down, whose registers are all taken).
+template <int CB>
 __global__ __launch_bounds__(256) void moe_sum_kernel(MoeArgs a) {
-    const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t r0 = (int64_t)blockIdx.x * 256, r = r0 + threadIdx.x;
     const int t = blockIdx.y;
-    if (r >= a.d) return;
+    const bool live = r < a.d;
+    const float* part = a.part + (int64_t)t * a.k * a.d + (live ? r : 0);
     float v = 0.f;
-    for (int j = 0; j < a.k; ++j) v += a.part[((int64_t)t * a.k + j) * a.d + r];
-    store_out(a.y, a.yt, (int64_t)t * a.d + r, v);
+    for (int j = 0; j < a.k; ++j) v += part[j * a.d];
+    if (__ballot(live && !(fabsf(v) < INFINITY)) != 0) {    // wave-uniform, rare
+        v = 0.f;
+        for (int j = 0; j < a.k; ++j) {
+            const int64_t pr = (int64_t)t * a.k + j;
+            v += finite_sum<CB>(
+                part[j * a.d], live, a.down, [&](int i) { return (int64_t)a.ids[pr] * a.d + r0 + i; },
+                [&](int, int64_t c, int m8, float (&x)[8]) {
+                    const uint16_t* h = a.inner + pr * a.f + c;
+                    load_x8<X_BF16>(h, m8, x);
+                    for (int q = 1; q < (a.yt == GPTQ_F32 ? 3 : 2); ++q) {
+                        float y[8];
+                        load_x8<X_BF16>(h + q * part_elems(a), m8, y);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] += y[e];
+                    }
+                });
+        }
+    }
+    if (live) store_out(a.y, a.yt, (int64_t)t * a.d + r, v);
 }
 
 template <int X, int CB, int RUN>
@@ -337,7 +385,7 @@ static gptq_status launch(const MoeArgs& a, hipStream_t s) {
     if (a.yt == GPTQ_F32) moe_down_kernel<CB, RUN, 3><<<down, 64 * down_waves<3>(), 0, s>>>(a);
     else moe_down_kernel<CB, RUN, 2><<<down, 64 * down_waves<2>(), 0, s>>>(a);
     GPTQ_LAUNCH_CHECK();
-    moe_sum_kernel<<<dim3((unsigned)((a.d + 255) / 256), (unsigned)a.n), 256, 0, s>>>(a);
+    moe_sum_kernel<CB><<<dim3((unsigned)((a.d + 255) / 256), (unsigned)a.n), 256, 0, s>>>(a);
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
 }

@@ -288,8 +288,10 @@ struct StoredGemm {
                     const float rz = f16_bits_to_f32((uint16_t)(rowE[nt].z & 0xFFFFu)) - part_of(rowE[nt].z >> 16);
                     settle(cs[mt][nt]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[mt][nt][i] = rowE[nt].S * fmaf(-rz, (float)xs[mt][i], (float)cs[mt][nt][i]);
+                    for (int i = 0; i < 4; ++i) {
+                        const float sum = (float)cs[mt][nt][i], less = fmaf(-rz, (float)xs[mt][i], sum);
+                        acc[mt][nt][i] = rowE[nt].S * (X != X_I8 && rz == 0.f ? sum : less);   // as in rests
+                    }
                 }
         }
     }
@@ -420,7 +422,11 @@ private:
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[mt][nt][i] = fmaf(-S[nt] * rz[nt], (float)xs[i], acc[mt][nt][i]);
+                for (int i = 0; i < 4; ++i) {
+                    const float less = fmaf(-S[nt] * rz[nt], (float)xs[i], acc[mt][nt][i]);
+                    // no rest, no sum of x: it may be infinite
+                    acc[mt][nt][i] = X != X_I8 && rz[nt] == 0.f ? acc[mt][nt][i] : less;
+                }
             __builtin_amdgcn_sched_barrier(0);
         }
     }

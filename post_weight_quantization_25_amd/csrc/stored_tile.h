@@ -453,8 +453,8 @@ struct Chunk {
 };
 
 // Sums of RB blocks of 16 weight rows with NTT tiles of 16 tokens over the chunks c0, c0 +
-// step, .. of a row.  DEEP chunks are in registers at a time: one is multiplied while the
-// others are on their way.
+// step, .. of a row.  DEEP chunks are in registers at a time: with two, one is multiplied
+// while the other is on its way; with one, only other waves' work covers its round trip.
 template <int X, int CB, int RUN, int NTT, int RB, int DEEP, typename XR>
 GPTQ_DEV void stored_accumulate(f32x4_t (&acc)[NTT][RB], const Stored& L, const int64_t (&row)[RB], const XR& xr, int c0,
                                 int step) {
@@ -486,6 +486,64 @@ GPTQ_DEV void stored_accumulate(f32x4_t (&acc)[NTT][RB], const Stored& L, const 
         ch[0].arrange();
         ch[0].arrange_x(xr);
         ch[0].multiply(acc);
+    }
+}
+
+// What[r] x by a whole wave as the definition has it, sum S (u - z) x: for sums that came out
+// as no number (see finite_sum).  x8(c, m, v) gives the m elements of x from column c on, m <=
+// 8.  8 columns per lane and step.
+template <int CB, typename F>
+GPTQ_DEV float wave_sum(const Stored& L, int64_t r, F&& x8) {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));             // addresses are formed here, not carried through the kernel
+    float s = 0.f;
+#pragma unroll 1
+    for (int64_t c = 8 * (int64_t)lane; c < L.d_col; c += 512) {
+        const int m = L.d_col - c < 8 ? (int)(L.d_col - c) : 8;
+        const uint8_t* src = L.codes + r * L.code_ld + c / 8 * CB;
+        const Raw<CB, 8> u = m == 8 ? load_raw<CB, 8>(src) : load_raw_tail<CB, 8>(src, m);
+        const int64_t at = r * L.n_groups + (L.n_groups == 1 ? 0 : c >> L.gshift);   // a group is whole steps
+        const float S = f16_bits_to_f32(L.scales[at]), z = f16_bits_to_f32(L.zeros[at]);
+        float x[8];
+        x8(c, m, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float w = S * ((float)((code_bytes4<CB, 8>(u, e >> 2) >> (8 * (e & 3))) & 0xFFu) - z);
+            if (e < m) s = fmaf(w, x[e], s);
+        }
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o);
+    return s;
+}
+
+// v, the lane's sum, or where that is not finite the sum taken again with wave_sum.  The
+// kernels' products can lose it: u x - z x, of codes that enter as they are, is infinity -
+// infinity for an infinite x, and so is what a zero's rest takes off; and sums of u x may
+// overflow where those of S (u - z) x do not.  The others keep their bits.  row_of(i) and
+// x8(i, ..) give thread i's row and its token's data.  The whole wave calls it; lanes
+// without an output pass live = false.
+template <int CB, typename R, typename F>
+GPTQ_DEV float finite_sum(float v, bool live, const Stored& L, R&& row_of, F&& x8) {
+    uint64_t todo = __ballot(live && !(fabsf(v) < INFINITY));
+    while (todo) {                                                 // wave-uniform, rare
+        const int l = __builtin_ctzll(todo), i = __builtin_amdgcn_readfirstlane((int)threadIdx.x & ~63) + l;
+        todo &= todo - 1;
+        const float s = wave_sum<CB>(L, row_of(i), [&](int64_t c, int m, float (&x)[8]) { x8(i, c, m, x); });
+        if ((int)(threadIdx.x & 63) == l) v = s;
+    }
+    return v;
+}
+
+// Eight 16-bit elements from p on, the first m of which exist.
+template <int X>
+GPTQ_DEV void load_x8(const uint16_t* p, int m, float (&v)[8]) {
+    const uint8_t* b = reinterpret_cast<const uint8_t*>(p);
+    const XRun<X, 8> r = m == 8 ? load_x<X, 8>(b) : load_x_tail<X, 8>(b, m);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint16_t h = (uint16_t)(r.w[e / 2] >> (16 * (e & 1)));
+        v[e] = X == X_BF16 ? bf16_bits_to_f32(h) : f16_bits_to_f32(h);
     }
 }
 

@@ -72,6 +72,36 @@ def test_norm_rows_whose_rstd_is_no_normal_fp32_number(d, size, wsize):
     assert bool(((rows.scale.double() - scale).abs() <= 2.0 ** -23 * scale).all())
 
 
+def signed_infinities(w):
+    """w times infinity: NaN where w is 0."""
+    return torch.where(w > 0, INF, torch.where(w < 0, -INF, float("nan")))
+
+
+@pytest.mark.parametrize("n", [1, 5, 20, 40, 60, 300, 7100])
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("bits,group", [(4, 128), (3, 32), (8, 64), (4, 0)])
+def test_lora_an_infinite_activation_gives_the_weights_signs(n, dt, bits, group):
+    """One infinite activation: y is What's column times infinity, whatever kernel the batch
+    takes; the other tokens keep their bits.  Zeros are whole numbers, but for one row's."""
+    import post_weight_quantization_25_amd as g
+    d_row, d_col, at = 150, 384, 261
+    q, _ = stored(d_row, d_col, bits, group, 5)
+    q.zeros[77] = 2.5
+    u = codes_of(q)
+    w = u[:, at] - q.zeros.cpu().double()[:, at // (group or d_col)]
+    x = torch.randn(n, d_col, generator=torch.Generator().manual_seed(1)).to(dt).cuda()
+    none = torch.empty(0, 1, d_col, dtype=dt, device="cuda"), torch.empty(0, d_row, 1, dtype=dt, device="cuda")
+    ids = torch.zeros(n, dtype=torch.int32, device="cuda")
+    y = g.linear_lora(q, x, *none, ids)
+    x[n // 2, at] = -INF
+    y2 = g.linear_lora(q, x, *none, ids)
+    keep = [r for r in range(d_row) if r != 77]
+    assert torch.equal(torch.nan_to_num(y2[n // 2].cpu()[keep], 5.0), torch.nan_to_num(-signed_infinities(w).float()[keep], 5.0))
+    assert not bool(torch.isfinite(y2[n // 2, 77]))
+    rest = [t for t in range(n) if t != n // 2]
+    assert torch.equal(y2[rest], y[rest]) and bool(torch.isfinite(y).all())
+
+
 def one_column_experts(E, d, f, bits, gate, up):
     """The up layer of experts whose gate and up rows see x's column 0 alone, with these scales."""
     import post_weight_quantization_25_amd as g
@@ -88,6 +118,34 @@ def packed_layer(codes, bits, zero, scale, group=32):
     return g.Quantized(torch.from_numpy(o.pack(codes.astype(np.uint8), bits)).cuda(),
                        torch.full((rows, cols // group), scale, dtype=HF, device="cuda"),
                        torch.full((rows, cols // group), float(zero), dtype=HF, device="cuda"), None, bits, group, cols)
+
+
+@pytest.mark.parametrize("n", [1, 20])
+@pytest.mark.parametrize("bits", [3, 4, 8])
+def test_moe_infinite_and_largest_inner_values(n, bits):
+    """One inner value that is infinite, or finite above bfloat16's largest: y is the down
+    column times it (codes within 1 of their zero: the unscaled sums stay finite).  gate =
+    S 2^64 and up = 2^64 give S 2^128."""
+    import post_weight_quantization_25_amd as g
+    d, f, j = 64, 32, 5
+    gen = torch.Generator().manual_seed(1)
+    codes = np.random.default_rng(2).integers(3, 6, size=(d, f))
+    down = packed_layer(codes, bits, 4, 2.0 ** -10)
+    Wd = torch.from_numpy(codes[:, j] - 4.0) * 2.0 ** -10
+    for S in (1.0, 0.9990234375):
+        gate = torch.zeros(1, f)
+        gate[0, j] = S
+        up = one_column_experts(1, d, f, bits, gate, torch.ones(1, f))
+        x = torch.zeros(n, d)
+        x[:, 0] = 2.0 ** 64
+        y, _, w = g.moe(x.to(BF).cuda(), torch.zeros(1, d, dtype=BF, device="cuda"), up, down, 1)
+        assert bool((w == 1).all())
+        if S == 1.0:
+            ref = signed_infinities(Wd).float().expand(n, d)
+            assert torch.equal(torch.nan_to_num(y.cpu(), 5.0), torch.nan_to_num(ref, 5.0))
+        else:
+            ref = (Wd * S * 2.0 ** 64 * 2.0 ** 64).expand(n, d)
+            assert bool(((y.cpu().double() - ref).abs() <= 2.0 ** -20 * ref.abs()).all())
 
 
 @pytest.mark.parametrize("n,E,k", [(1, 64, 8), (30, 16, 2), (200, 70, 1)])
