@@ -86,8 +86,8 @@ gptq_status gptqs_linear_int8(const uint8_t* codes, const uint16_t* scales_f16, 
  *   y[t] = What x[t] + scaling[a] B[a] (A[a] x[t]),  a = adapter_ids[t];
  * a token whose id is outside 0 .. n_adapters - 1 (by convention -1) takes What x[t]
  * alone.  Tokens may come in any order; runs of tokens with one adapter are cheapest.
- * A x is summed in fp32; scaling A x enters the second product in fp32 (small batches) or
- * as two bfloat16 parts.  An infinite x gives infinities with the weights' signs (NaN where
+ * A x is summed in fp32 and scaling A x enters the second product in fp32, whatever the
+ * batch (in large ones as three bfloat16 parts).  An infinite x gives infinities with the weights' signs (NaN where
  * a code is its zero), for every token count where zeros are whole numbers in -240 .. 240;
  * no other token's outputs change.
  *

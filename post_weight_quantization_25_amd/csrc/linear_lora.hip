@@ -202,10 +202,12 @@ __global__ __launch_bounds__(64 * TW, NTT == 1 ? 4 : 2) void lora_tile_kernel(Lo
 }
 
 // Large batches (see stored_gemm.h).  The adapters' product is added to the finished sums on
-// the matrix cores, 32 ranks at a time: s_a v as two bfloat16 parts (v is fp32; together
-// they keep it to 2^-17) with B's rows, bfloat16 as they are, fp16 as two exact bfloat16
-// parts (fp16's 11 bits and its range fit), for each distinct adapter among the wave's
-// tokens, into the rows of the tokens that have it.
+// the matrix cores, 32 ranks at a time: s_a v as its three bfloat16 parts (bf16_parts) with
+// B's rows, bfloat16 as they are, fp16 as two exact bfloat16 parts (fp16's 11 bits and its
+// range fit; the smallest part by the smallest, below 2^-25 of a product, is left out), for
+// each distinct adapter among the wave's tokens, into the rows of the tokens that have it.
+// Sums that are not finite, where a part of 0 may have met an infinity, are taken again
+// from the whole numbers.
 template <int X, int CB, int PIECE, int BM>
 __global__ __launch_bounds__(256, 2) void lora_gemm_kernel(LoraArgs a, int gm, int gn) {
     typedef StoredGemm<X, CB, PIECE, BM, 256> G;
@@ -218,10 +220,9 @@ __global__ __launch_bounds__(256, 2) void lora_gemm_kernel(LoraArgs a, int gm, i
 
     if (a.rank) {
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15, q = lane >> 4;
-        // the tile's scaled v for 32 ranks, as bfloat16 hi and lo: [token][rank], in the slabs' place
-        __bf16* vh = reinterpret_cast<__bf16*>(lds);
-        __bf16* vl = vh + BM * 32;
-        int* ids = reinterpret_cast<int*>(vl + BM * 32);
+        // the tile's scaled v for 32 ranks, by bfloat16 part: [part][token][rank], in the slabs' place
+        uint16_t* vp = reinterpret_cast<uint16_t*>(lds);
+        int* ids = reinterpret_cast<int*>(vp + 3 * BM * 32);
         __syncthreads();                                       // the last slab is read
         for (int m = threadIdx.x; m < BM; m += 256) ids[m] = adapter_of(a, tok0 + m);
         for (int k0 = 0; k0 < a.rank; k0 += 32) {
@@ -233,16 +234,19 @@ __global__ __launch_bounds__(256, 2) void lora_gemm_kernel(LoraArgs a, int gm, i
                     for (int p = 0; p < a.splits; ++p) v += a.v[((int64_t)p * a.n + tok0 + m) * a.rank + k];
                     if (a.scaling) v *= a.scaling[ad];
                 }
-                const __bf16 h = (__bf16)v;
-                vh[e] = h;
-                vl[e] = (__bf16)(v - (float)h);
+                uint16_t part[3];
+                bf16_parts(v, part);
+#pragma unroll
+                for (int j = 0; j < 3; ++j) vp[j * BM * 32 + e] = part[j];
             }
             __syncthreads();
 #pragma unroll 1
             for (int mt = 0; mt < G::MT; ++mt) {
                 const int id = ids[16 * mt + n16];
-                const u32x4_t ah = *reinterpret_cast<const u32x4_t*>(vh + (16 * mt + n16) * 32 + 8 * q);
-                const u32x4_t al = *reinterpret_cast<const u32x4_t*>(vl + (16 * mt + n16) * 32 + 8 * q);
+                u32x4_t av[3];
+#pragma unroll
+                for (int j = 0; j < 3; ++j)
+                    av[j] = *reinterpret_cast<const u32x4_t*>(vp + j * BM * 32 + (16 * mt + n16) * 32 + 8 * q);
                 f32x4_t sum[G::NT];
 #pragma unroll
                 for (int nt = 0; nt < G::NT; ++nt) sum[nt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -266,23 +270,43 @@ __global__ __launch_bounds__(256, 2) void lora_gemm_kernel(LoraArgs a, int gm, i
                         if constexpr (X == X_BF16) {
                             u32x4_t bb;
                             __builtin_memcpy(&bb, w, 16);
-                            c = mfma16<X_BF16>(ah, bb, c);
-                            c = mfma16<X_BF16>(al, bb, c);
+#pragma unroll
+                            for (int j = 2; j >= 0; --j) c = mfma16<X_BF16>(av[j], bb, c);
                         } else {
                             bf16x8_t bh, bl;
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
                                 const float f = f16_bits_to_f32(w[e]);
                                 bh[e] = (__bf16)f;
-                                bl[e] = (__bf16)(f - (float)bh[e]);
+                                bl[e] = (__bf16)(f - (float)bh[e]);   // (an infinity's: NaN, see lost)
                             }
                             const u32x4_t b0 = __builtin_bit_cast(u32x4_t, bh), b1 = __builtin_bit_cast(u32x4_t, bl);
-                            c = mfma16<X_BF16>(ah, b0, c);
-                            c = mfma16<X_BF16>(ah, b1, c);
-                            c = mfma16<X_BF16>(al, b0, c);
-                            c = mfma16<X_BF16>(al, b1, c);
+                            c = mfma16<X_BF16>(av[2], b0, c);
+                            c = mfma16<X_BF16>(av[1], b1, c);
+                            c = mfma16<X_BF16>(av[1], b0, c);
+                            c = mfma16<X_BF16>(av[0], b1, c);
+                            c = mfma16<X_BF16>(av[0], b0, c);
                         }
                         settle(c);
+                        bool lost = false;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) lost = lost || !(fabsf(c[i]) < INFINITY);
+                        if (__ballot(lost) != 0) {             // wave-uniform, rare
+                            f32x4_t again = {0.f, 0.f, 0.f, 0.f};
+                            const int kn = a.rank - k0 < 32 ? a.rank - k0 : 32;
+#pragma unroll 1
+                            for (int k = 0; k < kn; ++k) {
+                                const float bk = elem16<X>(b[k - 8 * q]);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const uint16_t* v = vp + (16 * mt + 4 * q + i) * 32 + k;
+                                    const float rest = bf16_bits_to_f32(v[BM * 32]) + bf16_bits_to_f32(v[2 * BM * 32]);
+                                    again[i] = fmaf(bf16_bits_to_f32(v[0]) + rest, bk, again[i]);
+                                }
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) c[i] = fabsf(c[i]) < INFINITY ? c[i] : again[i];
+                        }
 #pragma unroll
                         for (int i = 0; i < 4; ++i) sum[nt][i] = all || ((mine >> (4 * q + i)) & 1) ? c[i] : sum[nt][i];
                     }

@@ -102,6 +102,73 @@ def test_lora_an_infinite_activation_gives_the_weights_signs(n, dt, bits, group)
     assert torch.equal(y2[rest], y[rest]) and bool(torch.isfinite(y).all())
 
 
+@pytest.mark.parametrize("n", [1, 5, 40, 300, 7100])
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_lora_infinite_parts_of_an_adapter(n, dt):
+    """An infinity in B, or in v = A x, times the finite others: y is infinite with the sign
+    of the product, and NaN where an infinity meets a zero, whatever kernel the batch takes."""
+    import post_weight_quantization_25_amd as g
+    d_row, d_col, m, rank = 150, 384, 2, 16
+    q, _ = stored(d_row, d_col, 4, 128, 5)
+    gen = torch.Generator().manual_seed(2)
+    A = (torch.randn(m, rank, d_col, generator=gen) * d_col ** -0.5).to(dt)
+    B = torch.randn(m, d_row, rank, generator=gen).to(dt)
+    x = torch.randn(n, d_col, generator=gen).to(dt)
+    ids = torch.arange(n, dtype=torch.int32) % 2
+    if dt == BF:                              # v[.][0] = 2^127 * (x_0 + x_1 + x_2 + x_3): infinite for these x
+        A[1, 0] = 0
+        A[1, 0, :4] = 2.0 ** 127
+        x[1::2, :4] = 2.0
+        B[1, 7, 0] = 0.0                      # infinity times 0
+        ref = torch.where(B[1, :, 0] == 0, float("nan"), torch.sign(B[1, :, 0].float()) * INF).expand(n // 2, d_row)
+    else:
+        B[1, 9, 3] = -INF
+        v = x[1::2].double() @ A[1, 3].double()
+        ref = torch.zeros(n // 2, d_row)
+        ref[:, 9] = torch.where(v > 0, -INF, INF).float()
+    y = g.linear_lora(q, x.cuda(), A.cuda(), B.cuda(), ids.cuda()).cpu()
+    assert bool(torch.isfinite(y[::2]).all())
+    bad = ~torch.isfinite(ref)
+    got = y[1::2]
+    assert torch.equal(~torch.isfinite(got), bad)
+    assert torch.equal(torch.nan_to_num(got[bad], 5.0), torch.nan_to_num(ref[bad], 5.0))
+
+
+def whole_rows(d_row, d_col, group=32):
+    """A 4-bit layer of zeros: every code is its zero, 8."""
+    import post_weight_quantization_25_amd as g
+    return g.Quantized(torch.full((d_row, d_col // 2), 0x88, dtype=torch.uint8, device="cuda"),
+                       torch.ones(d_row, d_col // group, dtype=HF, device="cuda"),
+                       torch.full((d_row, d_col // group), 8.0, dtype=HF, device="cuda"), None, 4, group, d_col)
+
+
+@pytest.mark.parametrize("n", [8, 40, 7100])
+def test_lora_adapter_keeps_fp32_beside_a_large_batch(n):
+    """A zero projection and one rank: y = (s v) B with v one exact product.  Two roundings of
+    s v and of the last product, and additions of up to four parts of it: 6 units of 2^-23
+    (two bfloat16 parts of s v would be off by up to 2^-17).  Also just below fp32's largest
+    value, where bfloat16 has no finite number next to s v."""
+    import post_weight_quantization_25_amd as g
+    d_row, d_col, m = 300, 64, 50
+    gen = torch.Generator().manual_seed(3)
+    q = whole_rows(d_row, d_col)
+    for dt, size in ((BF, 1.0), (HF, 1.0), (BF, 2.0 ** 127 * 0.999)):
+        s = (size * (1 + torch.rand(m, generator=gen)) if size == 1.0 else size * (2 - 2.0 ** -9 * torch.rand(m, generator=gen)))
+        A, x = torch.zeros(m, 1, d_col), torch.zeros(n, d_col)
+        A[:, :, 5] = 1 + (torch.rand(m, 1, generator=gen) if size == 1.0 else 0.0)
+        x[:, 5] = 1 + (torch.rand(n, generator=gen) if size == 1.0 else 0.0)
+        A, x = A.to(dt), x.to(dt)
+        B = (torch.randn(m, d_row, 1, generator=gen) * 2.0 ** -10).to(dt)
+        s = s.float()
+        ids = torch.randint(0, m, (n,), generator=gen, dtype=torch.int32)
+        at = ids.long()
+        ref = (s[at].double() * x[:, 5].double() * A[at, 0, 5].double())[:, None] * B[at, :, 0].double()
+        y = g.linear_lora(q, x.cuda(), A.cuda(), B.cuda(), ids.cuda(), s.cuda()).cpu().double()
+        rel = ((y - ref).abs() / ref.abs().clamp_min(1e-300)).max()
+        log(f"  {dt} size {size:.1e}: max rel {float(rel):.2e}")
+        assert bool(((y - ref).abs() <= 6 * 2.0 ** -23 * ref.abs()).all())
+
+
 def one_column_experts(E, d, f, bits, gate, up):
     """The up layer of experts whose gate and up rows see x's column 0 alone, with these scales."""
     import post_weight_quantization_25_amd as g
