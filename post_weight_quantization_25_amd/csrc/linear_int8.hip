@@ -109,16 +109,8 @@ static void launch_tiles(const Int8Args& a, hipStream_t s) {
 
 template <int CB, int RUN, int PIECE>
 static gptq_status launch(const Int8Args& a, hipStream_t s) {
-    // Rules by size, both sides measured (int4 g128, us, replayed):
-    //  - the two kernels meet at about 2^21 outputs.  Rows x columns, tokens: tiles / LDS kernel:
-    //    4096 x 4096, 384: 26.3 / 29.4, 512: 33.9 / 30.1; 11008 x 4096, 128: 27.0 / 29.7, 192:
-    //    42.4 / 40.2; 4096 x 11008, 384: 60.7 / 72.2, 512: 78.7 / 73.9; 2048 x 1408, 768: 15.5 /
-    //    17.5, 1024: 19.5 / 17.6.
-    //  - 128 tokens per workgroup once that leaves more than 320 of them; 4096 columns, rows and
-    //    tokens (workgroups): 64 / 128: 4096, 1024 (256): 42.1 / 43.1, 1536 (384): 63.8 / 60.5,
-    //    2048 (512): 80.5 / 62.9; 11008, 320 (258): 41.7 / 57.5, 512 (344): 63.1 / 60.2.
-    if (a.n * a.d_row >= ((int64_t)1 << 21) && gemm_fits(a.L.d_col, a.ldx)) {
-        if ((a.n + 127) / 128 * ((a.d_row + 127) / 128) > 320) launch_gemm<CB, PIECE, 128>(a, s);
+    if (const int per = int8_kernel(a.n, a.d_row, a.L.d_col, a.ldx)) {
+        if (per == 128) launch_gemm<CB, PIECE, 128>(a, s);
         else launch_gemm<CB, PIECE, 64>(a, s);
         GPTQ_LAUNCH_CHECK();
         return GPTQ_OK;

@@ -333,17 +333,8 @@ static void launch_gemm(const LoraArgs& a, hipStream_t s) {
 
 template <int X, int CB, int RUN, int PIECE>
 static gptq_status launch(const LoraArgs& a, hipStream_t s) {
-    // Rules by size, both sides measured (int4 g128, bf16, rank 16, us, replayed):
-    //  - the two kernels meet at about 2^20 outputs.  Rows x columns, tokens: tiles / LDS kernel:
-    //    4096 x 4096, 256: 61.5 / 67.2, 320: 78.0 / 63.4; 11008 x 4096, 64: 44.5 / 63, 96: 77.3 /
-    //    62.9; 4096 x 11008, 256: 137 / 165, 320: 170 / 157; 2048 x 1408, 384: 27.6 / 31.0, 512:
-    //    35.0 / 32.2.
-    //  - 128 tokens per workgroup once that leaves more than 320 of them; 4096 columns, rows and
-    //    tokens (workgroups): 64 / 128: 4096, 1024 (256): 78 / 112, 1536 (384): 130 / 114, 2048
-    //    (512): 135 / 111; 11008, 512 (344): 136 / 117, 2048 (1376): 356 / 307.  Where the last
-    //    round of workgroups is nearly empty it can lose 5% (11008, 1024 (688): 213 / 222).
-    if (a.n * a.d_row > ((int64_t)1 << 20) && gemm_fits(a.L.d_col, 2 * a.ldx)) {
-        if ((a.n + 127) / 128 * ((a.d_row + 127) / 128) > 320) launch_gemm<X, CB, PIECE, 128>(a, s);
+    if (const int per = lora_kernel(a.n, a.d_row, a.L.d_col, 2 * a.ldx, PIECE)) {
+        if (per == 128) launch_gemm<X, CB, PIECE, 128>(a, s);
         else launch_gemm<X, CB, PIECE, 64>(a, s);
         GPTQ_LAUNCH_CHECK();
         return GPTQ_OK;

@@ -251,3 +251,32 @@ def test_moe_inner_values_keep_fp32_for_fp32_outputs(n, E, k, bits):
     units = (20 + 2 * k) * 2.0 ** -23
     log(f"  n={n} E={E} k={k} bits={bits}: max rel {float(((y.double() - ref).abs() / ref).max()):.2e} of {units:.2e}")
     assert bool(((y.double() - ref).abs() <= units * ref).all())
+
+
+@pytest.mark.parametrize("d_row,n,group,bits", [(65536, 20, 128, 4), (131075, 9, 32, 3), (40000, 33, 64, 4), (70001, 64, 0, 8)])
+def test_few_tokens_of_a_wide_layer(d_row, n, group, bits):
+    """A vocabulary's rows with few tokens: every output of both products, within (3 pieces + 12)
+    roundings (8-bit rows) and (d_col + 64) 2^-23 (16-bit rows) of what they add up."""
+    import post_weight_quantization_25_amd as g
+    from serving_helpers import zero_parts
+    d_col = 256
+    q, What = stored(d_row, d_col, bits, group, 3)
+    gen = torch.Generator().manual_seed(n)
+    xq = torch.randint(-128, 128, (n, d_col), generator=gen, dtype=torch.int8)
+    xs = torch.rand(n, generator=gen) * 0.1 + 0.001
+    x = xq.double() * xs.double()[:, None]
+    y = g.linear_int8(q, g.Int8Rows(xq.cuda(), xs.cuda())).cpu().double()
+    bound = (3 * d_col // 32 + 12) * 2.0 ** -24 * (1 + 2.0 ** -10) * zero_parts(q, x, eight=True)
+    assert bool(((y - x @ What.t()).abs() <= bound).all())
+    x = torch.randn(n, d_col, generator=gen).to(BF)
+    A = (torch.randn(3, 16, d_col, generator=gen) * d_col ** -0.5).to(BF)
+    B = torch.randn(3, d_row, 16, generator=gen).to(BF)
+    ids = torch.randint(-1, 3, (n,), generator=gen, dtype=torch.int32)
+    y = g.linear_lora(q, x.cuda(), A.cuda(), B.cuda(), ids.cuda()).cpu().double()
+    xd = x.double()
+    ref, bound = xd @ What.t(), (d_col + 64) * 2.0 ** -23 * zero_parts(q, xd)
+    for a in range(3):
+        t = torch.nonzero(ids == a)[:, 0]
+        ref[t] += (xd[t] @ A[a].double().t()) @ B[a].double().t()
+        bound[t] += (d_col + 16 + 72) * 2.0 ** -23 * ((xd[t].abs() @ A[a].double().abs().t()) @ B[a].double().abs().t())
+    assert bool(((y - ref).abs() <= bound * (1 + 2.0 ** -10)).all())

@@ -27,3 +27,32 @@ def test_rows_that_large_batch_tiles_take(tmp_path):
     assert longest == 2 ** 17 - 1
     holds(tmp_path, f"gemm_fits({longest}, {longest})", f"!gemm_fits({longest + 1}, {longest + 1})",
           "gemm_fits(4096, 1 << 24)", "!gemm_fits(4096, (1 << 24) + 1)")
+
+
+def test_few_tokens_of_a_wide_layer(tmp_path):
+    """A workgroup never multiplies 128 tokens where at most 64 exist, however wide the layer,
+    and a batch meets the large-batch kernel where it was measured to."""
+    wide = (32768, 40960, 41088, 65536, 128256, 131072, 262144)
+    no128 = [f"{f} != 128" for r in wide for n in (1, 9, 16, 17, 32, 48, 64)
+             for f in (f"int8_kernel({n}, {r}, 4096, 4096)", f"lora_kernel({n}, {r}, 4096, 8192, 128)",
+                       f"lora_kernel({n}, {r}, 4096, 8192, 32)")]
+    holds(tmp_path, *no128)
+
+    def int8(r, n):
+        return f"int8_kernel({n}, {r}, 4096, 4096)"
+
+    def lora(r, n, group=128):
+        return f"lora_kernel({n}, {r}, 4096, 8192, {group})"
+    holds(tmp_path, int8(4096, 384) + " == TILES", int8(4096, 512) + " == 64", int8(4096, 2048) + " == 128",
+          int8(32768, 48) + " == TILES", int8(32768, 64) + " == 64", int8(65536, 8) + " == TILES",
+          int8(65536, 16) + " == 64", int8(131072, 1) + " == TILES", int8(131072, 9) + " == 64",
+          int8(131072, 96) + " == 128",
+          lora(4096, 256) + " == TILES", lora(4096, 320) + " == 64", lora(4096, 2048) + " == 128",
+          lora(16384, 64) + " == TILES", lora(16384, 96) + " == 64", lora(32768, 8) + " == TILES",
+          lora(32768, 17) + " == 64", lora(131072, 2) + " == TILES", lora(131072, 9) + " == 64",
+          lora(131072, 96) + " == 128",
+          lora(4096, 96, 32) + " == TILES", lora(4096, 128, 32) + " == 64", lora(11008, 48, 32) + " == TILES",
+          lora(11008, 64, 32) + " == 64")
+    # rows too long, or too far apart, for the large-batch kernel's offsets
+    holds(tmp_path, "int8_kernel(4096, 4096, 1 << 17, 1 << 17) == TILES",
+          "lora_kernel(4096, 4096, 4096, (1 << 24) + 2, 128) == TILES")
