@@ -99,7 +99,8 @@ gptq_status gptqs_linear_int8(const uint8_t* codes, const uint16_t* scales_f16, 
  *  scaling      n_adapters fp32, or NULL for 1
  *  y            n_tokens x d_row, pitch d_row, dtype y_dtype
  *  ws           at least gptqs_linear_lora_workspace_size(n_tokens, d_col, rank) bytes,
- *               4-byte aligned; contents on entry are ignored
+ *               4-byte aligned; contents on entry are ignored.  The size does not fall as
+ *               n_tokens grows: one workspace for the largest batch serves all smaller ones.
  * Errors: as gptqs_linear_int8; x_dtype GPTQ_F32 -> GPTQ_ERR_UNSUPPORTED; rank outside
  * 1 .. 256 or n_adapters < 0 -> GPTQ_ERR_INVALID_ARG; a missing, misaligned or short
  * workspace -> GPTQ_ERR_WORKSPACE.  n_adapters == 0: A, B and ws may be NULL.

@@ -366,15 +366,23 @@ static gptq_status launch_bits(const LoraArgs& a, int bits, int group, hipStream
 }
 
 // Shares of the columns: enough workgroups to fill the device, none below 512 columns.
+static int64_t most_splits(int64_t d_col) {
+    const int64_t most = (d_col + SHARE - 1) / SHARE;
+    return most < 64 ? most : 64;
+}
 static int lora_splits(int64_t n, int64_t d_col, int rank) {
-    const int64_t tiles = (n + 15) / 16 * ((rank + 15) / 16), most = (d_col + SHARE - 1) / SHARE;
+    const int64_t tiles = (n + 15) / 16 * ((rank + 15) / 16), most = most_splits(d_col);
     const int64_t want = (512 + tiles - 1) / tiles;
-    const int64_t s = want < most ? want : most;
-    return (int)(s < 1 ? 1 : s < 64 ? s : 64);
+    return (int)(want < most ? want : most);
 }
 
+// n lora_splits(n) rows fall where a split less is taken, and a workspace made for the
+// largest batch has to do for every smaller one: so the size is of a bound that only grows
+// with n.  With R = ceil(rank / 16) there are at least n R / 16 tiles, so splits <= 511 / (n R
+// / 16) + 1 and n splits <= 8176 / R + n.
 size_t lora_ws_bytes(int64_t n, int64_t d_col, int rank) {
-    return (size_t)lora_splits(n, d_col, rank) * (size_t)n * (size_t)rank * sizeof(float);
+    const int64_t all = n * most_splits(d_col), some = 8176 / ((rank + 15) / 16) + n;
+    return (size_t)(all < some ? all : some) * (size_t)rank * sizeof(float);
 }
 
 gptq_status linear_lora_launch(const uint8_t* codes, const uint16_t* scales, const uint16_t* zeros, int64_t d_row,
