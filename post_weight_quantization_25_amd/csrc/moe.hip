@@ -148,14 +148,14 @@ __global__ __launch_bounds__(256) void moe_topk_kernel(MoeArgs a) {
 
 // The plan: the chosen experts in rising order, and the pairs (token, choice) sorted by
 // expert, in token order within one.  plan: [0] experts in use, [1 + 2 s] the s-th of them,
-// [2 + 2 s] where its pairs begin (and one more: where they end), from PAIRS on the pairs.
-constexpr int PAIRS = 2 + 2 * MAXE;
+// [2 + 2 s] where its pairs begin (the last one's end with the pairs), from PAIRS on the pairs.
+constexpr int PAIRS = 1 + 2 * MAXE;
 constexpr int PLAN_W = 16;
 
 // TOPK: the same workgroup chooses first (few tokens: one launch less).
 template <bool TOPK>
 __global__ __launch_bounds__(64 * PLAN_W) void moe_plan_kernel(MoeArgs a) {
-    __shared__ int count[MAXE], start[MAXE], slot[MAXE];
+    __shared__ int count[MAXE], start[MAXE];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, pairs = a.n * a.k;
     if (TOPK) {
         for (int t = wave; t < a.n; t += PLAN_W) topk_of(a, t);
@@ -182,11 +182,10 @@ __global__ __launch_bounds__(64 * PLAN_W) void moe_plan_kernel(MoeArgs a) {
         for (int i = 0; i < EPL; ++i) {
             const int e = EPL * lane + i;
             start[e] = at;
-            slot[e] = us;
             if (c[i]) { a.plan[1 + 2 * us] = e; a.plan[2 + 2 * us] = at; ++us; }
             at += c[i];
         }
-        if (lane == 0) { a.plan[0] = total; a.plan[2 + 2 * total] = pairs; }
+        if (lane == 0) a.plan[0] = total;
     }
     __syncthreads();
     // each expert's pairs, a wave per expert; experts are few, pairs at most 8192
@@ -410,7 +409,7 @@ static MoeWs moe_ws(int64_t n, int64_t d, int64_t f, int E, int k) {
     w.inner = up16((size_t)n * E * sizeof(float));
     w.part = w.inner + 3 * inner;
     w.plan = w.part + up16((size_t)n * k * (size_t)d * sizeof(float));
-    w.end = w.plan + up16((size_t)(PAIRS + 1 + n * k) * sizeof(int32_t));
+    w.end = w.plan + up16((size_t)(PAIRS + n * k) * sizeof(int32_t));
     return w;
 }
 

@@ -253,6 +253,26 @@ def test_moe_inner_values_keep_fp32_for_fp32_outputs(n, E, k, bits):
     assert bool(((y.double() - ref).abs() <= units * ref).all())
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+def test_moe_every_expert_of_512(bits):
+    """All 512 experts in use, the most a plan holds: each token's router row is its choices'."""
+    import post_weight_quantization_25_amd as g
+    n, d, f, E, k = 256, 256, 32, 512, 32
+    up, _ = stored(E * 2 * f, d, bits, 32, 1)
+    down, _ = stored(E * d, f, bits, 32, 2)
+    gen = torch.Generator().manual_seed(4)
+    x = torch.eye(n, d).to(BF)                       # token t's logits: router[:, t]
+    router = torch.zeros(E, d)
+    want = torch.stack([(torch.arange(k) * 16 + t) % E for t in range(n)])      # token t: experts t, t + 16, ..
+    for t in range(n):
+        router[want[t], t] = torch.arange(k, 0, -1).float() / 8
+    y, ids, w = g.moe(x.cuda(), router.to(BF).cuda(), up, down, k)
+    assert torch.equal(ids.cpu().long(), want) and len(set(ids.reshape(-1).tolist())) == E
+    one = [g.moe(x[t:t + 1].cuda(), router.to(BF).cuda(), up, down, k) for t in (0, 100, 255)]
+    for t, (y1, i1, w1) in zip((0, 100, 255), one):  # a token's outputs do not depend on the others'
+        assert torch.equal(y1[0], y[t]) and torch.equal(i1[0], ids[t]) and torch.equal(w1[0], w[t])
+
+
 @pytest.mark.parametrize("d_row,n,group,bits", [(65536, 20, 128, 4), (131075, 9, 32, 3), (40000, 33, 64, 4), (70001, 64, 0, 8)])
 def test_few_tokens_of_a_wide_layer(d_row, n, group, bits):
     """A vocabulary's rows with few tokens: every output of both products, within (3 pieces + 12)
