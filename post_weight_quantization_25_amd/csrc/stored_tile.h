@@ -164,6 +164,15 @@ GPTQ_DEV constexpr uint32_t ones_word() { return X == X_I8 ? 0x01010101u : X == 
 template <typename V>
 GPTQ_DEV void settle(V& v) { asm volatile("s_nop 7\n\ts_nop 7" : "+v"(v)); }
 
+// Orders LDS accesses before it, by any lane of the wave, with those after it: a release and
+// an acquire at the wave's scope.  A wave's LDS operations execute in order, so neither costs
+// an instruction; they keep the compiler from moving or forwarding accesses across.
+GPTQ_DEV void lds_handover() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // ---- activations of RUN columns
 template <int X, int RUN>
 struct XRun { uint32_t w[RUN * xbytes<X>() / 4]; };
@@ -315,14 +324,12 @@ struct Chunk {
         auto at = [&](int r, int piece) { return xr.stage + (r * PPR + (piece ^ (r & (PPR - 1)))) * 16; };
 #pragma unroll
         for (int tt = 0; tt < NTT; ++tt) {
-            // the wave's own memory, and its LDS operations keep their order: only the compiler
-            // is held back
-            __builtin_amdgcn_wave_barrier();
+            lds_handover();                                 // the last tile is read
 #pragma unroll
             for (int k = 0; k < XL; ++k)
                 *reinterpret_cast<u32x4_t*>(at((64 * k + lane) / PPR, (64 * k + lane) % PPR)) =
                     u32x4_t{x_word(tt, 4 * k), x_word(tt, 4 * k + 1), x_word(tt, 4 * k + 2), x_word(tt, 4 * k + 3)};
-            __builtin_amdgcn_wave_barrier();
+            lds_handover();
 #pragma unroll
             for (int p = 0; p < P; ++p) {
                 const int byte = p * 4 * B + q * B;
@@ -338,7 +345,7 @@ struct Chunk {
                 }
             }
         }
-        __builtin_amdgcn_wave_barrier();
+        lds_handover();
     }
 
     // lane (row n, group q) takes the codes that lane 4 n + q loaded
