@@ -83,6 +83,7 @@ __global__ __launch_bounds__(64 * SW) void lora_shrink_kernel(LoraArgs a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) cs = mfma16<X>(xf[e], af[e], cs);
         }
+        settle(cs);                                              // products end behind the loop's branch
 #pragma unroll
         for (int i = 0; i < 4; ++i) out[i] = (mine >> (4 * q + i)) & 1 ? cs[i] : out[i];
     }

@@ -66,6 +66,7 @@ __global__ __launch_bounds__(64 * LOGW) void moe_logits_kernel(MoeArgs a) {
             cs = mfma16<X>(u32x4_t{xr.w[4 * s], xr.w[4 * s + 1], xr.w[4 * s + 2], xr.w[4 * s + 3]},
                            u32x4_t{rr.w[4 * s], rr.w[4 * s + 1], rr.w[4 * s + 2], rr.w[4 * s + 3]}, cs);
     }
+    settle(cs);                                             // products end behind the loop's branch
 #pragma unroll
     for (int i = 0; i < 4; ++i) red[wave][i][lane] = cs[i];
     __syncthreads();
