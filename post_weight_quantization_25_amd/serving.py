@@ -115,6 +115,8 @@ def rmsnorm_int8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor |
         else:
             ldq = _rows(out.q, "out.q", torch.int8, shape, dev)
             _tensor(out.scale, "out.scale", torch.float32, (n,), dev)
+        if d == 0:
+            out.scale.fill_(1.0)     # the library leaves rows of no columns alone
         _check(lib.gptqs_rmsnorm_int8(
             x.data_ptr(), _DT[dt], ldx, None if residual is None else residual.data_ptr(), ldr, weight.data_ptr(),
             _DT[weight.dtype], eps, n, d, None if residual_out is None else residual_out.data_ptr(), ldo,
@@ -160,6 +162,8 @@ def linear_int8(q: Quantized, x: Int8Rows, out_dtype=torch.float32, out: torch.T
     d_row = _stored(q, "q", dev)
     with _On(dev, stream) as s:
         out = _out(out, n, d_row, out_dtype, dev)
+        if d_col == 0:
+            out.zero_()              # a sum of nothing; the library leaves it alone
         _check(lib.gptqs_linear_int8(q.codes.data_ptr(), q.scales.data_ptr(), q.zeros.data_ptr(), d_row, d_col, q.bits,
                                      q.group_size, x.q.data_ptr(), ldx, x.scale.data_ptr(), n, out.data_ptr(),
                                      _DT[out.dtype], s), "gptqs_linear_int8")
@@ -193,6 +197,8 @@ def linear_lora(q: Quantized, x: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
         _tensor(scaling, "scaling", torch.float32, (m,), dev)
     with _On(dev, stream) as s:
         out = _out(out, n, d_row, out_dtype, dev)
+        if d_col == 0:
+            out.zero_()              # a sum of nothing; the library leaves it alone
         ws = _workspace(linear_lora_workspace_size(n, d_col, rank) if m else 0, dev, ws)
         _check(lib.gptqs_linear_lora(q.codes.data_ptr(), q.scales.data_ptr(), q.zeros.data_ptr(), d_row, d_col, q.bits,
                                      q.group_size, x.data_ptr(), _DT[dt], n, ldx, A.data_ptr(), B.data_ptr(), m, rank,

@@ -273,6 +273,24 @@ def test_moe_every_expert_of_512(bits):
         assert torch.equal(y1[0], y[t]) and torch.equal(i1[0], ids[t]) and torch.equal(w1[0], w[t])
 
 
+def test_rows_of_no_columns():
+    """A product over no columns is 0, the norm of a row of none has no codes and the scale of
+    a row of zeros; buffers given by the caller are written."""
+    import post_weight_quantization_25_amd as g
+    q = g.Quantized(torch.empty(5, 0, dtype=torch.uint8, device="cuda"), torch.ones(5, 1, dtype=HF, device="cuda"),
+                    torch.zeros(5, 1, dtype=HF, device="cuda"), None, 8, 0, 0)
+    out = torch.full((3, 5), 7.0, device="cuda")
+    rows = g.Int8Rows(torch.empty(3, 0, dtype=torch.int8, device="cuda"), torch.ones(3, device="cuda"))
+    assert not bool(g.linear_int8(q, rows, out=out).any())
+    out.fill_(7.0)
+    x = torch.empty(3, 0, dtype=BF, device="cuda")
+    A, B = torch.ones(2, 4, 0, dtype=BF, device="cuda"), torch.ones(2, 5, 4, dtype=BF, device="cuda")
+    assert not bool(g.linear_lora(q, x, A, B, torch.zeros(3, dtype=torch.int32, device="cuda"), out=out).any())
+    scale = torch.full((3,), 7.0, device="cuda")
+    got, h = g.rmsnorm_int8(x, torch.empty(0, dtype=BF, device="cuda"), out=g.Int8Rows(rows.q, scale))
+    assert bool((scale == 1).all()) and h is x and got.scale is scale
+
+
 @pytest.mark.parametrize("d_row,n,group,bits", [(65536, 20, 128, 4), (131075, 9, 32, 3), (40000, 33, 64, 4), (70001, 64, 0, 8)])
 def test_few_tokens_of_a_wide_layer(d_row, n, group, bits):
     """A vocabulary's rows with few tokens: every output of both products, within (3 pieces + 12)
