@@ -505,18 +505,21 @@ GPTQ_DEV float wave_sum(const Stored& L, int64_t r, F&& x8) {
     asm volatile("" : "+v"(lane));             // addresses are formed here, not carried through the kernel
     float s = 0.f;
 #pragma unroll 1
-    for (int64_t c = 8 * (int64_t)lane; c < L.d_col; c += 512) {
-        const int m = L.d_col - c < 8 ? (int)(L.d_col - c) : 8;
-        const uint8_t* src = L.codes + r * L.code_ld + c / 8 * CB;
-        const Raw<CB, 8> u = m == 8 ? load_raw<CB, 8>(src) : load_raw_tail<CB, 8>(src, m);
-        const int64_t at = r * L.n_groups + (L.n_groups == 1 ? 0 : c >> L.gshift);   // a group is whole steps
-        const float S = f16_bits_to_f32(L.scales[at]), z = f16_bits_to_f32(L.zeros[at]);
-        float x[8];
-        x8(c, m, x);
+    for (int64_t c0 = 0; c0 < L.d_col && __ballot(s != s) == 0; c0 += 512) {   // a NaN stays one
+        const int64_t c = c0 + 8 * lane;
+        if (c < L.d_col) {
+            const int m = L.d_col - c < 8 ? (int)(L.d_col - c) : 8;
+            const uint8_t* src = L.codes + r * L.code_ld + c / 8 * CB;
+            const Raw<CB, 8> u = m == 8 ? load_raw<CB, 8>(src) : load_raw_tail<CB, 8>(src, m);
+            const int64_t at = r * L.n_groups + (L.n_groups == 1 ? 0 : c >> L.gshift);   // a group is whole steps
+            const float S = f16_bits_to_f32(L.scales[at]), z = f16_bits_to_f32(L.zeros[at]);
+            float x[8];
+            x8(c, m, x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float w = S * ((float)((code_bytes4<CB, 8>(u, e >> 2) >> (8 * (e & 3))) & 0xFFu) - z);
-            if (e < m) s = fmaf(w, x[e], s);
+            for (int e = 0; e < 8; ++e) {
+                const float w = S * ((float)((code_bytes4<CB, 8>(u, e >> 2) >> (8 * (e & 3))) & 0xFFu) - z);
+                if (e < m) s = fmaf(w, x[e], s);
+            }
         }
     }
 #pragma unroll
