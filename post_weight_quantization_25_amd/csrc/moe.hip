@@ -79,6 +79,7 @@ __global__ __launch_bounds__(64 * LOGW) void moe_logits_kernel(MoeArgs a) {
     }
 }
 
+static_assert(MOE_MAX_EXPERTS == 512, "a plan's expert has 9 bits");
 constexpr int MAXE = 512, EPL = MAXE / 64;   // experts per lane
 
 // Maximum over the wave, in every lane's copy of lane 63 (DPP, no LDS).
@@ -153,18 +154,36 @@ __global__ __launch_bounds__(256) void moe_topk_kernel(MoeArgs a) {
 constexpr int PAIRS = 1 + 2 * MAXE;
 constexpr int PLAN_W = 16;
 
+// A stable counting sort: each wave counts its share of the pairs, a prefix over the waves and
+// one over the experts say where each wave's pairs of an expert go, and a lane's place among
+// its 64 is the number of lower lanes with its expert (ballots of the expert's 9 bits).  256
+// tokens, 32 of 512 experts: 11 us, where a walk over all pairs for each expert took 708.
+//
 // TOPK: the same workgroup chooses first (few tokens: one launch less).
 template <bool TOPK>
 __global__ __launch_bounds__(64 * PLAN_W) void moe_plan_kernel(MoeArgs a) {
-    __shared__ int count[MAXE], start[MAXE];
+    __shared__ int next[PLAN_W][MAXE], count[MAXE], start[MAXE];   // next: a wave's counts, then where its next pair goes
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, pairs = a.n * a.k;
     if (TOPK) {
         for (int t = wave; t < a.n; t += PLAN_W) topk_of(a, t);
         __threadfence_block();
     }
-    for (int e = threadIdx.x; e < MAXE; e += 64 * PLAN_W) count[e] = 0;
+    const int share = (pairs + 64 * PLAN_W - 1) / (64 * PLAN_W) * 64;                       // pairs per wave
+    const int first = wave * share, last = first + share < pairs ? first + share : pairs;
+    for (int e = threadIdx.x; e < PLAN_W * MAXE; e += 64 * PLAN_W) (&next[0][0])[e] = 0;
     __syncthreads();
-    for (int p = threadIdx.x; p < pairs; p += 64 * PLAN_W) atomicAdd(&count[a.ids[p]], 1);   // whole numbers: any order
+    for (int p = first + lane; p < last; p += 64) atomicAdd(&next[wave][a.ids[p]], 1);      // whole numbers: any order
+    __syncthreads();
+    for (int e = threadIdx.x; e < MAXE; e += 64 * PLAN_W) {
+        int c = 0;
+#pragma unroll
+        for (int w = 0; w < PLAN_W; ++w) {
+            const int mine = next[w][e];
+            next[w][e] = c;
+            c += mine;
+        }
+        count[e] = c;
+    }
     __syncthreads();
     if (wave == 0) {                                        // prefix sums over the experts, EPL per lane
         int c[EPL], mine = 0, used = 0;
@@ -189,17 +208,21 @@ __global__ __launch_bounds__(64 * PLAN_W) void moe_plan_kernel(MoeArgs a) {
         if (lane == 0) a.plan[0] = total;
     }
     __syncthreads();
-    // each expert's pairs, a wave per expert; experts are few, pairs at most 8192
-    for (int e = wave; e < a.E; e += PLAN_W) {
-        if (count[e] == 0) continue;
-        int c = start[e];
-        for (int p0 = 0; p0 < pairs; p0 += 64) {
-            const int p = p0 + lane;
-            const bool hit = p < pairs && a.ids[p] == e;
-            const uint64_t b = __ballot(hit);
-            if (hit) a.plan[PAIRS + c + __popcll(b & ((1ull << lane) - 1))] = p;
-            c += __popcll(b);
+    for (int p0 = first; p0 < last; p0 += 64) {             // wave-uniform
+        const int p = p0 + lane, e = p < last ? a.ids[p] : 0;
+        uint64_t same = __ballot(p < last);                 // the lanes with this lane's expert
+#pragma unroll
+        for (int b = 0; b < 9; ++b) {
+            const uint64_t set = __ballot((e >> b) & 1);
+            same &= (e >> b) & 1 ? set : ~set;
         }
+        const int before = next[wave][e];
+        lds_handover();                                     // all read before the last of them adds
+        if (p < last) {
+            a.plan[PAIRS + start[e] + before + __popcll(same & ((1ull << lane) - 1))] = p;
+            if (same >> lane == 1) next[wave][e] = before + __popcll(same);
+        }
+        lds_handover();
     }
 }
 
@@ -367,9 +390,10 @@ static gptq_status launch(const MoeArgs& a, hipStream_t s) {
     moe_logits_kernel<X><<<dim3((unsigned)((a.E + 15) / 16), (unsigned)((a.n + 15) / 16)), 64 * LOGW, 0, s>>>(a);
     GPTQ_LAUNCH_CHECK();
     // While each of its waves has one token at most, one workgroup chooses and plans; beyond,
-    // choosing is spread over the device first.  Whole calls, one workgroup / two launches, us:
-    // 1 token, 8, 64 and 256 experts: 28.4 / 29.5, 31.9 / 32.9, 34.2 / 35.1; 16 tokens: 30.5 /
-    // 31.3, 40.7 / 39.1, 58.5 / 57.3; 32 tokens: 32.9 / 31.8, 52.2 / 45.2, 91.6 / 84.5.
+    // choosing is spread over the device first.  Whole calls, 512 x 256 int4 g128, one workgroup /
+    // two launches, us: 1 token, 8, 64 and 256 experts: 16.4 / 17.7, 17.1 / 18.3, 17.1 / 18.2; 16
+    // tokens: 18.8 / 19.1, 23.0 / 23.2, 23.0 / 23.2; 32 tokens: 22.2 / 19.5, 30.9 / 26.7, 32.9 /
+    // 30.8.
     if (a.n <= PLAN_W) moe_plan_kernel<true><<<1, 64 * PLAN_W, 0, s>>>(a);
     else {
         moe_topk_kernel<<<(unsigned)((a.n + 3) / 4), 256, 0, s>>>(a);
