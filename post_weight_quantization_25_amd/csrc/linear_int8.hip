@@ -7,9 +7,10 @@
 // waves take the rows' 128-column chunks in turn and meet in LDS at the end.  One token,
 // 4096 x 4096 int4 g128: 5.0 us; 48 tokens x 11008 x 4096 g64: 17 us (see stored_tile.h).
 //
-// Large ones (int8_gemm_kernel, stored_gemm.h): bound by the vector unit's issue, two
-// instructions per four sums and 128 columns to scale them beside two products of the
-// matrix unit, plus the decoding.  4096 tokens x 4096 x 4096 int4 g128: 114 us, 1.2 Pop/s,
+// Large ones (int8_gemm_kernel, stored_gemm.h): bound by the vector unit's issue (58% of the
+// cycles, the matrix unit 23%), two instructions per four sums and 128 columns to scale them
+// beside two products of the matrix unit, plus the decoding; with one scale per row (51% and
+// 21%) decoding alone.  4096 tokens x 4096 x 4096 int4 g128: 114 us, 1.2 Pop/s,
 // where the library's plain int8 product reaches 2.05.
 
 #include "serving.h"

@@ -12,12 +12,14 @@
 // adapters cost no extra pass over y.  Selecting rows, rather than multiplying by zero,
 // keeps an infinity or a NaN of one adapter away from the tokens of the others.
 //
-// One token, 4096 x 4096 int4 g128, rank 16: 3.3 + 6.8 us; 40 tokens with up to 32 adapters
-// of rank 32: 6.2 + 19 us; 2048 tokens x 11008 x 4096, rank 16, runs of 450 tokens: 300 us
-// together (10 the first), 620 Tflop/s of the 1286 that the library's bf16 product on plain
-// weights reaches:
-// there the decoding to bfloat16 (a conversion, a subtraction and half a packing per code)
-// shares the vector unit with the scaling.
+// One token, 4096 x 4096 int4 g128, rank 16: 3.3 + 7.0 us; 40 tokens with up to 32 adapters
+// of rank 32: 6.3 + 19 us; 2048 tokens x 11008 x 4096, rank 16, runs of 450 tokens: 308 us
+// together (10 the first), 605 Tflop/s of the 1286 that the library's bf16 product on plain
+// weights reaches: there the decoding to bfloat16 (a conversion, a subtraction and half a
+// packing per code) shares the vector unit, 44% busy, with the scaling.  From 64 to 256
+// tokens the projection alone (gptq_quantized_linear) is faster on few rows: 256 tokens x
+// 4096 x 4096, 32 us against 66, x 4096 x 11008, 62 against 141.  It multiplies 64 rows per
+// workgroup, the tiles here 16, so the activations are read from L2 four times as often.
 
 #include "serving.h"
 #include "stored_gemm.h"

@@ -11,11 +11,13 @@
 // Sums that are not finite are taken once more as sum S (u - z) x (finite_sum in
 // stored_tile.h), in up behind its tiles and for down in moe_sum_kernel.
 // Bound by the codes of the chosen experts, which up and down read once each.  One token,
-// 8 of 64 experts of 2048 x 1408 int4: 4.2 + 5.8 + 13 + 9.4 + 3.8 us for 35 MB of codes,
-// latency of five dependent launches; 32 tokens, 2 of 16 experts of 4096 x 5504: 8.7 + 4.6
-// + 4.8 + 118 + 88 + 4.7 us (choice and plan in two launches), up at 3.1 TB/s and down at
-// 2.1 (its two-part inner values are most of its loads; 32 rows per workgroup, gathered
-// loads of them through LDS, and two chunks ahead all measured slower).  A first form in
+// 8 of 64 experts of 2048 x 1408 int4: 4.2 + 5.7 + 14 + 10.6 + 3.9 us for 35 MB of codes,
+// latency of five dependent launches; 32 tokens, 2 of 16 experts of 4096 x 5504: 8.8 + 4.5
+// + 4.8 + 121 + 89 + 4.7 us (choice and plan in two launches), up at 3.0 TB/s and down at
+// 2.0: vector unit half busy, and nothing in flight while a wave multiplies (one chunk in
+// registers); in down the inner values' parts are most of the loads (32 rows per workgroup,
+// gathered loads of them through LDS, and two chunks ahead all measured slower).  Every 16
+// tokens of an expert read its codes again: 64 tokens 261 us, 256 679.  A first form in
 // which a workgroup of down walked all experts took 494 us.  Sums run in fixed orders
 // without atomics, and a token's do not depend on the other tokens' choices.
 

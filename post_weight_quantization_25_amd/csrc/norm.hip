@@ -15,7 +15,11 @@
 // conversion and one fp64 multiply-add per element, hidden behind the loads).  8192 x 4096
 // bf16 with a residual: 52 us, 4.5 TB/s of 5.4 a copy reaches; one row of 4096: 3.8 us, a
 // launch and one round trip.  With the 64-bit path's operands kept in registers beside the
-// others (138 registers against 68) the same rows took 89 us.
+// others (138 registers against 68) the same rows took 89 us.  333 rows of 11008 take 10.9 us,
+// 5 times their bytes: 1024 threads of 70 registers are one workgroup per compute unit, so
+// the rows come in two rounds.  fp32 weights or rows go through the two passes in 64 bits:
+// 8192 x 4096 with a residual, replayed, 57 us (bf16 rows, fp32 weights) and 103 (fp32)
+// against 43.
 //
 // Threads per row by width: a wave to 512, then 256 threads with one or two vectors of 8,
 // 512 and 1024 with two, so that a row is read in one or two loads per thread.

@@ -16,14 +16,18 @@
 // from a product of the same activations with ones, so every zero is served with exact
 // operands.
 //
-// What bounds these kernels is the L1's accesses rather than bytes: a lane's 16-byte load
-// of a row of its own is one access, four neighbouring lanes reading one row are a quarter
-// each.  So codes and the activations of several tiles are loaded contiguously and handed
-// to their lanes across the wave or through LDS (48 tokens x 11008 x 4096 int4 g64, 8-bit
-// rows: 25 us with every lane loading its own, 21 with codes contiguous, 17 with both); the
-// scales and zeros of two row blocks come in one load (33 -> 26 us with the rows without
-// tokens skipped).  Loading two chunks ahead costs registers, hence workgroups, and measured
-// the same or slower.
+// No unit is busy in these kernels (48 tokens x 11008 x 4096 int4 g64, 8-bit rows: matrix unit 4%
+// of the cycles, vector unit 27%, 0.2 L1 accesses per cycle and CU; 40 tokens with adapters
+// 5%, 17%, 0.16): waves wait for their loads.  From 33 tokens on a wave has one chunk in
+// registers, so nothing is in flight while it multiplies, and two to four waves per SIMD are
+// too few to cover it.  Fewer and wider loads shorten the wait: a lane's 16-byte load of a
+// row of its own is an L1 access, four neighbouring lanes reading one row are a quarter each.
+// So codes and the activations of several tiles are loaded contiguously and handed to their
+// lanes across the wave or through LDS (the 48 tokens: 25 us with every lane loading its own,
+// 21 with codes contiguous, 17 with both); the scales and zeros of two row blocks come in one
+// load (33 -> 26 us with the rows without tokens skipped).  Whole chunks loaded two ahead cost
+// registers, hence workgroups, and measured the same or slower.  With groups of 32 (and of
+// 64, four tiles) the chunk's pieces do not fit the registers beside the sums, and spill.
 #pragma once
 #include "common.h"
 
@@ -367,7 +371,9 @@ struct Chunk {
     }
 
     // 3- and 4-bit codes with 16-bit activations enter as they are (see plain_16); the whole
-    // zero is then a rest, taken off with sum x, which all the row blocks share
+    // zero is then a rest, taken off with sum x, which all the row blocks share.  The fp32 sums
+    // of u x and z x are larger than that of (u - z) x, by up to 2.7 for uniform codes: 1.2e-7
+    // of y in the norm in place of 7e-8
     static constexpr bool PLAIN = X != X_I8 && CB != 8;
     typedef typename Acc<X>::t sum_t;
 
