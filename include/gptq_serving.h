@@ -14,7 +14,8 @@
  * anything is enqueued).  Every call can be captured into a graph.  No call uses
  * atomics on results, so equal calls give equal bits.  Calls that may overlap in time
  * must not share outputs or workspaces; graphs that share a workspace must not be
- * replayed at the same time.  Rows need no alignment; pitches are in elements.
+ * replayed at the same time.  Outputs and workspaces overlap no input and no other output,
+ * but where a call allows it.  Rows need no alignment; pitches are in elements.
  */
 #ifndef GPTQ_SERVING_MI355X_H
 #define GPTQ_SERVING_MI355X_H

@@ -140,12 +140,16 @@ def _stored(q: Quantized, name: str, device) -> int:
     return d_row
 
 
-def _out(out, n: int, d_row: int, out_dtype, device):
+def _out(out, n: int, d_row: int, out_dtype, device, x):
     if out is None:
         if out_dtype not in _DT:
             raise ValueError("out_dtype must be f32/bf16/f16")
         return torch.empty((n, d_row), dtype=out_dtype, device=device)
     _tensor(out, "out", tuple(_DT), (n, d_row), device)
+    if n and d_row and x.shape[1]:                # a workgroup writes its rows of y while others read x
+        at, xat = out.data_ptr(), x.data_ptr()
+        if at < xat + ((n - 1) * x.stride(0) + x.shape[1]) * x.itemsize and xat < at + out.nbytes:
+            raise ValueError("out overlaps x")
     return out
 
 
@@ -161,7 +165,7 @@ def linear_int8(q: Quantized, x: Int8Rows, out_dtype=torch.float32, out: torch.T
     _tensor(x.scale, "x.scale", torch.float32, (n,), dev)
     d_row = _stored(q, "q", dev)
     with _On(dev, stream) as s:
-        out = _out(out, n, d_row, out_dtype, dev)
+        out = _out(out, n, d_row, out_dtype, dev, x.q)
         if d_col == 0:
             out.zero_()              # a sum of nothing; the library leaves it alone
         _check(lib.gptqs_linear_int8(q.codes.data_ptr(), q.scales.data_ptr(), q.zeros.data_ptr(), d_row, d_col, q.bits,
@@ -196,7 +200,7 @@ def linear_lora(q: Quantized, x: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
     if scaling is not None:
         _tensor(scaling, "scaling", torch.float32, (m,), dev)
     with _On(dev, stream) as s:
-        out = _out(out, n, d_row, out_dtype, dev)
+        out = _out(out, n, d_row, out_dtype, dev, x)
         if d_col == 0:
             out.zero_()              # a sum of nothing; the library leaves it alone
         ws = _workspace(linear_lora_workspace_size(n, d_col, rank) if m else 0, dev, ws)
@@ -239,7 +243,7 @@ def moe(x: torch.Tensor, router: torch.Tensor, up: Quantized, down: Quantized, t
         raise ValueError(f"up must be {e * 2 * f} x {d} and down {e * d} x {f}, not {up_rows} x {up.d_col} and "
                          f"{down_rows} x {f}")
     with _On(dev, stream) as s:
-        out = _out(out, n, d, out_dtype, dev)
+        out = _out(out, n, d, out_dtype, dev, x)
         if ids is None:
             ids = torch.empty((n, top_k), dtype=torch.int32, device=dev)
         _tensor(ids, "ids", torch.int32, (n, top_k), dev)
