@@ -13,7 +13,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgptq.so")
 SOURCES = ["api.hip", "hessian.hip", "prep.hip", "quant.hip", "sweep.hip", "linear.hip", "layers.hip", "obq.hip",
            "serving.hip", "norm.hip", "linear_int8.hip", "linear_lora.hip",
-           "moe.hip"]
+           "moe.hip", "tuning.hip", "grouped.hip", "grouped_back.hip", "head_loss.hip"]
 ARCH = "gfx950"
 
 

@@ -1,0 +1,423 @@
+// Cross entropy and distillation at a stored head (gptqt_cross_entropy, gptqt_distill), in
+// pieces of the vocabulary:
+//   z = What x[t] / T;  loss = w T^2 sum_j p_j (log p_j - (z_j - lse z));
+//   dx[t] = w T (sum_v softmax(z)_v What_v - sum_j p_j What_j),
+// j over the token's entries (cross entropy: one, p = 1, T = 1).
+//
+// The entries' own words are kept apart from the others: with p_j near softmax(z)_j the two
+// sums above nearly cancel, so a word v that is an entry takes the weight softmax(z)_v - p_j
+// in fp32 (head_final_kernel) and only the others enter the large product.
+//
+// The vocabulary is split into spans; a round takes R spans, each with sums of its own:
+//   logits  z of the round's words, fp32 (grouped.hip)
+//   stats   per token and span: the entries' z are picked out, the maximum m and the sum of
+//           exp(z - m) over the other words added to what the span's slot has, and exp(z - m)
+//           written in fp16 (times 2^14 and the weight row's power of two)
+//   sums    O = O exp(m_old - m) + exp(z - m) What, fp32 (back_gemm.h)
+// so the logits and the softmax are formed once, and nothing of the vocabulary's length is
+// kept beyond a round.  Then head_final_kernel joins the slots.
+
+#include "back_gemm.h"
+
+namespace gptq {
+
+constexpr int SPAN = 8192;                                      // most words of a span
+constexpr int64_t CHUNK = 4096;                                 // tokens taken at a time
+constexpr int64_t ROUND = (int64_t)1 << 25;                     // most logits of a round
+
+struct HeadPlan {
+    int64_t nc;                                                 // tokens at a time
+    int spans; int64_t span;                                    // span: words, a multiple of 64
+    int R;                                                      // spans per round
+};
+
+// Spans per round: until the sums' tiles fill the device, and at most ROUND logits.
+static int64_t wanted_spans(int64_t tiles_t, int64_t d, int spans, bool grad) {
+    const int64_t tiles = tiles_t * ((d + 127) / 128), want = grad ? (512 + tiles - 1) / tiles : spans;
+    return want < spans ? want : spans;
+}
+
+static HeadPlan plan_of(int64_t nc, int64_t d, int64_t vocab, bool grad) {
+    HeadPlan p;
+    p.nc = nc;
+    const int64_t spans = (vocab + SPAN - 1) / SPAN;
+    p.span = ((vocab + spans - 1) / spans + 63) / 64 * 64;
+    p.spans = (int)((vocab + p.span - 1) / p.span);
+    const int64_t want = wanted_spans((nc + 127) / 128, d, p.spans, grad), fit = ROUND / (nc * p.span);
+    p.R = (int)(fit < 1 ? 1 : want < fit ? want : fit);
+    return p;
+}
+
+struct HeadBuffers {
+    float* z;                                                   // nc x R span
+    uint16_t* A[2];                                             // the same in fp16
+    float* O;                                                   // R x nc x d
+    float* m; float* s; float* f;                               // R x nc
+    float* picked;                                              // nc x k
+    int8_t* e;                                                  // vocab
+    int32_t* emax;                                              // of blocks of rows
+};
+constexpr int EB = 1024;                                        // rows per block of emax
+
+// rows: nc R, or a bound of it.
+static size_t layout(HeadBuffers* b, uint8_t* w, int64_t nc, int64_t rows, int64_t span, int64_t d, int64_t vocab, int k, bool grad) {
+    size_t at = 0;
+    auto take = [&](size_t bytes) { const size_t here = at; at += up256(bytes); return w ? w + here : nullptr; };
+    const size_t zs = (size_t)(rows * span);
+    HeadBuffers h;
+    h.z = (float*)take(zs * 4);
+    h.m = (float*)take((size_t)rows * 4); h.s = (float*)take((size_t)rows * 4); h.f = (float*)take((size_t)rows * 4);
+    h.picked = (float*)take((size_t)(nc * k) * 4);
+    h.A[0] = h.A[1] = nullptr; h.O = nullptr; h.e = nullptr; h.emax = nullptr;
+    if (grad) {
+        h.A[0] = (uint16_t*)take(zs * 2);
+        h.A[1] = (uint16_t*)take(zs * 2);
+        h.O = (float*)take((size_t)(rows * d) * 4);
+        h.e = (int8_t*)take((size_t)vocab);
+        h.emax = (int32_t*)take((size_t)((vocab + EB - 1) / EB) * 4);
+    }
+    if (b) *b = h;
+    return at;
+}
+
+// A larger batch takes fewer spans per round, and a workspace made for the largest batch has to
+// do for every smaller one: so the size is of the most rows that any batch up to n has.  With T
+// tiles of tokens a batch of nc <= 128 T has nc min(wanted, ROUND / (nc span)) rows at most.
+size_t head_ws_bytes(int64_t n, int64_t d, int64_t vocab, int k, bool grad) {
+    const int64_t nc = n < CHUNK ? n : CHUNK;
+    const HeadPlan p = plan_of(nc, d, vocab, grad);
+    int64_t rows = 0;
+    for (int64_t T = 1; T <= (nc + 127) / 128; ++T) {
+        const int64_t most = 128 * T < nc ? 128 * T : nc, want = most * wanted_spans(T, d, p.spans, grad);
+        const int64_t fit = ROUND / p.span > most ? ROUND / p.span : most, r = want < fit ? want : fit;
+        rows = r > rows ? r : rows;
+    }
+    return layout(nullptr, nullptr, nc, rows, p.span, d, vocab, k, grad);
+}
+
+__global__ __launch_bounds__(256) void head_emax_kernel(const int8_t* e, int64_t vocab, int32_t* emax) {
+    __shared__ int red[4];
+    int m = -1000;
+    for (int i = threadIdx.x; i < EB; i += 256) {
+        const int64_t r = (int64_t)blockIdx.x * EB + i;
+        if (r < vocab) m = e[r] > m ? e[r] : m;
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) {
+        const int v = __shfl_xor(m, o);
+        m = v > m ? v : m;
+    }
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 4; ++w) m = red[w] > m ? red[w] : m;
+        emax[blockIdx.x] = m;
+    }
+}
+
+// Over the workgroup of 256, in a fixed order; every thread gets it.
+template <typename V, typename F>
+GPTQ_DEV V over_block(V v, F&& f, V* red) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) v = f(v, __shfl_xor(v, o));
+    __syncthreads();                                             // the last use of red is over
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return f(f(red[0], red[1]), f(red[2], red[3]));
+}
+
+GPTQ_DEV int emax_of(const int32_t* emax, int blocks, int* red) {
+    int m = -1000;
+    for (int i = threadIdx.x; i < blocks; i += 256) m = emax[i] > m ? emax[i] : m;
+    return over_block(m, [](int a, int b) { return a > b ? a : b; }, red);
+}
+
+struct HeadArgs {
+    int64_t n, tok0, vocab, d;                                  // n tokens from tok0 on
+    int k; const int32_t* ids;                                  // all tokens'
+    const void* top; gptq_dtype topt;
+    float T;
+    const float* weights;
+    HeadBuffers b;
+    int R, round, slots; int64_t span;                          // slots: spans of this round; of all, in head_final_kernel
+    int blocks;                                                 // of emax
+    Stored L;
+    float* loss; void* dx; gptq_dtype dxt;                      // all tokens'
+};
+
+GPTQ_DEV bool entry_there(const HeadArgs& a, int64_t t, int j, int& id) {
+    id = a.ids[(a.tok0 + t) * a.k + j];
+    return id >= 0 && id < a.vocab;
+}
+GPTQ_DEV float weight_of(const HeadArgs& a, int64_t t) { return a.weights ? a.weights[a.tok0 + t] : 1.f; }
+
+template <int PA>                                               // fp16 parts of exp(z - m); 0: no gradient
+__global__ __launch_bounds__(256) void head_stats_kernel(HeadArgs a) {
+    __shared__ uint32_t flag[SPAN / 32];
+    __shared__ float red[4];
+    __shared__ int redi[4];
+    const int tid = threadIdx.x, slot = blockIdx.y;
+    const int64_t t = blockIdx.x;
+    const int64_t v0 = ((int64_t)a.round * a.R + slot) * a.span;
+    const int words = (int)(a.vocab - v0 < a.span ? a.vocab - v0 : a.span);
+    const int64_t ldz = a.R * a.span;
+    const float* z = a.b.z + t * ldz + slot * a.span;
+    const float invT = 1.f / a.T;
+    flag[tid] = 0;
+    __syncthreads();
+    int live = 0;
+    for (int j = tid; j < a.k; j += 256) {
+        int id;
+        if (!entry_there(a, t, j, id)) continue;
+        live = 1;
+        const int64_t w = id - v0;
+        if (w < 0 || w >= words) continue;
+        atomicOr(&flag[w >> 5], 1u << (w & 31));
+        a.b.picked[t * a.k + j] = z[w] * invT;
+    }
+    live = over_block(live, [](int x, int y) { return x | y; }, redi);
+    if (weight_of(a, t) == 0.f) live = 0;
+    // thread tid's words: 4 tid .. 4 tid + 3 of every 1024
+    constexpr int U = SPAN / 1024;
+    float v[U][4];
+    float m = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int w = 1024 * u + 4 * tid;
+        f32x4_t q = {0.f, 0.f, 0.f, 0.f};
+        if (w < words) q = *reinterpret_cast<const f32x4_t*>(z + w);   // the span is whole fours
+        const uint32_t skip = flag[w >> 5] >> (w & 31);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool in = live && w + i < words && !((skip >> i) & 1);
+            v[u][i] = in ? q[i] * invT : -INFINITY;
+            m = v[u][i] > m ? v[u][i] : m;                       // (a NaN is met again in the sum)
+        }
+    }
+    m = over_block(m, [](float x, float y) { return x > y ? x : y; }, red);
+    const int64_t at = (int64_t)slot * a.n + t;
+    const float m_old = a.round ? a.b.m[at] : -INFINITY, s_old = a.round ? a.b.s[at] : 0.f;
+    m = m_old > m ? m_old : m;
+    const float fall = m_old == -INFINITY ? 0.f : expf(m_old - m);
+    const int em = PA ? emax_of(a.b.emax, a.blocks, redi) : 0;
+    float s = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int w = 1024 * u + 4 * tid;
+        uint16_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float p = v[u][i] == -INFINITY ? 0.f : expf(v[u][i] - m);
+            s += p;
+            if constexpr (PA != 0) {
+                const int e = w + i < words ? a.b.e[v0 + w + i] : 0;
+                f16_parts(ldexpf(p, 14 + e - em), hi[i], lo[i]);
+            }
+        }
+        if constexpr (PA != 0) {
+            if (w < a.span) {
+                const int64_t to = t * ldz + slot * a.span + w;
+                uint2 o;
+                o.x = hi[0] | ((uint32_t)hi[1] << 16); o.y = hi[2] | ((uint32_t)hi[3] << 16);
+                *reinterpret_cast<uint2*>(a.b.A[0] + to) = o;
+                if constexpr (PA == 2) {
+                    o.x = lo[0] | ((uint32_t)lo[1] << 16); o.y = lo[2] | ((uint32_t)lo[3] << 16);
+                    *reinterpret_cast<uint2*>(a.b.A[1] + to) = o;
+                }
+            }
+        }
+    }
+    s = over_block(s, [](float x, float y) { return x + y; }, red);
+    if (tid == 0) {
+        a.b.m[at] = m;
+        a.b.s[at] = s_old == 0.f ? s : fmaf(s_old, fall, s);
+        a.b.f[at] = fall;
+    }
+}
+
+template <int CB, int P>
+__global__ __launch_bounds__(256, P == 1 ? 2 : 1) void head_sums_kernel(BackArgs a, int gm, int gn, int64_t vocab, int64_t span, int v_first) {
+    typedef BackGemm<CB, P, P> G;
+    __shared__ __align__(16) uint8_t lds[G::LDS_BYTES];
+    const int tm = blockIdx.x % gm, tn = blockIdx.x / gm, slot = blockIdx.y;
+    const int64_t tok0 = (int64_t)tm * G::BM, c0 = (int64_t)tn * G::BN;
+    const int64_t k0 = v_first + slot * span, k1 = k0 + span < vocab ? k0 + span : vocab;
+    f32x4_t acc[G::NI][G::NJ];
+    G::run(acc, a, a.L, a.e, tok0, a.n, c0, k0, k1, lds);
+    float* O = a.acc + (int64_t)slot * a.n * a.L.d_col;
+    const float* f = a.f + (int64_t)slot * a.n;
+    G::each(acc, tok0, a.n, c0, a.L.d_col, [&](int64_t c, int64_t t, f32x4_t v, int have) {
+        float* o = O + t * a.L.d_col + c;
+        const float g = f[t];
+        for (int i = 0; i < have; ++i) o[i] = a.first || g == 0.f ? v[i] : fmaf(o[i], g, v[i]);
+    });
+}
+
+GPTQ_DEV float top_of(const HeadArgs& a, int64_t t, int j) {
+    const int64_t i = (a.tok0 + t) * a.k + j;
+    return a.topt == GPTQ_F32 ? load_as_f32<GPTQ_F32>(a.top, i) : a.topt == GPTQ_BF16 ? load_as_f32<GPTQ_BF16>(a.top, i)
+                                                                                        : load_as_f32<GPTQ_F16>(a.top, i);
+}
+
+// The loss and the gradient of one token.  Scalars in 64 bits: they cost nothing here, and
+// p_j - softmax_j and the loss of a token that the model is sure of are small differences.
+template <int CB>
+__global__ __launch_bounds__(256) void head_final_kernel(HeadArgs a) {
+    __shared__ double redd[4];
+    __shared__ float red[4];
+    __shared__ int redi[4];
+    __shared__ int id_of[TUNE_MAX_TOP];
+    __shared__ float coef[TUNE_MAX_TOP];
+    const int tid = threadIdx.x;
+    const int64_t t = blockIdx.x, tt = a.tok0 + t;
+    const float w = weight_of(a, t);
+    const auto larger = [](float x, float y) { return x > y ? x : y; };
+    const auto sum = [](double x, double y) { return x + y; };
+    int live = 0;
+    float tm = -INFINITY, zm = -INFINITY;                        // largest teacher's and model's among the entries
+    for (int j = tid; j < a.k; j += 256) {
+        int id;
+        const bool in = entry_there(a, t, j, id);
+        id_of[j] = in ? id : -1;
+        if (!in) continue;
+        live |= 1;
+        if (a.top) {
+            const float v = top_of(a, t, j);
+            if (v != v) live |= 2;                               // a NaN masks nothing
+            tm = larger(v / a.T, tm);
+        }
+        zm = larger(a.b.picked[t * a.k + j], zm);
+    }
+    live = over_block(live, [](int x, int y) { return x | y; }, redi);
+    tm = over_block(tm, larger, red);
+    if (!live || w == 0.f || (a.top && tm == -INFINITY && !(live & 2))) {   // no entry, or none with a weight
+        if (tid == 0) a.loss[tt] = 0.f;
+        if (a.dx)
+            for (int64_t c = tid; c < a.d; c += 256) store_out(a.dx, a.dxt, tt * a.d + c, 0.f);
+        return;
+    }
+    for (int i = tid; i < a.slots; i += 256) zm = larger(a.b.m[(int64_t)i * a.n + t], zm);
+    zm = over_block(zm, larger, red);
+    double pt = 0., zt = 0.;                                     // sum of exp over the teacher's entries; the model's words
+    for (int j = tid; j < a.k; j += 256) {
+        if (id_of[j] < 0) continue;
+        pt += a.top ? exp((double)(top_of(a, t, j) / a.T) - tm) : 1.;
+        bool first = true;
+        for (int i = 0; i < j && first; ++i) first = id_of[i] != id_of[j];
+        coef[j] = first ? 1.f : 0.f;
+        if (first) zt += exp((double)a.b.picked[t * a.k + j] - zm);
+    }
+    for (int i = tid; i < a.slots; i += 256) {
+        const float m = a.b.m[(int64_t)i * a.n + t], s = a.b.s[(int64_t)i * a.n + t];
+        if (s != 0.f) zt += s * exp((double)m - zm);
+    }
+    pt = over_block(pt, sum, redd);
+    zt = over_block(zt, sum, redd);
+    const double lpt = log(pt), lzt = log(zt);                   // lse z = zm + lzt
+    double l = 0.;
+    for (int j = tid; j < a.k; j += 256) {
+        if (id_of[j] < 0) continue;
+        const double lp = a.top ? (double)(top_of(a, t, j) / a.T) - tm - lpt : 0., lq = (double)a.b.picked[t * a.k + j] - zm - lzt;
+        const double p = exp(lp);
+        if (p != 0.) l += p * (lp - lq);
+        coef[j] = (float)((coef[j] != 0.f ? exp(lq) : 0.) - p);
+    }
+    l = over_block(l, sum, redd);
+    const float gain = w * a.T;
+    if (tid == 0) a.loss[tt] = (float)((double)w * a.T * a.T * l);
+    if (!a.dx) return;
+    const int em = emax_of(a.b.emax, a.blocks, redi);            // (and a barrier: coef is complete)
+    for (int64_t c = 8 * tid; c < a.d; c += 2048) {
+        const int have = (int)(a.d - c < 8 ? a.d - c : 8);
+        float g[8] = {};
+        for (int i = 0; i < a.R; ++i) {
+            const float m = a.b.m[(int64_t)i * a.n + t], s = a.b.s[(int64_t)i * a.n + t];
+            if (s == 0.f) continue;
+            const float q = ldexpf((float)exp((double)m - zm - lzt), em - 14);
+            const float* o = a.b.O + ((int64_t)i * a.n + t) * a.d + c;
+            for (int e = 0; e < have; ++e) g[e] = fmaf(q, o[e], g[e]);
+        }
+        for (int j = 0; j < a.k; ++j) {
+            const int64_t r = id_of[j];
+            if (r < 0) continue;
+            const uint8_t* src = a.L.codes + r * a.L.code_ld + c / 8 * CB;
+            const Raw<CB, 8> u = have == 8 ? load_raw<CB, 8>(src) : load_raw_tail<CB, 8>(src, have);
+            const int64_t i = r * a.L.n_groups + (a.L.n_groups == 1 ? 0 : c >> a.L.gshift);
+            const float S = f16_bits_to_f32(a.L.scales[i]), zero = f16_bits_to_f32(a.L.zeros[i]), k = coef[j];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float x = S * ((float)((code_bytes4<CB, 8>(u, e >> 2) >> (8 * (e & 3))) & 0xFFu) - zero);
+                g[e] = fmaf(k, x, g[e]);
+            }
+        }
+        for (int e = 0; e < have; ++e) store_out(a.dx, a.dxt, tt * a.d + c + e, gain * g[e]);
+    }
+}
+
+template <int CB>
+static void launch_sums(const BackArgs& b, int parts, int slots, int64_t vocab, int64_t span, int first_word, hipStream_t s) {
+    const int gm = (int)((b.n + 127) / 128), gn = (int)((b.L.d_col + 127) / 128);
+    const dim3 grid((unsigned)(gm * gn), (unsigned)slots);
+    if (parts == 1) head_sums_kernel<CB, 1><<<grid, 256, 0, s>>>(b, gm, gn, vocab, span, first_word);
+    else head_sums_kernel<CB, 2><<<grid, 256, 0, s>>>(b, gm, gn, vocab, span, first_word);
+}
+
+gptq_status head_launch(const HeadCall& c, hipStream_t s) {
+    const int64_t d = c.L.d_col;
+    const bool grad = c.dx != nullptr;
+    const int parts = !grad ? 0 : c.dxt == GPTQ_BF16 ? 1 : 2;
+    HeadArgs a = {};
+    a.vocab = c.vocab; a.d = d; a.k = c.k; a.ids = c.ids; a.top = c.top; a.topt = c.topt; a.T = c.temperature;
+    a.weights = c.weights; a.L = c.L; a.loss = c.loss; a.dx = c.dx; a.dxt = c.dxt;
+    a.blocks = (int)((c.vocab + EB - 1) / EB);
+    for (int64_t tok0 = 0; tok0 < c.n; tok0 += CHUNK) {
+        const int64_t nc = c.n - tok0 < CHUNK ? c.n - tok0 : CHUNK;
+        const HeadPlan p = plan_of(nc, d, c.vocab, grad);
+        layout(&a.b, (uint8_t*)c.ws, nc, nc * p.R, p.span, d, c.vocab, c.k, grad);
+        a.n = nc; a.tok0 = tok0; a.R = p.R; a.span = p.span;
+        if (grad) {
+            row_exponents(c.L, c.vocab, a.b.e, s);
+            head_emax_kernel<<<(unsigned)a.blocks, 256, 0, s>>>(a.b.e, c.vocab, a.b.emax);
+            GPTQ_LAUNCH_CHECK();
+        }
+        int round = 0;
+        for (int first = 0; first < p.spans; first += p.R, ++round) {
+            const int slots = p.spans - first < p.R ? p.spans - first : p.R;
+            const int64_t v0 = first * p.span, v1 = v0 + slots * p.span < c.vocab ? v0 + slots * p.span : c.vocab;
+            GroupedArgs g = {};
+            g.L = c.L;
+            g.L.codes += v0 * c.L.code_ld;
+            g.L.scales += v0 * c.L.n_groups;
+            g.L.zeros += v0 * c.L.n_groups;
+            g.d_row = v1 - v0; g.ldy = p.R * p.span;
+            g.x = (const uint16_t*)c.x + tok0 * c.ldx; g.ldx = c.ldx; g.n = nc;
+            g.offsets = nullptr; g.E = 1; g.y = a.b.z; g.yt = GPTQ_F32;
+            const gptq_status st = grouped_launch(g, c.xt, c.bits, c.group, s);
+            if (st != GPTQ_OK) return st;
+            a.round = round; a.slots = slots;
+            const dim3 grid((unsigned)nc, (unsigned)slots);
+            if (parts == 0) head_stats_kernel<0><<<grid, 256, 0, s>>>(a);
+            else if (parts == 1) head_stats_kernel<1><<<grid, 256, 0, s>>>(a);
+            else head_stats_kernel<2><<<grid, 256, 0, s>>>(a);
+            GPTQ_LAUNCH_CHECK();
+            if (grad) {
+                BackArgs b = {};
+                b.L = c.L; b.d_row = c.vocab; b.e = a.b.e;
+                b.A[0] = a.b.A[0]; b.A[1] = a.b.A[1]; b.lda = p.R * p.span; b.a0 = v0;
+                b.n = nc; b.acc = a.b.O; b.f = a.b.f; b.first = round == 0;
+                if (c.bits == 3) launch_sums<3>(b, parts, slots, c.vocab, p.span, (int)v0, s);
+                else if (c.bits == 4) launch_sums<4>(b, parts, slots, c.vocab, p.span, (int)v0, s);
+                else launch_sums<8>(b, parts, slots, c.vocab, p.span, (int)v0, s);
+                GPTQ_LAUNCH_CHECK();
+            }
+        }
+        a.slots = p.R;
+        if (c.bits == 3) head_final_kernel<3><<<(unsigned)nc, 256, 0, s>>>(a);
+        else if (c.bits == 4) head_final_kernel<4><<<(unsigned)nc, 256, 0, s>>>(a);
+        else head_final_kernel<8><<<(unsigned)nc, 256, 0, s>>>(a);
+        GPTQ_LAUNCH_CHECK();
+    }
+    return GPTQ_OK;
+}
+
+}  // namespace gptq

@@ -1,0 +1,161 @@
+"""The tuning operators' C ABI without a GPU: the library exports exactly the functions that
+include/gptq_tuning.h declares, every call that argument validation decides returns its
+documented status before any device work, and workspaces of large batches do for smaller
+ones."""
+import ctypes
+import os
+import re
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "gptq_tuning.h")
+LIB = os.path.join(ROOT, "post_weight_quantization_25_amd", "libgptq.so")
+
+OK, INVALID_ARG, UNSUPPORTED, WORKSPACE = range(4)
+F32, BF16, F16 = 0, 1, 2
+FAKE = ctypes.c_void_p(0x1000)   # never dereferenced: validation rejects the call first
+vp, i64, i32, sz, dt = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t, ctypes.c_int
+
+SIG = {
+    "gptqt_linear_grouped": (dt, [vp, vp, vp, i32, i64, i64, i32, i32, vp, dt, i64, i64, vp, vp, dt, vp]),
+    "gptqt_linear_grouped_backward_workspace_size": (sz, [i64, i32, i64, i64]),
+    "gptqt_linear_grouped_backward": (dt, [vp, vp, vp, i32, i64, i64, i32, i32, vp, dt, i64, i64, vp, vp, dt, vp, sz, vp]),
+    "gptqt_cross_entropy_workspace_size": (sz, [i64, i64, i64, i32]),
+    "gptqt_cross_entropy": (dt, [vp, vp, vp, i64, i64, i32, i32, vp, dt, i64, i64, vp, vp, vp, vp, dt, vp, sz, vp]),
+    "gptqt_distill_workspace_size": (sz, [i64, i64, i64, i32, i32]),
+    "gptqt_distill": (dt, [vp, vp, vp, i64, i64, i32, i32, vp, dt, i64, i64, vp, vp, dt, i32, ctypes.c_float, vp, vp, vp, dt,
+                           vp, sz, vp]),
+}
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(LIB):
+        import __graft_entry__
+        __graft_entry__.build()
+    L = ctypes.CDLL(LIB)
+    for name, (res, args) in SIG.items():
+        f = getattr(L, name)
+        f.restype, f.argtypes = res, args
+    return L
+
+
+def test_exports(lib):
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    declared = sorted(set(re.findall(r"^[A-Za-z_][\w \t\*]*?\b(gptqt_\w+)\s*\(", text, flags=re.M)))
+    assert declared == sorted(SIG)
+    nm = subprocess.run(["nm", "-D", "--defined-only", LIB], capture_output=True, text=True, check=True).stdout
+    assert sorted({ln.split()[-1] for ln in nm.splitlines() if " T " in ln and "gptqt_" in ln}) == declared
+
+
+def test_header_compiles_as_c_and_cpp(tmp_path):
+    if shutil.which("gcc") is None or shutil.which("g++") is None:
+        pytest.skip("gcc/g++ not installed")
+    src = tmp_path / "use.c"
+    src.write_text('#include "gptq_tuning.h"\nint main(void) { return GPTQ_OK; }\n')
+    inc = f"-I{os.path.dirname(HEADER)}"
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-pedantic", "-Werror", inc, "-fsyntax-only", str(src)], check=True)
+    subprocess.run(["g++", "-std=c++11", "-Wall", "-Werror", inc, "-fsyntax-only", "-x", "c++", str(src)], check=True)
+
+
+def layer_errors(call):
+    """What every operator refuses of a stored layer: call(bits=, G=, d_col=)."""
+    assert call(bits=5) == UNSUPPORTED
+    assert call(G=16) == UNSUPPORTED and call(G=256, d_col=512) == UNSUPPORTED
+    assert call(G=128, d_col=320) == INVALID_ARG           # the group does not divide the width
+    assert call(G=-2) == INVALID_ARG
+    assert call(G=0, d_col=255) == INVALID_ARG             # odd width, two codes per byte
+    assert call(G=0, d_col=252, bits=3) == INVALID_ARG     # 3-bit rows are whole 8-code groups
+    assert call(d_col=0) == INVALID_ARG and call(d_row=0) == INVALID_ARG and call(n=-1) == INVALID_ARG
+    assert call(d_col=1 << 17, ldx=1 << 17) == UNSUPPORTED and call(d_row=(1 << 25) + 1, ldx=1 << 26) == UNSUPPORTED
+    assert call(n=65535 * 64 + 1) == UNSUPPORTED
+    assert call(xt=7) == INVALID_ARG and call(yt=7) == INVALID_ARG and call(xt=F32) == UNSUPPORTED
+
+
+def test_grouped_argument_errors(lib):
+    def call(codes=FAKE, S=FAKE, Z=FAKE, E=3, d_row=4, d_col=256, bits=4, G=128, x=FAKE, xt=BF16, n=2, ldx=512, offs=FAKE,
+             y=FAKE, yt=F32):
+        return lib.gptqt_linear_grouped(codes, S, Z, E, d_row, d_col, bits, G, x, xt, n, ldx, offs, y, yt, None)
+
+    layer_errors(call)
+    assert call(E=0) == INVALID_ARG and call(E=4097) == UNSUPPORTED
+    assert call(E=3, offs=None) == INVALID_ARG             # several experts need their rows
+    assert call(ldx=255) == INVALID_ARG and call(ldx=(1 << 23) + 1) == UNSUPPORTED
+    assert call(E=4096, d_row=(1 << 14) + 1) == UNSUPPORTED
+    assert call(n=1 << 22, d_row=1 << 15) == UNSUPPORTED    # more than 2^24 tiles
+    for name in ("codes", "S", "Z", "x", "y"):
+        assert call(**{name: None}) == INVALID_ARG, name
+    assert call(n=0, codes=None, x=None, y=None) == OK
+
+
+def test_backward_argument_errors(lib):
+    size = lib.gptqt_linear_grouped_backward_workspace_size
+    for bad in ((0, 3, 4, 256), (2, 0, 4, 256), (2, 3, 0, 256), (2, 3, 4, 0), (2, 4097, 4, 256), (2, 3, 1 << 26, 256)):
+        assert size(*bad) == 0, bad
+    need = size(2, 3, 4, 256)
+    assert need >= 2 * 64 * 2 + 2 * 4 + 12                 # fp16 rows, their exponents, the weights' exponents
+
+    def call(codes=FAKE, S=FAKE, Z=FAKE, E=3, d_row=4, d_col=256, bits=4, G=128, x=FAKE, xt=BF16, n=2, ldx=512, offs=FAKE,
+             y=FAKE, yt=F32, ws=FAKE, wsb=1 << 40):
+        return lib.gptqt_linear_grouped_backward(codes, S, Z, E, d_row, d_col, bits, G, x, xt, n, ldx, offs, y, yt, ws, wsb,
+                                                 None)
+
+    layer_errors(call)
+    assert call(E=0) == INVALID_ARG and call(E=4097) == UNSUPPORTED and call(E=3, offs=None) == INVALID_ARG
+    assert call(ldx=3) == INVALID_ARG                      # below d_row
+    for name in ("codes", "S", "Z", "x", "y"):
+        assert call(**{name: None}) == INVALID_ARG, name
+    assert call(ws=None) == WORKSPACE and call(wsb=need - 1) == WORKSPACE
+    assert call(ws=ctypes.c_void_p(0x1008)) == WORKSPACE   # not 16-byte aligned
+    assert call(n=0, codes=None, x=None, y=None, ws=None) == OK
+
+
+@pytest.mark.parametrize("op", ["ce", "distill"])
+def test_head_argument_errors(lib, op):
+    def size(n, d, V, grad=1):
+        return (lib.gptqt_cross_entropy_workspace_size(n, d, V, grad) if op == "ce"
+                else lib.gptqt_distill_workspace_size(n, d, V, 5, grad))
+    for bad in ((0, 256, 4), (2, 0, 4), (2, 256, 0), (65535 * 64 + 1, 256, 4), (2, 1 << 17, 4), (2, 256, (1 << 25) + 1)):
+        assert size(*bad) == 0, bad
+    need = size(2, 256, 4)
+    assert 0 < size(2, 256, 4, 0) < need
+
+    def call(codes=FAKE, S=FAKE, Z=FAKE, d_row=4, d_col=256, bits=4, G=128, x=FAKE, xt=BF16, n=2, ldx=512, ids=FAKE, top=FAKE,
+             tt=F32, k=5, T=1.0, loss=FAKE, dx=FAKE, yt=F32, ws=FAKE, wsb=1 << 40):
+        if op == "ce":
+            return lib.gptqt_cross_entropy(codes, S, Z, d_row, d_col, bits, G, x, xt, n, ldx, ids, None, loss, dx, yt, ws, wsb,
+                                           None)
+        return lib.gptqt_distill(codes, S, Z, d_row, d_col, bits, G, x, xt, n, ldx, ids, top, tt, k, T, None, loss, dx, yt, ws,
+                                 wsb, None)
+
+    layer_errors(lambda **kw: call(**{"ldx": 1 << 20, **kw}))
+    assert call(ldx=255) == INVALID_ARG and call(ldx=(1 << 23) + 1) == UNSUPPORTED
+    for name in ("codes", "S", "Z", "x", "ids", "loss") + (("top",) if op == "distill" else ()):
+        assert call(**{name: None}) == INVALID_ARG, name
+    assert call(ws=None) == WORKSPACE and call(wsb=need - 1) == WORKSPACE
+    assert call(ws=ctypes.c_void_p(0x1008)) == WORKSPACE
+    assert call(n=0, codes=None, x=None, loss=None, ws=None) == OK
+    if op == "distill":
+        assert call(k=0) == INVALID_ARG and call(k=1025) == UNSUPPORTED and call(tt=7) == INVALID_ARG
+        for T in (0.0, -1.0, float("nan"), float("inf")):
+            assert call(T=T) == INVALID_ARG
+        assert lib.gptqt_distill_workspace_size(2, 256, 4, 0, 1) == 0
+        assert lib.gptqt_distill_workspace_size(2, 256, 4, 1025, 1) == 0
+
+
+@pytest.mark.parametrize("d,vocab", [(64, 1), (64, 9000), (1024, 50021), (4096, 131072), (5504, 32000)])
+@pytest.mark.parametrize("grad", [0, 1])
+def test_workspaces_do_not_fall(lib, d, vocab, grad):
+    last = 0
+    for n in list(range(1, 700)) + list(range(700, 9000, 41)):
+        v = lib.gptqt_distill_workspace_size(n, d, vocab, 7, grad)
+        assert v >= last, n
+        last = v
+    last = 0
+    for n in range(1, 2000):
+        v = lib.gptqt_linear_grouped_backward_workspace_size(n, 8, vocab, d)
+        assert v >= last, n
+        last = v
