@@ -8,21 +8,28 @@
 // two (PB = 2: 2^-23).  A comes as fp16 planes (PA parts) with 2^e_r and a power of two per
 // token multiplied in, zeros behind the last row.
 //
-// A workgroup of four waves owns BM x BN outputs, a wave a quarter of them.  Slabs of 64 rows:
-// A's pieces and the codes of the next slab are on their way into registers while this one is
-// multiplied; codes are decoded where they lie transposed, 4 rows x 8 columns per thread, and
-// written to LDS by column.  Two buffers, one barrier per slab.
+// A workgroup owns BM tokens x BN columns in slabs of 32 rows; a wave MT x 4 tiles of 16 x 16.
+// Both operands go through LDS as fp16 with a slab's rows together, the codes decoded once per
+// workgroup: a thread takes 4 rows x 4 columns, pairs two rows' codes in a register (1024 + u
+// as fp16 is 0x6400 | u, so u - z and its product with the scale are one packed instruction
+// each) and so writes them transposed.  One barrier per slab.
 #pragma once
+#include "stored_gemm.h"
 #include "tuning.h"
 
 namespace gptq {
 
-constexpr int BK = 64;                                          // rows per slab
+constexpr int BK = 32;                                          // rows per slab
+
+// Four rows' scales times 2^-e_r and 1024 + their zeros, fp16, as the product takes them.  A
+// zero that is no whole number in -1024 .. 1024 has the sign bit of its 1024 + z set: such
+// rows' zeros are read from the layer (decode_any).
+struct Quad { uint32_t S01, zz01, S23, zz23; };
 
 struct BackArgs {
     Stored L; int64_t d_row;                                    // rows of each expert
-    const int8_t* e;                                            // e_r of every row
-    const uint16_t* A[2]; int64_t lda, a0;                      // n x lda each, lda a multiple of 64: rows a0 .. a0 + lda - 1
+    const Quad* T; int64_t quads;                               // per expert and group: `quads` for its rows, zeros behind the last
+    const uint16_t* A[2]; int64_t a0;                           // [slab][token][32 rows] each, from row a0 on
     int64_t n;
     const int32_t* offsets; int E;
     // rounded outputs: out = acc 2^-shift[t]
@@ -44,176 +51,301 @@ GPTQ_DEV void f16_parts(float v, uint16_t& hi, uint16_t& lo) {
     lo = f32_to_f16_bits(fabsf(v) < INFINITY ? r : 0.f);
 }
 
-GPTQ_DEV f32x4_t mfma_f16(u32x4_t a, u32x4_t b, f32x4_t c) { return mfma16<X_F16>(a, b, c); }
+GPTQ_DEV f16x2_t as_f16x2(uint32_t v) { return __builtin_bit_cast(f16x2_t, v); }
+GPTQ_DEV uint32_t as_u32(f16x2_t v) { return __builtin_bit_cast(uint32_t, v); }
 
-template <int CB, int PA, int PB>
+// LDS holds a slab as 256-byte lines of four columns (or tokens), 16 bytes for 8 of the slab's 32
+// rows, a line's 16 pieces XOR-swizzled.  A read of 16 columns by a wave serves columns 0 - 3
+// and 12 - 15 of one lane group and the other 8 of the next at a time: with these swizzles
+// they lie in 16 places.  The writes of every fourth column's two halves of a piece do, too.
+GPTQ_DEV int line_swizzle(int line) { return (line & 12) | (((line ^ (line >> 1)) & 1) << 1) | ((line >> 1) & 1); }
+GPTQ_DEV int slab_at(int c, int piece) { return (c >> 2) * 256 + 16 * ((((c & 3) << 2) | piece) ^ line_swizzle(c >> 2)); }
+
+// The barrier of a workgroup whose waves have waited for what the others read; loads stay in flight.
+GPTQ_DEV void barrier_only() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Waits until at most the wave's loads of the last two slabs are in flight: `each` per slab, or
+// the largest number below that the code has a wait for.
+GPTQ_DEV void wait_two_slabs(int each) {
+    if (each >= 6) wait_vm_lgkm0<12>();
+    else if (each >= 4) wait_vm_lgkm0<8>();
+    else if (each == 3) wait_vm_lgkm0<6>();
+    else if (each == 2) wait_vm_lgkm0<4>();
+    else wait_vm_lgkm0<2>();                                    // (0: nothing is in flight)
+}
+
+// DIRECT: the codes' rows are whole and aligned 16 bytes (direct_codes) and go straight to LDS.
+inline bool direct_codes(const Stored& L) { return ((reinterpret_cast<uintptr_t>(L.codes) | (uintptr_t)L.code_ld) & 15) == 0; }
+
+template <int CB, int PA, int PB, int MT, int WT, int WC, bool DIRECT>
 struct BackGemm {
-    static constexpr int BM = 128, BN = 128;
+    static constexpr int BM = 16 * MT * WT, BN = 64 * WC, THREADS = 64 * WT * WC, WAVES = WT * WC, NI = 4;
     static constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2;
-    static constexpr int BUF = PA * A_BYTES + PB * B_BYTES;
-    static constexpr int MAXG = BN / 32;                        // groups of a tile's columns
-    static constexpr int TAB = BK * MAXG * 8;                   // scale 2^-e and zero of a slab
-    static constexpr int LDS_BYTES = 2 * BUF + 2 * TAB;
-    static constexpr int NI = 4, NJ = 4;                        // 16 x 16 tiles of a wave: columns, tokens
-    struct Entry { float S, z; };
+    static constexpr int ROW = BN * CB / 8, PIECES = ROW / 16, C_BYTES = BK * ROW, T_BYTES = 1024;   // codes of a slab; its Quads
+    static constexpr int BUFS = 4;
+    static constexpr int LDS_BYTES = BUFS * (PA * A_BYTES + C_BYTES + T_BYTES) + 2 * PB * B_BYTES;
+    static constexpr int AP = BM / 16 / WAVES > 0 ? BM / 16 / WAVES : 1;   // loads of a plane's slab per wave: 16 tokens each
+    static_assert(WT == 2 && BK * PIECES <= THREADS, "a thread decodes one patch of 4 rows x 4 columns and copies at most one piece");
 
-    // Byte of 16-byte piece `piece` (8 of the slab's 64 rows) of column or token `at`.  Reads of
-    // 16 consecutive columns and writes of every eighth one spread over the banks.
-    static GPTQ_DEV int at(int row, int piece) { return row * 128 + 16 * (piece ^ ((row ^ (row >> 3)) & 7)); }
-
-    // acc[i][j]: lane l's value v is column 64 (wave / 2) + 16 i + 4 (l / 16) + v, token 64 (wave % 2) + 16 j + l % 16.
-    // Rows k0 .. k1 - 1 of the layer enter.
-    static GPTQ_DEV void run(f32x4_t (&acc)[NI][NJ], const BackArgs& a, const Stored& L, const int8_t* e, int64_t tok0, int64_t end,
+    // acc[i][j]: lane l's value v is column 64 (wave % WC) + 16 i + 4 (l / 16) + v, token 16 MT (wave / WC) + 16 j + l % 16.
+    // Rows k0 .. k1 - 1 of the layer enter; k0 and k0 - a.a0 are multiples of 32, and k1 is one or d_row.
+    // T: the layer's Quads.
+    static GPTQ_DEV void run(f32x4_t (&acc)[NI][MT], const BackArgs& a, const Stored& L, const Quad* T, int64_t tok0, int64_t end,
                              int64_t c0, int64_t k0, int64_t k1, uint8_t* lds) {
-        const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n16 = lane & 15, q = lane >> 4;
-        const int wc = 64 * (wave >> 1), wt = 64 * (wave & 1);
+        const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n16 = lane & 15, q = lane >> 4;
+        const int wc = 64 * (wave % WC), wt = 16 * MT * (wave / WC);
         const int gs = L.n_groups == 1 ? 30 : L.gshift;          // one scale per row: every column in group 0
-        const int g0 = (int)(c0 >> gs), ngr = L.n_groups - g0;   // the tile's first group; groups from it on
-        const int tile_groups = gs >= 7 ? 1 : BN >> gs;
-        Entry* tab = reinterpret_cast<Entry*>(lds + 2 * BUF);
+        const int slabs = (int)((k1 - k0 + BK - 1) / BK);
+        uint8_t* bb = lds + BUFS * PA * A_BYTES;
+        uint8_t* cc = bb + 2 * PB * B_BYTES;
+        uint8_t* tt = cc + BUFS * C_BYTES;
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int j = 0; j < MT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        if (slabs <= 0) return;
 
-        const int64_t left_c = L.d_col - c0;
-        const int cp = tid & 15, rp = tid >> 4;                  // the thread's patch: columns 8 cp .., rows 4 rp ..
-        const int pc = (int)(left_c - 8 * cp < 8 ? left_c - 8 * cp : 8);   // its columns that exist
-        const uint8_t* ct = L.codes + (c0 + 8 * cp) / 8 * CB;
+        // Wave w loads tokens 16 (w + WAVES j) .. + 15 of A: 4 lines of slab_at, lane l the line's piece l % 16.
+        uint32_t aoff[AP];
+#pragma unroll
+        for (int j = 0; j < AP; ++j) {
+            const int line = 4 * (wave + WAVES * j) + (lane >> 4), x = (lane & 15) ^ line_swizzle(line);
+            int m = 4 * line + (x >> 2);
+            if (tok0 + m >= end) m = (int)(end - 1 - tok0);
+            aoff[j] = (uint32_t)m * (2 * BK) + 16 * (x & 3);
+        }
+        const bool loads_a = BM / 16 >= WAVES || wave < BM / 16;
+        const uint8_t* a_next[PA];
+#pragma unroll
+        for (int p = 0; p < PA; ++p) a_next[p] = reinterpret_cast<const uint8_t*>(a.A[p] + ((k0 - a.a0) / BK * a.n + tok0) * BK);
 
-        u32x4_t av[PA][4];
-        auto load_a = [&](int64_t k) {
+        // Piece `tid` of a slab's codes: row tid / PIECES.  Pieces behind the columns: the row's first.
+        const uint32_t ld = (uint32_t)L.code_ld;
+        const int64_t row_left = L.code_ld - c0 * CB / 8;        // bytes of the row from the tile's first column on
+        const int crow = tid / PIECES, ccol = 16 * (tid % PIECES) < row_left ? 16 * (tid % PIECES) : 0;
+        const bool has_piece = tid < BK * PIECES;
+        const bool loads_c = DIRECT && wave * 64 < BK * PIECES;
+        const int tail = (int)(a.d_row - k0 - (int64_t)(slabs - 1) * BK < BK ? a.d_row - k0 - (int64_t)(slabs - 1) * BK : BK);   // rows of the last slab
+        const uint32_t coff = (uint32_t)crow * ld + ccol, coff_last = (uint32_t)(crow < tail ? crow : tail - 1) * ld + ccol;
+        const uint8_t* c_next = L.codes + k0 * L.code_ld + c0 * CB / 8;
+        const uint8_t* c_end = L.codes + a.d_row * L.code_ld;
+
+        // Quads: lane 8 g + quad of the last wave, group g of the tile's.
+        const int64_t tg = (c0 >> gs) + (lane >> 3) < L.n_groups ? lane >> 3 : L.n_groups - 1 - (c0 >> gs);
+        const uint32_t toff = (uint32_t)(((gs >= 30 ? 0 : tg) * a.quads + (lane & 7)) * (int64_t)sizeof(Quad));
+        const Quad* t_next = T + (c0 >> gs) * a.quads + k0 / 4;
+        const bool loads_t = wave == WAVES - 1;
+
+        const uint32_t m_lds = lds_addr(reinterpret_cast<const uint16_t*>(lds));
+        const uint32_t m_a = m_lds + wave * 1024, m_c = m_lds + (uint32_t)(cc - lds) + wave * 1024, m_t = m_lds + (uint32_t)(tt - lds);
+        const int each = (loads_a ? PA * AP : 0) + (loads_c ? 1 : 0) + (loads_t ? 1 : 0);
+        const int64_t a_step = a.n * (2 * BK), c_step = BK * L.code_ld;
+
+        // Behind the last slab that one is loaded again, so that every step counts the same loads.
+        int a_at = 0, c_at = 0;
+        auto load_a = [&](int buf) {
+            if (loads_a) {
 #pragma unroll
-            for (int p = 0; p < PA; ++p)
+                for (int p = 0; p < PA; ++p)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int u = tid + 256 * j, m = u >> 3, piece = u & 7;
-                    const int64_t t = tok0 + m < end ? tok0 + m : end - 1;
-                    av[p][j] = *reinterpret_cast<const u32x4_t*>(a.A[p] + t * a.lda + (k - a.a0) + 8 * piece);
-                }
+                    for (int j = 0; j < AP; ++j) dma16<0>(aoff[j], a_next[p], m_a + (buf * PA + p) * A_BYTES + j * (WAVES * 1024));
+            }
+            const bool last = a_at == slabs - 1;                 // uniform
+            a_at += last ? 0 : 1;
+#pragma unroll
+            for (int p = 0; p < PA; ++p) a_next[p] += last ? 0 : a_step;
         };
-        auto store_a = [&](uint8_t* buf) {
+        u32x4_t piece = {0u, 0u, 0u, 0u};                        // codes on their way through registers
+        auto load_c = [&](int buf) {
+            const bool last = c_at == slabs - 1;                 // uniform
+            const uint32_t off = last ? coff_last : coff;
+            if constexpr (DIRECT) {
+                if (loads_c && has_piece) dma16<0>(off, c_next, m_c + buf * C_BYTES);
+            } else if (has_piece) {
+                const uint8_t* src = c_next + off;
+                if (c_end - src >= 16) {
+                    __builtin_memcpy(&piece, src, 16);
+                } else {                                         // the layer ends in the piece
+                    uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-            for (int p = 0; p < PA; ++p)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int u = tid + 256 * j;
-                    *reinterpret_cast<u32x4_t*>(buf + p * A_BYTES + at(u >> 3, u & 7)) = av[p][j];
+                    for (int i = 0; i < 15; ++i)
+                        if (src + i < c_end) w[i >> 2] |= (uint32_t)src[i] << (8 * (i & 3));
+                    piece = u32x4_t{w[0], w[1], w[2], w[3]};
                 }
+            }
+            if (loads_t) dma16<0>(toff, t_next, m_t + buf * T_BYTES);
+            c_at += last ? 0 : 1;
+            c_next += last ? 0 : c_step;
+            t_next += last ? 0 : BK / 4;
         };
-        Raw<CB, 8> cv[4];
-        auto load_b = [&](int64_t k) {
+        auto put_piece = [&](int buf) {
+            if (!DIRECT && has_piece) *reinterpret_cast<u32x4_t*>(cc + buf * C_BYTES + 16 * tid) = piece;
+        };
+
+        // The thread's patch: columns 4 cp .. of rows 4 rp .. of a slab.
+        const int cp = (tid >> 1) % (BN / 4), rp = 2 * (tid / (BN / 2)) + (tid & 1);
+        const int pg = gs >= 30 ? 0 : (4 * cp) >> gs;            // the patch's group (a tile starts a group)
+        const uint8_t* patch = cc + 4 * rp * ROW + (CB == 3 ? (12 * cp / 32) * 4 : 4 * cp * CB / 8);
+        struct Ahead { uint32_t b[4]; u32x4_t t; };              // codes of 4 columns of 4 rows, their Quad
+        auto read_patch = [&](Ahead& r, int buf) {
+            r.t = *reinterpret_cast<const u32x4_t*>(tt + buf * T_BYTES + (8 * pg + rp) * 16);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int64_t r = k + 4 * rp + j, rr = r < k1 ? r : k1 - 1;
-                const uint8_t* src = ct + rr * L.code_ld;
-                cv[j] = pc == 8 ? load_raw<CB, 8>(src) : load_raw_tail<CB, 8>(src, pc);
+                const uint8_t* at = patch + buf * C_BYTES + j * ROW;
+                if constexpr (CB == 8) r.b[j] = *reinterpret_cast<const uint32_t*>(at);
+                else if constexpr (CB == 4) r.b[j] = *reinterpret_cast<const uint16_t*>(at);
+                else {                                           // 12 bits of two words (behind the last row: whatever LDS holds)
+                    const uint32_t lo = reinterpret_cast<const uint32_t*>(at)[0], hi = reinterpret_cast<const uint32_t*>(at)[1];
+                    r.b[j] = (uint32_t)((((uint64_t)hi << 32) | lo) >> (12 * cp & 31)) & 0xFFFu;
+                }
             }
         };
-        auto load_tab = [&](int64_t k) {                          // the thread's entry: row tid % 64, group tid / 64
-            Entry t = {0.f, 0.f};
-            const int64_t r = k + (tid & 63);
-            const int g = tid >> 6;
-            if (g < tile_groups && g < ngr && r < k1) {
-                const int64_t i = r * L.n_groups + g0 + g;
-                t.S = ldexpf(f16_bits_to_f32(L.scales[i]), -(int)e[r]);
-                t.z = f16_bits_to_f32(L.zeros[i]);
+        struct Decoded { uint32_t o[PB][4][2]; };                // [part][column][rows 0, 1 or 2, 3]
+        // 1024 + u and 1024 + z are fp16 numbers, and so is their difference.
+        auto decode_one = [&](Decoded& d, const Ahead& r, int h, int i) {
+            uint32_t u;
+            if constexpr (CB == 8) u = __builtin_amdgcn_perm(r.b[2 * h + 1], r.b[2 * h], 0x0C000C00u | i | ((4 + i) << 16));
+            else u = ((r.b[2 * h] | (r.b[2 * h + 1] << 16)) >> (CB * i)) & (CB == 4 ? 0x000F000Fu : 0x00070007u);
+            const f16x2_t v = as_f16x2(u | 0x64006400u) - as_f16x2(r.t[2 * h + 1]), S = as_f16x2(r.t[2 * h]);
+            const f16x2_t hi = v * S;
+            d.o[0][i][h] = as_u32(hi);
+            asm volatile("" : "+v"(d.o[0][i][h]));               // here, between the products
+            if constexpr (PB == 2) {
+                d.o[1][i][h] = as_u32(__builtin_elementwise_fma(v, S, -hi));
+                asm volatile("" : "+v"(d.o[1][i][h]));
             }
-            return t;
         };
-        auto decode = [&](const Entry* tb, uint8_t* buf) {
-            const Entry* te = tb + (gs >= 7 ? 0 : ((8 * cp) >> gs)) * BK + 4 * rp;
-            Entry en[4];
+        auto odd = [&](const Ahead& r) { return ((r.t[1] | r.t[3]) & 0x80008000u) != 0; };
+        // Any zeros, in fp32.
+        auto decode_any = [&](Decoded& d, const Ahead& r, int s) {
+            int64_t g = (c0 >> gs) + pg;
+            g = g < L.n_groups ? g : L.n_groups - 1;             // columns that are not there
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+                const int64_t row = k0 + (int64_t)s * BK + 4 * rp + j;
+                const float z = f16_bits_to_f32(L.zeros[(row < a.d_row ? row : a.d_row - 1) * L.n_groups + g]);
+                const uint32_t word = j == 0 ? r.b[0] : j == 1 ? r.b[1] : j == 2 ? r.b[2] : r.b[3];
+                const float S = f16_bits_to_f32((uint16_t)((j < 2 ? r.t[0] : r.t[2]) >> (16 * (j & 1))));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) en[j] = te[j];
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t u = (word >> (CB * i)) & ((1u << CB) - 1);
+                    uint16_t part[2];
+                    f16_parts(S * ((float)u - z), part[0], part[1]);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                float w[4];
+                    for (int p = 0; p < PB; ++p)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float u = (float)((code_bytes4<CB, 8>(cv[j], c >> 2) >> (8 * (c & 3))) & 0xFFu);
-                    w[j] = en[j].S * (u - en[j].z);
+                        for (int h = 0; h < 2; ++h)
+                            if (h == j >> 1)
+                                d.o[p][i][h] = j & 1 ? (d.o[p][i][h] & 0xFFFFu) | ((uint32_t)part[p] << 16) : (d.o[p][i][h] & 0xFFFF0000u) | part[p];
                 }
-                uint16_t hi[4], lo[4];
+            }
+        };
+        auto store = [&](const Decoded& d, int buf) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) f16_parts(w[j], hi[j], lo[j]);
-                uint8_t* dst = buf + PA * A_BYTES + at(8 * cp + c, rp >> 1) + 8 * (rp & 1);
-                uint2 v;
-                v.x = hi[0] | ((uint32_t)hi[1] << 16); v.y = hi[2] | ((uint32_t)hi[3] << 16);
-                *reinterpret_cast<uint2*>(dst) = v;
-                if constexpr (PB == 2) {
-                    v.x = lo[0] | ((uint32_t)lo[1] << 16); v.y = lo[2] | ((uint32_t)lo[3] << 16);
-                    *reinterpret_cast<uint2*>(dst + B_BYTES) = v;
+            for (int p = 0; p < PB; ++p)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint2 v;
+                    v.x = d.o[p][i][0]; v.y = d.o[p][i][1];
+                    *reinterpret_cast<uint2*>(bb + (buf * PB + p) * B_BYTES + slab_at(4 * cp + i, rp >> 1) + 8 * (rp & 1)) = v;
                 }
+        };
+        // The products of a slab, a token tile after the other, and in between the next slab's
+        // codes: fragments are read two tiles ahead, and a tile's products are issued with a share
+        // of the decoding, so that both units are fed.
+        auto multiply = [&](int abuf, int bbuf, int next, Decoded& d, Ahead& r, auto&& loads) {
+            constexpr int RING = MT < 3 ? MT : 3;
+            u32x4_t bf[PB][NI], af[RING][PA];
+            auto read_a = [&](int j) {
+#pragma unroll
+                for (int p = 0; p < PA; ++p)
+                    af[j % RING][p] = *reinterpret_cast<const u32x4_t*>(lds + (abuf * PA + p) * A_BYTES + slab_at(wt + 16 * j + n16, q));
+            };
+#pragma unroll
+            for (int p = 0; p < PB; ++p)
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+                    bf[p][i] = *reinterpret_cast<const u32x4_t*>(bb + (bbuf * PB + p) * B_BYTES + slab_at(wc + 16 * i + n16, q));
+#pragma unroll
+            for (int j = 0; j < RING - 1; ++j) read_a(j);
+            read_patch(r, next);
+            __builtin_amdgcn_sched_barrier(0);
+            loads();
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                if (j + RING - 1 < MT || RING == 1) read_a(j + RING - 1);
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const u32x4_t (&x)[PA] = af[j % RING];
+                    if constexpr (PA == 2) acc[i][j] = mfma16<X_F16>(bf[0][i], x[1], acc[i][j]);
+                    if constexpr (PB == 2) acc[i][j] = mfma16<X_F16>(bf[1][i], x[0], acc[i][j]);
+                    acc[i][j] = mfma16<X_F16>(bf[0][i], x[0], acc[i][j]);
+                }
+#pragma unroll
+                for (int u = 8 * j / MT; u < 8 * (j + 1) / MT; ++u) decode_one(d, r, u & 1, u >> 1);
+                __builtin_amdgcn_sched_barrier(0);
             }
         };
 
+        // Step s multiplies slab s, decodes slab s + 1 into LDS and sends for A of slab s + 3 and
+        // the codes of slab s + 4.  At its barrier the loads of the last two steps may be in
+        // flight: A of slab s and the codes of slab s + 1 are in LDS, and nobody reads the buffers
+        // any more that this step's loads and stores fill.  Codes that go through registers reach
+        // LDS a step later.
+        Ahead r;
+        Decoded d = {};
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        const int slabs = (int)((k1 - k0 + BK - 1) / BK);
-        if (slabs == 0) return;
-        load_a(k0);
-        load_b(k0);
-        tab[tid] = load_tab(k0);
-        tab[BK * MAXG + tid] = load_tab(k0 + BK);
-        __syncthreads();
-        store_a(lds);
-        decode(tab, lds);
-        for (int s = 0; s < slabs; ++s) {
-            __syncthreads();
-            const int64_t k = k0 + (int64_t)(s + 1) * BK;
-            const bool more = s + 1 < slabs;
-            Entry next = {0.f, 0.f};
-            if (more) {
-                load_a(k);
-                load_b(k);
-                next = load_tab(k + BK);
-            }
-            uint8_t* buf = lds + (s & 1) * BUF;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {                         // 32 rows each
-                u32x4_t bf[PB][NI], af[PA][NJ];
-#pragma unroll
-                for (int i = 0; i < NI; ++i)
-#pragma unroll
-                    for (int p = 0; p < PB; ++p)
-                        bf[p][i] = *reinterpret_cast<const u32x4_t*>(buf + PA * A_BYTES + p * B_BYTES + at(wc + 16 * i + n16, 4 * h + q));
-#pragma unroll
-                for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                    for (int p = 0; p < PA; ++p)
-                        af[p][j] = *reinterpret_cast<const u32x4_t*>(buf + p * A_BYTES + at(wt + 16 * j + n16, 4 * h + q));
-#pragma unroll
-                for (int i = 0; i < NI; ++i)
-#pragma unroll
-                    for (int j = 0; j < NJ; ++j) {
-                        acc[i][j] = mfma_f16(bf[0][i], af[0][j], acc[i][j]);
-                        if constexpr (PB == 2) acc[i][j] = mfma_f16(bf[1][i], af[0][j], acc[i][j]);
-                        if constexpr (PA == 2) acc[i][j] = mfma_f16(bf[0][i], af[1][j], acc[i][j]);
-                    }
-            }
-            if (more) {
-                uint8_t* to = lds + ((s + 1) & 1) * BUF;
-                store_a(to);
-                decode(tab + ((s + 1) & 1) * BK * MAXG, to);
-                tab[(s & 1) * BK * MAXG + tid] = next;
-            }
+        for (int k = 0; k < 4; ++k) {
+            if (k < 3) load_a(k);
+            load_c(k);
+            put_piece(k);
         }
+        wait_vm_lgkm0<0>();
+        barrier_only();
+        read_patch(r, 0);
+        decode_any(d, r, 0);
+        store(d, 0);
+        auto step = [&](auto K, int s) {
+            constexpr int k = decltype(K)::value;
+            wait_two_slabs(each);
+            barrier_only();
+            multiply(k, k & 1, (k + 1) & 3, d, r, [&] {
+                if (s > 0) put_piece((k + 3) & 3);
+                load_a((k + 3) & 3);
+                load_c(k);
+            });
+            if (__ballot(odd(r)) != 0) decode_any(d, r, s + 1);  // wave-uniform
+            store(d, (k + 1) & 1);                               // (behind the last slab: not used)
+        };
+        for (int s = 0; s < slabs; s += 4) {
+            step(std::integral_constant<int, 0>{}, s);
+            if (s + 1 < slabs) step(std::integral_constant<int, 1>{}, s + 1);
+            if (s + 2 < slabs) step(std::integral_constant<int, 2>{}, s + 2);
+            if (s + 3 < slabs) step(std::integral_constant<int, 3>{}, s + 3);
+        }
+        wait_vm_lgkm0<0>();                                      // no load into LDS outlives the workgroup
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) settle(acc[i][j]);
+            for (int j = 0; j < MT; ++j) settle(acc[i][j]);
     }
 
     // f(column, token of the call, the lane's 4 values from that column on, how many exist)
     template <typename F>
-    static GPTQ_DEV void each(const f32x4_t (&acc)[NI][NJ], int64_t tok0, int64_t end, int64_t c0, int64_t d_col, F&& f) {
+    static GPTQ_DEV void each(const f32x4_t (&acc)[NI][MT], int64_t tok0, int64_t end, int64_t c0, int64_t d_col, F&& f) {
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15, q = lane >> 4;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const int64_t t = tok0 + 64 * (wave & 1) + 16 * j + n16;
+        for (int j = 0; j < MT; ++j) {
+            const int64_t t = tok0 + 16 * MT * (wave / WC) + 16 * j + n16;
             if (t >= end) continue;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                const int64_t c = c0 + 64 * (wave >> 1) + 16 * i + 4 * q;
+                const int64_t c = c0 + 64 * (wave % WC) + 16 * i + 4 * q;
                 const int have = (int)(d_col - c < 4 ? d_col - c : 4);
                 if (have > 0) f(c, t, acc[i][j], have);
             }
@@ -221,28 +353,77 @@ struct BackGemm {
     }
 };
 
-static_assert(BackGemm<4, 1, 1>::MAXG * BK == 256, "a thread holds one entry of a slab's scales");
-
-// e_r: the exponent of the row's largest scale.  A wave per row.
-static __global__ __launch_bounds__(256) void row_exponents_kernel(const uint16_t* scales, int64_t rows, int n_groups, int8_t* e) {
-    const int lane = threadIdx.x & 63;
-    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (r >= rows) return;
-    int m = -1000;
-    for (int g = lane; g < n_groups; g += 64) {
-        const int v = exponent_of(f16_bits_to_f32(scales[r * n_groups + g]));
-        m = v > m ? v : m;
-    }
+// Four outputs, or those of them that exist, from element idx on.
+template <gptq_dtype T>
+GPTQ_DEV void store_four(void* y, int64_t idx, f32x4_t v, int have) {
+    if (have == 4 && T != GPTQ_F32) {
+        uint16_t h[4];
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) {
+        for (int i = 0; i < 4; ++i) store_as<T>(h, i, v[i]);
+        __builtin_memcpy(reinterpret_cast<uint16_t*>(y) + idx, h, 8);
+    } else if (have == 4) {
+        __builtin_memcpy(reinterpret_cast<float*>(y) + idx, &v, 16);
+    } else {
+        for (int i = 0; i < have; ++i) store_as<T>(y, idx + i, v[i]);
+    }
+}
+
+// e_r, the exponent of the row's largest scale, and the layer's Quads.  A workgroup takes 64
+// rows of an expert (blockIdx.y); rows behind the last have zeros.
+struct RowsArgs {
+    const uint16_t* scales; const uint16_t* zeros;
+    int64_t d_row; int n_groups;
+    int8_t* e; Quad* T; int64_t quads;
+};
+static __global__ __launch_bounds__(256) void rows_kernel(RowsArgs a) {
+    __shared__ int es[64];
+    const int tid = threadIdx.x;
+    const int64_t row0 = (int64_t)blockIdx.x * 64, base = blockIdx.y * a.d_row;
+    const int64_t r = row0 + (tid >> 2);
+    int m = -1000;
+    if (r < a.d_row)
+        for (int g = tid & 3; g < a.n_groups; g += 4) {
+            const int v = exponent_of(f16_bits_to_f32(a.scales[(base + r) * a.n_groups + g]));
+            m = v > m ? v : m;
+        }
+#pragma unroll
+    for (int o = 2; o >= 1; o >>= 1) {
         const int v = __shfl_xor(m, o);
         m = v > m ? v : m;
     }
-    if (lane == 0) e[r] = (int8_t)(m == -1000 ? 0 : m);
+    if (m == -1000) m = 0;
+    if ((tid & 3) == 0) {
+        es[tid >> 2] = m;
+        if (r < a.d_row) a.e[base + r] = (int8_t)m;
+    }
+    __syncthreads();
+    for (int i = tid; i < 16 * a.n_groups; i += 256) {
+        const int quad = i & 15, g = i >> 4;
+        uint32_t S[4], z4[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t row = row0 + 4 * quad + j;
+            S[j] = 0;
+            z4[j] = 0x6400u;
+            if (row < a.d_row) {
+                const int64_t at = (base + row) * a.n_groups + g;
+                S[j] = f32_to_f16_bits(ldexpf(f16_bits_to_f32(a.scales[at]), -es[4 * quad + j]));
+                const float z = f16_bits_to_f32(a.zeros[at]);
+                const bool plain = z >= -1024.f && z <= 1024.f && rintf(z) == z;
+                z4[j] = plain ? f32_to_f16_bits(1024.f + z) : 0x8000u;
+            }
+        }
+        a.T[((int64_t)blockIdx.y * a.n_groups + g) * a.quads + row0 / 4 + quad] =
+            Quad{S[0] | (S[1] << 16), z4[0] | (z4[1] << 16), S[2] | (S[3] << 16), z4[2] | (z4[3] << 16)};
+    }
 }
 
-inline void row_exponents(const Stored& L, int64_t rows, int8_t* e, hipStream_t s) {
-    row_exponents_kernel<<<(unsigned)((rows + 3) / 4), 256, 0, s>>>(L.scales, rows, L.n_groups, e);
+inline int64_t quads_of(int64_t d_row) { return (d_row + 63) / 64 * 16; }
+inline size_t quads_bytes(int64_t E, int64_t d_row, int64_t n_groups) { return (size_t)(E * n_groups * quads_of(d_row)) * sizeof(Quad); }
+
+inline void rows_launch(const Stored& L, int64_t E, int64_t d_row, int8_t* e, Quad* T, hipStream_t s) {
+    const RowsArgs a = {L.scales, L.zeros, d_row, L.n_groups, e, T, quads_of(d_row)};
+    rows_kernel<<<dim3((unsigned)((d_row + 63) / 64), (unsigned)E), 256, 0, s>>>(a);
 }
 
 }  // namespace gptq

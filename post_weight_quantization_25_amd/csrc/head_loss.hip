@@ -50,11 +50,11 @@ static HeadPlan plan_of(int64_t nc, int64_t d, int64_t vocab, bool grad) {
 
 struct HeadBuffers {
     float* z;                                                   // nc x R span
-    uint16_t* A[2];                                             // the same in fp16
+    uint16_t* A[2];                                             // exp(z - m) in fp16: [slab of 32 words][token][32]
     float* O;                                                   // R x nc x d
     float* m; float* s; float* f;                               // R x nc
     float* picked;                                              // nc x k
-    int8_t* e;                                                  // vocab
+    int8_t* e; Quad* T;                                         // vocab; d / 32 groups of quads_of(vocab) at most
     int32_t* emax;                                              // of blocks of rows
 };
 constexpr int EB = 1024;                                        // rows per block of emax
@@ -68,12 +68,13 @@ static size_t layout(HeadBuffers* b, uint8_t* w, int64_t nc, int64_t rows, int64
     h.z = (float*)take(zs * 4);
     h.m = (float*)take((size_t)rows * 4); h.s = (float*)take((size_t)rows * 4); h.f = (float*)take((size_t)rows * 4);
     h.picked = (float*)take((size_t)(nc * k) * 4);
-    h.A[0] = h.A[1] = nullptr; h.O = nullptr; h.e = nullptr; h.emax = nullptr;
+    h.A[0] = h.A[1] = nullptr; h.O = nullptr; h.e = nullptr; h.T = nullptr; h.emax = nullptr;
     if (grad) {
         h.A[0] = (uint16_t*)take(zs * 2);
         h.A[1] = (uint16_t*)take(zs * 2);
         h.O = (float*)take((size_t)(rows * d) * 4);
         h.e = (int8_t*)take((size_t)vocab);
+        h.T = (Quad*)take(quads_bytes(1, vocab, (d + 31) / 32));
         h.emax = (int32_t*)take((size_t)((vocab + EB - 1) / EB) * 4);
     }
     if (b) *b = h;
@@ -216,7 +217,7 @@ __global__ __launch_bounds__(256) void head_stats_kernel(HeadArgs a) {
         }
         if constexpr (PA != 0) {
             if (w < a.span) {
-                const int64_t to = t * ldz + slot * a.span + w;
+                const int64_t to = ((slot * a.span + w) / BK * a.n + t) * BK + w % BK;
                 uint2 o;
                 o.x = hi[0] | ((uint32_t)hi[1] << 16); o.y = hi[2] | ((uint32_t)hi[3] << 16);
                 *reinterpret_cast<uint2*>(a.b.A[0] + to) = o;
@@ -235,21 +236,33 @@ __global__ __launch_bounds__(256) void head_stats_kernel(HeadArgs a) {
     }
 }
 
-template <int CB, int P>
-__global__ __launch_bounds__(256, P == 1 ? 2 : 1) void head_sums_kernel(BackArgs a, int gm, int gn, int64_t vocab, int64_t span, int v_first) {
-    typedef BackGemm<CB, P, P> G;
+template <int CB, int P, int MT, int WC, bool DIRECT>
+__global__ __launch_bounds__(128 * WC, P == 1 || MT == 1 ? 2 : 1) void head_sums_kernel(BackArgs a, int gm, int gn, int64_t vocab, int64_t span, int v_first) {
+    typedef BackGemm<CB, P, P, MT, 2, WC, DIRECT> G;
     __shared__ __align__(16) uint8_t lds[G::LDS_BYTES];
-    const int tm = blockIdx.x % gm, tn = blockIdx.x / gm, slot = blockIdx.y;
+    int tm, tn;
+    tile_of(gm, gn, tm, tn);
+    const int slot = blockIdx.y;
     const int64_t tok0 = (int64_t)tm * G::BM, c0 = (int64_t)tn * G::BN;
     const int64_t k0 = v_first + slot * span, k1 = k0 + span < vocab ? k0 + span : vocab;
-    f32x4_t acc[G::NI][G::NJ];
-    G::run(acc, a, a.L, a.e, tok0, a.n, c0, k0, k1, lds);
+    f32x4_t acc[G::NI][MT];
+    G::run(acc, a, a.L, a.T, tok0, a.n, c0, k0, k1, lds);
     float* O = a.acc + (int64_t)slot * a.n * a.L.d_col;
     const float* f = a.f + (int64_t)slot * a.n;
     G::each(acc, tok0, a.n, c0, a.L.d_col, [&](int64_t c, int64_t t, f32x4_t v, int have) {
         float* o = O + t * a.L.d_col + c;
         const float g = f[t];
-        for (int i = 0; i < have; ++i) o[i] = a.first || g == 0.f ? v[i] : fmaf(o[i], g, v[i]);
+        if (!a.first && g != 0.f) {
+            if (have == 4) {
+                f32x4_t was;
+                __builtin_memcpy(&was, o, 16);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = fmaf(was[i], g, v[i]);
+            } else {
+                for (int i = 0; i < have; ++i) v[i] = fmaf(o[i], g, v[i]);
+            }
+        }
+        store_four<GPTQ_F32>(o, 0, v, have);
     });
 }
 
@@ -354,12 +367,26 @@ __global__ __launch_bounds__(256) void head_final_kernel(HeadArgs a) {
     }
 }
 
+template <int CB, int P, int MT, int WC>
+static void launch_tiles(const BackArgs& b, int slots, int64_t vocab, int64_t span, int first_word, hipStream_t s) {
+    typedef BackGemm<CB, P, P, MT, 2, WC, true> G;
+    const int gm = (int)((b.n + G::BM - 1) / G::BM), gn = (int)((b.L.d_col + G::BN - 1) / G::BN);
+    const dim3 grid((unsigned)(gm * gn), (unsigned)slots);
+    if (direct_codes(b.L)) head_sums_kernel<CB, P, MT, WC, true><<<grid, G::THREADS, 0, s>>>(b, gm, gn, vocab, span, first_word);
+    else head_sums_kernel<CB, P, MT, WC, false><<<grid, G::THREADS, 0, s>>>(b, gm, gn, vocab, span, first_word);
+}
+
+template <int CB, int P>
+static void launch_parts(const BackArgs& b, int slots, int64_t vocab, int64_t span, int first_word, hipStream_t s) {
+    if (b.n > 128) launch_tiles<CB, P, P == 1 ? 8 : 4, P == 1 ? 4 : 2>(b, slots, vocab, span, first_word, s);
+    else if (b.n > 32) launch_tiles<CB, P, 4, 2>(b, slots, vocab, span, first_word, s);
+    else launch_tiles<CB, P, 1, 2>(b, slots, vocab, span, first_word, s);
+}
+
 template <int CB>
 static void launch_sums(const BackArgs& b, int parts, int slots, int64_t vocab, int64_t span, int first_word, hipStream_t s) {
-    const int gm = (int)((b.n + 127) / 128), gn = (int)((b.L.d_col + 127) / 128);
-    const dim3 grid((unsigned)(gm * gn), (unsigned)slots);
-    if (parts == 1) head_sums_kernel<CB, 1><<<grid, 256, 0, s>>>(b, gm, gn, vocab, span, first_word);
-    else head_sums_kernel<CB, 2><<<grid, 256, 0, s>>>(b, gm, gn, vocab, span, first_word);
+    if (parts == 1) launch_parts<CB, 1>(b, slots, vocab, span, first_word, s);
+    else launch_parts<CB, 2>(b, slots, vocab, span, first_word, s);
 }
 
 gptq_status head_launch(const HeadCall& c, hipStream_t s) {
@@ -376,7 +403,7 @@ gptq_status head_launch(const HeadCall& c, hipStream_t s) {
         layout(&a.b, (uint8_t*)c.ws, nc, nc * p.R, p.span, d, c.vocab, c.k, grad);
         a.n = nc; a.tok0 = tok0; a.R = p.R; a.span = p.span;
         if (grad) {
-            row_exponents(c.L, c.vocab, a.b.e, s);
+            rows_launch(c.L, 1, c.vocab, a.b.e, a.b.T, s);
             head_emax_kernel<<<(unsigned)a.blocks, 256, 0, s>>>(a.b.e, c.vocab, a.b.emax);
             GPTQ_LAUNCH_CHECK();
         }
@@ -402,8 +429,8 @@ gptq_status head_launch(const HeadCall& c, hipStream_t s) {
             GPTQ_LAUNCH_CHECK();
             if (grad) {
                 BackArgs b = {};
-                b.L = c.L; b.d_row = c.vocab; b.e = a.b.e;
-                b.A[0] = a.b.A[0]; b.A[1] = a.b.A[1]; b.lda = p.R * p.span; b.a0 = v0;
+                b.L = c.L; b.d_row = c.vocab; b.T = a.b.T; b.quads = quads_of(c.vocab);
+                b.A[0] = a.b.A[0]; b.A[1] = a.b.A[1]; b.a0 = v0;
                 b.n = nc; b.acc = a.b.O; b.f = a.b.f; b.first = round == 0;
                 if (c.bits == 3) launch_sums<3>(b, parts, slots, c.vocab, p.span, (int)v0, s);
                 else if (c.bits == 4) launch_sums<4>(b, parts, slots, c.vocab, p.span, (int)v0, s);
