@@ -35,13 +35,13 @@ struct BackArgs {
     // rounded outputs: out = acc 2^-shift[t]
     void* y; gptq_dtype yt;
     const int32_t* shift;
-    // or running sums in fp32, one buffer per share of the rows: out = out f[t] + acc
-    float* acc; const float* f; int64_t share; int first;
+    // or sums in fp32, a buffer per share of the rows: out = acc, or from the second round on out f[t] + acc
+    float* sums; int64_t share; const float* f; int first;
 };
 
 // log2 of the power of two below |v|: of a subnormal too; a zero or no number: -1000.
 GPTQ_DEV int exponent_of(float v) {
-    return v == 0.f || !(fabsf(v) < INFINITY) ? -1000 : ilogbf(v);
+    return v == 0.f || !(fabsf(v) < INFINITY) ? -1000 : __builtin_amdgcn_frexp_expf(v) - 1;
 }
 
 // v 2^k in fp16 parts: the nearest, and the nearest to what it leaves.
@@ -68,16 +68,6 @@ GPTQ_DEV void barrier_only() {
     asm volatile("" ::: "memory");
 }
 
-// Waits until at most the wave's loads of the last two slabs are in flight: `each` per slab, or
-// the largest number below that the code has a wait for.
-GPTQ_DEV void wait_two_slabs(int each) {
-    if (each >= 6) wait_vm_lgkm0<12>();
-    else if (each >= 4) wait_vm_lgkm0<8>();
-    else if (each == 3) wait_vm_lgkm0<6>();
-    else if (each == 2) wait_vm_lgkm0<4>();
-    else wait_vm_lgkm0<2>();                                    // (0: nothing is in flight)
-}
-
 // DIRECT: the codes' rows are whole and aligned 16 bytes (direct_codes) and go straight to LDS.
 inline bool direct_codes(const Stored& L) { return ((reinterpret_cast<uintptr_t>(L.codes) | (uintptr_t)L.code_ld) & 15) == 0; }
 
@@ -87,8 +77,9 @@ struct BackGemm {
     static constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2;
     static constexpr int ROW = BN * CB / 8, PIECES = ROW / 16, C_BYTES = BK * ROW, T_BYTES = 1024;   // codes of a slab; its Quads
     static constexpr int BUFS = 4;
-    static constexpr int LDS_BYTES = BUFS * (PA * A_BYTES + C_BYTES + T_BYTES) + 2 * PB * B_BYTES;
+    static constexpr int LDS_BYTES = BUFS * (PA * A_BYTES + C_BYTES + 2 * T_BYTES) + 2 * PB * B_BYTES;
     static constexpr int AP = BM / 16 / WAVES > 0 ? BM / 16 / WAVES : 1;   // loads of a plane's slab per wave: 16 tokens each
+    static constexpr bool ALL_C = BK * PIECES == THREADS;       // every wave loads codes
     static_assert(WT == 2 && BK * PIECES <= THREADS, "a thread decodes one patch of 4 rows x 4 columns and copies at most one piece");
 
     // acc[i][j]: lane l's value v is column 64 (wave % WC) + 16 i + 4 (l / 16) + v, token 16 MT (wave / WC) + 16 j + l % 16.
@@ -102,23 +93,24 @@ struct BackGemm {
         const int slabs = (int)((k1 - k0 + BK - 1) / BK);
         uint8_t* bb = lds + BUFS * PA * A_BYTES;
         uint8_t* cc = bb + 2 * PB * B_BYTES;
-        uint8_t* tt = cc + BUFS * C_BYTES;
+        uint8_t* tt = cc + BUFS * C_BYTES;                       // two turns of four slabs
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
             for (int j = 0; j < MT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         if (slabs <= 0) return;
 
-        // Wave w loads tokens 16 (w + WAVES j) .. + 15 of A: 4 lines of slab_at, lane l the line's piece l % 16.
+        // Wave w loads tokens 16 (w + WAVES j) .. + 15 of A: 4 lines of slab_at, lane l the line's
+        // piece l % 16.  (Few tokens: several waves the same ones, so that all count alike.)
+        const int block = BM / 16 < WAVES ? wave % (BM / 16) : wave;
         uint32_t aoff[AP];
 #pragma unroll
         for (int j = 0; j < AP; ++j) {
-            const int line = 4 * (wave + WAVES * j) + (lane >> 4), x = (lane & 15) ^ line_swizzle(line);
+            const int line = 4 * (block + WAVES * j) + (lane >> 4), x = (lane & 15) ^ line_swizzle(line);
             int m = 4 * line + (x >> 2);
             if (tok0 + m >= end) m = (int)(end - 1 - tok0);
             aoff[j] = (uint32_t)m * (2 * BK) + 16 * (x & 3);
         }
-        const bool loads_a = BM / 16 >= WAVES || wave < BM / 16;
         const uint8_t* a_next[PA];
 #pragma unroll
         for (int p = 0; p < PA; ++p) a_next[p] = reinterpret_cast<const uint8_t*>(a.A[p] + ((k0 - a.a0) / BK * a.n + tok0) * BK);
@@ -134,37 +126,34 @@ struct BackGemm {
         const uint8_t* c_next = L.codes + k0 * L.code_ld + c0 * CB / 8;
         const uint8_t* c_end = L.codes + a.d_row * L.code_ld;
 
-        // Quads: lane 8 g + quad of the last wave, group g of the tile's.
+        // Quads: lane 8 g + quad, group g of the tile's; wave w those of slab w % 4 of a turn.  Behind
+        // the last slab the zeros that end a group's, so that turns are whole.
         const int64_t tg = (c0 >> gs) + (lane >> 3) < L.n_groups ? lane >> 3 : L.n_groups - 1 - (c0 >> gs);
         const uint32_t toff = (uint32_t)(((gs >= 30 ? 0 : tg) * a.quads + (lane & 7)) * (int64_t)sizeof(Quad));
-        const Quad* t_next = T + (c0 >> gs) * a.quads + k0 / 4;
-        const bool loads_t = wave == WAVES - 1;
+        const Quad* t_first = T + (c0 >> gs) * a.quads;
 
         const uint32_t m_lds = lds_addr(reinterpret_cast<const uint16_t*>(lds));
-        const uint32_t m_a = m_lds + wave * 1024, m_c = m_lds + (uint32_t)(cc - lds) + wave * 1024, m_t = m_lds + (uint32_t)(tt - lds);
-        const int each = (loads_a ? PA * AP : 0) + (loads_c ? 1 : 0) + (loads_t ? 1 : 0);
+        const uint32_t m_a = m_lds + block * 1024, m_c = m_lds + (uint32_t)(cc - lds) + wave * 1024, m_t = m_lds + (uint32_t)(tt - lds) + (wave & 3) * T_BYTES;
         const int64_t a_step = a.n * (2 * BK), c_step = BK * L.code_ld;
 
-        // Behind the last slab that one is loaded again, so that every step counts the same loads.
-        int a_at = 0, c_at = 0;
+        // Behind the last slab that one is loaded again.
+        int a_left = slabs - 1, c_left = slabs - 1;
         auto load_a = [&](int buf) {
-            if (loads_a) {
 #pragma unroll
-                for (int p = 0; p < PA; ++p)
+            for (int p = 0; p < PA; ++p)
 #pragma unroll
-                    for (int j = 0; j < AP; ++j) dma16<0>(aoff[j], a_next[p], m_a + (buf * PA + p) * A_BYTES + j * (WAVES * 1024));
-            }
-            const bool last = a_at == slabs - 1;                 // uniform
-            a_at += last ? 0 : 1;
+                for (int j = 0; j < AP; ++j) dma16<0>(aoff[j], a_next[p], m_a + (buf * PA + p) * A_BYTES + j * (WAVES * 1024));
+            const int64_t by = a_left > 0 ? a_step : 0;
+            --a_left;
 #pragma unroll
-            for (int p = 0; p < PA; ++p) a_next[p] += last ? 0 : a_step;
+            for (int p = 0; p < PA; ++p) a_next[p] += by;
         };
         u32x4_t piece = {0u, 0u, 0u, 0u};                        // codes on their way through registers
         auto load_c = [&](int buf) {
-            const bool last = c_at == slabs - 1;                 // uniform
-            const uint32_t off = last ? coff_last : coff;
+            const bool more = c_left > 0;                        // uniform
+            const uint32_t off = more ? coff : coff_last;
             if constexpr (DIRECT) {
-                if (loads_c && has_piece) dma16<0>(off, c_next, m_c + buf * C_BYTES);
+                if (ALL_C || (loads_c && has_piece)) dma16<0>(off, c_next, m_c + buf * C_BYTES);
             } else if (has_piece) {
                 const uint8_t* src = c_next + off;
                 if (c_end - src >= 16) {
@@ -177,10 +166,12 @@ struct BackGemm {
                     piece = u32x4_t{w[0], w[1], w[2], w[3]};
                 }
             }
-            if (loads_t) dma16<0>(toff, t_next, m_t + buf * T_BYTES);
-            c_at += last ? 0 : 1;
-            c_next += last ? 0 : c_step;
-            t_next += last ? 0 : BK / 4;
+            --c_left;
+            c_next += more ? c_step : 0;
+        };
+        auto load_t = [&](int turn) {                            // slabs 4 turn ..
+            const int s = 4 * turn + (wave & 3);
+            dma16<0>(toff, t_first + (s < slabs ? k0 / 4 + (int64_t)s * (BK / 4) : a.quads - 16), m_t + (turn & 1) * (4 * T_BYTES));
         };
         auto put_piece = [&](int buf) {
             if (!DIRECT && has_piece) *reinterpret_cast<u32x4_t*>(cc + buf * C_BYTES + 16 * tid) = piece;
@@ -191,8 +182,8 @@ struct BackGemm {
         const int pg = gs >= 30 ? 0 : (4 * cp) >> gs;            // the patch's group (a tile starts a group)
         const uint8_t* patch = cc + 4 * rp * ROW + (CB == 3 ? (12 * cp / 32) * 4 : 4 * cp * CB / 8);
         struct Ahead { uint32_t b[4]; u32x4_t t; };              // codes of 4 columns of 4 rows, their Quad
-        auto read_patch = [&](Ahead& r, int buf) {
-            r.t = *reinterpret_cast<const u32x4_t*>(tt + buf * T_BYTES + (8 * pg + rp) * 16);
+        auto read_patch = [&](Ahead& r, int buf, int turn) {
+            r.t = *reinterpret_cast<const u32x4_t*>(tt + ((turn & 1) * 4 + buf) * T_BYTES + (8 * pg + rp) * 16);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const uint8_t* at = patch + buf * C_BYTES + j * ROW;
@@ -257,7 +248,7 @@ struct BackGemm {
         // The products of a slab, a token tile after the other, and in between the next slab's
         // codes: fragments are read two tiles ahead, and a tile's products are issued with a share
         // of the decoding, so that both units are fed.
-        auto multiply = [&](int abuf, int bbuf, int next, Decoded& d, Ahead& r, auto&& loads) {
+        auto multiply = [&](int abuf, int bbuf, int next, int turn, Decoded& d, Ahead& r, auto&& loads) {
             constexpr int RING = MT < 3 ? MT : 3;
             u32x4_t bf[PB][NI], af[RING][PA];
             auto read_a = [&](int j) {
@@ -272,7 +263,7 @@ struct BackGemm {
                     bf[p][i] = *reinterpret_cast<const u32x4_t*>(bb + (bbuf * PB + p) * B_BYTES + slab_at(wc + 16 * i + n16, q));
 #pragma unroll
             for (int j = 0; j < RING - 1; ++j) read_a(j);
-            read_patch(r, next);
+            read_patch(r, next, turn);
             __builtin_amdgcn_sched_barrier(0);
             loads();
             __builtin_amdgcn_sched_barrier(0);
@@ -293,12 +284,14 @@ struct BackGemm {
         };
 
         // Step s multiplies slab s, decodes slab s + 1 into LDS and sends for A of slab s + 3 and
-        // the codes of slab s + 4.  At its barrier the loads of the last two steps may be in
-        // flight: A of slab s and the codes of slab s + 1 are in LDS, and nobody reads the buffers
-        // any more that this step's loads and stores fill.  Codes that go through registers reach
-        // LDS a step later.
+        // the codes of slab s + 4 (Quads: a turn of four slabs at its first step).  At its barrier
+        // the loads of the last two steps may be in flight: A of slab s and the codes of slab s + 1
+        // are in LDS, and nobody reads the buffers any more that this step's loads and stores fill.
+        // Codes that go through registers reach LDS a step later.  A step has no branch but those
+        // for odd zeros and for waves without codes: with 8 waves in step a taken branch costs all.
         Ahead r;
         Decoded d = {};
+        load_t(0);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             if (k < 3) load_a(k);
@@ -307,26 +300,28 @@ struct BackGemm {
         }
         wait_vm_lgkm0<0>();
         barrier_only();
-        read_patch(r, 0);
+        read_patch(r, 0, 0);
         decode_any(d, r, 0);
         store(d, 0);
-        auto step = [&](auto K, int s) {
+        const int turns = (slabs + 3) / 4;
+        auto step = [&](auto K, int turn) {
             constexpr int k = decltype(K)::value;
-            wait_two_slabs(each);
+            wait_vm_lgkm0<2 * PA * AP>();
             barrier_only();
-            multiply(k, k & 1, (k + 1) & 3, d, r, [&] {
-                if (s > 0) put_piece((k + 3) & 3);
+            multiply(k, k & 1, (k + 1) & 3, turn + (k == 3), d, r, [&] {
+                if (k != 0 || turn > 0) put_piece((k + 3) & 3);
                 load_a((k + 3) & 3);
                 load_c(k);
+                if (k == 0) load_t(turn + 1);
             });
-            if (__ballot(odd(r)) != 0) decode_any(d, r, s + 1);  // wave-uniform
+            if (__builtin_expect(__ballot(odd(r)) != 0, 0)) decode_any(d, r, 4 * turn + k + 1);   // wave-uniform
             store(d, (k + 1) & 1);                               // (behind the last slab: not used)
         };
-        for (int s = 0; s < slabs; s += 4) {
-            step(std::integral_constant<int, 0>{}, s);
-            if (s + 1 < slabs) step(std::integral_constant<int, 1>{}, s + 1);
-            if (s + 2 < slabs) step(std::integral_constant<int, 2>{}, s + 2);
-            if (s + 3 < slabs) step(std::integral_constant<int, 3>{}, s + 3);
+        for (int turn = 0; turn < turns; ++turn) {
+            step(std::integral_constant<int, 0>{}, turn);
+            step(std::integral_constant<int, 1>{}, turn);
+            step(std::integral_constant<int, 2>{}, turn);
+            step(std::integral_constant<int, 3>{}, turn);
         }
         wait_vm_lgkm0<0>();                                      // no load into LDS outlives the workgroup
 #pragma unroll
@@ -418,12 +413,13 @@ static __global__ __launch_bounds__(256) void rows_kernel(RowsArgs a) {
     }
 }
 
-inline int64_t quads_of(int64_t d_row) { return (d_row + 63) / 64 * 16; }
+// A group's Quads: of rows up to whole 64, and 64 rows of zeros.
+inline int64_t quads_of(int64_t d_row) { return (d_row + 63) / 64 * 16 + 16; }
 inline size_t quads_bytes(int64_t E, int64_t d_row, int64_t n_groups) { return (size_t)(E * n_groups * quads_of(d_row)) * sizeof(Quad); }
 
 inline void rows_launch(const Stored& L, int64_t E, int64_t d_row, int8_t* e, Quad* T, hipStream_t s) {
     const RowsArgs a = {L.scales, L.zeros, d_row, L.n_groups, e, T, quads_of(d_row)};
-    rows_kernel<<<dim3((unsigned)((d_row + 63) / 64), (unsigned)E), 256, 0, s>>>(a);
+    rows_kernel<<<dim3((unsigned)((d_row + 63) / 64 + 1), (unsigned)E), 256, 0, s>>>(a);
 }
 
 }  // namespace gptq

@@ -1,12 +1,15 @@
 // The gradient through products grouped by expert (gptqt_linear_grouped_backward):
 //   dx[t] = What_e^T dy[t] for the rows t of expert e.
 //
-// Three launches: the rows' exponents; dy as fp16 rows (back_pack_kernel), each element times
+// Launches: the rows' exponents and Quads; dy as fp16 rows (back_pack_kernel), each element times
 // its weight row's power of two and all of a token's times one, which brings the largest to
 // 2^14 .. 2^15: bfloat16 and fp16 elements down to 2^-28 of it are themselves, smaller ones are
-// off by 2^-39 of it at most; the product (back_gemm.h).
+// off by 2^-39 of it at most; the product (back_gemm.h).  Where its tiles would leave CUs
+// without work, the weight rows are split among workgroups, whose fp32 sums back_join_kernel
+// adds in order.
 
 #include <stdlib.h>
+
 #include "back_gemm.h"
 
 namespace gptq {
@@ -18,17 +21,39 @@ struct PackArgs {
     uint16_t* A; int64_t lda; int32_t* shift;
 };
 
+// A workgroup per row, 8 elements per thread and step.
 template <gptq_dtype T>
 __global__ __launch_bounds__(256) void back_pack_kernel(PackArgs a) {
+    constexpr int X = T == GPTQ_BF16 ? X_BF16 : X_F16;
     __shared__ int red[4];
     Segment s;
-    if (!segment_of(a.offsets, a.E, a.n, 1, (int)blockIdx.x, s)) return;   // tiles of one row: only rows of experts
+    if (!segment_of(a.offsets, a.E, a.n, 1, (int)blockIdx.x, s)) return;   // tiles of one row: rows of experts alone
     const int64_t t = s.tok0;
     const int8_t* e = a.e + (int64_t)s.e * a.d_row;
+    const uint16_t* row = reinterpret_cast<const uint16_t*>(a.dy) + t * a.ldy;
+    auto eight = [&](int64_t r, float (&v)[8], int (&ev)[8]) {
+        const int have = (int)(a.d_row - r < 8 ? a.d_row - r : 8);
+        load_x8<X>(row + r, have, v);
+        if (have == 8) {
+            int8_t b[8];
+            __builtin_memcpy(b, e + r, 8);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ev[i] = b[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ev[i] = i < have ? e[r + i] : 0;
+        }
+    };
     int m = -1000;
-    for (int64_t r = threadIdx.x; r < a.d_row; r += 256) {
-        const int v = exponent_of(load_as_f32<T>(a.dy, t * a.ldy + r)) + e[r];
-        m = v > m ? v : m;
+    for (int64_t r = 8 * threadIdx.x; r < a.d_row; r += 2048) {
+        float v[8];
+        int ev[8];
+        eight(r, v, ev);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int k = exponent_of(v[i]) + ev[i];
+            m = k > m ? k : m;
+        }
     }
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) {
@@ -37,15 +62,31 @@ __global__ __launch_bounds__(256) void back_pack_kernel(PackArgs a) {
     }
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
     __syncthreads();
-    m = red[0];
 #pragma unroll
-    for (int w = 1; w < 4; ++w) m = red[w] > m ? red[w] : m;
+    for (int w = 0; w < 4; ++w) m = red[w] > m ? red[w] : m;
     const int k = m < -900 ? 0 : 14 - m;                         // nothing but zeros
     if (threadIdx.x == 0) a.shift[t] = k;
-    for (int64_t r = threadIdx.x; r < a.lda; r += 256) {
-        const float v = r < a.d_row ? ldexpf(load_as_f32<T>(a.dy, t * a.ldy + r), e[r] + k) : 0.f;
-        a.A[((r / BK) * a.n + t) * BK + r % BK] = f32_to_f16_bits(v);
+    for (int64_t r = 8 * threadIdx.x; r < a.lda; r += 2048) {
+        u32x4_t o = {0u, 0u, 0u, 0u};
+        if (r < a.d_row) {
+            float v[8];
+            int ev[8];
+            eight(r, v, ev);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                o[i] = f32_to_f16_bits(__builtin_amdgcn_ldexpf(v[2 * i], ev[2 * i] + k)) |
+                       ((uint32_t)f32_to_f16_bits(__builtin_amdgcn_ldexpf(v[2 * i + 1], ev[2 * i + 1] + k)) << 16);
+        }
+        *reinterpret_cast<u32x4_t*>(a.A + ((r / BK) * a.n + t) * BK + r % BK) = o;
     }
+}
+
+GPTQ_DEV void store_scaled(const BackArgs& a, int64_t at, f32x4_t v, int k, int have) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = ldexpf(v[i], k);
+    if (a.yt == GPTQ_F32) store_four<GPTQ_F32>(a.y, at, v, have);
+    else if (a.yt == GPTQ_BF16) store_four<GPTQ_BF16>(a.y, at, v, have);
+    else store_four<GPTQ_F16>(a.y, at, v, have);
 }
 
 template <int CB, int PB, int MT, int WC, bool DIRECT>
@@ -56,26 +97,62 @@ __global__ __launch_bounds__(128 * WC, 2) void back_gemm_kernel(BackArgs a, int 
     tile_of(gm, gn, tm, tn);
     Segment s;
     if (!segment_of(a.offsets, a.E, a.n, G::BM, tm, s)) return;
-    const int64_t c0 = (int64_t)tn * G::BN;
+    const int64_t c0 = (int64_t)tn * G::BN, k0 = blockIdx.y * a.share, k1 = k0 + a.share < a.d_row ? k0 + a.share : a.d_row;
     f32x4_t acc[G::NI][MT];
-    G::run(acc, a, expert_of(a.L, a.d_row, s.e), a.T + s.e * a.quads * a.L.n_groups, s.tok0, s.end, c0, 0, a.d_row, lds);
+    G::run(acc, a, expert_of(a.L, a.d_row, s.e), a.T + s.e * a.quads * a.L.n_groups, s.tok0, s.end, c0, k0, k1, lds);
+    float* sums = a.sums ? a.sums + blockIdx.y * a.n * a.L.d_col : nullptr;
     G::each(acc, s.tok0, s.end, c0, a.L.d_col, [&](int64_t c, int64_t t, f32x4_t v, int have) {
-        const int k = -a.shift[t];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = ldexpf(v[i], k);
         const int64_t at = t * a.L.d_col + c;
-        if (a.yt == GPTQ_F32) store_four<GPTQ_F32>(a.y, at, v, have);
-        else if (a.yt == GPTQ_BF16) store_four<GPTQ_BF16>(a.y, at, v, have);
-        else store_four<GPTQ_F16>(a.y, at, v, have);
+        if (sums) store_four<GPTQ_F32>(sums, at, v, have);
+        else store_scaled(a, at, v, -a.shift[t], have);
     });
 }
 
+// The shares' sums of one row of an expert.
+__global__ __launch_bounds__(256) void back_join_kernel(BackArgs a, int shares) {
+    Segment s;
+    if (!segment_of(a.offsets, a.E, a.n, 1, (int)blockIdx.x, s)) return;
+    const int64_t t = s.tok0, c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4;
+    const int have = (int)(a.L.d_col - c < 4 ? a.L.d_col - c : 4);
+    if (have <= 0) return;
+    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < shares; ++i) {
+        const float* p = a.sums + (i * a.n + t) * a.L.d_col + c;
+        if (have == 4) {
+            f32x4_t w;
+            __builtin_memcpy(&w, p, 16);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] += w[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+                if (j < have) v[j] += p[j];
+        }
+    }
+    store_scaled(a, t * a.L.d_col + c, v, -a.shift[t], have);
+}
+
+// Shares of the weight rows: workgroups for every place there is for a tile, none below 256 rows.
+constexpr int64_t MOST_SUMS = (int64_t)64 << 20;                // bytes of all shares' sums
+static int shares_of(int64_t tiles, int64_t places, int64_t d_row) {
+    int64_t s = places / tiles;
+    if (s > (d_row + 255) / 256) s = (d_row + 255) / 256;
+    return (int)(s < 1 ? 1 : s);
+}
+
 template <int CB, int PB, int MT, int WC>
-static void launch_tiles(const BackArgs& a, hipStream_t s) {
+static void launch_tiles(BackArgs a, int places, hipStream_t s) {
     typedef BackGemm<CB, 1, PB, MT, 2, WC, true> G;
     const int gm = (int)most_tiles(a.offsets, a.E, a.n, G::BM), gn = (int)((a.L.d_col + G::BN - 1) / G::BN);
-    if (direct_codes(a.L)) back_gemm_kernel<CB, PB, MT, WC, true><<<(unsigned)(gm * gn), G::THREADS, 0, s>>>(a, gm, gn);
-    else back_gemm_kernel<CB, PB, MT, WC, false><<<(unsigned)(gm * gn), G::THREADS, 0, s>>>(a, gm, gn);
+    int shares = shares_of((int64_t)gm * gn, places, a.d_row);
+    while (shares > 1 && shares * a.n * a.L.d_col * 4 > MOST_SUMS) --shares;
+    a.share = ((a.d_row + shares - 1) / shares + 63) / 64 * 64;
+    shares = (int)((a.d_row + a.share - 1) / a.share);
+    if (shares == 1) a.sums = nullptr;
+    const dim3 grid((unsigned)(gm * gn), (unsigned)shares);
+    if (direct_codes(a.L)) back_gemm_kernel<CB, PB, MT, WC, true><<<grid, G::THREADS, 0, s>>>(a, gm, gn);
+    else back_gemm_kernel<CB, PB, MT, WC, false><<<grid, G::THREADS, 0, s>>>(a, gm, gn);
+    if (shares > 1) back_join_kernel<<<dim3((unsigned)a.n, (unsigned)((a.L.d_col + 1023) / 1024)), 256, 0, s>>>(a, shares);
 }
 
 template <int CB, int PB>
@@ -83,10 +160,9 @@ static void launch_parts(const BackArgs& a, hipStream_t s) {
     const int64_t each = (a.n + a.E - 1) / a.E;
     const char* force = getenv("BACK_TILE");
     const int f = force ? atoi(force) : 0;
-    if constexpr (PB == 1) if (f == 256 || (!f && each > 128)) return launch_tiles<CB, PB, 8, 4>(a, s);
-    if (f == 128 || (!f && each > 64)) launch_tiles<CB, PB, 4, 4>(a, s);
-    else if (f == 64 || (!f && each > 32)) launch_tiles<CB, PB, 4, 2>(a, s);
-    else launch_tiles<CB, PB, 1, 2>(a, s);
+    if constexpr (PB == 1) if (f == 256 || (!f && each > 160)) return launch_tiles<CB, PB, 8, 4>(a, 256, s);
+    if (f == 64 || (!f && each > 32)) launch_tiles<CB, PB, 4, 2>(a, PB == 1 || CB != 8 ? 512 : 256, s);
+    else launch_tiles<CB, PB, 1, 2>(a, 512, s);
 }
 
 template <int CB>
@@ -97,27 +173,29 @@ static void launch_gemm(const BackArgs& a, hipStream_t s) {
 
 static int64_t padded(int64_t d_row) { return (d_row + 63) / 64 * 64; }
 
-// A scale may belong to as few columns as 32: d_col / 32 groups at most.
+// A scale may belong to as few columns as 32: d_col / 32 groups at most.  Sums: as many shares as
+// there may be, and no more than MOST_SUMS.
 size_t back_ws_bytes(int64_t n, int64_t E, int64_t d_row, int64_t d_col) {
+    const int64_t shares = (d_row + 255) / 256, sums = n * d_col * 4;
+    const int64_t all = shares == 1 ? 0 : sums > MOST_SUMS / shares ? MOST_SUMS : sums * shares;
     return up256((size_t)(n * padded(d_row)) * 2) + up256((size_t)n * 4) + up256((size_t)(E * d_row)) +
-           quads_bytes(E, d_row, (d_col + 31) / 32);
+           up256(quads_bytes(E, d_row, (d_col + 31) / 32)) + up256((size_t)all);
 }
 
 gptq_status back_launch(const BackCall& c, hipStream_t s) {
-    BackArgs a = {};
-    a.L = c.L; a.d_row = c.d_row; a.n = c.n; a.offsets = c.offsets; a.E = c.E;
     const int64_t lda = padded(c.d_row);
     uint8_t* w = (uint8_t*)c.ws;
-    uint16_t* A = (uint16_t*)w;
-    w += up256((size_t)(c.n * lda) * 2);
-    int32_t* shift = (int32_t*)w;
-    w += up256((size_t)c.n * 4);
-    int8_t* e = (int8_t*)w;
-    w += up256((size_t)(c.E * c.d_row));
-    a.A[0] = A; a.A[1] = nullptr; a.shift = shift;
-    a.T = (Quad*)w; a.quads = quads_of(c.d_row);
+    auto take = [&](size_t bytes) { uint8_t* at = w; w += up256(bytes); return at; };
+    uint16_t* A = (uint16_t*)take((size_t)(c.n * lda) * 2);
+    int32_t* shift = (int32_t*)take((size_t)c.n * 4);
+    int8_t* e = (int8_t*)take((size_t)(c.E * c.d_row));
+    Quad* T = (Quad*)take(quads_bytes(c.E, c.d_row, (c.L.d_col + 31) / 32));
+    BackArgs a = {};
+    a.L = c.L; a.d_row = c.d_row; a.n = c.n; a.offsets = c.offsets; a.E = c.E;
+    a.A[0] = A; a.shift = shift; a.T = T; a.quads = quads_of(c.d_row);
+    a.sums = (float*)w;
     a.y = c.dx; a.yt = c.dxt;
-    rows_launch(c.L, c.E, c.d_row, e, (Quad*)w, s);
+    rows_launch(c.L, c.E, c.d_row, e, T, s);
     GPTQ_LAUNCH_CHECK();
     const PackArgs p = {c.dy, c.ldy, c.n, c.d_row, e, c.offsets, c.E, A, lda, shift};
     if (c.dyt == GPTQ_BF16) back_pack_kernel<GPTQ_BF16><<<(unsigned)c.n, 256, 0, s>>>(p);

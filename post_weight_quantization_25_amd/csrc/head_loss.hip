@@ -247,7 +247,7 @@ __global__ __launch_bounds__(128 * WC, P == 1 || MT == 1 ? 2 : 1) void head_sums
     const int64_t k0 = v_first + slot * span, k1 = k0 + span < vocab ? k0 + span : vocab;
     f32x4_t acc[G::NI][MT];
     G::run(acc, a, a.L, a.T, tok0, a.n, c0, k0, k1, lds);
-    float* O = a.acc + (int64_t)slot * a.n * a.L.d_col;
+    float* O = a.sums + (int64_t)slot * a.n * a.L.d_col;
     const float* f = a.f + (int64_t)slot * a.n;
     G::each(acc, tok0, a.n, c0, a.L.d_col, [&](int64_t c, int64_t t, f32x4_t v, int have) {
         float* o = O + t * a.L.d_col + c;
@@ -431,7 +431,7 @@ gptq_status head_launch(const HeadCall& c, hipStream_t s) {
                 BackArgs b = {};
                 b.L = c.L; b.d_row = c.vocab; b.T = a.b.T; b.quads = quads_of(c.vocab);
                 b.A[0] = a.b.A[0]; b.A[1] = a.b.A[1]; b.a0 = v0;
-                b.n = nc; b.acc = a.b.O; b.f = a.b.f; b.first = round == 0;
+                b.n = nc; b.sums = a.b.O; b.f = a.b.f; b.first = round == 0;
                 if (c.bits == 3) launch_sums<3>(b, parts, slots, c.vocab, p.span, (int)v0, s);
                 else if (c.bits == 4) launch_sums<4>(b, parts, slots, c.vocab, p.span, (int)v0, s);
                 else launch_sums<8>(b, parts, slots, c.vocab, p.span, (int)v0, s);

@@ -59,7 +59,8 @@ GPTQ_DEV bool segment_of(const int32_t* offsets, int E, int64_t n, int per, int 
 
 // Most tiles that n rows of E experts have: every expert with a row may end in a part of one.
 inline int64_t most_tiles(const int32_t* offsets, int64_t E, int64_t n, int per) {
-    return offsets ? n / per + (E < n ? E : n) : (n + per - 1) / per;
+    const int64_t used = offsets ? (E < n ? E : n) : 1;
+    return (n + used * (per - 1)) / per;
 }
 
 // The layer of expert e.
