@@ -24,6 +24,7 @@ namespace gptq {
 constexpr int SPAN = 8192;                                      // most words of a span
 constexpr int64_t CHUNK = 4096;                                 // tokens taken at a time
 constexpr int64_t ROUND = (int64_t)1 << 25;                     // most logits of a round
+constexpr int MOST_SPANS = 1024;                                // of a round
 
 struct HeadPlan {
     int64_t nc;                                                 // tokens at a time
@@ -31,20 +32,46 @@ struct HeadPlan {
     int R;                                                      // spans per round
 };
 
-// Spans per round: until the sums' tiles fill the device, and at most ROUND logits.
-static int64_t wanted_spans(int64_t tiles_t, int64_t d, int spans, bool grad) {
-    const int64_t tiles = tiles_t * ((d + 127) / 128), want = grad ? (512 + tiles - 1) / tiles : spans;
-    return want < spans ? want : spans;
+// The sums' tile of a batch: tokens, columns, and how many tiles the device takes at once.
+struct SumTile { int bm, bn, places; };
+static SumTile tile_for(int64_t nc, int parts, int bits) {
+    if (nc > 128 && parts == 1) return SumTile{256, 256, 256};
+    if (nc > 32 && parts == 2 && bits != 8) return SumTile{128, 256, 256};   // (8-bit codes: LDS)
+    if (nc > 32) return SumTile{128, 128, parts == 1 ? 512 : 256};
+    return SumTile{32, 128, 512};
 }
 
-static HeadPlan plan_of(int64_t nc, int64_t d, int64_t vocab, bool grad) {
+// Spans: with few tiles, as many as fill the device once, twice, .. with each span's tiles in a
+// round of its own, of 512 to 8192 words; else of 8192 words, one after the other.  A round has
+// at most ROUND logits.
+static HeadPlan plan_of(int64_t nc, int64_t d, int64_t vocab, int parts, int bits) {
     HeadPlan p;
     p.nc = nc;
-    const int64_t spans = (vocab + SPAN - 1) / SPAN;
+    int64_t spans = (vocab + SPAN - 1) / SPAN, R = spans;
+    if (parts) {
+        const SumTile t = tile_for(nc, parts, bits);
+        const int64_t tiles = (nc + t.bm - 1) / t.bm * ((d + t.bn - 1) / t.bn);
+        if (2 * tiles <= t.places) {
+            int64_t times = 1;
+            while (times * t.places / tiles < spans) ++times;
+            spans = times * t.places / tiles;
+            const int64_t most = (vocab + 511) / 512;
+            if (spans > most) spans = most;
+            if (spans > MOST_SPANS && vocab <= SPAN * (int64_t)MOST_SPANS) spans = MOST_SPANS;
+            R = spans;
+        } else {
+            R = 1;
+        }
+    }
     p.span = ((vocab + spans - 1) / spans + 63) / 64 * 64;
     p.spans = (int)((vocab + p.span - 1) / p.span);
-    const int64_t want = wanted_spans((nc + 127) / 128, d, p.spans, grad), fit = ROUND / (nc * p.span);
-    p.R = (int)(fit < 1 ? 1 : want < fit ? want : fit);
+    const int64_t fit = ROUND / (nc * p.span);
+    if (R > p.spans) R = p.spans;
+    if (R > MOST_SPANS) R = MOST_SPANS;
+    if (R > fit) R = fit;
+    if (R < 1) R = 1;
+    const int64_t rounds = (p.spans + R - 1) / R;
+    p.R = (int)((p.spans + rounds - 1) / rounds);               // the same number in each
     return p;
 }
 
@@ -59,19 +86,17 @@ struct HeadBuffers {
 };
 constexpr int EB = 1024;                                        // rows per block of emax
 
-// rows: nc R, or a bound of it.
-static size_t layout(HeadBuffers* b, uint8_t* w, int64_t nc, int64_t rows, int64_t span, int64_t d, int64_t vocab, int k, bool grad) {
+// words: nc R span, rows: nc R, or bounds of them.
+static size_t layout(HeadBuffers* b, uint8_t* w, int64_t nc, int64_t words, int64_t rows, int64_t d, int64_t vocab, int k, int parts) {
     size_t at = 0;
     auto take = [&](size_t bytes) { const size_t here = at; at += up256(bytes); return w ? w + here : nullptr; };
-    const size_t zs = (size_t)(rows * span);
-    HeadBuffers h;
-    h.z = (float*)take(zs * 4);
+    HeadBuffers h = {};
+    h.z = (float*)take((size_t)words * 4);
     h.m = (float*)take((size_t)rows * 4); h.s = (float*)take((size_t)rows * 4); h.f = (float*)take((size_t)rows * 4);
     h.picked = (float*)take((size_t)(nc * k) * 4);
-    h.A[0] = h.A[1] = nullptr; h.O = nullptr; h.e = nullptr; h.T = nullptr; h.emax = nullptr;
-    if (grad) {
-        h.A[0] = (uint16_t*)take(zs * 2);
-        h.A[1] = (uint16_t*)take(zs * 2);
+    if (parts) {
+        h.A[0] = (uint16_t*)take((size_t)words * 2);
+        h.A[1] = (uint16_t*)take(parts == 2 ? (size_t)words * 2 : 0);
         h.O = (float*)take((size_t)(rows * d) * 4);
         h.e = (int8_t*)take((size_t)vocab);
         h.T = (Quad*)take(quads_bytes(1, vocab, (d + 31) / 32));
@@ -82,18 +107,25 @@ static size_t layout(HeadBuffers* b, uint8_t* w, int64_t nc, int64_t rows, int64
 }
 
 // A larger batch takes fewer spans per round, and a workspace made for the largest batch has to
-// do for every smaller one: so the size is of the most rows that any batch up to n has.  With T
-// tiles of tokens a batch of nc <= 128 T has nc min(wanted, ROUND / (nc span)) rows at most.
+// do for every smaller one, of any dx type and bits: so the size is of the most logits and sums
+// that any batch up to n has.  With T 32-token tiles a batch has at most 32 T tokens; spans per
+// round and words per span are those of its larger tiles' numbers, or what ROUND allows.
 size_t head_ws_bytes(int64_t n, int64_t d, int64_t vocab, int k, bool grad) {
     const int64_t nc = n < CHUNK ? n : CHUNK;
-    const HeadPlan p = plan_of(nc, d, vocab, grad);
-    int64_t rows = 0;
-    for (int64_t T = 1; T <= (nc + 127) / 128; ++T) {
-        const int64_t most = 128 * T < nc ? 128 * T : nc, want = most * wanted_spans(T, d, p.spans, grad);
-        const int64_t fit = ROUND / p.span > most ? ROUND / p.span : most, r = want < fit ? want : fit;
-        rows = r > rows ? r : rows;
-    }
-    return layout(nullptr, nullptr, nc, rows, p.span, d, vocab, k, grad);
+    int64_t words = 0, rows = 0;
+    auto most = [&](int64_t tokens, int64_t R, int64_t span) {
+        const int64_t cap = ROUND > tokens * span ? ROUND : tokens * span, w = tokens * R * span;
+        words = (w < cap ? w : cap) > words ? (w < cap ? w : cap) : words;
+        rows = tokens * R > rows ? tokens * R : rows;
+    };
+    for (int parts = grad ? 1 : 0; parts <= (grad ? 2 : 0); ++parts)
+        for (int bits = 4; bits <= (parts == 2 ? 8 : 4); bits += 4)
+            for (int64_t T = 1; T <= (nc + 31) / 32; ++T) {
+                const int64_t tokens = 32 * T < nc ? 32 * T : nc;
+                const HeadPlan a = plan_of(32 * (T - 1) + 1, d, vocab, parts, bits);   // the fewest tokens: the most spans that fit
+                most(tokens, a.R, a.span);
+            }
+    return layout(nullptr, nullptr, nc, words, rows, d, vocab, k, grad ? 2 : 0);
 }
 
 __global__ __launch_bounds__(256) void head_emax_kernel(const int8_t* e, int64_t vocab, int32_t* emax) {
@@ -161,7 +193,7 @@ __global__ __launch_bounds__(256) void head_stats_kernel(HeadArgs a) {
     const int64_t t = blockIdx.x;
     const int64_t v0 = ((int64_t)a.round * a.R + slot) * a.span;
     const int words = (int)(a.vocab - v0 < a.span ? a.vocab - v0 : a.span);
-    const int64_t ldz = a.R * a.span;
+    const int64_t ldz = a.R * a.span;                           // (of the round's words, as in head_launch)
     const float* z = a.b.z + t * ldz + slot * a.span;
     const float invT = 1.f / a.T;
     flag[tid] = 0;
@@ -184,6 +216,7 @@ __global__ __launch_bounds__(256) void head_stats_kernel(HeadArgs a) {
     float m = -INFINITY;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+        if (1024 * u >= a.span) break;                           // uniform
         const int w = 1024 * u + 4 * tid;
         f32x4_t q = {0.f, 0.f, 0.f, 0.f};
         if (w < words) q = *reinterpret_cast<const f32x4_t*>(z + w);   // the span is whole fours
@@ -204,6 +237,7 @@ __global__ __launch_bounds__(256) void head_stats_kernel(HeadArgs a) {
     float s = 0.f;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+        if (1024 * u >= a.span) break;                           // uniform
         const int w = 1024 * u + 4 * tid;
         uint16_t hi[4], lo[4];
 #pragma unroll
@@ -237,7 +271,7 @@ __global__ __launch_bounds__(256) void head_stats_kernel(HeadArgs a) {
 }
 
 template <int CB, int P, int MT, int WC, bool DIRECT>
-__global__ __launch_bounds__(128 * WC, P == 1 || MT == 1 ? 2 : 1) void head_sums_kernel(BackArgs a, int gm, int gn, int64_t vocab, int64_t span, int v_first) {
+__global__ __launch_bounds__(128 * WC, P == 1 || MT == 1 || WC == 4 ? 2 : 1) void head_sums_kernel(BackArgs a, int gm, int gn, int64_t vocab, int64_t span, int v_first) {
     typedef BackGemm<CB, P, P, MT, 2, WC, DIRECT> G;
     __shared__ __align__(16) uint8_t lds[G::LDS_BYTES];
     int tm, tn;
@@ -281,6 +315,8 @@ __global__ __launch_bounds__(256) void head_final_kernel(HeadArgs a) {
     __shared__ int redi[4];
     __shared__ int id_of[TUNE_MAX_TOP];
     __shared__ float coef[TUNE_MAX_TOP];
+    __shared__ float slot_of[MOST_SPANS];
+    __shared__ float joint[256][8];
     const int tid = threadIdx.x;
     const int64_t t = blockIdx.x, tt = a.tok0 + t;
     const float w = weight_of(a, t);
@@ -339,31 +375,74 @@ __global__ __launch_bounds__(256) void head_final_kernel(HeadArgs a) {
     const float gain = w * a.T;
     if (tid == 0) a.loss[tt] = (float)((double)w * a.T * a.T * l);
     if (!a.dx) return;
-    const int em = emax_of(a.b.emax, a.blocks, redi);            // (and a barrier: coef is complete)
-    for (int64_t c = 8 * tid; c < a.d; c += 2048) {
+    const int em = emax_of(a.b.emax, a.blocks, redi);
+    for (int i = tid; i < a.R; i += 256) {                       // the slots' weights
+        const float m = a.b.m[(int64_t)i * a.n + t], s = a.b.s[(int64_t)i * a.n + t];
+        slot_of[i] = s == 0.f ? 0.f : ldexpf((float)exp((double)m - zm - lzt), em - 14);
+    }
+    __syncthreads();
+    // 8 columns per thread; with fewer than 2048 columns several threads share a column's slots and
+    // entries.
+    int share = 1;
+    while (share < 8 && a.d * share <= 1024) share *= 2;
+    const int per = 256 / share, col = tid % per, part = tid / per;
+    for (int64_t c0 = 0; c0 < a.d; c0 += 8 * per) {
+        const int64_t c = c0 + 8 * col;
         const int have = (int)(a.d - c < 8 ? a.d - c : 8);
         float g[8] = {};
-        for (int i = 0; i < a.R; ++i) {
-            const float m = a.b.m[(int64_t)i * a.n + t], s = a.b.s[(int64_t)i * a.n + t];
-            if (s == 0.f) continue;
-            const float q = ldexpf((float)exp((double)m - zm - lzt), em - 14);
-            const float* o = a.b.O + ((int64_t)i * a.n + t) * a.d + c;
-            for (int e = 0; e < have; ++e) g[e] = fmaf(q, o[e], g[e]);
-        }
-        for (int j = 0; j < a.k; ++j) {
-            const int64_t r = id_of[j];
-            if (r < 0) continue;
-            const uint8_t* src = a.L.codes + r * a.L.code_ld + c / 8 * CB;
-            const Raw<CB, 8> u = have == 8 ? load_raw<CB, 8>(src) : load_raw_tail<CB, 8>(src, have);
-            const int64_t i = r * a.L.n_groups + (a.L.n_groups == 1 ? 0 : c >> a.L.gshift);
-            const float S = f16_bits_to_f32(a.L.scales[i]), zero = f16_bits_to_f32(a.L.zeros[i]), k = coef[j];
+        if (have > 0) {
+#pragma unroll 2
+            for (int i = part; i < a.R; i += share) {
+                const float q = slot_of[i];
+                const float* o = a.b.O + ((int64_t)i * a.n + t) * a.d + c;
+                float v[8];
+                if (have == 8) __builtin_memcpy(v, o, 32);
+                else
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float x = S * ((float)((code_bytes4<CB, 8>(u, e >> 2) >> (8 * (e & 3))) & 0xFFu) - zero);
-                g[e] = fmaf(k, x, g[e]);
+                    for (int e = 0; e < 8; ++e) v[e] = e < have ? o[e] : 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) g[e] = q == 0.f ? g[e] : fmaf(q, v[e], g[e]);
+            }
+            // entries four at a time, so that their loads are in flight together
+            for (int j0 = part; j0 < a.k; j0 += 4 * share) {
+                Raw<CB, 8> u[4];
+                uint16_t S[4], zero[4];
+                float k[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int j = j0 + x * share;
+                    const bool in = j < a.k && id_of[j] >= 0;
+                    const int64_t r = in ? id_of[j] : 0;
+                    k[x] = in ? coef[j] : 0.f;
+                    const uint8_t* src = a.L.codes + r * a.L.code_ld + c / 8 * CB;
+                    if (have == 8) u[x] = load_raw<CB, 8>(src);
+                    else u[x] = load_raw_tail<CB, 8>(src, have);
+                    const int64_t i = r * a.L.n_groups + (a.L.n_groups == 1 ? 0 : c >> a.L.gshift);
+                    S[x] = a.L.scales[i];
+                    zero[x] = a.L.zeros[i];
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float s = f16_bits_to_f32(S[x]), z = f16_bits_to_f32(zero[x]);
+                    if (k[x] == 0.f) continue;                   // an infinity in a word without a weight does not count
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        g[e] = fmaf(k[x], s * ((float)((code_bytes4<CB, 8>(u[x], e >> 2) >> (8 * (e & 3))) & 0xFFu) - z), g[e]);
+                }
             }
         }
-        for (int e = 0; e < have; ++e) store_out(a.dx, a.dxt, tt * a.d + c + e, gain * g[e]);
+        if (share > 1) {                                         // uniform; one turn
+            if (part > 0)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) joint[(part - 1) * per + col][e] = g[e];
+            __syncthreads();
+            if (part == 0)
+                for (int p = 1; p < share; ++p)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) g[e] += joint[(p - 1) * per + col][e];
+        }
+        if (part == 0 && have > 0)
+            for (int e = 0; e < have; ++e) store_out(a.dx, a.dxt, tt * a.d + c + e, gain * g[e]);
     }
 }
 
@@ -378,8 +457,10 @@ static void launch_tiles(const BackArgs& b, int slots, int64_t vocab, int64_t sp
 
 template <int CB, int P>
 static void launch_parts(const BackArgs& b, int slots, int64_t vocab, int64_t span, int first_word, hipStream_t s) {
-    if (b.n > 128) launch_tiles<CB, P, P == 1 ? 8 : 4, P == 1 ? 4 : 2>(b, slots, vocab, span, first_word, s);
-    else if (b.n > 32) launch_tiles<CB, P, 4, 2>(b, slots, vocab, span, first_word, s);
+    const int bm = tile_for(b.n, P, CB).bm;
+    if constexpr (P == 1) if (bm == 256) return launch_tiles<CB, P, 8, 4>(b, slots, vocab, span, first_word, s);
+    if constexpr (P == 2 && CB != 8) if (bm == 128) return launch_tiles<CB, P, 4, 4>(b, slots, vocab, span, first_word, s);
+    if (bm == 128) launch_tiles<CB, P, 4, 2>(b, slots, vocab, span, first_word, s);
     else launch_tiles<CB, P, 1, 2>(b, slots, vocab, span, first_word, s);
 }
 
@@ -399,8 +480,8 @@ gptq_status head_launch(const HeadCall& c, hipStream_t s) {
     a.blocks = (int)((c.vocab + EB - 1) / EB);
     for (int64_t tok0 = 0; tok0 < c.n; tok0 += CHUNK) {
         const int64_t nc = c.n - tok0 < CHUNK ? c.n - tok0 : CHUNK;
-        const HeadPlan p = plan_of(nc, d, c.vocab, grad);
-        layout(&a.b, (uint8_t*)c.ws, nc, nc * p.R, p.span, d, c.vocab, c.k, grad);
+        const HeadPlan p = plan_of(nc, d, c.vocab, parts, c.bits);
+        layout(&a.b, (uint8_t*)c.ws, nc, nc * p.R * p.span, nc * p.R, d, c.vocab, c.k, parts);
         a.n = nc; a.tok0 = tok0; a.R = p.R; a.span = p.span;
         if (grad) {
             rows_launch(c.L, 1, c.vocab, a.b.e, a.b.T, s);
