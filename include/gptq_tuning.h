@@ -37,16 +37,22 @@ extern "C" {
  *  offsets    n_experts + 1 int32, or NULL with n_experts == 1: all rows.  Taken clamped to 0 ..
  *             n_rows and to never fall; rows of no expert are left as they were in y.
  *  y          n_rows x d_row, pitch d_row, dtype y_dtype
+ *  ws         at least gptqt_linear_grouped_workspace_size(...) bytes, 16-byte aligned; NULL where
+ *             that is 0 (few rows per expert)
  * Errors: n_rows < 0, n_experts, d_row or d_col < 1, a pitch below d_col, a group that does not
  * divide d_col, odd d_col with 4-bit codes (3-bit: not a multiple of 8), a bad dtype, a NULL
  * pointer -> GPTQ_ERR_INVALID_ARG; x_dtype GPTQ_F32, bits or group_size not listed, n_rows >
  * 4194240, n_experts > 4096, d_col >= 2^17, ldx > 2^23, d_row > 2^25, n_experts * d_row > 2^26,
- * more than 2^24 tiles of 64 x 128 outputs -> GPTQ_ERR_UNSUPPORTED.  n_rows == 0 is a no-op.
+ * more than 2^24 tiles of 64 x 128 outputs -> GPTQ_ERR_UNSUPPORTED; a missing, misaligned or short
+ * workspace -> GPTQ_ERR_WORKSPACE.  n_rows == 0 is a no-op.
  */
+size_t gptqt_linear_grouped_workspace_size(int64_t n_rows, int32_t n_experts, int64_t d_row, int64_t d_col,
+                                           int32_t group_size);
 gptq_status gptqt_linear_grouped(const uint8_t* codes, const uint16_t* scales_f16, const uint16_t* zeros_f16,
                                  int32_t n_experts, int64_t d_row, int64_t d_col, int32_t bits, int32_t group_size,
                                  const void* x, gptq_dtype x_dtype, int64_t n_rows, int64_t ldx,
-                                 const int32_t* offsets, void* y, gptq_dtype y_dtype, void* stream);
+                                 const int32_t* offsets, void* y, gptq_dtype y_dtype, void* ws, size_t ws_bytes,
+                                 void* stream);
 
 /*
  * The gradient through them: dx[t] = What_e^T dy[t] for the rows t of expert e; with n_experts
@@ -61,7 +67,8 @@ gptq_status gptqt_linear_grouped(const uint8_t* codes, const uint16_t* scales_f1
  *  ws         at least gptqt_linear_grouped_backward_workspace_size(...) bytes, 16-byte aligned
  * Errors: as gptqt_linear_grouped; a missing, misaligned or short workspace -> GPTQ_ERR_WORKSPACE.
  */
-size_t gptqt_linear_grouped_backward_workspace_size(int64_t n_rows, int32_t n_experts, int64_t d_row, int64_t d_col);
+size_t gptqt_linear_grouped_backward_workspace_size(int64_t n_rows, int32_t n_experts, int64_t d_row, int64_t d_col,
+                                                    int32_t group_size);
 gptq_status gptqt_linear_grouped_backward(const uint8_t* codes, const uint16_t* scales_f16, const uint16_t* zeros_f16,
                                           int32_t n_experts, int64_t d_row, int64_t d_col, int32_t bits,
                                           int32_t group_size, const void* dy, gptq_dtype dy_dtype, int64_t n_rows,
@@ -89,7 +96,8 @@ gptq_status gptqt_linear_grouped_backward(const uint8_t* codes, const uint16_t* 
  *             16-byte aligned
  * Errors: as gptqt_linear_grouped_backward, vocab for d_row, d for d_col.
  */
-size_t gptqt_cross_entropy_workspace_size(int64_t n_tokens, int64_t d, int64_t vocab, int32_t with_grad);
+size_t gptqt_cross_entropy_workspace_size(int64_t n_tokens, int64_t d, int64_t vocab, int32_t group_size,
+                                          int32_t with_grad);
 gptq_status gptqt_cross_entropy(const uint8_t* codes, const uint16_t* scales_f16, const uint16_t* zeros_f16,
                                 int64_t vocab, int64_t d, int32_t bits, int32_t group_size, const void* x,
                                 gptq_dtype x_dtype, int64_t n_tokens, int64_t ldx, const int32_t* targets,
@@ -112,7 +120,8 @@ gptq_status gptqt_cross_entropy(const uint8_t* codes, const uint16_t* scales_f16
  * Errors: as gptqt_cross_entropy; top_k < 1, a temperature that is not positive and finite ->
  * GPTQ_ERR_INVALID_ARG; top_k > 1024 -> GPTQ_ERR_UNSUPPORTED.
  */
-size_t gptqt_distill_workspace_size(int64_t n_tokens, int64_t d, int64_t vocab, int32_t top_k, int32_t with_grad);
+size_t gptqt_distill_workspace_size(int64_t n_tokens, int64_t d, int64_t vocab, int32_t group_size, int32_t top_k,
+                                    int32_t with_grad);
 gptq_status gptqt_distill(const uint8_t* codes, const uint16_t* scales_f16, const uint16_t* zeros_f16, int64_t vocab,
                           int64_t d, int32_t bits, int32_t group_size, const void* x, gptq_dtype x_dtype,
                           int64_t n_tokens, int64_t ldx, const int32_t* ids, const void* top, gptq_dtype top_dtype,

@@ -85,15 +85,16 @@ def _load():
         "gptqs_moe": (ctypes.c_int, [vp, ctypes.c_int, i64, i64, i64, vp, i32, i32, i32, i64, vp, vp, vp, vp, vp, vp, i32,
                                      i32, vp, ctypes.c_int, vp, vp, vp, sz, vp]),
         # include/gptq_tuning.h
+        "gptqt_linear_grouped_workspace_size": (sz, [i64, i32, i64, i64, i32]),
         "gptqt_linear_grouped": (ctypes.c_int, [vp, vp, vp, i32, i64, i64, i32, i32, vp, ctypes.c_int, i64, i64, vp, vp,
-                                                ctypes.c_int, vp]),
-        "gptqt_linear_grouped_backward_workspace_size": (sz, [i64, i32, i64, i64]),
+                                                ctypes.c_int, vp, sz, vp]),
+        "gptqt_linear_grouped_backward_workspace_size": (sz, [i64, i32, i64, i64, i32]),
         "gptqt_linear_grouped_backward": (ctypes.c_int, [vp, vp, vp, i32, i64, i64, i32, i32, vp, ctypes.c_int, i64, i64,
                                                          vp, vp, ctypes.c_int, vp, sz, vp]),
-        "gptqt_cross_entropy_workspace_size": (sz, [i64, i64, i64, i32]),
+        "gptqt_cross_entropy_workspace_size": (sz, [i64, i64, i64, i32, i32]),
         "gptqt_cross_entropy": (ctypes.c_int, [vp, vp, vp, i64, i64, i32, i32, vp, ctypes.c_int, i64, i64, vp, vp, vp, vp,
                                                ctypes.c_int, vp, sz, vp]),
-        "gptqt_distill_workspace_size": (sz, [i64, i64, i64, i32, i32]),
+        "gptqt_distill_workspace_size": (sz, [i64, i64, i64, i32, i32, i32]),
         "gptqt_distill": (ctypes.c_int, [vp, vp, vp, i64, i64, i32, i32, vp, ctypes.c_int, i64, i64, vp, vp, ctypes.c_int,
                                          i32, ctypes.c_float, vp, vp, vp, ctypes.c_int, vp, sz, vp]),
     }
@@ -513,4 +514,5 @@ def check_info(info: torch.Tensor, what: str = "gptq"):
 from .serving import (Int8Rows, linear_int8, linear_lora, linear_lora_workspace_size, moe,  # noqa: E402,F401
                       moe_workspace_size, rmsnorm_int8)  # (the module uses the names above)
 from .tuning import (cross_entropy, cross_entropy_workspace_size, distill, distill_workspace_size,  # noqa: E402,F401
-                     linear_grouped, linear_grouped_backward, linear_grouped_backward_workspace_size)
+                     linear_grouped, linear_grouped_backward, linear_grouped_backward_workspace_size,
+                     linear_grouped_workspace_size)

@@ -1,12 +1,14 @@
 // Products grouped by expert (gptqt_linear_grouped): y[t] = What_e x[t] for the rows t of
 // expert e, and the logits of the losses at a stored head (one expert).
 //
+// Many tokens per expert: forward_gemm.h, with the activations as fp16 rows and the scales' ratios
+// laid out first.  Others, and layers that it leaves: stored_gemm.h; few tokens: stored_tile.h.
+//
 // Workgroups find their expert and rows from the offsets on the device (segment_of), so the
 // call needs no count on the host: the grid holds the most tiles that n rows of E experts can
 // have, and workgroups behind the last one end.
 
-#include "tuning.h"
-#include "stored_gemm.h"
+#include "forward_gemm.h"
 
 namespace gptq {
 
@@ -45,6 +47,7 @@ template <int X, int CB, int PIECE, int BM>
 __global__ __launch_bounds__(256, 2) void grouped_gemm_kernel(GroupedArgs a, int gm, int gn) {
     typedef StoredGemm<X, CB, PIECE, BM, 256> G;
     __shared__ __align__(16) uint8_t lds[G::LDS_BYTES];
+    if (a.unless_zero && *a.unless_zero == 0) return;
     int tm, tn;
     tile_of(gm, gn, tm, tn);
     Segment s;
@@ -73,6 +76,183 @@ static void launch_gemm(const GroupedArgs& a, hipStream_t s) {
     grouped_gemm_kernel<X, CB, PIECE, BM><<<(unsigned)(gm * gn), 256, 0, s>>>(a, gm, gn);
 }
 
+// ---- many tokens
+struct ForwardPackArgs {
+    const uint16_t* x; int64_t ldx, n, d_col, columns;
+    uint16_t* A; int32_t* shift; int32_t* odd; int natural;     // natural: columns in order (8-bit codes)
+};
+
+// A workgroup per token, 8 elements per thread and step.
+template <int X>
+__global__ __launch_bounds__(256) void forward_pack_kernel(ForwardPackArgs a) {
+    __shared__ int red[4];
+    const int64_t t = blockIdx.x;
+    const uint16_t* row = a.x + t * a.ldx;
+    int k = 0;
+    if constexpr (X == X_BF16) {
+        int m = -1000;
+        for (int64_t c = 8 * threadIdx.x; c < a.d_col; c += 2048) {
+            float v[8];
+            load_x8<X>(row + c, (int)(a.d_col - c < 8 ? a.d_col - c : 8), v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int e = exponent_of(v[i]);
+                m = e > m ? e : m;
+            }
+        }
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) {
+            const int v = __shfl_xor(m, o);
+            m = v > m ? v : m;
+        }
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < 4; ++w) m = red[w] > m ? red[w] : m;
+        k = m < -900 ? 0 : 14 - m;                               // nothing but zeros
+    }
+    if (threadIdx.x == 0) a.shift[t] = k;
+    for (int64_t c = 8 * threadIdx.x; c < a.columns; c += 2048) {
+        float v[8] = {};
+        if (c < a.d_col) load_x8<X>(row + c, (int)(a.d_col - c < 8 ? a.d_col - c : 8), v);
+        uint16_t h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = f32_to_f16_bits(X == X_BF16 ? __builtin_amdgcn_ldexpf(v[i], k) : v[i]);
+        u32x4_t o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = a.natural ? h[2 * i] | ((uint32_t)h[2 * i + 1] << 16) : h[i] | ((uint32_t)h[i + 4] << 16);
+        *reinterpret_cast<u32x4_t*>(a.A + ((c / BK) * a.n + t) * BK + c % BK) = o;
+    }
+}
+
+__global__ void forward_flag_kernel(int32_t* odd) { *odd = 0; }
+
+// Ratios of a row's scales, its zeros as fp16 pairs, its last scale; the flag where one of them is
+// not for this kernel.  64 rows of an expert per workgroup, threads along the rows.
+__global__ __launch_bounds__(256) void forward_rows_kernel(Stored L, int64_t d_row, ForwardBuffers b) {
+    __shared__ float S[64][33];
+    __shared__ uint16_t Z[64][34];
+    const int64_t row0 = (int64_t)blockIdx.x * 64, base = blockIdx.y * d_row, at = blockIdx.y * b.pitch * b.groups;
+    bool odd = false;
+    float before = 0.f;                                          // thread r's row: the scale of the group before
+    for (int g0 = 0; g0 < b.groups; g0 += 32) {
+        const int take = (int)(b.groups - g0 < 32 ? b.groups - g0 : 32);
+        __syncthreads();
+        for (int i = threadIdx.x; i < 64 * take; i += 256) {
+            const int r = i / take, g = g0 + i % take;
+            float s = 1.f, z = 0.f;
+            if (row0 + r < d_row) {
+                const int64_t p = (base + row0 + r) * L.n_groups + (g < L.n_groups ? g : L.n_groups - 1);   // behind the last: that one
+                s = f16_bits_to_f32(L.scales[p]);
+                z = f16_bits_to_f32(L.zeros[p]);
+                odd = odd || !(s != 0.f && fabsf(s) < INFINITY && fabsf(z) <= 1024.f && rintf(z) == z);
+            }
+            S[r][g - g0] = s;
+            Z[r][g - g0] = f32_to_f16_bits(1024.f + z);
+        }
+        __syncthreads();
+        const int r = threadIdx.x & 63;
+        for (int g = threadIdx.x >> 6; g < take; g += 4) {
+            const float s = S[r][g], was = g > 0 ? S[r][g - 1] : g0 > 0 ? before : s;
+            if (row0 + r < b.pitch) {
+                b.rho[at + (int64_t)(g0 + g) * b.pitch + row0 + r] = was / s;
+                b.zz[at + (int64_t)(g0 + g) * b.pitch + row0 + r] = Z[r][g] * 0x10001u;
+                if (g0 + g == b.groups - 1) b.S_last[blockIdx.y * b.pitch + row0 + r] = s;
+            }
+        }
+        before = S[r][take - 1];
+    }
+    if (__ballot(odd) != 0 && (threadIdx.x & 63) == 0) atomicOr(b.odd, 1);
+}
+
+template <int CB, int GPT>
+__global__ __launch_bounds__(512, 2) void forward_gemm_kernel(ForwardArgs a, int gm, int gn) {
+    typedef ForwardGemm<CB, GPT> G;
+    __shared__ __align__(16) uint8_t lds[G::LDS_BYTES];
+    if (*a.odd != 0) return;
+    int tm, tn;
+    tile_of(gm, gn, tm, tn);
+    Segment s;
+    if (!segment_of(a.offsets, a.E, a.n, G::BM, tm, s)) return;
+    const int64_t row0 = (int64_t)tn * G::BN, table = s.e * a.expert_pitch;
+    f32x4_t acc[G::NI][G::MT];
+    G::run(acc, a, expert_of(a.L, a.d_row, s.e), a.rho + table, a.zz + table, s.tok0, s.end, row0, lds);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15, q = lane >> 4;
+    float last[G::NI];
+#pragma unroll
+    for (int i = 0; i < G::NI; ++i) {
+        const int64_t r = row0 + 64 * (wave & 3) + 16 * i + n16;
+        last[i] = a.S_last[s.e * a.pitch + (r < a.d_row ? r : a.d_row - 1)];
+    }
+#pragma unroll
+    for (int j = 0; j < G::MT; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int64_t t = s.tok0 + 128 * (wave >> 2) + 16 * j + 4 * q + v;
+            if (t >= s.end) continue;
+            const int k = -a.shift[t];
+#pragma unroll
+            for (int i = 0; i < G::NI; ++i) {
+                const int64_t r = row0 + 64 * (wave & 3) + 16 * i + n16;
+                if (r < a.d_row) store_out(a.y, a.yt, t * a.ldy + r, ldexpf(acc[i][j][v] * last[i], k));
+            }
+        }
+}
+
+template <int CB, int GPT>
+static void launch_forward(const ForwardArgs& a, hipStream_t s) {
+    typedef ForwardGemm<CB, GPT> G;
+    const int gm = (int)most_tiles(a.offsets, a.E, a.n, G::BM), gn = (int)((a.d_row + G::BN - 1) / G::BN);
+    forward_gemm_kernel<CB, GPT><<<(unsigned)(gm * gn), G::THREADS, 0, s>>>(a, gm, gn);
+}
+
+template <int CB>
+static void launch_forward_groups(const ForwardArgs& a, int group, hipStream_t s) {
+    if (group == 32) launch_forward<CB, 4>(a, s);
+    else if (group == 64) launch_forward<CB, 2>(a, s);
+    else if (group == 128) launch_forward<CB, 1>(a, s);
+    else launch_forward<CB, 0>(a, s);
+}
+
+// Rows per expert from which the 256 x 256 tiles are taken.
+constexpr int64_t MANY = 160;
+static bool many(int64_t n, int64_t E) { return (n + E - 1) / E > MANY; }
+
+static size_t forward_layout(ForwardBuffers* b, uint8_t* w, int64_t n, int64_t E, int64_t d_row, int64_t d_col, int group) {
+    size_t at = 0;
+    auto take = [&](size_t bytes) { const size_t here = at; at += up256(bytes); return w ? w + here : nullptr; };
+    const Stored L = stored_layer(nullptr, nullptr, nullptr, d_col, 8, group);
+    ForwardBuffers h;
+    h.pitch = (d_row + 3) / 4 * 4;
+    h.groups = forward_groups(L);
+    h.odd = (int32_t*)take(4);
+    h.A = (uint16_t*)take((size_t)(n * forward_columns(d_col)) * 2);
+    h.shift = (int32_t*)take((size_t)n * 4);
+    // a tile's loads of 256 rows may run over a table's end
+    h.rho = (float*)take((size_t)(E * h.pitch * h.groups) * 4 + 1024);
+    h.zz = (uint32_t*)take((size_t)(E * h.pitch * h.groups) * 4 + 1024);
+    h.S_last = (float*)take((size_t)(E * h.pitch) * 4);
+    if (b) *b = h;
+    return at;
+}
+
+size_t grouped_ws_bytes(int64_t n, int64_t E, int64_t d_row, int64_t d_col, int group) {
+    return many(n, E) ? forward_layout(nullptr, nullptr, n, E, d_row, d_col, group) : 0;
+}
+
+gptq_status grouped_prepare(const GroupedArgs& a, gptq_dtype xt, int bits, int group, void* ws, hipStream_t s) {
+    if (!many(a.n, a.E) || !direct_codes(a.L)) return GPTQ_OK;
+    ForwardBuffers b;
+    forward_layout(&b, (uint8_t*)ws, a.n, a.E, a.d_row, a.L.d_col, group);
+    const ForwardPackArgs p = {a.x, a.ldx, a.n, a.L.d_col, forward_columns(a.L.d_col), b.A, b.shift, b.odd, bits == 8};
+    forward_flag_kernel<<<1, 1, 0, s>>>(b.odd);
+    if (xt == GPTQ_BF16) forward_pack_kernel<X_BF16><<<(unsigned)a.n, 256, 0, s>>>(p);
+    else forward_pack_kernel<X_F16><<<(unsigned)a.n, 256, 0, s>>>(p);
+    forward_rows_kernel<<<dim3((unsigned)((a.d_row + 63) / 64), (unsigned)a.E), 256, 0, s>>>(a.L, a.d_row, b);
+    GPTQ_LAUNCH_CHECK();
+    return GPTQ_OK;
+}
+
 template <int X, int CB, int RUN, int PIECE>
 static gptq_status launch(const GroupedArgs& a, hipStream_t s) {
     const int64_t each = a.n / a.E;
@@ -99,7 +279,24 @@ static gptq_status launch_bits(const GroupedArgs& a, int bits, int group, hipStr
     return bits == 3 ? launch_runs<X, 3>(a, group, s) : bits == 4 ? launch_runs<X, 4>(a, group, s) : launch_runs<X, 8>(a, group, s);
 }
 
-gptq_status grouped_launch(const GroupedArgs& a, gptq_dtype xt, int bits, int group, hipStream_t s) {
+gptq_status grouped_launch(const GroupedArgs& given, gptq_dtype xt, int bits, int group, void* ws, int64_t all_rows, int64_t row0,
+                           hipStream_t s) {
+    GroupedArgs a = given;
+    a.unless_zero = nullptr;
+    if (many(a.n, a.E) && direct_codes(a.L)) {
+        ForwardBuffers b;
+        forward_layout(&b, (uint8_t*)ws, a.n, a.E, all_rows, a.L.d_col, group);
+        ForwardArgs f;
+        f.L = a.L; f.d_row = a.d_row; f.A = b.A; f.shift = b.shift;
+        f.rho = b.rho + row0; f.zz = b.zz + row0; f.S_last = b.S_last + row0;
+        f.pitch = b.pitch; f.expert_pitch = b.pitch * b.groups; f.odd = b.odd;
+        f.n = a.n; f.offsets = a.offsets; f.E = a.E; f.y = a.y; f.yt = a.yt; f.ldy = a.ldy;
+        if (bits == 3) launch_forward_groups<3>(f, group, s);
+        else if (bits == 4) launch_forward_groups<4>(f, group, s);
+        else launch_forward_groups<8>(f, group, s);
+        GPTQ_LAUNCH_CHECK();
+        a.unless_zero = b.odd;
+    }
     return xt == GPTQ_BF16 ? launch_bits<X_BF16>(a, bits, group, s) : launch_bits<X_F16>(a, bits, group, s);
 }
 

@@ -173,13 +173,12 @@ static void launch_gemm(const BackArgs& a, hipStream_t s) {
 
 static int64_t padded(int64_t d_row) { return (d_row + 63) / 64 * 64; }
 
-// A scale may belong to as few columns as 32: d_col / 32 groups at most.  Sums: as many shares as
-// there may be, and no more than MOST_SUMS.
-size_t back_ws_bytes(int64_t n, int64_t E, int64_t d_row, int64_t d_col) {
+// Sums: as many shares as there may be, and no more than MOST_SUMS.
+size_t back_ws_bytes(int64_t n, int64_t E, int64_t d_row, int64_t d_col, int group) {
     const int64_t shares = (d_row + 255) / 256, sums = n * d_col * 4;
     const int64_t all = shares == 1 ? 0 : sums > MOST_SUMS / shares ? MOST_SUMS : sums * shares;
     return up256((size_t)(n * padded(d_row)) * 2) + up256((size_t)n * 4) + up256((size_t)(E * d_row)) +
-           up256(quads_bytes(E, d_row, (d_col + 31) / 32)) + up256((size_t)all);
+           up256(quads_bytes(E, d_row, group ? d_col / group : 1)) + up256((size_t)all);
 }
 
 gptq_status back_launch(const BackCall& c, hipStream_t s) {
@@ -189,7 +188,7 @@ gptq_status back_launch(const BackCall& c, hipStream_t s) {
     uint16_t* A = (uint16_t*)take((size_t)(c.n * lda) * 2);
     int32_t* shift = (int32_t*)take((size_t)c.n * 4);
     int8_t* e = (int8_t*)take((size_t)(c.E * c.d_row));
-    Quad* T = (Quad*)take(quads_bytes(c.E, c.d_row, (c.L.d_col + 31) / 32));
+    Quad* T = (Quad*)take(quads_bytes(c.E, c.d_row, c.L.n_groups));
     BackArgs a = {};
     a.L = c.L; a.d_row = c.d_row; a.n = c.n; a.offsets = c.offsets; a.E = c.E;
     a.A[0] = A; a.shift = shift; a.T = T; a.quads = quads_of(c.d_row);

@@ -81,25 +81,27 @@ struct HeadBuffers {
     float* O;                                                   // R x nc x d
     float* m; float* s; float* f;                               // R x nc
     float* picked;                                              // nc x k
-    int8_t* e; Quad* T;                                         // vocab; d / 32 groups of quads_of(vocab) at most
+    void* forward;                                              // of grouped_prepare
+    int8_t* e; Quad* T;                                         // vocab; a group's quads_of(vocab)
     int32_t* emax;                                              // of blocks of rows
 };
 constexpr int EB = 1024;                                        // rows per block of emax
 
 // words: nc R span, rows: nc R, or bounds of them.
-static size_t layout(HeadBuffers* b, uint8_t* w, int64_t nc, int64_t words, int64_t rows, int64_t d, int64_t vocab, int k, int parts) {
+static size_t layout(HeadBuffers* b, uint8_t* w, int64_t nc, int64_t words, int64_t rows, int64_t d, int64_t vocab, int group, int k, int parts) {
     size_t at = 0;
     auto take = [&](size_t bytes) { const size_t here = at; at += up256(bytes); return w ? w + here : nullptr; };
     HeadBuffers h = {};
     h.z = (float*)take((size_t)words * 4);
     h.m = (float*)take((size_t)rows * 4); h.s = (float*)take((size_t)rows * 4); h.f = (float*)take((size_t)rows * 4);
     h.picked = (float*)take((size_t)(nc * k) * 4);
+    h.forward = take(grouped_ws_bytes(nc, 1, vocab, d, group));
     if (parts) {
         h.A[0] = (uint16_t*)take((size_t)words * 2);
         h.A[1] = (uint16_t*)take(parts == 2 ? (size_t)words * 2 : 0);
         h.O = (float*)take((size_t)(rows * d) * 4);
         h.e = (int8_t*)take((size_t)vocab);
-        h.T = (Quad*)take(quads_bytes(1, vocab, (d + 31) / 32));
+        h.T = (Quad*)take(quads_bytes(1, vocab, group ? d / group : 1));
         h.emax = (int32_t*)take((size_t)((vocab + EB - 1) / EB) * 4);
     }
     if (b) *b = h;
@@ -110,7 +112,7 @@ static size_t layout(HeadBuffers* b, uint8_t* w, int64_t nc, int64_t words, int6
 // do for every smaller one, of any dx type and bits: so the size is of the most logits and sums
 // that any batch up to n has.  With T 32-token tiles a batch has at most 32 T tokens; spans per
 // round and words per span are those of its larger tiles' numbers, or what ROUND allows.
-size_t head_ws_bytes(int64_t n, int64_t d, int64_t vocab, int k, bool grad) {
+size_t head_ws_bytes(int64_t n, int64_t d, int64_t vocab, int group, int k, bool grad) {
     const int64_t nc = n < CHUNK ? n : CHUNK;
     int64_t words = 0, rows = 0;
     auto most = [&](int64_t tokens, int64_t R, int64_t span) {
@@ -125,7 +127,7 @@ size_t head_ws_bytes(int64_t n, int64_t d, int64_t vocab, int k, bool grad) {
                 const HeadPlan a = plan_of(32 * (T - 1) + 1, d, vocab, parts, bits);   // the fewest tokens: the most spans that fit
                 most(tokens, a.R, a.span);
             }
-    return layout(nullptr, nullptr, nc, words, rows, d, vocab, k, grad ? 2 : 0);
+    return layout(nullptr, nullptr, nc, words, rows, d, vocab, group, k, grad ? 2 : 0);
 }
 
 __global__ __launch_bounds__(256) void head_emax_kernel(const int8_t* e, int64_t vocab, int32_t* emax) {
@@ -481,26 +483,27 @@ gptq_status head_launch(const HeadCall& c, hipStream_t s) {
     for (int64_t tok0 = 0; tok0 < c.n; tok0 += CHUNK) {
         const int64_t nc = c.n - tok0 < CHUNK ? c.n - tok0 : CHUNK;
         const HeadPlan p = plan_of(nc, d, c.vocab, parts, c.bits);
-        layout(&a.b, (uint8_t*)c.ws, nc, nc * p.R * p.span, nc * p.R, d, c.vocab, c.k, parts);
+        layout(&a.b, (uint8_t*)c.ws, nc, nc * p.R * p.span, nc * p.R, d, c.vocab, c.group, c.k, parts);
         a.n = nc; a.tok0 = tok0; a.R = p.R; a.span = p.span;
         if (grad) {
             rows_launch(c.L, 1, c.vocab, a.b.e, a.b.T, s);
             head_emax_kernel<<<(unsigned)a.blocks, 256, 0, s>>>(a.b.e, c.vocab, a.b.emax);
             GPTQ_LAUNCH_CHECK();
         }
+        GroupedArgs g = {};                                      // the whole head
+        g.L = c.L; g.d_row = c.vocab; g.x = (const uint16_t*)c.x + tok0 * c.ldx; g.ldx = c.ldx; g.n = nc; g.E = 1;
+        const gptq_status ready = grouped_prepare(g, c.xt, c.bits, c.group, a.b.forward, s);
+        if (ready != GPTQ_OK) return ready;
         int round = 0;
         for (int first = 0; first < p.spans; first += p.R, ++round) {
             const int slots = p.spans - first < p.R ? p.spans - first : p.R;
             const int64_t v0 = first * p.span, v1 = v0 + slots * p.span < c.vocab ? v0 + slots * p.span : c.vocab;
-            GroupedArgs g = {};
-            g.L = c.L;
-            g.L.codes += v0 * c.L.code_ld;
-            g.L.scales += v0 * c.L.n_groups;
-            g.L.zeros += v0 * c.L.n_groups;
-            g.d_row = v1 - v0; g.ldy = p.R * p.span;
-            g.x = (const uint16_t*)c.x + tok0 * c.ldx; g.ldx = c.ldx; g.n = nc;
-            g.offsets = nullptr; g.E = 1; g.y = a.b.z; g.yt = GPTQ_F32;
-            const gptq_status st = grouped_launch(g, c.xt, c.bits, c.group, s);
+            GroupedArgs h = g;
+            h.L.codes += v0 * c.L.code_ld;
+            h.L.scales += v0 * c.L.n_groups;
+            h.L.zeros += v0 * c.L.n_groups;
+            h.d_row = v1 - v0; h.y = a.b.z; h.yt = GPTQ_F32; h.ldy = p.R * p.span;
+            const gptq_status st = grouped_launch(h, c.xt, c.bits, c.group, a.b.forward, c.vocab, v0, s);
             if (st != GPTQ_OK) return st;
             a.round = round; a.slots = slots;
             const dim3 grid((unsigned)nc, (unsigned)slots);

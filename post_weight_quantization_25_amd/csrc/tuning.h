@@ -77,8 +77,15 @@ struct GroupedArgs {
     const uint16_t* x; int64_t ldx; int64_t n;
     const int32_t* offsets; int E;
     void* y; gptq_dtype yt; int64_t ldy;
+    const int32_t* unless_zero;                                 // the kernel of stored_gemm.h: not nullptr: works only if not 0
 };
-gptq_status grouped_launch(const GroupedArgs& a, gptq_dtype xt, int bits, int group, hipStream_t s);
+// grouped_prepare lays the activations and the scales of all E d_row rows out for many tokens, once
+// for products of several spans of the rows; grouped_launch takes rows row0 .. row0 + a.d_row - 1
+// of them (with experts: all).  ws: grouped_ws_bytes, which is 0 where nothing is laid out.
+size_t grouped_ws_bytes(int64_t n, int64_t E, int64_t d_row, int64_t d_col, int group);
+gptq_status grouped_prepare(const GroupedArgs& a, gptq_dtype xt, int bits, int group, void* ws, hipStream_t s);
+gptq_status grouped_launch(const GroupedArgs& a, gptq_dtype xt, int bits, int group, void* ws, int64_t all_rows, int64_t row0,
+                           hipStream_t s);
 
 // ---- dx[t] = What_e^T dy[t] (grouped_back.hip)
 struct BackCall {
@@ -88,7 +95,7 @@ struct BackCall {
     void* dx; gptq_dtype dxt;                                   // pitch d_col
     void* ws;
 };
-size_t back_ws_bytes(int64_t n, int64_t E, int64_t d_row, int64_t d_col);
+size_t back_ws_bytes(int64_t n, int64_t E, int64_t d_row, int64_t d_col, int group);
 gptq_status back_launch(const BackCall& c, hipStream_t s);
 
 // ---- losses at a stored head (head_loss.hip)
@@ -103,7 +110,7 @@ struct HeadCall {
     void* dx; gptq_dtype dxt;                                   // or nullptr
     void* ws;
 };
-size_t head_ws_bytes(int64_t n, int64_t d, int64_t vocab, int k, bool grad);
+size_t head_ws_bytes(int64_t n, int64_t d, int64_t vocab, int group, int k, bool grad);
 gptq_status head_launch(const HeadCall& c, hipStream_t s);
 
 inline size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }

@@ -55,7 +55,7 @@ static gptq_status head(const uint8_t* codes, const uint16_t* scales, const uint
     if (xt == GPTQ_F32 || ldx > TUNE_MAX_PITCH || k > TUNE_MAX_TOP) return GPTQ_ERR_UNSUPPORTED;
     if (n == 0) return GPTQ_OK;
     if (!codes || !scales || !zeros || !x || !ids || !loss) return GPTQ_ERR_INVALID_ARG;
-    if (misfit(ws, ws_bytes, head_ws_bytes(n, d, vocab, k, dx != nullptr))) return GPTQ_ERR_WORKSPACE;
+    if (misfit(ws, ws_bytes, head_ws_bytes(n, d, vocab, group, k, dx != nullptr))) return GPTQ_ERR_WORKSPACE;
     HeadCall c;
     c.L = stored_layer(codes, scales, zeros, d, bits, group);
     c.vocab = vocab; c.bits = bits; c.group = group;
@@ -65,35 +65,43 @@ static gptq_status head(const uint8_t* codes, const uint16_t* scales, const uint
     return head_launch(c, (hipStream_t)stream);
 }
 
-static bool head_sized(int64_t n, int64_t d, int64_t vocab) {
-    return n > 0 && n <= SERVE_MAX_TOKENS && d > 0 && d <= TUNE_MAX_WIDTH && vocab > 0 && vocab <= ((int64_t)1 << 25);
-}
-
 #pragma GCC visibility push(default)
 extern "C" {
 
 gptq_status gptqt_linear_grouped(const uint8_t* codes, const uint16_t* scales_f16, const uint16_t* zeros_f16,
                                  int32_t n_experts, int64_t d_row, int64_t d_col, int32_t bits, int32_t group_size,
                                  const void* x, gptq_dtype x_dtype, int64_t n_rows, int64_t ldx,
-                                 const int32_t* offsets, void* y, gptq_dtype y_dtype, void* stream) {
+                                 const int32_t* offsets, void* y, gptq_dtype y_dtype, void* ws, size_t ws_bytes, void* stream) {
     const gptq_status st = check_grouped(n_experts, d_row, d_col, bits, group_size, n_rows, x_dtype, y_dtype, ldx, d_col,
                                          d_row, offsets);
     if (st != GPTQ_OK) return st;
     if (ldx > TUNE_MAX_PITCH) return GPTQ_ERR_UNSUPPORTED;
     if (n_rows == 0) return GPTQ_OK;
     if (!codes || !scales_f16 || !zeros_f16 || !x || !y) return GPTQ_ERR_INVALID_ARG;
-    GroupedArgs a;
+    const size_t need = grouped_ws_bytes(n_rows, n_experts, d_row, d_col, group_size);
+    if (need && misfit(ws, ws_bytes, need)) return GPTQ_ERR_WORKSPACE;
+    GroupedArgs a = {};
     a.L = stored_layer(codes, scales_f16, zeros_f16, d_col, bits, group_size);
     a.d_row = d_row; a.x = (const uint16_t*)x; a.ldx = ldx; a.n = n_rows; a.offsets = offsets; a.E = n_experts;
     a.y = y; a.yt = y_dtype; a.ldy = d_row;
-    return grouped_launch(a, x_dtype, bits, group_size, (hipStream_t)stream);
+    const gptq_status ready = grouped_prepare(a, x_dtype, bits, group_size, ws, (hipStream_t)stream);
+    return ready != GPTQ_OK ? ready : grouped_launch(a, x_dtype, bits, group_size, ws, d_row, 0, (hipStream_t)stream);
 }
 
-size_t gptqt_linear_grouped_backward_workspace_size(int64_t n_rows, int32_t n_experts, int64_t d_row, int64_t d_col) {
-    if (n_rows <= 0 || n_rows > SERVE_MAX_TOKENS || n_experts < 1 || n_experts > TUNE_MAX_EXPERTS || d_row < 1 ||
-        d_row > ((int64_t)1 << 25) || n_experts * d_row > ((int64_t)1 << 26) || d_col < 1 || d_col > TUNE_MAX_WIDTH)
-        return 0;
-    return back_ws_bytes(n_rows, n_experts, d_row, d_col);
+static bool layer_sized(int64_t n, int64_t E, int64_t d_row, int64_t d_col, int32_t& group) {
+    int32_t g = group;
+    const bool ok = check_layer(E, d_row, d_col, 8, g, n) == GPTQ_OK && n > 0;
+    group = g;
+    return ok;
+}
+
+size_t gptqt_linear_grouped_workspace_size(int64_t n_rows, int32_t n_experts, int64_t d_row, int64_t d_col, int32_t group_size) {
+    return layer_sized(n_rows, n_experts, d_row, d_col, group_size) ? grouped_ws_bytes(n_rows, n_experts, d_row, d_col, group_size) : 0;
+}
+
+size_t gptqt_linear_grouped_backward_workspace_size(int64_t n_rows, int32_t n_experts, int64_t d_row, int64_t d_col,
+                                                    int32_t group_size) {
+    return layer_sized(n_rows, n_experts, d_row, d_col, group_size) ? back_ws_bytes(n_rows, n_experts, d_row, d_col, group_size) : 0;
 }
 
 gptq_status gptqt_linear_grouped_backward(const uint8_t* codes, const uint16_t* scales_f16, const uint16_t* zeros_f16,
@@ -106,7 +114,7 @@ gptq_status gptqt_linear_grouped_backward(const uint8_t* codes, const uint16_t* 
     if (st != GPTQ_OK) return st;
     if (n_rows == 0) return GPTQ_OK;
     if (!codes || !scales_f16 || !zeros_f16 || !dy || !dx) return GPTQ_ERR_INVALID_ARG;
-    if (misfit(ws, ws_bytes, back_ws_bytes(n_rows, n_experts, d_row, d_col))) return GPTQ_ERR_WORKSPACE;
+    if (misfit(ws, ws_bytes, back_ws_bytes(n_rows, n_experts, d_row, d_col, group_size))) return GPTQ_ERR_WORKSPACE;
     BackCall c;
     c.L = stored_layer(codes, scales_f16, zeros_f16, d_col, bits, group_size);
     c.d_row = d_row; c.bits = bits; c.dy = dy; c.dyt = dy_dtype; c.ldy = ld_dy; c.n = n_rows;
@@ -114,8 +122,8 @@ gptq_status gptqt_linear_grouped_backward(const uint8_t* codes, const uint16_t* 
     return back_launch(c, (hipStream_t)stream);
 }
 
-size_t gptqt_cross_entropy_workspace_size(int64_t n_tokens, int64_t d, int64_t vocab, int32_t with_grad) {
-    return head_sized(n_tokens, d, vocab) ? head_ws_bytes(n_tokens, d, vocab, 1, with_grad != 0) : 0;
+size_t gptqt_cross_entropy_workspace_size(int64_t n_tokens, int64_t d, int64_t vocab, int32_t group_size, int32_t with_grad) {
+    return layer_sized(n_tokens, 1, vocab, d, group_size) ? head_ws_bytes(n_tokens, d, vocab, group_size, 1, with_grad != 0) : 0;
 }
 
 gptq_status gptqt_cross_entropy(const uint8_t* codes, const uint16_t* scales_f16, const uint16_t* zeros_f16,
@@ -127,9 +135,10 @@ gptq_status gptqt_cross_entropy(const uint8_t* codes, const uint16_t* scales_f16
                 GPTQ_F32, 1, 1.f, weights, loss, dx, dx_dtype, ws, ws_bytes, stream);
 }
 
-size_t gptqt_distill_workspace_size(int64_t n_tokens, int64_t d, int64_t vocab, int32_t top_k, int32_t with_grad) {
-    return head_sized(n_tokens, d, vocab) && top_k >= 1 && top_k <= TUNE_MAX_TOP
-               ? head_ws_bytes(n_tokens, d, vocab, top_k, with_grad != 0) : 0;
+size_t gptqt_distill_workspace_size(int64_t n_tokens, int64_t d, int64_t vocab, int32_t group_size, int32_t top_k,
+                                    int32_t with_grad) {
+    return layer_sized(n_tokens, 1, vocab, d, group_size) && top_k >= 1 && top_k <= TUNE_MAX_TOP
+               ? head_ws_bytes(n_tokens, d, vocab, group_size, top_k, with_grad != 0) : 0;
 }
 
 gptq_status gptqt_distill(const uint8_t* codes, const uint16_t* scales_f16, const uint16_t* zeros_f16, int64_t vocab,

@@ -39,8 +39,12 @@ def _layers(q: Quantized, offsets, device):
     return e, rows // e
 
 
+def linear_grouped_workspace_size(n_rows: int, n_experts: int, d_row: int, d_col: int, group_size: int = 128) -> int:
+    return lib.gptqt_linear_grouped_workspace_size(n_rows, n_experts, d_row, d_col, group_size)
+
+
 def linear_grouped(q: Quantized, x: torch.Tensor, offsets: torch.Tensor | None = None, out_dtype=torch.float32,
-                   out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                   out: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y[t] = What_e x[t] for the rows t of expert e, offsets[e] <= t < offsets[e + 1]
     (gptqt_linear_grouped).  ``q`` holds the experts' rows one after another (``torch.cat`` of
     their codes, scales and zeros); ``offsets``: n_experts + 1 int32 on the device, or None for
@@ -51,15 +55,17 @@ def linear_grouped(q: Quantized, x: torch.Tensor, offsets: torch.Tensor | None =
     ldx, n = _activations(x, "x", q.d_col)
     with _On(dev, stream) as s:
         out = _out(out, n, d_row, out_dtype, dev, x)
+        ws = _workspace(linear_grouped_workspace_size(n, e, d_row, q.d_col, q.group_size), dev, ws)
         _check(lib.gptqt_linear_grouped(q.codes.data_ptr(), q.scales.data_ptr(), q.zeros.data_ptr(), e, d_row, q.d_col,
                                         q.bits, q.group_size, x.data_ptr(), _DT[x.dtype], n, ldx,
                                         None if offsets is None else offsets.data_ptr(), out.data_ptr(),
-                                        _DT[out.dtype], s), "gptqt_linear_grouped")
+                                        _DT[out.dtype], None if ws is None else ws.data_ptr(),
+                                        0 if ws is None else ws.numel(), s), "gptqt_linear_grouped")
     return out
 
 
-def linear_grouped_backward_workspace_size(n_rows: int, n_experts: int, d_row: int, d_col: int) -> int:
-    return lib.gptqt_linear_grouped_backward_workspace_size(n_rows, n_experts, d_row, d_col)
+def linear_grouped_backward_workspace_size(n_rows: int, n_experts: int, d_row: int, d_col: int, group_size: int = 128) -> int:
+    return lib.gptqt_linear_grouped_backward_workspace_size(n_rows, n_experts, d_row, d_col, group_size)
 
 
 def linear_grouped_backward(q: Quantized, dy: torch.Tensor, offsets: torch.Tensor | None = None, out_dtype=None,
@@ -73,7 +79,7 @@ def linear_grouped_backward(q: Quantized, dy: torch.Tensor, offsets: torch.Tenso
     ld, n = _activations(dy, "dy", d_row)
     with _On(dev, stream) as s:
         out = _out(out, n, q.d_col, dy.dtype if out_dtype is None else out_dtype, dev, dy)
-        ws = _workspace(linear_grouped_backward_workspace_size(n, e, d_row, q.d_col), dev, ws)
+        ws = _workspace(linear_grouped_backward_workspace_size(n, e, d_row, q.d_col, q.group_size), dev, ws)
         _check(lib.gptqt_linear_grouped_backward(
             q.codes.data_ptr(), q.scales.data_ptr(), q.zeros.data_ptr(), e, d_row, q.d_col, q.bits, q.group_size,
             dy.data_ptr(), _DT[dy.dtype], n, ld, None if offsets is None else offsets.data_ptr(), out.data_ptr(),
@@ -99,8 +105,8 @@ def _head(q, x, weights, loss, dx, grad, dx_dtype):
     return vocab, ldx, n, loss, dx
 
 
-def cross_entropy_workspace_size(n_tokens: int, d: int, vocab: int, grad: bool = True) -> int:
-    return lib.gptqt_cross_entropy_workspace_size(n_tokens, d, vocab, int(bool(grad)))
+def cross_entropy_workspace_size(n_tokens: int, d: int, vocab: int, group_size: int = 128, grad: bool = True) -> int:
+    return lib.gptqt_cross_entropy_workspace_size(n_tokens, d, vocab, group_size, int(bool(grad)))
 
 
 def cross_entropy(q: Quantized, x: torch.Tensor, targets: torch.Tensor, weights: torch.Tensor | None = None,
@@ -115,7 +121,7 @@ def cross_entropy(q: Quantized, x: torch.Tensor, targets: torch.Tensor, weights:
     _tensor(targets, "targets", torch.int32, x.shape[:1], dev)
     with _On(dev, stream) as s:
         vocab, ldx, n, loss, dx = _head(q, x, weights, loss, dx, grad, dx_dtype)
-        ws = _workspace(cross_entropy_workspace_size(n, q.d_col, vocab, grad), dev, ws)
+        ws = _workspace(cross_entropy_workspace_size(n, q.d_col, vocab, q.group_size, grad), dev, ws)
         _check(lib.gptqt_cross_entropy(
             q.codes.data_ptr(), q.scales.data_ptr(), q.zeros.data_ptr(), vocab, q.d_col, q.bits, q.group_size,
             x.data_ptr(), _DT[x.dtype], n, ldx, targets.data_ptr(), None if weights is None else weights.data_ptr(),
@@ -124,8 +130,8 @@ def cross_entropy(q: Quantized, x: torch.Tensor, targets: torch.Tensor, weights:
     return loss, dx
 
 
-def distill_workspace_size(n_tokens: int, d: int, vocab: int, top_k: int, grad: bool = True) -> int:
-    return lib.gptqt_distill_workspace_size(n_tokens, d, vocab, top_k, int(bool(grad)))
+def distill_workspace_size(n_tokens: int, d: int, vocab: int, top_k: int, group_size: int = 128, grad: bool = True) -> int:
+    return lib.gptqt_distill_workspace_size(n_tokens, d, vocab, group_size, top_k, int(bool(grad)))
 
 
 def distill(q: Quantized, x: torch.Tensor, ids: torch.Tensor, top: torch.Tensor, temperature: float = 1.0,
@@ -144,7 +150,7 @@ def distill(q: Quantized, x: torch.Tensor, ids: torch.Tensor, top: torch.Tensor,
     _tensor(top, "top", None, (x.shape[0], k), dev)
     with _On(dev, stream) as s:
         vocab, ldx, n, loss, dx = _head(q, x, weights, loss, dx, grad, dx_dtype)
-        ws = _workspace(distill_workspace_size(n, q.d_col, vocab, k, grad), dev, ws)
+        ws = _workspace(distill_workspace_size(n, q.d_col, vocab, k, q.group_size, grad), dev, ws)
         _check(lib.gptqt_distill(
             q.codes.data_ptr(), q.scales.data_ptr(), q.zeros.data_ptr(), vocab, q.d_col, q.bits, q.group_size,
             x.data_ptr(), _DT[x.dtype], n, ldx, ids.data_ptr(), top.data_ptr(), _DT[top.dtype], k, float(temperature),

@@ -38,6 +38,14 @@ CASES = [
     (40, 64, 8, 32, 9, 130, BF, F32, "fraction"), (130, 320, 4, 64, 1000, 3, HF, HF, "far"),
     (70, 384, 3, 64, 400, 20, BF, F32, "whole"), (257, 258, 4, 0, 500, 2, BF, BF, "whole"),
     (64, 128, 8, 128, 1, 64, BF, BF, "whole"), (1, 8, 3, 0, 5, 4, HF, F32, "whole"),
+    # many rows per expert: every width and group, rows that end in a slab, a turn, a chunk and a tile
+    (300, 128, 4, 128, 300, 0, BF, F32, "whole"), (257, 320, 4, 64, 513, 0, HF, F32, "whole"),
+    (64, 96, 4, 32, 161, 0, BF, BF, "whole"), (100, 160, 4, 32, 700, 3, HF, F32, "symmetric"),
+    (520, 256, 8, 128, 400, 0, HF, HF, "whole"), (33, 192, 8, 64, 600, 2, BF, F32, "whole"), (300, 352, 8, 32, 300, 0, BF, F32, "whole"),
+    (130, 384, 3, 128, 520, 0, BF, F32, "whole"), (90, 448, 3, 64, 260, 0, HF, F32, "symmetric"), (77, 128, 3, 32, 300, 0, BF, BF, "whole"),
+    (300, 416, 4, 0, 300, 0, BF, F32, "symmetric"), (70, 48, 8, 0, 333, 0, HF, F32, "whole"), (260, 128, 3, 0, 270, 0, BF, F32, "whole"),
+    (90, 250, 4, 0, 500, 2, BF, F32, "whole"), (300, 256, 4, 64, 290, 0, BF, F32, "fraction"), (64, 160, 8, 32, 700, 3, HF, F32, "far"),
+    (2000, 64, 4, 32, 2100, 9, BF, F32, "whole"),
 ]
 
 
@@ -69,6 +77,8 @@ def test_parity(d_row, d_col, bits, group, n, E, dt, yt, zeros, back):
                 ref, bound = back_reference(qe, We, x, yt)
             else:
                 ref, bound = x @ We.t(), (d_col + 64) * U * zero_parts(qe, x)
+                # bfloat16 as fp16 rows: what is below 2^-28 of a row's largest
+                bound = bound + 2.0 ** -39 * x.abs().amax(1, keepdim=True) * We.abs().sum(1)[None]
             check(y, ref, bound, yt, slice(r0, r1))
     assert bool((y.cpu()[~inside] == 7.0).all())
     again = f(q, a, None if offs is None else offs.cuda(), out_dtype=yt)
@@ -93,7 +103,7 @@ def test_offsets_that_fall_or_leave_the_rows(back):
             check(y, ref, bound, F32, slice(r0, r1))
 
 
-@pytest.mark.parametrize("n", [4, 200])
+@pytest.mark.parametrize("n", [4, 200, 500])
 @pytest.mark.parametrize("back", [False, True])
 def test_strided_rows(n, back):
     """Rows of an odd pitch, as views of wider matrices."""
@@ -122,7 +132,7 @@ def test_backward_against_differences():
 
 
 @pytest.mark.parametrize("back", [False, True])
-@pytest.mark.parametrize("n", [3, 150])
+@pytest.mark.parametrize("n", [3, 150, 300])
 def test_infinities_stay_in_their_rows(n, back):
     import post_weight_quantization_25_amd as g
     q, _ = stored(128, 128, 4, 128, 4)
@@ -154,6 +164,45 @@ def test_backward_of_far_apart_magnitudes():
         y = g.linear_grouped_backward(q, dy.cuda(), out_dtype=t)
         ref, bound = back_reference(q, What, dy, t)
         check(y, ref, bound, t, slice(None))
+    assert bool((y[3] == 0).all())
+
+
+@pytest.mark.parametrize("n", [5, 300])
+def test_scales_of_zero_and_far_apart(n):
+    """Groups without a scale give nothing, whatever their codes; scales from 2^-14 to 2^10 in a row."""
+    import post_weight_quantization_25_amd as g
+    from serving_helpers import weights
+    for dead in (False, True):
+        q, _ = stored(150, 256, 4, 32, 8)
+        gen = torch.Generator().manual_seed(7)
+        S = 2.0 ** torch.randint(-14, 11, q.scales.shape, generator=gen).double()
+        if dead:
+            S[3] = 0
+            S[5, 2] = 0
+            S[6, 0] = 0
+            S[7, -1] = 0
+        q.scales.copy_(S.half())
+        What = torch.from_numpy(weights(q.codes.cpu().numpy(), q.scales.cpu().numpy(), q.zeros.cpu().numpy(), 4, 32))
+        x = torch.randn(n, 256, generator=gen).to(BF)
+        y = g.linear_grouped(q, x.cuda())
+        check(y, x.double() @ What.t(), (256 + 64) * U * zero_parts(q, x.double()), F32, slice(None))
+        assert not dead or bool((y[:, 3] == 0).all())
+
+
+def test_forward_of_far_apart_magnitudes():
+    """Elements of x from 2^-20 to 2^20 of each other, rows of zeros and of subnormals: bfloat16
+    elements below 2^-28 of their row's largest are off by 2^-39 of it."""
+    import post_weight_quantization_25_amd as g
+    q, What = stored(200, 256, 4, 64, 6)
+    gen = torch.Generator().manual_seed(2)
+    x = (torch.randn(300, 256, generator=gen) * 2.0 ** torch.randint(-20, 21, (300, 256), generator=gen)).to(BF)
+    x[3] = 0
+    x[4] *= 2.0 ** -126
+    x[5] *= 2.0 ** 100
+    y = g.linear_grouped(q, x.cuda())
+    d = x.double()
+    bound = (256 + 64) * U * zero_parts(q, d) + 2.0 ** -39 * d.abs().amax(1, keepdim=True) * What.abs().sum(1)[None]
+    check(y, d @ What.t(), bound, F32, slice(None))
     assert bool((y[3] == 0).all())
 
 

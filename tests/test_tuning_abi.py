@@ -20,12 +20,13 @@ FAKE = ctypes.c_void_p(0x1000)   # never dereferenced: validation rejects the ca
 vp, i64, i32, sz, dt = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t, ctypes.c_int
 
 SIG = {
-    "gptqt_linear_grouped": (dt, [vp, vp, vp, i32, i64, i64, i32, i32, vp, dt, i64, i64, vp, vp, dt, vp]),
-    "gptqt_linear_grouped_backward_workspace_size": (sz, [i64, i32, i64, i64]),
+    "gptqt_linear_grouped_workspace_size": (sz, [i64, i32, i64, i64, i32]),
+    "gptqt_linear_grouped": (dt, [vp, vp, vp, i32, i64, i64, i32, i32, vp, dt, i64, i64, vp, vp, dt, vp, sz, vp]),
+    "gptqt_linear_grouped_backward_workspace_size": (sz, [i64, i32, i64, i64, i32]),
     "gptqt_linear_grouped_backward": (dt, [vp, vp, vp, i32, i64, i64, i32, i32, vp, dt, i64, i64, vp, vp, dt, vp, sz, vp]),
-    "gptqt_cross_entropy_workspace_size": (sz, [i64, i64, i64, i32]),
+    "gptqt_cross_entropy_workspace_size": (sz, [i64, i64, i64, i32, i32]),
     "gptqt_cross_entropy": (dt, [vp, vp, vp, i64, i64, i32, i32, vp, dt, i64, i64, vp, vp, vp, vp, dt, vp, sz, vp]),
-    "gptqt_distill_workspace_size": (sz, [i64, i64, i64, i32, i32]),
+    "gptqt_distill_workspace_size": (sz, [i64, i64, i64, i32, i32, i32]),
     "gptqt_distill": (dt, [vp, vp, vp, i64, i64, i32, i32, vp, dt, i64, i64, vp, vp, dt, i32, ctypes.c_float, vp, vp, vp, dt,
                            vp, sz, vp]),
 }
@@ -77,8 +78,8 @@ def layer_errors(call):
 
 def test_grouped_argument_errors(lib):
     def call(codes=FAKE, S=FAKE, Z=FAKE, E=3, d_row=4, d_col=256, bits=4, G=128, x=FAKE, xt=BF16, n=2, ldx=512, offs=FAKE,
-             y=FAKE, yt=F32):
-        return lib.gptqt_linear_grouped(codes, S, Z, E, d_row, d_col, bits, G, x, xt, n, ldx, offs, y, yt, None)
+             y=FAKE, yt=F32, ws=FAKE, wsb=1 << 40):
+        return lib.gptqt_linear_grouped(codes, S, Z, E, d_row, d_col, bits, G, x, xt, n, ldx, offs, y, yt, ws, wsb, None)
 
     layer_errors(call)
     assert call(E=0) == INVALID_ARG and call(E=4097) == UNSUPPORTED
@@ -89,13 +90,22 @@ def test_grouped_argument_errors(lib):
     for name in ("codes", "S", "Z", "x", "y"):
         assert call(**{name: None}) == INVALID_ARG, name
     assert call(n=0, codes=None, x=None, y=None) == OK
+    size = lib.gptqt_linear_grouped_workspace_size
+    for bad in ((0, 3, 4, 256, 128), (2, 0, 4, 256, 128), (2, 3, 0, 256, 128), (2, 3, 4, 0, 128), (2000, 3, 4, 256, 96)):
+        assert size(*bad) == 0, bad
+    assert size(2, 3, 4, 256, 128) == 0                    # few rows: nothing is laid out
+    need = size(2000, 3, 4, 256, 128)
+    assert need >= 2000 * 256 * 2 + 2000 * 4 + 3 * 4 * 2 * 8
+    assert call(n=2000, ws=None) == WORKSPACE and call(n=2000, wsb=need - 1) == WORKSPACE
+    assert call(n=2000, ws=ctypes.c_void_p(0x1008)) == WORKSPACE
 
 
 def test_backward_argument_errors(lib):
     size = lib.gptqt_linear_grouped_backward_workspace_size
-    for bad in ((0, 3, 4, 256), (2, 0, 4, 256), (2, 3, 0, 256), (2, 3, 4, 0), (2, 4097, 4, 256), (2, 3, 1 << 26, 256)):
+    for bad in ((0, 3, 4, 256, 128), (2, 0, 4, 256, 128), (2, 3, 0, 256, 128), (2, 3, 4, 0, 128), (2, 4097, 4, 256, 128),
+                (2, 3, 1 << 26, 256, 128), (2, 3, 4, 256, 48)):
         assert size(*bad) == 0, bad
-    need = size(2, 3, 4, 256)
+    need = size(2, 3, 4, 256, 128)
     assert need >= 2 * 64 * 2 + 2 * 4 + 12                 # fp16 rows, their exponents, the weights' exponents
 
     def call(codes=FAKE, S=FAKE, Z=FAKE, E=3, d_row=4, d_col=256, bits=4, G=128, x=FAKE, xt=BF16, n=2, ldx=512, offs=FAKE,
@@ -116,8 +126,8 @@ def test_backward_argument_errors(lib):
 @pytest.mark.parametrize("op", ["ce", "distill"])
 def test_head_argument_errors(lib, op):
     def size(n, d, V, grad=1):
-        return (lib.gptqt_cross_entropy_workspace_size(n, d, V, grad) if op == "ce"
-                else lib.gptqt_distill_workspace_size(n, d, V, 5, grad))
+        return (lib.gptqt_cross_entropy_workspace_size(n, d, V, 128, grad) if op == "ce"
+                else lib.gptqt_distill_workspace_size(n, d, V, 128, 5, grad))
     for bad in ((0, 256, 4), (2, 0, 4), (2, 256, 0), (65535 * 64 + 1, 256, 4), (2, 1 << 17, 4), (2, 256, (1 << 25) + 1)):
         assert size(*bad) == 0, bad
     need = size(2, 256, 4)
@@ -142,8 +152,8 @@ def test_head_argument_errors(lib, op):
         assert call(k=0) == INVALID_ARG and call(k=1025) == UNSUPPORTED and call(tt=7) == INVALID_ARG
         for T in (0.0, -1.0, float("nan"), float("inf")):
             assert call(T=T) == INVALID_ARG
-        assert lib.gptqt_distill_workspace_size(2, 256, 4, 0, 1) == 0
-        assert lib.gptqt_distill_workspace_size(2, 256, 4, 1025, 1) == 0
+        assert lib.gptqt_distill_workspace_size(2, 256, 4, 128, 0, 1) == 0
+        assert lib.gptqt_distill_workspace_size(2, 256, 4, 128, 1025, 1) == 0
 
 
 @pytest.mark.parametrize("d,vocab", [(64, 1), (64, 9000), (1024, 50021), (4096, 131072), (5504, 32000)])
@@ -151,11 +161,12 @@ def test_head_argument_errors(lib, op):
 def test_workspaces_do_not_fall(lib, d, vocab, grad):
     last = 0
     for n in list(range(1, 700)) + list(range(700, 9000, 41)):
-        v = lib.gptqt_distill_workspace_size(n, d, vocab, 7, grad)
+        v = lib.gptqt_distill_workspace_size(n, d, vocab, 32, 7, grad)
         assert v >= last, n
         last = v
-    last = 0
-    for n in range(1, 2000):
-        v = lib.gptqt_linear_grouped_backward_workspace_size(n, 8, vocab, d)
-        assert v >= last, n
-        last = v
+    for size in (lib.gptqt_linear_grouped_backward_workspace_size, lib.gptqt_linear_grouped_workspace_size):
+        last = 0
+        for n in range(1, 2000):
+            v = size(n, 8, vocab, d, 64)
+            assert v >= last, n
+            last = v
