@@ -47,7 +47,7 @@ struct ForwardGemm {
     static constexpr int ROW = CB == 3 ? 48 : 64, SPC = CB == 8 ? 2 : 4;      // bytes of a row in a chunk; slabs of a chunk
     static constexpr int C_BYTES = BN * ROW, PIECES = ROW / 16, C_LOADS = BN * PIECES / 64;   // 16 or 12 loads of a wave
     static constexpr int SETS = GPT ? GPT : 1, T_BYTES = 2048 * SETS;         // a turn's rho and zz, 1 KB each per group
-    static constexpr int LDS_BYTES = 4 * A_BYTES + 2 * B_BYTES + 3 * C_BYTES + 2 * T_BYTES;
+    static constexpr int LDS_BYTES = 4 * A_BYTES + 2 * B_BYTES + 2 * C_BYTES + 2 * T_BYTES;
     static constexpr int SPG = GPT ? 4 / GPT : 4;                             // slabs of a group
 
     // acc[i][j]: lane l's value v is row 64 (wave % 4) + 16 i + l % 16, token 128 (wave / 4) + 16 j + 4 (l / 16) + v.
@@ -57,7 +57,7 @@ struct ForwardGemm {
         const int wr = 64 * (wave & 3), wt = 128 * (wave >> 2);
         uint8_t* bb = lds + 4 * A_BYTES;
         uint8_t* cc = bb + 2 * B_BYTES;
-        uint8_t* tt = cc + 3 * C_BYTES;
+        uint8_t* tt = cc + 2 * C_BYTES;
         const int slabs = (int)((L.d_col + BK - 1) / BK), turns = (slabs + 3) / 4;
 
         uint32_t aoff[2];
@@ -101,13 +101,10 @@ struct ForwardGemm {
             a_next += a_left > 0 ? a_step : 0;
             --a_left;
         };
-        uint32_t c_in = 0, c_out = 0;                            // the ring's places to fill, and of the next slab's chunk
-        auto after = [&](uint32_t at) { return at == 2 * C_BYTES ? 0 : at + C_BYTES; };
-        auto load_c = [&]() {
+        auto load_c = [&](int place) {
             const bool more = c_left > 0;                        // uniform
-            dma16<0>(more ? coff[0] : coff_last[0], c_next, m_c + c_in);
-            if (C_LOADS == 16 || wave < C_LOADS - 8) dma16<0>(more ? coff[1] : coff_last[1], c_next, m_c + c_in + 8 * 1024);
-            c_in = after(c_in);
+            dma16<0>(more ? coff[0] : coff_last[0], c_next, m_c + place * C_BYTES);
+            if (C_LOADS == 16 || wave < C_LOADS - 8) dma16<0>(more ? coff[1] : coff_last[1], c_next, m_c + place * C_BYTES + 8 * 1024);
             c_next += more ? ROW : 0;
             --c_left;
         };
@@ -120,9 +117,9 @@ struct ForwardGemm {
         // The thread's codes: row tid % 256, columns 16 half .. of a slab.
         const int crow = tid & 255, half = tid >> 8;
         struct Codes { uint32_t w[4]; uint32_t zz; };
-        auto read_codes = [&](Codes& r, int sub, int set, int turn) {   // slab `sub` of its chunk, group `set` of its turn
+        auto read_codes = [&](Codes& r, int place, int sub, int set, int turn) {   // slab `sub` of its chunk, group `set` of its turn
             r.zz = *reinterpret_cast<const uint32_t*>(tt + (turn & 1) * T_BYTES + set * 2048 + 1024 + 4 * crow);
-            const uint8_t* row = cc + c_out + crow * ROW;
+            const uint8_t* row = cc + place * C_BYTES + crow * ROW;
             if constexpr (CB == 8) {
                 const u32x4_t v = *reinterpret_cast<const u32x4_t*>(row + 16 * ((2 * sub + half) ^ ((crow >> 2) & 3)));
 #pragma unroll
@@ -159,32 +156,30 @@ struct ForwardGemm {
 #pragma unroll
             for (int j = 0; j < MT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-        // As in BackGemm: step s multiplies slab s, decodes slab s + 1 and sends for A of slab s + 3;
-        // chunks two ahead where one begins, tables a turn ahead.
+        u32x4_t bf[2][NI], af[4];
+        auto read_a = [&](int buf, int j) { af[j & 3] = *reinterpret_cast<const u32x4_t*>(lds + buf * A_BYTES + slab_at(wt + 16 * j + n16, q)); };
+        auto read_b = [&](int buf, int i) { bf[buf][i] = *reinterpret_cast<const u32x4_t*>(bb + buf * B_BYTES + slab_at(wr + 16 * i + n16, q)); };
+
+        // As in BackGemm: step s multiplies slab s, decodes slab s + 2 and sends for A of slab s + 3;
+        // a chunk as soon as the one in its place is decoded, two or four steps before its first slab
+        // is; the next turn's tables at a turn's first step.
         Codes r;
         Decoded d;
         auto step = [&](auto K, int turn) {
-            constexpr int k = decltype(K)::value, next = (k + 1) & 3;
-            wait_vm_lgkm0<4>();
+            constexpr int k = decltype(K)::value, ahead = (k + 2) & 3;
+            wait_vm_lgkm0<2>();
             barrier_only();
-            constexpr int RING = 3;
-            u32x4_t bf[NI], af[RING];
-            auto read_a = [&](int j) { af[j % RING] = *reinterpret_cast<const u32x4_t*>(lds + k * A_BYTES + slab_at(wt + 16 * j + n16, q)); };
-#pragma unroll
-            for (int i = 0; i < NI; ++i) bf[i] = *reinterpret_cast<const u32x4_t*>(bb + (k & 1) * B_BYTES + slab_at(wr + 16 * i + n16, q));
-            read_a(0);
-            read_a(1);
             constexpr bool begins = GPT != 0 && k % SPG == 0;    // a group (rho of the first one is 1)
             float scale[NI];
             if constexpr (begins)
 #pragma unroll
                 for (int i = 0; i < NI; ++i)
                     scale[i] = *reinterpret_cast<const float*>(tt + (turn & 1) * T_BYTES + (k / SPG) * 2048 + 4 * (wr + 16 * i + n16));
-            if (next % SPC == 0) c_out = after(c_out);
-            read_codes(r, next % SPC, GPT ? next / SPG : 0, turn + (k == 3));
-            __builtin_amdgcn_sched_barrier(0);
+            const int other = turn + (k >= 2);                   // turn of slab s + 2
+            read_codes(r, SPC == 4 ? other & 1 : ahead / 2, ahead % SPC, GPT ? ahead / SPG : 0, other);
             load_a((k + 3) & 3);
-            if (k % SPC == 0) load_c();
+            if (SPC == 4 && k == 2) load_c(turn & 1);            // chunk turn + 2; slab 4 turn + 3 was decoded a step ago
+            if (SPC == 2 && k % 2 == 0) load_c(k / 2);           // chunk of slabs s + 4, s + 5; slab s + 1 was decoded a step ago
             if (k == 0) load_t(turn + 1);
             __builtin_amdgcn_sched_barrier(0);
             auto rescale = [&](int j) {
@@ -197,26 +192,38 @@ struct ForwardGemm {
             rescale(0);
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
-                if (j + RING - 1 < MT) read_a(j + RING - 1);
+                read_a(j + 2 < MT ? k : (k + 1) & 3, (j + 2) % MT);
 #pragma unroll
-                for (int i = 0; i < NI; ++i) acc[i][j] = mfma16<X_F16>(af[j % RING], bf[i], acc[i][j]);
+                for (int i = 0; i < NI; ++i) acc[i][j] = mfma16<X_F16>(af[j & 3], bf[k & 1][i], acc[i][j]);
+                if (j >= MT - NI) read_b((k + 1) & 1, j - (MT - NI));   // slab s + 1's
                 if (j + 1 < MT) rescale(j + 1);
-                decode_one(d, r, j);
+                if (j >= 1)
+#pragma unroll
+                    for (int u = 8 * (j - 1) / (MT - 1); u < 8 * j / (MT - 1); ++u) decode_one(d, r, u);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            store(d, (k + 1) & 1);                               // (behind the last slab: not used)
+            store(d, k & 1);                                     // (behind the last slab: not used)
         };
         load_t(0);
-        load_c();
-        load_c();
+        load_c(0);
+        load_c(1);
 #pragma unroll
         for (int k = 0; k < 3; ++k) load_a(k);
         wait_vm_lgkm0<0>();
         barrier_only();
-        read_codes(r, 0, 0, 0);
 #pragma unroll
-        for (int p = 0; p < 8; ++p) decode_one(d, r, p);
-        store(d, 0);
+        for (int k = 0; k < 2; ++k) {
+            read_codes(r, 0, k, GPT ? k / SPG : 0, 0);
+#pragma unroll
+            for (int p = 0; p < 8; ++p) decode_one(d, r, p);
+            store(d, k);
+        }
+        wait_vm_lgkm0<0>();
+        barrier_only();
+#pragma unroll
+        for (int i = 0; i < NI; ++i) read_b(0, i);
+        read_a(0, 0);
+        read_a(0, 1);
         for (int turn = 0; turn < turns; ++turn) {
             step(std::integral_constant<int, 0>{}, turn);
             step(std::integral_constant<int, 1>{}, turn);

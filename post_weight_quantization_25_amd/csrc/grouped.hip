@@ -214,10 +214,6 @@ static void launch_forward_groups(const ForwardArgs& a, int group, hipStream_t s
     else launch_forward<CB, 0>(a, s);
 }
 
-// Rows per expert from which the 256 x 256 tiles are taken.
-constexpr int64_t MANY = 160;
-static bool many(int64_t n, int64_t E) { return (n + E - 1) / E > MANY; }
-
 static size_t forward_layout(ForwardBuffers* b, uint8_t* w, int64_t n, int64_t E, int64_t d_row, int64_t d_col, int group) {
     size_t at = 0;
     auto take = [&](size_t bytes) { const size_t here = at; at += up256(bytes); return w ? w + here : nullptr; };
@@ -237,11 +233,12 @@ static size_t forward_layout(ForwardBuffers* b, uint8_t* w, int64_t n, int64_t E
 }
 
 size_t grouped_ws_bytes(int64_t n, int64_t E, int64_t d_row, int64_t d_col, int group) {
-    return many(n, E) ? forward_layout(nullptr, nullptr, n, E, d_row, d_col, group) : 0;
+    return many_rows(n, E) ? forward_layout(nullptr, nullptr, n, E, d_row, d_col, group) : 0;
 }
 
+bool grouped_large(const GroupedArgs& a, int64_t rows) { return direct_codes(a.L) && forward_pays(a.n, a.E, rows, a.L.d_col); }
+
 gptq_status grouped_prepare(const GroupedArgs& a, gptq_dtype xt, int bits, int group, void* ws, hipStream_t s) {
-    if (!many(a.n, a.E) || !direct_codes(a.L)) return GPTQ_OK;
     ForwardBuffers b;
     forward_layout(&b, (uint8_t*)ws, a.n, a.E, a.d_row, a.L.d_col, group);
     const ForwardPackArgs p = {a.x, a.ldx, a.n, a.L.d_col, forward_columns(a.L.d_col), b.A, b.shift, b.odd, bits == 8};
@@ -255,11 +252,10 @@ gptq_status grouped_prepare(const GroupedArgs& a, gptq_dtype xt, int bits, int g
 
 template <int X, int CB, int RUN, int PIECE>
 static gptq_status launch(const GroupedArgs& a, hipStream_t s) {
-    const int64_t each = a.n / a.E;
-    if (each <= 16) {
+    if (small_tiles(a.n, a.E, a.d_row)) {
         const dim3 grid((unsigned)((a.d_row + 15) / 16), (unsigned)most_tiles(a.offsets, a.E, a.n, 16));
         grouped_tile_kernel<X, CB, RUN><<<grid, 64 * TW, 0, s>>>(a);
-    } else if (each <= 96) {
+    } else if (a.n / a.E <= 96) {
         launch_gemm<X, CB, PIECE, 64>(a, s);
     } else {
         launch_gemm<X, CB, PIECE, 128>(a, s);
@@ -279,11 +275,11 @@ static gptq_status launch_bits(const GroupedArgs& a, int bits, int group, hipStr
     return bits == 3 ? launch_runs<X, 3>(a, group, s) : bits == 4 ? launch_runs<X, 4>(a, group, s) : launch_runs<X, 8>(a, group, s);
 }
 
-gptq_status grouped_launch(const GroupedArgs& given, gptq_dtype xt, int bits, int group, void* ws, int64_t all_rows, int64_t row0,
-                           hipStream_t s) {
+gptq_status grouped_launch(const GroupedArgs& given, gptq_dtype xt, int bits, int group, bool large, void* ws, int64_t all_rows,
+                           int64_t row0, hipStream_t s) {
     GroupedArgs a = given;
     a.unless_zero = nullptr;
-    if (many(a.n, a.E) && direct_codes(a.L)) {
+    if (large) {
         ForwardBuffers b;
         forward_layout(&b, (uint8_t*)ws, a.n, a.E, all_rows, a.L.d_col, group);
         ForwardArgs f;

@@ -8,8 +8,6 @@
 // without work, the weight rows are split among workgroups, whose fp32 sums back_join_kernel
 // adds in order.
 
-#include <stdlib.h>
-
 #include "back_gemm.h"
 
 namespace gptq {
@@ -132,20 +130,11 @@ __global__ __launch_bounds__(256) void back_join_kernel(BackArgs a, int shares) 
     store_scaled(a, t * a.L.d_col + c, v, -a.shift[t], have);
 }
 
-// Shares of the weight rows: workgroups for every place there is for a tile, none below 256 rows.
-constexpr int64_t MOST_SUMS = (int64_t)64 << 20;                // bytes of all shares' sums
-static int shares_of(int64_t tiles, int64_t places, int64_t d_row) {
-    int64_t s = places / tiles;
-    if (s > (d_row + 255) / 256) s = (d_row + 255) / 256;
-    return (int)(s < 1 ? 1 : s);
-}
-
 template <int CB, int PB, int MT, int WC>
 static void launch_tiles(BackArgs a, int places, hipStream_t s) {
     typedef BackGemm<CB, 1, PB, MT, 2, WC, true> G;
     const int gm = (int)most_tiles(a.offsets, a.E, a.n, G::BM), gn = (int)((a.L.d_col + G::BN - 1) / G::BN);
-    int shares = shares_of((int64_t)gm * gn, places, a.d_row);
-    while (shares > 1 && shares * a.n * a.L.d_col * 4 > MOST_SUMS) --shares;
+    int shares = (int)shares_of((int64_t)gm * gn, places, a.d_row, a.n * a.L.d_col * 4);
     a.share = ((a.d_row + shares - 1) / shares + 63) / 64 * 64;
     shares = (int)((a.d_row + a.share - 1) / a.share);
     if (shares == 1) a.sums = nullptr;
@@ -157,12 +146,10 @@ static void launch_tiles(BackArgs a, int places, hipStream_t s) {
 
 template <int CB, int PB>
 static void launch_parts(const BackArgs& a, hipStream_t s) {
-    const int64_t each = (a.n + a.E - 1) / a.E;
-    const char* force = getenv("BACK_TILE");
-    const int f = force ? atoi(force) : 0;
-    if constexpr (PB == 1) if (f == 256 || (!f && each > 160)) return launch_tiles<CB, PB, 8, 4>(a, 256, s);
-    if (f == 64 || (!f && each > 32)) launch_tiles<CB, PB, 4, 2>(a, PB == 1 || CB != 8 ? 512 : 256, s);
-    else launch_tiles<CB, PB, 1, 2>(a, 512, s);
+    const SumTile t = sum_tile(ceil_div(a.n, a.E), PB, CB);
+    if constexpr (PB == 1) if (t.bm == 256) return launch_tiles<CB, PB, 8, 4>(a, t.places, s);
+    if (t.bm == 128) launch_tiles<CB, PB, 4, 2>(a, t.places, s);
+    else launch_tiles<CB, PB, 1, 2>(a, t.places, s);
 }
 
 template <int CB>

@@ -21,60 +21,6 @@
 
 namespace gptq {
 
-constexpr int SPAN = 8192;                                      // most words of a span
-constexpr int64_t CHUNK = 4096;                                 // tokens taken at a time
-constexpr int64_t ROUND = (int64_t)1 << 25;                     // most logits of a round
-constexpr int MOST_SPANS = 1024;                                // of a round
-
-struct HeadPlan {
-    int64_t nc;                                                 // tokens at a time
-    int spans; int64_t span;                                    // span: words, a multiple of 64
-    int R;                                                      // spans per round
-};
-
-// The sums' tile of a batch: tokens, columns, and how many tiles the device takes at once.
-struct SumTile { int bm, bn, places; };
-static SumTile tile_for(int64_t nc, int parts, int bits) {
-    if (nc > 128 && parts == 1) return SumTile{256, 256, 256};
-    if (nc > 32 && parts == 2 && bits != 8) return SumTile{128, 256, 256};   // (8-bit codes: LDS)
-    if (nc > 32) return SumTile{128, 128, parts == 1 ? 512 : 256};
-    return SumTile{32, 128, 512};
-}
-
-// Spans: with few tiles, as many as fill the device once, twice, .. with each span's tiles in a
-// round of its own, of 512 to 8192 words; else of 8192 words, one after the other.  A round has
-// at most ROUND logits.
-static HeadPlan plan_of(int64_t nc, int64_t d, int64_t vocab, int parts, int bits) {
-    HeadPlan p;
-    p.nc = nc;
-    int64_t spans = (vocab + SPAN - 1) / SPAN, R = spans;
-    if (parts) {
-        const SumTile t = tile_for(nc, parts, bits);
-        const int64_t tiles = (nc + t.bm - 1) / t.bm * ((d + t.bn - 1) / t.bn);
-        if (2 * tiles <= t.places) {
-            int64_t times = 1;
-            while (times * t.places / tiles < spans) ++times;
-            spans = times * t.places / tiles;
-            const int64_t most = (vocab + 511) / 512;
-            if (spans > most) spans = most;
-            if (spans > MOST_SPANS && vocab <= SPAN * (int64_t)MOST_SPANS) spans = MOST_SPANS;
-            R = spans;
-        } else {
-            R = 1;
-        }
-    }
-    p.span = ((vocab + spans - 1) / spans + 63) / 64 * 64;
-    p.spans = (int)((vocab + p.span - 1) / p.span);
-    const int64_t fit = ROUND / (nc * p.span);
-    if (R > p.spans) R = p.spans;
-    if (R > MOST_SPANS) R = MOST_SPANS;
-    if (R > fit) R = fit;
-    if (R < 1) R = 1;
-    const int64_t rounds = (p.spans + R - 1) / R;
-    p.R = (int)((p.spans + rounds - 1) / rounds);               // the same number in each
-    return p;
-}
-
 struct HeadBuffers {
     float* z;                                                   // nc x R span
     uint16_t* A[2];                                             // exp(z - m) in fp16: [slab of 32 words][token][32]
@@ -108,26 +54,9 @@ static size_t layout(HeadBuffers* b, uint8_t* w, int64_t nc, int64_t words, int6
     return at;
 }
 
-// A larger batch takes fewer spans per round, and a workspace made for the largest batch has to
-// do for every smaller one, of any dx type and bits: so the size is of the most logits and sums
-// that any batch up to n has.  With T 32-token tiles a batch has at most 32 T tokens; spans per
-// round and words per span are those of its larger tiles' numbers, or what ROUND allows.
 size_t head_ws_bytes(int64_t n, int64_t d, int64_t vocab, int group, int k, bool grad) {
-    const int64_t nc = n < CHUNK ? n : CHUNK;
-    int64_t words = 0, rows = 0;
-    auto most = [&](int64_t tokens, int64_t R, int64_t span) {
-        const int64_t cap = ROUND > tokens * span ? ROUND : tokens * span, w = tokens * R * span;
-        words = (w < cap ? w : cap) > words ? (w < cap ? w : cap) : words;
-        rows = tokens * R > rows ? tokens * R : rows;
-    };
-    for (int parts = grad ? 1 : 0; parts <= (grad ? 2 : 0); ++parts)
-        for (int bits = 4; bits <= (parts == 2 ? 8 : 4); bits += 4)
-            for (int64_t T = 1; T <= (nc + 31) / 32; ++T) {
-                const int64_t tokens = 32 * T < nc ? 32 * T : nc;
-                const HeadPlan a = plan_of(32 * (T - 1) + 1, d, vocab, parts, bits);   // the fewest tokens: the most spans that fit
-                most(tokens, a.R, a.span);
-            }
-    return layout(nullptr, nullptr, nc, words, rows, d, vocab, group, k, grad ? 2 : 0);
+    const HeadMost most = head_most(n, d, vocab, grad);
+    return layout(nullptr, nullptr, n < CHUNK ? n : CHUNK, most.words, most.rows, d, vocab, group, k, grad ? 2 : 0);
 }
 
 __global__ __launch_bounds__(256) void head_emax_kernel(const int8_t* e, int64_t vocab, int32_t* emax) {
@@ -459,7 +388,7 @@ static void launch_tiles(const BackArgs& b, int slots, int64_t vocab, int64_t sp
 
 template <int CB, int P>
 static void launch_parts(const BackArgs& b, int slots, int64_t vocab, int64_t span, int first_word, hipStream_t s) {
-    const int bm = tile_for(b.n, P, CB).bm;
+    const int bm = head_tile(b.n, P, CB).bm;
     if constexpr (P == 1) if (bm == 256) return launch_tiles<CB, P, 8, 4>(b, slots, vocab, span, first_word, s);
     if constexpr (P == 2 && CB != 8) if (bm == 128) return launch_tiles<CB, P, 4, 4>(b, slots, vocab, span, first_word, s);
     if (bm == 128) launch_tiles<CB, P, 4, 2>(b, slots, vocab, span, first_word, s);
@@ -482,7 +411,7 @@ gptq_status head_launch(const HeadCall& c, hipStream_t s) {
     a.blocks = (int)((c.vocab + EB - 1) / EB);
     for (int64_t tok0 = 0; tok0 < c.n; tok0 += CHUNK) {
         const int64_t nc = c.n - tok0 < CHUNK ? c.n - tok0 : CHUNK;
-        const HeadPlan p = plan_of(nc, d, c.vocab, parts, c.bits);
+        const HeadPlan p = head_plan(nc, d, c.vocab, parts, c.bits);
         layout(&a.b, (uint8_t*)c.ws, nc, nc * p.R * p.span, nc * p.R, d, c.vocab, c.group, c.k, parts);
         a.n = nc; a.tok0 = tok0; a.R = p.R; a.span = p.span;
         if (grad) {
@@ -492,7 +421,8 @@ gptq_status head_launch(const HeadCall& c, hipStream_t s) {
         }
         GroupedArgs g = {};                                      // the whole head
         g.L = c.L; g.d_row = c.vocab; g.x = (const uint16_t*)c.x + tok0 * c.ldx; g.ldx = c.ldx; g.n = nc; g.E = 1;
-        const gptq_status ready = grouped_prepare(g, c.xt, c.bits, c.group, a.b.forward, s);
+        const bool large = grouped_large(g, p.R * p.span < c.vocab ? p.R * p.span : c.vocab);
+        const gptq_status ready = large ? grouped_prepare(g, c.xt, c.bits, c.group, a.b.forward, s) : GPTQ_OK;
         if (ready != GPTQ_OK) return ready;
         int round = 0;
         for (int first = 0; first < p.spans; first += p.R, ++round) {
@@ -503,7 +433,7 @@ gptq_status head_launch(const HeadCall& c, hipStream_t s) {
             h.L.scales += v0 * c.L.n_groups;
             h.L.zeros += v0 * c.L.n_groups;
             h.d_row = v1 - v0; h.y = a.b.z; h.yt = GPTQ_F32; h.ldy = p.R * p.span;
-            const gptq_status st = grouped_launch(h, c.xt, c.bits, c.group, a.b.forward, c.vocab, v0, s);
+            const gptq_status st = grouped_launch(h, c.xt, c.bits, c.group, large, a.b.forward, c.vocab, v0, s);
             if (st != GPTQ_OK) return st;
             a.round = round; a.slots = slots;
             const dim3 grid((unsigned)nc, (unsigned)slots);

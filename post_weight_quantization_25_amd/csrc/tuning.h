@@ -4,6 +4,7 @@
 #include "gptq_tuning.h"
 #include "serving.h"
 #include "stored_tile.h"
+#include "tuning_rules.h"
 
 namespace gptq {
 
@@ -79,13 +80,15 @@ struct GroupedArgs {
     void* y; gptq_dtype yt; int64_t ldy;
     const int32_t* unless_zero;                                 // the kernel of stored_gemm.h: not nullptr: works only if not 0
 };
-// grouped_prepare lays the activations and the scales of all E d_row rows out for many tokens, once
-// for products of several spans of the rows; grouped_launch takes rows row0 .. row0 + a.d_row - 1
-// of them (with experts: all).  ws: grouped_ws_bytes, which is 0 where nothing is laid out.
+// grouped_large: whether products of `rows` rows (of each expert) are for the large tiles.  Then
+// grouped_prepare lays the activations and the scales of all E d_row rows out, once for products
+// of several spans of the rows, and grouped_launch takes rows row0 .. row0 + a.d_row - 1 of
+// all_rows (with experts: all).  ws: grouped_ws_bytes, which is 0 where they never are.
 size_t grouped_ws_bytes(int64_t n, int64_t E, int64_t d_row, int64_t d_col, int group);
+bool grouped_large(const GroupedArgs& a, int64_t rows);
 gptq_status grouped_prepare(const GroupedArgs& a, gptq_dtype xt, int bits, int group, void* ws, hipStream_t s);
-gptq_status grouped_launch(const GroupedArgs& a, gptq_dtype xt, int bits, int group, void* ws, int64_t all_rows, int64_t row0,
-                           hipStream_t s);
+gptq_status grouped_launch(const GroupedArgs& a, gptq_dtype xt, int bits, int group, bool large, void* ws, int64_t all_rows,
+                           int64_t row0, hipStream_t s);
 
 // ---- dx[t] = What_e^T dy[t] (grouped_back.hip)
 struct BackCall {

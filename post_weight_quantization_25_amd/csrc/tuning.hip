@@ -84,8 +84,9 @@ gptq_status gptqt_linear_grouped(const uint8_t* codes, const uint16_t* scales_f1
     a.L = stored_layer(codes, scales_f16, zeros_f16, d_col, bits, group_size);
     a.d_row = d_row; a.x = (const uint16_t*)x; a.ldx = ldx; a.n = n_rows; a.offsets = offsets; a.E = n_experts;
     a.y = y; a.yt = y_dtype; a.ldy = d_row;
-    const gptq_status ready = grouped_prepare(a, x_dtype, bits, group_size, ws, (hipStream_t)stream);
-    return ready != GPTQ_OK ? ready : grouped_launch(a, x_dtype, bits, group_size, ws, d_row, 0, (hipStream_t)stream);
+    const bool large = grouped_large(a, d_row);
+    const gptq_status ready = large ? grouped_prepare(a, x_dtype, bits, group_size, ws, (hipStream_t)stream) : GPTQ_OK;
+    return ready != GPTQ_OK ? ready : grouped_launch(a, x_dtype, bits, group_size, large, ws, d_row, 0, (hipStream_t)stream);
 }
 
 static bool layer_sized(int64_t n, int64_t E, int64_t d_row, int64_t d_col, int32_t& group) {
