@@ -29,8 +29,10 @@ extern "C" {
 
 /*
  * Products grouped by expert: y[t] = What_e x[t] for the rows t of expert e, offsets[e] <= t <
- * offsets[e + 1].  Codes enter as exact 16-bit numbers and sums are fp32.  An infinity or a NaN
- * in a row stays in that row.
+ * offsets[e + 1].  Products are exact and sums are fp32.  In calls of many rows per expert (more
+ * than 160, by sizes alone) bfloat16 elements of x enter as fp16 relative to their row: themselves
+ * down to 2^-28 of the row's largest, below that to 2^-39 of it.  An infinity or a NaN in a row
+ * stays in that row.
  *
  *  codes ..   the experts' rows one after another: n_experts * d_row rows of d_col columns
  *  x          n_rows x d_col, pitch ldx >= d_col, dtype x_dtype: GPTQ_BF16 or GPTQ_F16
@@ -82,7 +84,7 @@ gptq_status gptqt_linear_grouped_backward(const uint8_t* codes, const uint16_t* 
  *   dx[t]   = w_t (sum_v softmax(z)_v What_v - What_target)        (the gradient of sum_t loss[t]).
  * A token whose target is outside 0 .. vocab - 1 (by convention -100) or whose weight is 0 is
  * masked: loss and gradient 0, whatever its x holds.
- * Logits are fp32, exact products of 16-bit numbers added in fp32.  In dx the target's own
+ * Logits are fp32, as gptqt_linear_grouped gives them.  In dx the target's own
  * weight softmax - 1 is fp32; the other words' enter as in gptqt_linear_grouped_backward, the
  * weights in one or two fp16 parts by dx_dtype and exp(z - max) likewise.
  *

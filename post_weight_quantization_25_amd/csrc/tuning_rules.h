@@ -13,18 +13,18 @@ constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr int64_t FORWARD_ROWS = 160;
 constexpr bool many_rows(int64_t n, int64_t E) { return ceil_div(n, E) > FORWARD_ROWS; }
 
-// Whether they pay: a round of them (256 workgroups) takes 125 us at 4096 columns and laying out
-// about 35, a round of the 128 x 128 tiles (512 workgroups) 82 us, and 60 however few.  An expert
-// ends in half a tile on average.  Both measured, us, 256 / 128 tiles, int4 g128, rows x columns,
+// Whether they pay: a round of them (256 workgroups) takes 125 us at 4096 columns and 20 more to
+// begin, a round of the 128 x 128 tiles (512 workgroups) 82 us and 30, and 60 however few.  An
+// expert ends in half a tile on average.  Both measured, us, 256 / 128 tiles, int4 g128, rows x columns,
 // tokens (experts): 4096 x 4096, 1024: 144 / 74, 4096: 160 / 175; 11008 x 4096, 1024: 146 / 144,
 // 2048: 272 / 255, 2048 (4): 272 / 293, 4096 (16): 790 / 656, 8192 (16): 1059 / 1096; 8-bit 32000 x
 // 4096, 256: 143 / 110, 512: 154 / 190; 4096 x 4096, 4096 tokens: g64 185 / 201, g32 198 / 261,
 // int3 g128 159 / 175, 8-bit per row 153 / 174.
 constexpr bool forward_pays(int64_t n, int64_t E, int64_t rows, int64_t d_col) {
     const int64_t used = E < n ? E : n, partly = used > 1 ? used : 0;
-    const int64_t large = (n + partly * 127 + (partly ? 0 : 255)) / 256 * ceil_div(rows, 256);
-    const int64_t small = (n + partly * 64 + (partly ? 0 : 127)) / 128 * ceil_div(rows, 128);
-    const int64_t a = ceil_div(large, 256) * 125 + 35 * 4096 / (d_col > 0 ? d_col : 1), b = small * 82 / 512;
+    const int64_t large = (n + partly * 127 + 255) / 256 * ceil_div(rows, 256);
+    const int64_t small = (n + partly * 64 + 127) / 128 * ceil_div(rows, 128);
+    const int64_t a = ceil_div(large, 256) * 125 + 20 * 4096 / (d_col > 0 ? d_col : 1), b = 30 + small * 82 / 512;
     return many_rows(n, E) && a < (b > 60 ? b : 60);
 }
 
