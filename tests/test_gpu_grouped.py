@@ -46,6 +46,10 @@ CASES = [
     (300, 416, 4, 0, 300, 0, BF, F32, "symmetric"), (70, 48, 8, 0, 333, 0, HF, F32, "whole"), (260, 128, 3, 0, 270, 0, BF, F32, "whole"),
     (90, 250, 4, 0, 500, 2, BF, F32, "whole"), (300, 256, 4, 64, 290, 0, BF, F32, "fraction"), (64, 160, 8, 32, 700, 3, HF, F32, "far"),
     (2000, 64, 4, 32, 2100, 9, BF, F32, "whole"),
+    # more than 1024 rows: the gradient's 256 x 256 tiles, with codes of whole 16 bytes and others
+    (300, 256, 4, 128, 1100, 0, BF, BF, "whole"), (70, 384, 3, 64, 1030, 0, HF, BF, "symmetric"), (513, 128, 8, 32, 1200, 0, BF, BF, "whole"),
+    (33, 288, 4, 32, 1025, 0, BF, BF, "fraction"), (90, 250, 4, 0, 1100, 0, HF, BF, "whole"), (64, 100, 8, 0, 1100, 0, BF, BF, "whole"),
+    (700, 520, 3, 0, 1300, 0, BF, BF, "symmetric"), (1500, 128, 4, 128, 2500, 2, BF, BF, "far"), (1000, 64, 4, 64, 99, 0, HF, HF, "whole"),
 ]
 
 

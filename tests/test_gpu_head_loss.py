@@ -36,6 +36,8 @@ CASES = [
     (1000, 128, 4, 128, 33, HF, F32, "whole"), (777, 136, 3, 0, 130, BF, F32, "symmetric"),
     (8192, 64, 8, 32, 20, BF, BF, "whole"), (8193, 64, 4, 32, 17, HF, HF, "whole"), (20000, 96, 4, 32, 129, BF, F32, "fraction"),
     (9001, 130, 4, 0, 300, BF, BF, "whole"), (30000, 64, 8, 0, 2, BF, F32, "whole"), (300, 256, 8, 128, 64, HF, F32, "far"),
+    (3000, 256, 4, 128, 200, BF, BF, "whole"), (500, 128, 8, 64, 130, HF, F32, "whole"), (700, 128, 4, 64, 1100, BF, BF, "whole"),
+    (999, 64, 3, 64, 99, HF, HF, "symmetric"), (640, 100, 8, 0, 1030, BF, BF, "whole"),
 ]
 
 
@@ -181,7 +183,8 @@ def test_nan_in_a_live_token():
     assert torch.equal(torch.isnan(dx).any(1), bad)
 
 
-def test_more_tokens_than_a_chunk():
+@pytest.mark.parametrize("gt", [BF, F32])
+def test_more_tokens_than_a_chunk(gt):
     """Batches longer than the tokens taken at a time give each token what a short batch does, to
     the order of fp32 sums."""
     import post_weight_quantization_25_amd as g
@@ -189,12 +192,12 @@ def test_more_tokens_than_a_chunk():
     n = 4096 + 4096 + 5
     x = tokens(n, 64, BF, 3)
     t = (torch.arange(n) % 9000).int().cuda()
-    loss, dx = g.cross_entropy(q, x, t, dx_dtype=F32)
+    loss, dx = g.cross_entropy(q, x, t, dx_dtype=gt)
     pick = torch.tensor([0, 1, 4095, 4096, 8191, 8192, n - 1])
     l, bl, r, br = head_reference(q, What, x.cpu()[pick], torch.ones(7, 1).double(), t.cpu().long()[pick][:, None],
-                                  torch.ones(7).double(), 1.0, F32)
+                                  torch.ones(7).double(), 1.0, gt)
     near(loss[pick.cuda()], l, bl, F32, "loss")
-    near(dx[pick.cuda()], r, br, F32, "dx")
+    near(dx[pick.cuda()], r, br, gt, "dx")
 
 
 def test_one_workspace_for_smaller_batches():
