@@ -67,7 +67,8 @@ gptq_status gptqt_linear_grouped(const uint8_t* codes, const uint16_t* scales_f1
  *  dy         n_rows x d_row, pitch ld_dy >= d_row, dtype dy_dtype: GPTQ_BF16 or GPTQ_F16
  *  dx         n_rows x d_col, pitch d_col, dtype dx_dtype; rows of no expert are left as they were
  *  ws         at least gptqt_linear_grouped_backward_workspace_size(...) bytes, 16-byte aligned
- * Errors: as gptqt_linear_grouped; a missing, misaligned or short workspace -> GPTQ_ERR_WORKSPACE.
+ * Errors: as gptqt_linear_grouped, but any ld_dy, and tiles of 32 x 128 outputs; a missing,
+ * misaligned or short workspace -> GPTQ_ERR_WORKSPACE.
  */
 size_t gptqt_linear_grouped_backward_workspace_size(int64_t n_rows, int32_t n_experts, int64_t d_row, int64_t d_col,
                                                     int32_t group_size);

@@ -238,7 +238,8 @@ struct ForwardGemm {
     }
 };
 
-// Host side (grouped.hip).  What a product of many tokens keeps in the workspace.
+// What a product of many tokens keeps in the workspace (grouped.hip): the arrays of ForwardArgs, `groups`
+// groups of `pitch` rows of each expert.
 struct ForwardBuffers {
     uint16_t* A; int32_t* shift; float* rho; uint32_t* zz; float* S_last; int32_t* odd;
     int64_t pitch, groups;

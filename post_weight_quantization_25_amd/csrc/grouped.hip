@@ -111,7 +111,10 @@ __global__ __launch_bounds__(256) void forward_pack_kernel(ForwardPackArgs a) {
         for (int w = 0; w < 4; ++w) m = red[w] > m ? red[w] : m;
         k = m < -900 ? 0 : 14 - m;                               // nothing but zeros
     }
-    if (threadIdx.x == 0) a.shift[t] = k;
+    if (threadIdx.x == 0) {
+        a.shift[t] = k;
+        if (t == 0) *a.odd = 0;                                  // for forward_rows_kernel, which runs next
+    }
     for (int64_t c = 8 * threadIdx.x; c < a.columns; c += 2048) {
         float v[8] = {};
         if (c < a.d_col) load_x8<X>(row + c, (int)(a.d_col - c < 8 ? a.d_col - c : 8), v);
@@ -124,8 +127,6 @@ __global__ __launch_bounds__(256) void forward_pack_kernel(ForwardPackArgs a) {
         *reinterpret_cast<u32x4_t*>(a.A + ((c / BK) * a.n + t) * BK + c % BK) = o;
     }
 }
-
-__global__ void forward_flag_kernel(int32_t* odd) { *odd = 0; }
 
 // Ratios of a row's scales, its zeros as fp16 pairs, its last scale; the flag where one of them is
 // not for this kernel.  64 rows of an expert per workgroup, threads along the rows.
@@ -242,7 +243,6 @@ gptq_status grouped_prepare(const GroupedArgs& a, gptq_dtype xt, int bits, int g
     ForwardBuffers b;
     forward_layout(&b, (uint8_t*)ws, a.n, a.E, a.d_row, a.L.d_col, group);
     const ForwardPackArgs p = {a.x, a.ldx, a.n, a.L.d_col, forward_columns(a.L.d_col), b.A, b.shift, b.odd, bits == 8};
-    forward_flag_kernel<<<1, 1, 0, s>>>(b.odd);
     if (xt == GPTQ_BF16) forward_pack_kernel<X_BF16><<<(unsigned)a.n, 256, 0, s>>>(p);
     else forward_pack_kernel<X_F16><<<(unsigned)a.n, 256, 0, s>>>(p);
     forward_rows_kernel<<<dim3((unsigned)((a.d_row + 63) / 64), (unsigned)a.E), 256, 0, s>>>(a.L, a.d_row, b);

@@ -87,8 +87,9 @@ GPTQ_DEV void store_scaled(const BackArgs& a, int64_t at, f32x4_t v, int k, int 
     else store_four<GPTQ_F16>(a.y, at, v, have);
 }
 
+// (8-bit codes with two parts: LDS holds one workgroup of 128 x 128)
 template <int CB, int PB, int MT, int WC, bool DIRECT>
-__global__ __launch_bounds__(128 * WC, 2) void back_gemm_kernel(BackArgs a, int gm, int gn) {
+__global__ __launch_bounds__(128 * WC, CB != 8 || PB == 1 || MT == 1 ? 2 : 1) void back_gemm_kernel(BackArgs a, int gm, int gn) {
     typedef BackGemm<CB, 1, PB, MT, 2, WC, DIRECT> G;
     __shared__ __align__(16) uint8_t lds[G::LDS_BYTES];
     int tm, tn;

@@ -28,19 +28,19 @@ static gptq_status check_layer(int64_t E, int64_t d_row, int64_t d_col, int32_t 
     return GPTQ_OK;
 }
 
-// Tiles of 64 x 128 outputs are one launch extent.
-static bool many_tiles(int64_t n, int64_t E, int64_t width) {
-    return (n / 64 + (E < n ? E : n) + 1) * ((width + 127) / 128) > ((int64_t)1 << 24);
+// The smallest tiles of many rows, `per` x 128 outputs, are one launch extent (of less than 2^32 threads).
+static bool many_tiles(int64_t n, int64_t E, int64_t width, int per) {
+    return (n / per + (E < n ? E : n) + 1) * ((width + 127) / 128) > ((int64_t)1 << 24);
 }
 
 static gptq_status check_grouped(int64_t E, int64_t d_row, int64_t d_col, int32_t bits, int32_t& group, int64_t n,
                                  gptq_dtype in, gptq_dtype out, int64_t ld, int64_t in_width, int64_t out_width,
-                                 const int32_t* offsets) {
+                                 const int32_t* offsets, int tile) {
     if (!valid_dtype(in) || !valid_dtype(out)) return GPTQ_ERR_INVALID_ARG;
     const gptq_status st = check_layer(E, d_row, d_col, bits, group, n);
     if (st != GPTQ_OK) return st;
     if (ld < in_width || (!offsets && E != 1)) return GPTQ_ERR_INVALID_ARG;
-    if (in == GPTQ_F32 || many_tiles(n, E, out_width)) return GPTQ_ERR_UNSUPPORTED;
+    if (in == GPTQ_F32 || many_tiles(n, E, out_width, tile)) return GPTQ_ERR_UNSUPPORTED;
     return GPTQ_OK;
 }
 
@@ -73,7 +73,7 @@ gptq_status gptqt_linear_grouped(const uint8_t* codes, const uint16_t* scales_f1
                                  const void* x, gptq_dtype x_dtype, int64_t n_rows, int64_t ldx,
                                  const int32_t* offsets, void* y, gptq_dtype y_dtype, void* ws, size_t ws_bytes, void* stream) {
     const gptq_status st = check_grouped(n_experts, d_row, d_col, bits, group_size, n_rows, x_dtype, y_dtype, ldx, d_col,
-                                         d_row, offsets);
+                                         d_row, offsets, 64);
     if (st != GPTQ_OK) return st;
     if (ldx > TUNE_MAX_PITCH) return GPTQ_ERR_UNSUPPORTED;
     if (n_rows == 0) return GPTQ_OK;
@@ -111,7 +111,7 @@ gptq_status gptqt_linear_grouped_backward(const uint8_t* codes, const uint16_t* 
                                           int64_t ld_dy, const int32_t* offsets, void* dx, gptq_dtype dx_dtype,
                                           void* ws, size_t ws_bytes, void* stream) {
     const gptq_status st = check_grouped(n_experts, d_row, d_col, bits, group_size, n_rows, dy_dtype, dx_dtype, ld_dy,
-                                         d_row, d_col, offsets);
+                                         d_row, d_col, offsets, 32);
     if (st != GPTQ_OK) return st;
     if (n_rows == 0) return GPTQ_OK;
     if (!codes || !scales_f16 || !zeros_f16 || !dy || !dx) return GPTQ_ERR_INVALID_ARG;

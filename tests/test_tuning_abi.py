@@ -116,6 +116,7 @@ def test_backward_argument_errors(lib):
     layer_errors(call)
     assert call(E=0) == INVALID_ARG and call(E=4097) == UNSUPPORTED and call(E=3, offs=None) == INVALID_ARG
     assert call(ldx=3) == INVALID_ARG                      # below d_row
+    assert call(n=97 * 4096, E=4096, d_col=131071, G=0, bits=8) == UNSUPPORTED   # 32-row tiles beyond a launch's extent
     for name in ("codes", "S", "Z", "x", "y"):
         assert call(**{name: None}) == INVALID_ARG, name
     assert call(ws=None) == WORKSPACE and call(wsb=need - 1) == WORKSPACE
