@@ -12,9 +12,17 @@
 
 namespace gptq {
 
-constexpr int TW = 8;         // waves per workgroup of the tile kernel
+// Few tokens: TW waves share a row's chunks, each with one chunk in registers.  Instructions bound
+// it (about 170 a chunk of 16 rows x 128 columns, most of them decoding and arranging the
+// operands): 131072 x 4096 int4 g128, one token: 81 us, 3.5 TB/s, with 4 or 8 waves and 1, 2 or 3
+// chunks in flight alike.  Two chunks cost registers and a workgroup's time to begin: 131072 x 2048
+// int3, 3 tokens: 44 us with one, 58 with two; 64 experts of 2816 x 2048, 8 rows: 13.6 / 16.
+// 4 waves for narrow rows, which have few chunks for each: 131072 x 2048 int3: 37 us with 4, 44 with
+// 8; 65536 x 512: 12.6 / 14; 4096 x 11008: 15.2 / 12.6; 131072 x 4096: 88 / 81; 64 experts of 2816 x
+// 2048: 13.7 / 13.6.
+constexpr bool few_waves(int64_t d_col) { return d_col <= 2048; }
 
-template <int X, int CB, int RUN>
+template <int X, int CB, int RUN, int TW>
 __global__ __launch_bounds__(64 * TW, 4) void grouped_tile_kernel(GroupedArgs a) {
     __shared__ float red[TW][4][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15;
@@ -28,7 +36,7 @@ __global__ __launch_bounds__(64 * TW, 4) void grouped_tile_kernel(GroupedArgs a)
     f32x4_t acc[1][1];
     acc[0][0] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     const XScattered<1> xr = {{t < s.end ? reinterpret_cast<const uint8_t*>(a.x + t * a.ldx) : nullptr}};
-    stored_accumulate<X, CB, RUN, 1, 1, 2>(acc, L, row, xr, wave, TW);
+    stored_accumulate<X, CB, RUN, 1, 1, 1>(acc, L, row, xr, wave, TW);
 #pragma unroll
     for (int i = 0; i < 4; ++i) red[wave][i][lane] = acc[0][0][i];
     __syncthreads();
@@ -254,7 +262,8 @@ template <int X, int CB, int RUN, int PIECE>
 static gptq_status launch(const GroupedArgs& a, hipStream_t s) {
     if (small_tiles(a.n, a.E, a.d_row)) {
         const dim3 grid((unsigned)((a.d_row + 15) / 16), (unsigned)most_tiles(a.offsets, a.E, a.n, 16));
-        grouped_tile_kernel<X, CB, RUN><<<grid, 64 * TW, 0, s>>>(a);
+        if (few_waves(a.L.d_col)) grouped_tile_kernel<X, CB, RUN, 4><<<grid, 256, 0, s>>>(a);
+        else grouped_tile_kernel<X, CB, RUN, 8><<<grid, 512, 0, s>>>(a);
     } else if (a.n / a.E <= 96) {
         launch_gemm<X, CB, PIECE, 64>(a, s);
     } else {
