@@ -260,7 +260,7 @@ gptq_status grouped_prepare(const GroupedArgs& a, gptq_dtype xt, int bits, int g
 
 template <int X, int CB, int RUN, int PIECE>
 static gptq_status launch(const GroupedArgs& a, hipStream_t s) {
-    if (small_tiles(a.n, a.E, a.d_row)) {
+    if (!a.unless_zero && small_tiles(a.n, a.E, a.d_row)) {
         const dim3 grid((unsigned)((a.d_row + 15) / 16), (unsigned)most_tiles(a.offsets, a.E, a.n, 16));
         if (few_waves(a.L.d_col)) grouped_tile_kernel<X, CB, RUN, 4><<<grid, 256, 0, s>>>(a);
         else grouped_tile_kernel<X, CB, RUN, 8><<<grid, 512, 0, s>>>(a);

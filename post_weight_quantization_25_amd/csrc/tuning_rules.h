@@ -28,15 +28,26 @@ constexpr bool forward_pays(int64_t n, int64_t E, int64_t rows, int64_t d_col) {
     return many_rows(n, E) && a < (b > 60 ? b : 60);
 }
 
-// Few rows per expert: tiles of 16 x 16 up to 16 rows, but the 64-token tiles of the LDS kernel from 8
-// rows on where those are 1024 workgroups or more.  Both measured, us, 16 x 16 / 64-token tiles:
-// 61 experts of 2047 x 1408 int3 per row, 777 rows (1440 workgroups): 90 / 55; 64 of 2816 x 2048
-// int4, 8 rows: 15.7 / 15.6, 64: 93 / 94, 256: 99 / 96, 512 (1408): 126 / 107; one of 4096 x 4096,
-// 1 to 16 rows: 13.5 / 42; 4 of 11008 x 4096, 16 rows: 22 / 55; 32000 x 4096 8-bit, 16 rows: 48 / 53;
-// 131072 x 4096, 1 row: 97 / 118.
+// Tiles of 16 x 16, or the LDS kernel's of 64 (up to 96 tokens per expert) or 128 tokens x 128
+// rows, by what either takes at 4096 columns, in ns: a 16 x 16 tile 9 and 9 / 16 for each of its
+// tokens; a tile of the LDS kernel 120 (128 tokens: 160) where there are many, and the call 37000
+// (60000) however few.  Both measured, us, int4 g128, 16 x 16 / LDS: 4096 x 4096, 16 tokens: 12 / 37,
+// 32: 14 / 38, 64: 24 / 39, 96: 33 / 39, 128: 43 / 60; 11008 x 4096, 32: 32 / 39, 48: 48 / 41, 128:
+// 106 / 61; 4096 x 11008, 64: 50 / 97, 128: 94 / 146; 2048 x 1024, 128: 11 / 23; 131072 x 4096, 1: 81 /
+// 104, 8: 114 / 107, 16: 158 / 107; 131072 x 2048 int3 per row, 8: 48 / 48, 16: 70 / 49; 32000 x 4096
+// 8-bit, 16: 47 / 48, 24: 77 / 49; 64 experts of 2816 x 2048, 8 rows: 14 / 24, 256: 67 / 86, 512: 81 /
+// 99, 1024: 130 / 103; 61 of 2047 x 1408 int3, 488: 33 / 45, 777: 43 / 46; 16 of 11008 x 4096, 128:
+// 155 / 155, 256: 239 / 182; 8 of 4096 x 4096, 128: 50 / 54, 256: 85 / 55.
+constexpr int64_t likely_tiles(int64_t n, int64_t E, int per) { // of n rows spread over E experts
+    if (E == 1) return ceil_div(n, per);
+    const int64_t used = E < n ? E : n, t = n / per + used / 2;
+    return t > used ? t : used;
+}
 constexpr bool small_tiles(int64_t n, int64_t E, int64_t d_row) {
-    const int64_t each = n / E, used = E < n ? E : n;
-    return each <= 16 && (each < 8 || (n + used * 63) / 64 * ceil_div(d_row, 128) < 1024);
+    const bool many = n / E > 96;
+    const int64_t tile = ceil_div(d_row, 16) * (9 * likely_tiles(n, E, 16) + 9 * n / 16);
+    const int64_t lds = likely_tiles(n, E, many ? 128 : 64) * ceil_div(d_row, 128) * (many ? 160 : 120), least = many ? 60000 : 37000;
+    return tile < (lds > least ? lds : least) && n / 16 + E < 65536;   // the tiles of a launch
 }
 
 // ---- dx = What^T dy, and the sums of the losses: tokens and columns of a tile, and how many tiles

@@ -46,6 +46,12 @@ CASES = [
     (300, 416, 4, 0, 300, 0, BF, F32, "symmetric"), (70, 48, 8, 0, 333, 0, HF, F32, "whole"), (260, 128, 3, 0, 270, 0, BF, F32, "whole"),
     (90, 250, 4, 0, 500, 2, BF, F32, "whole"), (300, 256, 4, 64, 290, 0, BF, F32, "fraction"), (64, 160, 8, 32, 700, 3, HF, F32, "far"),
     (2000, 64, 4, 32, 2100, 9, BF, F32, "whole"),
+    # many weight rows: the forward product's tiles of 64 and 128 tokens, every width and group, odd rows and ends
+    (17000, 128, 4, 128, 64, 0, BF, F32, "whole"), (17001, 64, 4, 64, 97, 0, HF, HF, "whole"), (17003, 96, 4, 32, 65, 0, BF, BF, "symmetric"),
+    (17000, 130, 4, 0, 130, 0, BF, F32, "whole"), (17000, 128, 8, 128, 300, 0, BF, BF, "whole"), (17001, 64, 8, 64, 40, 0, HF, F32, "whole"),
+    (17003, 96, 8, 32, 96, 0, HF, HF, "fraction"), (17000, 100, 8, 0, 130, 0, BF, F32, "whole"), (17000, 128, 3, 128, 64, 0, HF, F32, "whole"),
+    (17001, 64, 3, 64, 130, 0, BF, BF, "symmetric"), (17003, 96, 3, 32, 300, 0, BF, F32, "whole"), (17000, 136, 3, 0, 65, 0, HF, F32, "whole"),
+    (17000, 128, 4, 64, 130, 0, HF, F32, "far"), (5666, 64, 4, 32, 700, 3, BF, F32, "far"),
     # more than 1024 rows: the gradient's 256 x 256 tiles, with codes of whole 16 bytes and others
     (300, 256, 4, 128, 1100, 0, BF, BF, "whole"), (70, 384, 3, 64, 1030, 0, HF, BF, "symmetric"), (513, 128, 8, 32, 1200, 0, BF, BF, "whole"),
     (33, 288, 4, 32, 1025, 0, BF, BF, "fraction"), (90, 250, 4, 0, 1100, 0, HF, BF, "whole"), (64, 100, 8, 0, 1100, 0, BF, BF, "whole"),

@@ -28,8 +28,14 @@ int main() {
     for (int c : {288, 320, 384}) CHECK(forward_pays(17001, 1, 17000, c));
     CHECK(forward_pays(16000, 5, 4000, 2048));
     CHECK(head_plan(4096, 2048, 16384, 1, 8).R * head_plan(4096, 2048, 16384, 1, 8).span == 8192 && forward_pays(4096, 1, 8192, 2048));
-    CHECK(small_tiles(1, 1, 131072) && small_tiles(16, 1, 32000) && small_tiles(256, 64, 2816) && !small_tiles(17, 1, 64));
-    CHECK(!small_tiles(777, 61, 2047) && !small_tiles(512, 64, 2816) && small_tiles(16, 4, 11008) && small_tiles(488, 61, 100));
+    CHECK(small_tiles(1, 1, 131072) && !small_tiles(16, 1, 131072) && small_tiles(16, 1, 32000) && !small_tiles(24, 1, 32000));
+    CHECK(small_tiles(128, 1, 4096) && small_tiles(32, 1, 11008) && !small_tiles(48, 1, 11008) && !small_tiles(128, 1, 11008));
+    CHECK(small_tiles(8, 64, 2816) && small_tiles(512, 64, 2816) && !small_tiles(1024, 64, 2816) && small_tiles(488, 61, 2047));
+    CHECK(small_tiles(128, 16, 11008) && !small_tiles(256, 16, 11008) && !small_tiles(256, 8, 4096));
+    CHECK(!small_tiles((int64_t)1 << 22, 1, 1) && !small_tiles((int64_t)1 << 20, 4096, 16));
+    // what the tests of the LDS kernel mean to take
+    for (int n : {40, 64, 65, 96, 97, 130, 300}) CHECK(!small_tiles(n, 1, 17000));
+    CHECK(!small_tiles(700, 3, 17000 / 3) && !small_tiles(301, 1, 20000));
     CHECK(sum_tile(1025, 1, 4).bm == 256 && sum_tile(1024, 1, 4).bm == 128 && sum_tile(1025, 2, 4).bm == 128);
     CHECK(sum_tile(97, 1, 8).bm == 128 && sum_tile(96, 1, 8).bm == 32);
     CHECK(shares_of(128, 256, 11008, 1 << 20) == 2 && shares_of(300, 256, 11008, 1) == 1 && shares_of(1, 512, 700, 1) == 3);
