@@ -16,6 +16,13 @@
 // are decoded, once per workgroup, between the products of this one.  A thread decodes 16
 // columns of a row; 3- and 4-bit codes come out as columns 0, 4, 1, 5, 2, 6, 3, 7 of every 8, the
 // order in which the activations are packed.
+//
+// Measured: 4096 tokens x 8192 x 4096 8-bit g128 268 us (1025 Tflop/s), the matrix unit busy 43% of the
+// cycles, the vector unit 32%; a dense product of 8192^3 bfloat16 reaches 1286.  The matrix
+// instructions alone would take 0.7 of it; decoding, LDS reads and issuing loads add to them
+// rather than hide, since a CU holds one workgroup.  The weight fragments of the next slab are
+// read into a second set during the step (16 experts of 11008 x 4096, 8192 rows: 1120 to 1190 us).  The
+// 128 x 128 tiles, two workgroups per CU, took 368 for the 4096 tokens.
 #pragma once
 #include "back_gemm.h"
 

@@ -90,7 +90,8 @@ struct ForwardPackArgs {
     uint16_t* A; int32_t* shift; int32_t* odd; int natural;     // natural: columns in order (8-bit codes)
 };
 
-// A workgroup per token, 8 elements per thread and step.
+// A workgroup per token, 8 elements per thread and step; the second reading of a row comes from
+// the cache.  Bound by memory: 8192 x 4096 bfloat16, 134 MB, 28 us (4.7 TB/s).
 template <int X>
 __global__ __launch_bounds__(256) void forward_pack_kernel(ForwardPackArgs a) {
     __shared__ int red[4];
@@ -137,7 +138,8 @@ __global__ __launch_bounds__(256) void forward_pack_kernel(ForwardPackArgs a) {
 }
 
 // Ratios of a row's scales, its zeros as fp16 pairs, its last scale; the flag where one of them is
-// not for this kernel.  64 rows of an expert per workgroup, threads along the rows.
+// not for this kernel.  64 rows of an expert per workgroup, threads along the rows: the layer has a
+// row's groups together, the tables a group's rows (131072 rows of 32 groups: 16 us, through LDS).
 __global__ __launch_bounds__(256) void forward_rows_kernel(Stored L, int64_t d_row, ForwardBuffers b) {
     __shared__ float S[64][33];
     __shared__ uint16_t Z[64][34];
