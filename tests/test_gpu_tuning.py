@@ -278,3 +278,77 @@ def test_only_the_outputs_are_written():
         assert all(bool((p == 7).all()) for p in pads)
     now = [t for q in (s.up, s.down, s.head) for t in (q.codes, q.scales, q.zeros)] + [s.x, s.targets]
     assert all(torch.equal(a, b) for a, b in zip(keep, now))
+
+
+def test_more_than_2_to_31_elements():
+    """Outputs, gradients and the planes between them beyond 32-bit offsets: rows at both ends and
+    around the 2^31st element against the definition."""
+    import post_weight_quantization_25_amd as g
+    rows, cols, n = 32000, 64, 70001
+    q, What = stored(rows, cols, 4, 32, 5)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(n, cols, generator=gen, device="cuda").to(HF)
+    pick = torch.tensor([0, 1, 67107, 67108, 67109, 69888, n - 1])
+    y = g.linear_grouped(q, x, out_dtype=HF)
+    xp = x[pick.cuda()].cpu().double()
+    ref = xp @ What.t()
+    assert bool(((y[pick.cuda()].cpu().double() - ref).abs() <= ((cols + 64) * U * zero_parts(q, xp)) * (1 + 2.0 ** -10) + out_rounding(ref, HF)).all())
+    dx = g.linear_grouped_backward(q, y)                   # y as any other gradient
+    r, bound = back_reference(q, What, y[pick.cuda()], HF)
+    assert bool(((dx[pick.cuda()].cpu().double() - r).abs() <= bound * (1 + 2.0 ** -10) + out_rounding(r, HF)).all())
+
+
+def test_no_rows():
+    import post_weight_quantization_25_amd as g
+    s = Step(5)
+    x = torch.empty(0, s.d, dtype=BF, device="cuda")
+    offs = torch.zeros(s.E + 1, dtype=torch.int32, device="cuda")
+    assert g.linear_grouped(s.up, x, offs).shape == (0, s.f)
+    assert g.linear_grouped_backward(s.down, x, offs).shape == (0, s.f)
+    y = torch.full((7, s.f), 3.0, device="cuda")           # rows, but none of an expert
+    x = torch.randn(7, s.d, device="cuda").to(BF)
+    assert bool((g.linear_grouped(s.up, x, offs, out=y) == 3.0).all())
+    assert bool((g.linear_grouped_backward(s.down, x, offs, out=y) == 3.0).all())
+
+
+@pytest.mark.parametrize("vocab", [30, 5000])
+def test_the_most_entries(vocab):
+    """1024 entries a token, every word several times among 30."""
+    import post_weight_quantization_25_amd as g
+    from tuning_helpers import teacher_weights
+    q, What = stored(vocab, 64, 8, 32, 4)
+    q.scales.mul_(2.0 / float(What.pow(2).sum(1).mean().sqrt()))
+    from serving_helpers import weights
+    What = torch.from_numpy(weights(q.codes.cpu().numpy(), q.scales.cpu().numpy(), q.zeros.cpu().numpy(), 8, 32))
+    gen = torch.Generator().manual_seed(2)
+    x = torch.randn(3, 64, generator=gen).to(HF)
+    ids = torch.randint(0, vocab, (3, 1024), generator=gen, dtype=torch.int32)
+    top = torch.randn(3, 1024, generator=gen)
+    loss, dx = g.distill(q, x.cuda(), ids.cuda(), top.cuda(), 1.5, dx_dtype=F32)
+    p, at, _ = teacher_weights(ids, top, 1.5, vocab)
+    l, bl, r, br = head_reference(q, What, x, p, at, torch.ones(3).double(), 1.5, F32)
+    for got, ref, bound in ((loss, l, bl), (dx, r, br)):
+        assert bool(((got.cpu().double() - ref).abs() <= bound * (1 + 2.0 ** -10) + out_rounding(ref, F32)).all())
+
+
+@pytest.mark.parametrize("n", [3, 130, 4096])
+def test_codes_at_any_address(n):
+    """A layer whose codes begin at an odd byte: the kernels that load whole aligned pieces leave it
+    to the others."""
+    import post_weight_quantization_25_amd as g
+    from tuning_helpers import layer_parts
+    rows = 4096 if n == 4096 else 300
+    q, _ = stored(rows, 128, 4, 64, 6)
+    room = torch.empty(q.codes.numel() + 1, dtype=torch.uint8, device="cuda")
+    codes = room[1:].view(q.codes.shape)
+    codes.copy_(q.codes)
+    odd = g.Quantized(codes, q.scales, q.zeros, None, 4, 64, 128)
+    x = torch.randn(n, 128, generator=torch.Generator().manual_seed(3)).to(HF).cuda()
+    a, b = g.linear_grouped(q, x), g.linear_grouped(odd, x)
+    size = (x.double().abs() @ torch.ones(128, rows, dtype=torch.float64, device="cuda")) * layer_parts(q)[0].max() * 32
+    assert bool(((a - b).double().abs() <= 2 * (128 + 64) * U * size).all())
+    dy = torch.randn(n, rows, generator=torch.Generator().manual_seed(4)).to(BF).cuda()
+    assert torch.equal(g.linear_grouped_backward(q, dy), g.linear_grouped_backward(odd, dy))
+    t = torch.arange(n, dtype=torch.int32, device="cuda") % rows
+    (l0, d0), (l1, d1) = g.cross_entropy(q, x, t), g.cross_entropy(odd, x, t)
+    assert float((l0 - l1).abs().max()) <= 1e-3 * float(l0.abs().max()) and d0.isfinite().all() and d1.isfinite().all()
