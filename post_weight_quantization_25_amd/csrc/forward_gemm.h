@@ -197,6 +197,7 @@ struct ForwardGemm {
                         for (int v = 0; v < 4; ++v) acc[i][j][v] *= scale[i];
             };
             rescale(0);
+            __builtin_amdgcn_s_setprio(1);                       // as in BackGemm
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
                 read_a(j + 2 < MT ? k : (k + 1) & 3, (j + 2) % MT);
@@ -209,6 +210,7 @@ struct ForwardGemm {
                     for (int u = 8 * (j - 1) / (MT - 1); u < 8 * j / (MT - 1); ++u) decode_one(d, r, u);
                 __builtin_amdgcn_sched_barrier(0);
             }
+            __builtin_amdgcn_s_setprio(0);
             store(d, k & 1);                                     // (behind the last slab: not used)
         };
         load_t(0);
