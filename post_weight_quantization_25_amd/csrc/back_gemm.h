@@ -373,37 +373,37 @@ GPTQ_DEV void store_four(void* y, int64_t idx, f32x4_t v, int have) {
     }
 }
 
-// e_r, the exponent of the row's largest scale, and the layer's Quads.  A workgroup takes 64
-// rows of an expert (blockIdx.y); rows behind the last have zeros.
+// e_r, the exponent of the row's largest scale, and the layer's Quads.  A workgroup takes
+// 16 rows of an expert (blockIdx.y), 16 threads a row; rows behind the last have zeros.
 struct RowsArgs {
     const uint16_t* scales; const uint16_t* zeros;
     int64_t d_row; int n_groups;
     int8_t* e; Quad* T; int64_t quads;
 };
 static __global__ __launch_bounds__(256) void rows_kernel(RowsArgs a) {
-    __shared__ int es[64];
+    __shared__ int es[16];
     const int tid = threadIdx.x;
-    const int64_t row0 = (int64_t)blockIdx.x * 64, base = blockIdx.y * a.d_row;
-    const int64_t r = row0 + (tid >> 2);
+    const int64_t row0 = (int64_t)blockIdx.x * 16, base = blockIdx.y * a.d_row;
+    const int64_t r = row0 + (tid >> 4);
     int m = -1000;
     if (r < a.d_row)
-        for (int g = tid & 3; g < a.n_groups; g += 4) {
+        for (int g = tid & 15; g < a.n_groups; g += 16) {
             const int v = exponent_of(f16_bits_to_f32(a.scales[(base + r) * a.n_groups + g]));
             m = v > m ? v : m;
         }
 #pragma unroll
-    for (int o = 2; o >= 1; o >>= 1) {
+    for (int o = 8; o >= 1; o >>= 1) {
         const int v = __shfl_xor(m, o);
         m = v > m ? v : m;
     }
     if (m == -1000) m = 0;
-    if ((tid & 3) == 0) {
-        es[tid >> 2] = m;
+    if ((tid & 15) == 0) {
+        es[tid >> 4] = m;
         if (r < a.d_row) a.e[base + r] = (int8_t)m;
     }
     __syncthreads();
-    for (int i = tid; i < 16 * a.n_groups; i += 256) {
-        const int quad = i & 15, g = i >> 4;
+    for (int i = tid; i < 4 * a.n_groups; i += 256) {
+        const int quad = i & 3, g = i >> 2;
         uint32_t S[4], z4[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -429,7 +429,7 @@ inline size_t quads_bytes(int64_t E, int64_t d_row, int64_t n_groups) { return (
 
 inline void rows_launch(const Stored& L, int64_t E, int64_t d_row, int8_t* e, Quad* T, hipStream_t s) {
     const RowsArgs a = {L.scales, L.zeros, d_row, L.n_groups, e, T, quads_of(d_row)};
-    rows_kernel<<<dim3((unsigned)((d_row + 63) / 64 + 1), (unsigned)E), 256, 0, s>>>(a);
+    rows_kernel<<<dim3((unsigned)(((d_row + 63) / 64 + 1) * 4), (unsigned)E), 256, 0, s>>>(a);
 }
 
 }  // namespace gptq

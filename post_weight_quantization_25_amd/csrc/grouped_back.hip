@@ -115,19 +115,22 @@ __global__ __launch_bounds__(256) void back_join_kernel(BackArgs a, int shares) 
     const int64_t t = s.tok0, c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4;
     const int have = (int)(a.L.d_col - c < 4 ? a.L.d_col - c : 4);
     if (have <= 0) return;
+    const float* p = a.sums + t * a.L.d_col + c;
+    const int64_t step = a.n * a.L.d_col;
     f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < shares; ++i) {
-        const float* p = a.sums + (i * a.n + t) * a.L.d_col + c;
-        if (have == 4) {
+    if (have == 4) {
+#pragma unroll 4
+        for (int i = 0; i < shares; ++i) {
             f32x4_t w;
-            __builtin_memcpy(&w, p, 16);
+            __builtin_memcpy(&w, p + i * step, 16);
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] += w[j];
-        } else {
+        }
+    } else {
+        for (int i = 0; i < shares; ++i)
 #pragma unroll
             for (int j = 0; j < 3; ++j)
-                if (j < have) v[j] += p[j];
-        }
+                if (j < have) v[j] += p[i * step + j];
     }
     store_scaled(a, t * a.L.d_col + c, v, -a.shift[t], have);
 }
