@@ -14,8 +14,8 @@
 // as fp16 is 0x6400 | u, so u - z and its product with the scale are one packed instruction
 // each) and so writes them transposed.  One barrier per slab.
 //
-// Measured: 2048 tokens x 11008 x 4096 int4 g128, one part, 183 us (1010 Tflop/s), the matrix unit busy
-// 45% of the cycles, the vector unit 33%; 4096 x 8192 x 4096 8-bit 240 to 265 (1040 to 1150).  Of 246
+// Measured: 2048 tokens x 11008 x 4096 int4 g128, one part, 180 us (1030 Tflop/s), the matrix unit busy
+// 47% of the cycles, the vector unit 34%; 4096 x 8192 x 4096 8-bit 240 to 265 (1040 to 1150).  Of 246
 // us for 256 slabs the matrix instructions and barriers alone take 174, with the LDS reads 180,
 // without the loads 220; the loads alone 117.  A second set of weight fragments spills (510 us).
 // Decoding per wave from registers, without LDS, took 461 for the 8-bit case.

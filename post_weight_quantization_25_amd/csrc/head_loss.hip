@@ -214,7 +214,7 @@ __global__ __launch_bounds__(256) void head_stats_kernel(HeadArgs a) {
 
 // A span's O = O f + exp(z - m) What.  back_gemm.h says what bounds it; with two parts in both
 // operands three products are formed (lo x lo is below the rounding): 301 tokens x 50021 x 2048 int4
-// g64 239 us, 770 Tflop/s.
+// g64 227 us, 810 Tflop/s.
 template <int CB, int P, int MT, int WC, bool DIRECT>
 __global__ __launch_bounds__(128 * WC, P == 1 || MT == 1 || WC == 4 ? 2 : 1) void head_sums_kernel(BackArgs a, int gm, int gn, int64_t vocab, int64_t span, int v_first) {
     typedef BackGemm<CB, P, P, MT, 2, WC, DIRECT> G;
