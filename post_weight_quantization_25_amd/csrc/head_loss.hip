@@ -105,6 +105,7 @@ struct HeadArgs {
     HeadBuffers b;
     int R, round, slots; int64_t span;                          // slots: spans of this round; of all, in head_final_kernel
     int blocks;                                                 // of emax
+    int64_t cols;                                               // columns of a workgroup of head_final_kernel
     Stored L;
     float* loss; void* dx; gptq_dtype dxt;                      // all tokens'
 };
@@ -251,11 +252,12 @@ GPTQ_DEV float top_of(const HeadArgs& a, int64_t t, int j) {
                                                                                         : load_as_f32<GPTQ_F16>(a.top, i);
 }
 
-// The loss and the gradient of one token.  Scalars in 64 bits: they cost nothing here, and
+// The loss and the gradient of one token; where there are few tokens, of a.cols of its columns, the
+// scalars by every workgroup anew.  Scalars in 64 bits: they cost nothing here, and
 // p_j - softmax_j and the loss of a token that the model is sure of are small differences.
 // Bound by its round trips: one after another the entries, the slots, the sums and the entries'
 // rows.  4096 tokens x 4096, one entry, one slot: 51 us (100 MB); 2048 tokens, 64 entries: 128 us; 33 tokens x
-// 1024, 8 entries, 32 slots: 18 us.
+// 1024, 8 entries, 32 slots: 12 us.
 template <int CB>
 __global__ __launch_bounds__(256) void head_final_kernel(HeadArgs a) {
     __shared__ double redd[4];
@@ -267,6 +269,8 @@ __global__ __launch_bounds__(256) void head_final_kernel(HeadArgs a) {
     __shared__ float joint[256][8];
     const int tid = threadIdx.x;
     const int64_t t = blockIdx.x, tt = a.tok0 + t;
+    const int64_t col0 = blockIdx.y * a.cols, col1 = col0 + a.cols < a.d ? col0 + a.cols : a.d;
+    const bool first_part = tid == 0 && blockIdx.y == 0;
     const float w = weight_of(a, t);
     const auto larger = [](float x, float y) { return x > y ? x : y; };
     const auto sum = [](double x, double y) { return x + y; };
@@ -288,9 +292,9 @@ __global__ __launch_bounds__(256) void head_final_kernel(HeadArgs a) {
     live = over_block(live, [](int x, int y) { return x | y; }, redi);
     tm = over_block(tm, larger, red);
     if (!live || w == 0.f || (a.top && tm == -INFINITY && !(live & 2))) {   // no entry, or none with a weight
-        if (tid == 0) a.loss[tt] = 0.f;
+        if (first_part) a.loss[tt] = 0.f;
         if (a.dx)
-            for (int64_t c = tid; c < a.d; c += 256) store_out(a.dx, a.dxt, tt * a.d + c, 0.f);
+            for (int64_t c = col0 + tid; c < col1; c += 256) store_out(a.dx, a.dxt, tt * a.d + c, 0.f);
         return;
     }
     for (int i = tid; i < a.slots; i += 256) zm = larger(a.b.m[(int64_t)i * a.n + t], zm);
@@ -321,7 +325,7 @@ __global__ __launch_bounds__(256) void head_final_kernel(HeadArgs a) {
     }
     l = over_block(l, sum, redd);
     const float gain = w * a.T;
-    if (tid == 0) a.loss[tt] = (float)((double)w * a.T * a.T * l);
+    if (first_part) a.loss[tt] = (float)((double)w * a.T * a.T * l);
     if (!a.dx) return;
     const int em = emax_of(a.b.emax, a.blocks, redi);
     for (int i = tid; i < a.R; i += 256) {                       // the slots' weights
@@ -329,14 +333,14 @@ __global__ __launch_bounds__(256) void head_final_kernel(HeadArgs a) {
         slot_of[i] = s == 0.f ? 0.f : ldexpf((float)exp((double)m - zm - lzt), em - 14);
     }
     __syncthreads();
-    // 8 columns per thread; with fewer than 2048 columns several threads share a column's slots and
+    // 8 columns per thread; with fewer than 2048 of them several threads share a column's slots and
     // entries.
     int share = 1;
-    while (share < 8 && a.d * share <= 1024) share *= 2;
+    while (share < 8 && a.cols * share <= 1024) share *= 2;
     const int per = 256 / share, col = tid % per, part = tid / per;
-    for (int64_t c0 = 0; c0 < a.d; c0 += 8 * per) {
+    for (int64_t c0 = col0; c0 < col1; c0 += 8 * per) {
         const int64_t c = c0 + 8 * col;
-        const int have = (int)(a.d - c < 8 ? a.d - c : 8);
+        const int have = (int)(col1 - c < 8 ? col1 - c : 8);
         float g[8] = {};
         if (have > 0) {
 #pragma unroll 2
@@ -470,9 +474,13 @@ gptq_status head_launch(const HeadCall& c, hipStream_t s) {
             }
         }
         a.slots = p.R;
-        if (c.bits == 3) head_final_kernel<3><<<(unsigned)nc, 256, 0, s>>>(a);
-        else if (c.bits == 4) head_final_kernel<4><<<(unsigned)nc, 256, 0, s>>>(a);
-        else head_final_kernel<8><<<(unsigned)nc, 256, 0, s>>>(a);
+        // 33 tokens x 1024 columns: 12 us in parts, 18 whole; 301 x 2048: 16 either way
+        const int64_t most = grad ? ceil_div(d, 256) : 1, parts_of = 512 / nc < most ? 512 / nc : most;
+        a.cols = parts_of > 1 ? ceil_div(ceil_div(d, parts_of), 64) * 64 : d;
+        const dim3 grid((unsigned)nc, (unsigned)ceil_div(d, a.cols));
+        if (c.bits == 3) head_final_kernel<3><<<grid, 256, 0, s>>>(a);
+        else if (c.bits == 4) head_final_kernel<4><<<grid, 256, 0, s>>>(a);
+        else head_final_kernel<8><<<grid, 256, 0, s>>>(a);
         GPTQ_LAUNCH_CHECK();
     }
     return GPTQ_OK;
