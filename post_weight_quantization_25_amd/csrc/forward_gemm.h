@@ -41,12 +41,8 @@ struct ForwardArgs {
 };
 
 inline int64_t forward_columns(int64_t d_col) { return (d_col + 127) / 128 * 128; }   // whole turns of four slabs
-inline int64_t forward_groups(const Stored& L) {                // whole turns
-    const int64_t per = L.n_groups == 1 ? 1 : 128 >> L.gshift;
-    return (L.n_groups + per - 1) / per * per;
-}
 
-// GPT: groups per turn of four slabs (128 columns): 1, 2 or 4; 0: one scale per row.
+// GPT: groups per turn of four slabs (forward_turn_groups); 0: one scale per row.
 template <int CB, int GPT>
 struct ForwardGemm {
     static constexpr int BM = 256, BN = 256, THREADS = 512, WAVES = 8, MT = 8, NI = 4;

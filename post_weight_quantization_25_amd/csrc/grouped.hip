@@ -219,9 +219,10 @@ static void launch_forward(const ForwardArgs& a, hipStream_t s) {
 
 template <int CB>
 static void launch_forward_groups(const ForwardArgs& a, int group, hipStream_t s) {
-    if (group == 32) launch_forward<CB, 4>(a, s);
-    else if (group == 64) launch_forward<CB, 2>(a, s);
-    else if (group == 128) launch_forward<CB, 1>(a, s);
+    const int per = forward_turn_groups(a.L.n_groups, group);
+    if (per == 4) launch_forward<CB, 4>(a, s);
+    else if (per == 2) launch_forward<CB, 2>(a, s);
+    else if (per == 1) launch_forward<CB, 1>(a, s);
     else launch_forward<CB, 0>(a, s);
 }
 
@@ -231,7 +232,7 @@ static size_t forward_layout(ForwardBuffers* b, uint8_t* w, int64_t n, int64_t E
     const Stored L = stored_layer(nullptr, nullptr, nullptr, d_col, 8, group);
     ForwardBuffers h;
     h.pitch = (d_row + 3) / 4 * 4;
-    h.groups = forward_groups(L);
+    h.groups = forward_groups(L.n_groups, group);
     h.odd = (int32_t*)take(4);
     h.A = (uint16_t*)take((size_t)(n * forward_columns(d_col)) * 2);
     h.shift = (int32_t*)take((size_t)n * 4);

@@ -28,6 +28,15 @@ constexpr bool forward_pays(int64_t n, int64_t E, int64_t rows, int64_t d_col) {
     return many_rows(n, E) && a < (b > 60 ? b : 60);
 }
 
+// Groups that the 256 x 256 tiles take per turn of four slabs (128 columns): 1, 2 or 4; 0: one scale
+// per row, as a row of a single group has, however few its columns.  Their tables hold whole
+// turns of groups, and one where there is one scale per row.
+constexpr int forward_turn_groups(int64_t n_groups, int group) { return n_groups == 1 || group <= 0 ? 0 : 128 / group; }
+constexpr int64_t forward_groups(int64_t n_groups, int group) {
+    const int per = forward_turn_groups(n_groups, group);
+    return per ? ceil_div(n_groups, per) * per : 1;
+}
+
 // Tiles of 16 x 16, or the LDS kernel's of 64 (up to 96 tokens per expert) or 128 tokens x 128
 // rows, by what either takes at 4096 columns, in ns: a 16 x 16 tile 9 and 9 / 16 for each of its
 // tokens; a tile of the LDS kernel 120 (128 tokens: 160) where there are many, and the call 37000
