@@ -7,6 +7,11 @@
 // off by 2^-39 of it at most; the product (back_gemm.h).  Where its tiles would leave CUs
 // without work, the weight rows are split among workgroups, whose fp32 sums back_join_kernel
 // adds in order.
+//
+// The product has no place for a row of dy with an infinity or a NaN: a second part of a weight may
+// be zero or of the other sign than the first, and the slabs that end a turn multiply the last
+// rows of dy by zeros.  back_pack_kernel writes dx of such a row itself and marks it, and the
+// kernels behind it leave the marked rows alone.
 
 #include "back_gemm.h"
 
@@ -17,7 +22,57 @@ struct PackArgs {
     const int8_t* e;
     const int32_t* offsets; int E;
     uint16_t* A; int64_t lda; int32_t* shift;
+    Stored L; int bits;
+    void* dx; gptq_dtype dxt;
 };
+
+constexpr int NOT_FINITE = 2000;                                // the exponent of an infinity or a NaN, and the mark of its row
+
+// dx of a row with infinities or NaNs, by the whole workgroup: those elements alone decide it, the
+// sum of their products (an infinity with the weights' sign; NaN of a zero weight, of both signs or
+// of a NaN).  8 columns per thread; mask: which of 2048 elements of dy count.
+template <int X>
+GPTQ_DEV void not_finite_row(const PackArgs& a, const uint16_t* row, const Segment& s, uint8_t* mask) {
+    const Stored L = expert_of(a.L, a.d_row, s.e);
+    const int tid = threadIdx.x;
+    for (int64_t c0 = 0; c0 < L.d_col; c0 += 2048) {
+        const int64_t c = c0 + 8 * tid;
+        const int have = c < L.d_col ? (int)(L.d_col - c < 8 ? L.d_col - c : 8) : 0, bytes = (have * a.bits + 7) / 8;
+        const int64_t group = L.n_groups == 1 ? 0 : c >> L.gshift;
+        float g[8] = {};
+        bool open = have > 0;                                    // a sum that is not NaN yet
+        for (int64_t r0 = 0; r0 < a.d_row; r0 += 2048) {
+            const int64_t first = r0 + 8 * tid;
+            uint32_t found = 0;
+            if (first < a.d_row) {
+                float v[8];
+                load_x8<X>(row + first, (int)(a.d_row - first < 8 ? a.d_row - first : 8), v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) found |= fabsf(v[i]) < INFINITY ? 0u : 1u << i;
+            }
+            __syncthreads();                                     // the last reading of the mask is over
+            mask[tid] = (uint8_t)found;
+            __syncthreads();
+            for (int w = 0; w < 256; ++w)
+                for (uint32_t left = mask[w]; left != 0; left &= left - 1) {
+                    if (!open) continue;
+                    const int64_t r = r0 + 8 * w + __builtin_ctz(left);
+                    const float v = X == X_BF16 ? bf16_bits_to_f32(row[r]) : f16_bits_to_f32(row[r]);
+                    const uint8_t* src = L.codes + r * L.code_ld + c / 8 * a.bits;
+                    uint64_t u = 0;
+                    for (int b = 0; b < bytes; ++b) u |= (uint64_t)src[b] << (8 * b);
+                    const float S = f16_bits_to_f32(L.scales[r * L.n_groups + group]), z = f16_bits_to_f32(L.zeros[r * L.n_groups + group]);
+                    open = false;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        g[i] = fmaf(v, S * ((float)((u >> (a.bits * i)) & ((1u << a.bits) - 1)) - z), g[i]);
+                        open = open || (i < have && g[i] == g[i]);
+                    }
+                }
+        }
+        for (int i = 0; i < have; ++i) store_out(a.dx, a.dxt, s.tok0 * L.d_col + c + i, g[i]);
+    }
+}
 
 // A workgroup per row, 8 elements per thread and step.  2048 x 11008 bfloat16, 90 MB, 26 us: memory, and
 // the maximum's round trip before the second reading.
@@ -25,6 +80,7 @@ template <gptq_dtype T>
 __global__ __launch_bounds__(256) void back_pack_kernel(PackArgs a) {
     constexpr int X = T == GPTQ_BF16 ? X_BF16 : X_F16;
     __shared__ int red[4];
+    __shared__ uint8_t mask[256];
     Segment s;
     if (!segment_of(a.offsets, a.E, a.n, 1, (int)blockIdx.x, s)) return;   // tiles of one row: rows of experts alone
     const int64_t t = s.tok0;
@@ -50,7 +106,7 @@ __global__ __launch_bounds__(256) void back_pack_kernel(PackArgs a) {
         eight(r, v, ev);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int k = exponent_of(v[i]) + ev[i];
+            const int k = fabsf(v[i]) < INFINITY ? exponent_of(v[i]) + ev[i] : NOT_FINITE;
             m = k > m ? k : m;
         }
     }
@@ -63,6 +119,11 @@ __global__ __launch_bounds__(256) void back_pack_kernel(PackArgs a) {
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < 4; ++w) m = red[w] > m ? red[w] : m;
+    if (m == NOT_FINITE) {                                       // the whole workgroup
+        if (threadIdx.x == 0) a.shift[t] = NOT_FINITE;
+        not_finite_row<X>(a, row, s, mask);
+        return;
+    }
     const int k = m < -900 ? 0 : 14 - m;                         // nothing but zeros
     if (threadIdx.x == 0) a.shift[t] = k;
     for (int64_t r = 8 * threadIdx.x; r < a.lda; r += 2048) {
@@ -80,9 +141,10 @@ __global__ __launch_bounds__(256) void back_pack_kernel(PackArgs a) {
     }
 }
 
-GPTQ_DEV void store_scaled(const BackArgs& a, int64_t at, f32x4_t v, int k, int have) {
+GPTQ_DEV void store_scaled(const BackArgs& a, int64_t at, f32x4_t v, int shift, int have) {
+    if (shift == NOT_FINITE) return;                             // back_pack_kernel wrote the row
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = ldexpf(v[i], k);
+    for (int i = 0; i < 4; ++i) v[i] = ldexpf(v[i], -shift);
     if (a.yt == GPTQ_F32) store_four<GPTQ_F32>(a.y, at, v, have);
     else if (a.yt == GPTQ_BF16) store_four<GPTQ_BF16>(a.y, at, v, have);
     else store_four<GPTQ_F16>(a.y, at, v, have);
@@ -104,7 +166,7 @@ __global__ __launch_bounds__(128 * WC, CB != 8 || PB == 1 || MT == 1 ? 2 : 1) vo
     G::each(acc, s.tok0, s.end, c0, a.L.d_col, [&](int64_t c, int64_t t, f32x4_t v, int have) {
         const int64_t at = t * a.L.d_col + c;
         if (sums) store_four<GPTQ_F32>(sums, at, v, have);
-        else store_scaled(a, at, v, -a.shift[t], have);
+        else store_scaled(a, at, v, a.shift[t], have);
     });
 }
 
@@ -132,7 +194,7 @@ __global__ __launch_bounds__(256) void back_join_kernel(BackArgs a, int shares) 
             for (int j = 0; j < 3; ++j)
                 if (j < have) v[j] += p[i * step + j];
     }
-    store_scaled(a, t * a.L.d_col + c, v, -a.shift[t], have);
+    store_scaled(a, t * a.L.d_col + c, v, a.shift[t], have);
 }
 
 template <int CB, int PB, int MT, int WC>
@@ -188,7 +250,7 @@ gptq_status back_launch(const BackCall& c, hipStream_t s) {
     a.y = c.dx; a.yt = c.dxt;
     rows_launch(c.L, c.E, c.d_row, e, T, s);
     GPTQ_LAUNCH_CHECK();
-    const PackArgs p = {c.dy, c.ldy, c.n, c.d_row, e, c.offsets, c.E, A, lda, shift};
+    const PackArgs p = {c.dy, c.ldy, c.n, c.d_row, e, c.offsets, c.E, A, lda, shift, c.L, c.bits, c.dx, c.dxt};
     if (c.dyt == GPTQ_BF16) back_pack_kernel<GPTQ_BF16><<<(unsigned)c.n, 256, 0, s>>>(p);
     else back_pack_kernel<GPTQ_F16><<<(unsigned)c.n, 256, 0, s>>>(p);
     GPTQ_LAUNCH_CHECK();
