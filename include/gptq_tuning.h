@@ -31,8 +31,9 @@ extern "C" {
  * Products grouped by expert: y[t] = What_e x[t] for the rows t of expert e, offsets[e] <= t <
  * offsets[e + 1].  Products are exact and sums are fp32.  In calls of many rows per expert (more
  * than 160, by sizes alone) bfloat16 elements of x enter as fp16 relative to their row: themselves
- * down to 2^-28 of the row's largest, below that to 2^-39 of it.  An infinity or a NaN in a row
- * stays in that row.
+ * down to 2^-28 of the row's largest, below that to 2^-39 of it.  A row of x with infinities gives
+ * infinities with the weights' signs (NaN where a weight there is zero or the signs differ), one
+ * with a NaN gives NaN; others are not touched by it.
  *
  *  codes ..   the experts' rows one after another: n_experts * d_row rows of d_col columns
  *  x          n_rows x d_col, pitch ldx >= d_col, dtype x_dtype: GPTQ_BF16 or GPTQ_F16

@@ -76,6 +76,36 @@ __global__ __launch_bounds__(256, 2) void grouped_gemm_kernel(GroupedArgs a, int
                 if (r < a.d_row) store_out(a.y, a.yt, t * a.ldy + r, acc[mt][nt][i]);
             }
         }
+    // Outputs that are not finite, once more as finite_sum does (a zero's rest is infinity - infinity,
+    // and sums of u - z may overflow where those of S (u - z) do not).  One instruction per output
+    // tells whether there is any; behind the stores, whose registers the rest would take, they are
+    // found in y.
+    float none = 0.f;
+#pragma unroll
+    for (int mt = 0; mt < G::MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < G::NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) none = fmaf(acc[mt][nt][i], 0.f, none);
+    if (__ballot(none != 0.f) == 0) return;                      // wave-uniform; no barrier below
+    const Stored L = expert_of(a.L, a.d_row, s.e);
+#pragma unroll 1
+    for (int k = 0; k < 4 * G::MT * G::NT; ++k) {
+        const auto token = [&](int l) { return s.tok0 + 16 * (k / (4 * G::NT)) + 4 * (l >> 4) + k / G::NT % 4; };
+        const auto row = [&](int l) { return row0 + 32 * wave + 16 * (k % G::NT) + (l & 15); };
+        const int64_t at = token(lane) * a.ldy + row(lane);
+        bool lost = false;
+        if (token(lane) < s.end && row(lane) < a.d_row)
+            lost = !(fabsf(a.yt == GPTQ_F32 ? load_as_f32<GPTQ_F32>(a.y, at) : a.yt == GPTQ_BF16 ? load_as_f32<GPTQ_BF16>(a.y, at)
+                                                                                                 : load_as_f32<GPTQ_F16>(a.y, at)) < INFINITY);
+        uint64_t todo = __ballot(lost);
+        while (todo) {                                           // wave-uniform
+            const int l = __builtin_ctzll(todo);
+            todo &= todo - 1;
+            const float v = wave_sum<CB>(L, row(l), [&](int64_t c, int m, float (&x)[8]) { load_x8<X>(a.x + token(l) * a.ldx + c, m, x); });
+            if (lane == l) store_out(a.y, a.yt, at, v);
+        }
+    }
 }
 
 template <int X, int CB, int PIECE, int BM>
