@@ -116,13 +116,14 @@ GPTQ_DEV bool entry_there(const HeadArgs& a, int64_t t, int j, int& id) {
 }
 GPTQ_DEV float weight_of(const HeadArgs& a, int64_t t) { return a.weights ? a.weights[a.tok0 + t] : 1.f; }
 
-// e^d of d <= 0, to 2^-22 of it (0 below 2^-126): 2^t with t the rounded d log2(e), times 1 + ln(2)
-// times what the rounding and the constant left out.
+// e^d of d <= 0, to 2^-22 of it (0 below 2^-126, for d of -infinity too; NaN of a NaN): 2^t with t
+// the rounded d log2(e), times 1 + ln(2) times what the rounding and the constant left out, which
+// are no numbers where t overflows.
 GPTQ_DEV float exp_of(float d) {
     const float t = d * 1.44269504f;
     const float rest = fmaf(d, 1.92596303e-8f, fmaf(d, 1.44269504f, -t));
     const float p = __builtin_amdgcn_exp2f(t);
-    return fmaf(p, rest * 0.693147181f, p);
+    return d < -128.f ? 0.f : fmaf(p, rest * 0.693147181f, p);
 }
 
 // A workgroup per token and span, which it holds in registers: the logits are read once.  4096
@@ -177,6 +178,7 @@ __global__ __launch_bounds__(256) void head_stats_kernel(HeadArgs a) {
     const float m_old = a.round ? a.b.m[at] : -INFINITY, s_old = a.round ? a.b.s[at] : 0.f;
     m = m_old > m ? m_old : m;
     const float fall = m_old == -INFINITY ? 0.f : expf(m_old - m);
+    const float top = m == -INFINITY ? 0.f : m;                  // (no word: every v is -infinity)
     const int em = PA ? emax_of(a.b.emax, a.blocks, redi) : 0;
     float s = 0.f;
 #pragma unroll
@@ -188,7 +190,7 @@ __global__ __launch_bounds__(256) void head_stats_kernel(HeadArgs a) {
         if (PA != 0 && w < words) e4 = *reinterpret_cast<const uint32_t*>(a.b.e + v0 + w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float p = v[u][i] == -INFINITY ? 0.f : exp_of(v[u][i] - m);
+            const float p = exp_of(v[u][i] - top);
             s += p;
             if constexpr (PA != 0) f16_parts(__builtin_amdgcn_ldexpf(p, 14 + (int8_t)(e4 >> (8 * i)) - em), hi[i], lo[i]);
         }
