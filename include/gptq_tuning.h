@@ -63,9 +63,9 @@ gptq_status gptqt_linear_grouped(const uint8_t* codes, const uint16_t* scales_f1
  * each row's relative to its largest scale: one part (2^-12 of a weight, at least 2^-25 of that
  * scale) where dx is bfloat16, two (2^-23) where it is fp16 or fp32.  Elements of dy are
  * themselves down to 2^-28 of their row's largest (elements taken times their weight row's
- * largest scale), below that to 2^-39 of it.  For zeros between -32000 and 32000.  A row of dy
- * with infinities gives infinities with the weights' signs (NaN where a weight there is zero or
- * the signs differ), one with a NaN gives NaN; others are not touched by it.
+ * largest scale, four times that where a zero of the row is beyond 32000), below that to 2^-39 of
+ * it.  A row of dy with infinities gives infinities with the weights' signs (NaN where a weight
+ * there is zero or the signs differ), one with a NaN gives NaN; others are not touched by it.
  *
  *  dy         n_rows x d_row, pitch ld_dy >= d_row, dtype dy_dtype: GPTQ_BF16 or GPTQ_F16
  *  dx         n_rows x d_col, pitch d_col, dtype dx_dtype; rows of no expert are left as they were

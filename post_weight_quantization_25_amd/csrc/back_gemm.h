@@ -373,8 +373,12 @@ GPTQ_DEV void store_four(void* y, int64_t idx, f32x4_t v, int have) {
     }
 }
 
-// e_r, the exponent of the row's largest scale, and the layer's Quads.  A workgroup takes
-// 16 rows of an expert (blockIdx.y), 16 threads a row; rows behind the last have zeros.
+// The power of two that a group with scale S and zero z asks of its row, so that S (u - z) 2^-e is an
+// fp16 number: S 2^-e is below 2 with zeros up to 32000 (2 x 32255 = 64510), below 1/2 with any.
+GPTQ_DEV int group_exponent(float S, float z) { return exponent_of(S) + (fabsf(z) <= 32000.f ? 0 : 2); }
+
+// e_r, the largest of the row's groups, and the layer's Quads.  A workgroup takes 16 rows of an
+// expert (blockIdx.y), 16 threads a row; rows behind the last have zeros.
 struct RowsArgs {
     const uint16_t* scales; const uint16_t* zeros;
     int64_t d_row; int n_groups;
@@ -388,7 +392,8 @@ static __global__ __launch_bounds__(256) void rows_kernel(RowsArgs a) {
     int m = -1000;
     if (r < a.d_row)
         for (int g = tid & 15; g < a.n_groups; g += 16) {
-            const int v = exponent_of(f16_bits_to_f32(a.scales[(base + r) * a.n_groups + g]));
+            const int64_t at = (base + r) * a.n_groups + g;
+            const int v = group_exponent(f16_bits_to_f32(a.scales[at]), f16_bits_to_f32(a.zeros[at]));
             m = v > m ? v : m;
         }
 #pragma unroll
@@ -396,7 +401,7 @@ static __global__ __launch_bounds__(256) void rows_kernel(RowsArgs a) {
         const int v = __shfl_xor(m, o);
         m = v > m ? v : m;
     }
-    if (m == -1000) m = 0;
+    if (m < -900) m = 0;                                         // no scale but zeros
     if ((tid & 15) == 0) {
         es[tid >> 4] = m;
         if (r < a.d_row) a.e[base + r] = (int8_t)m;
