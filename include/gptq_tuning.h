@@ -59,12 +59,13 @@ gptq_status gptqt_linear_grouped(const uint8_t* codes, const uint16_t* scales_f1
 
 /*
  * The gradient through them: dx[t] = What_e^T dy[t] for the rows t of expert e; with n_experts
- * == 1 and offsets NULL, through any stored layer.  Sums are fp32.  Weights enter in fp16 parts,
- * each row's relative to its largest scale: one part (2^-12 of a weight, at least 2^-25 of that
- * scale) where dx is bfloat16, two (2^-23) where it is fp16 or fp32.  Elements of dy are
- * themselves down to 2^-28 of their row's largest (elements taken times their weight row's
- * largest scale, four times that where a zero of the row is beyond 32000), below that to 2^-39 of
- * it.  A row of dy with infinities gives infinities with the weights' signs (NaN where a weight
+ * == 1 and offsets NULL, through any stored layer.  Sums are fp32.  Weights enter in fp16 parts
+ * times a power of two that brings their row's largest scale to 16 .. 32 (where zeros beyond 1024
+ * need it to 1 .. 2, beyond 32000 to 1/4 .. 1/2): one part, 2^-11 of a weight and 2^-25, where dx
+ * is bfloat16; two, 2^-23 of it and 2^-25, where dx is fp16 or fp32.  (A scale of 32 or more may cost
+ * the smallest scales of its row their last bits, 2^-25 again.)  Elements of dy are themselves
+ * down to 2^-28 of their row's largest (elements taken times their weight row's power of two),
+ * below that to 2^-39 of it.  A row of dy with infinities gives infinities with the weights' signs (NaN where a weight
  * there is zero or the signs differ), one with a NaN gives NaN; others are not touched by it.
  *
  *  dy         n_rows x d_row, pitch ld_dy >= d_row, dtype dy_dtype: GPTQ_BF16 or GPTQ_F16

@@ -2,10 +2,10 @@
 // What[r][c].
 //
 // The sum runs over the rows, whose scales differ, so a scale cannot be taken out of it: the
-// weights enter as numbers.  A row is taken times 2^-e_r, its largest scale's power of two
-// (row_exponents_kernel), which fp16 then holds to 2^-12 of each weight, down to 2^-25 of the
-// row's largest: in one part (PB = 1, for bfloat16 outputs, whose own rounding is 2^-9) or in
-// two (PB = 2: 2^-23).  A comes as fp16 planes (PA parts) with 2^e_r and a power of two per
+// weights enter as numbers.  A row is taken times 2^-e_r (group_exponent, rows_kernel), which brings
+// its largest scale to 16 .. 32 for zeros up to 1024, and which fp16 then holds to 2^-11 of each
+// weight and 2^-25: in one part (PB = 1, for bfloat16 outputs, whose own rounding is 2^-8) or in
+// two (PB = 2: 2^-23, and 2^-25).  A comes as fp16 planes (PA parts) with 2^e_r and a power of two per
 // token multiplied in, zeros behind the last row.
 //
 // A workgroup owns BM tokens x BN columns in slabs of 32 rows; a wave MT x 4 tiles of 16 x 16.
@@ -373,9 +373,12 @@ GPTQ_DEV void store_four(void* y, int64_t idx, f32x4_t v, int have) {
     }
 }
 
-// The power of two that a group with scale S and zero z asks of its row, so that S (u - z) 2^-e is an
-// fp16 number: S 2^-e is below 2 with zeros up to 32000 (2 x 32255 = 64510), below 1/2 with any.
-GPTQ_DEV int group_exponent(float S, float z) { return exponent_of(S) + (fabsf(z) <= 32000.f ? 0 : 2); }
+// The power of two that a group with scale S and zero z asks of its row: the least with which S (u - z)
+// 2^-e is an fp16 number, so that the row's other scales lie as far above fp16's subnormals as
+// they can.  S 2^-e is below 32 with zeros up to 1024 (32 x 1279 = 40928), 2 up to 32000 (2 x
+// 32255 = 64510), 1/2 with any.  In rows whose scales are below 32 (e <= 0) every one keeps all its
+// bits; with 2 as the limit for all zeros, scales below 2^-11 next to one of 8 lost some.
+GPTQ_DEV int group_exponent(float S, float z) { return exponent_of(S) - (fabsf(z) <= 1024.f ? 4 : fabsf(z) <= 32000.f ? 0 : -2); }
 
 // e_r, the largest of the row's groups, and the layer's Quads.  A workgroup takes 16 rows of an
 // expert (blockIdx.y), 16 threads a row; rows behind the last have zeros.
