@@ -29,7 +29,8 @@ def _activations(x: torch.Tensor, name: str, width: int):
     ld = _rows(x, name)
     if x.dtype not in _HALF or x.shape[1] != width:
         raise ValueError(f"{name} must be bf16/f16 with {width} columns")
-    return ld, x.shape[0]
+    n = x.shape[0]
+    return (ld if n > 1 else width), n                # one row's pitch leads nowhere (a view's may be beyond the limit)
 
 
 def _layers(q: Quantized, offsets, device):
