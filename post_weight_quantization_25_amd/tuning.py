@@ -89,13 +89,27 @@ def linear_grouped_backward(q: Quantized, dy: torch.Tensor, offsets: torch.Tenso
     return out
 
 
-def _head(q, x, weights, loss, dx, grad, dx_dtype):
+def _apart(outputs, inputs):
+    """The outputs that the caller gives overlap no input and not each other: a token's weight, entries
+    and activations are read by several workgroups, others of which write."""
+    def spans(tensors):
+        return [(name, t.data_ptr(), t.data_ptr() + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.itemsize)
+                for name, t in tensors if t is not None and t.numel()]
+    mine, theirs = spans(outputs), spans(inputs)
+    for i, (name, at, end) in enumerate(mine):
+        for other, a, b in mine[i + 1:] + theirs:
+            if at < b and a < end:
+                raise ValueError(f"{name} overlaps {other}")
+
+
+def _head(q, x, weights, loss, dx, grad, dx_dtype, entries):
     """Checks what both losses share and makes their outputs; the head's words, x's pitch."""
     dev = x.device
     vocab = _stored(q, "q", dev)
     ldx, n = _activations(x, "x", q.d_col)
     if weights is not None:
         _tensor(weights, "weights", torch.float32, (n,), dev)
+    given = [("loss", loss), ("dx", dx)]
     if loss is None:
         loss = torch.empty(n, dtype=torch.float32, device=dev)
     _tensor(loss, "loss", torch.float32, (n,), dev)
@@ -103,6 +117,8 @@ def _head(q, x, weights, loss, dx, grad, dx_dtype):
         dx = _out(dx, n, q.d_col, x.dtype if dx_dtype is None else dx_dtype, dev, x)
     elif dx is not None:
         raise ValueError("dx without grad")
+    if given[0][1] is not None or given[1][1] is not None:
+        _apart(given, [("x", x), ("weights", weights)] + entries)
     return vocab, ldx, n, loss, dx
 
 
@@ -121,7 +137,7 @@ def cross_entropy(q: Quantized, x: torch.Tensor, targets: torch.Tensor, weights:
     dev = x.device
     _tensor(targets, "targets", torch.int32, x.shape[:1], dev)
     with _On(dev, stream) as s:
-        vocab, ldx, n, loss, dx = _head(q, x, weights, loss, dx, grad, dx_dtype)
+        vocab, ldx, n, loss, dx = _head(q, x, weights, loss, dx, grad, dx_dtype, [("targets", targets)])
         ws = _workspace(cross_entropy_workspace_size(n, q.d_col, vocab, q.group_size, grad), dev, ws)
         _check(lib.gptqt_cross_entropy(
             q.codes.data_ptr(), q.scales.data_ptr(), q.zeros.data_ptr(), vocab, q.d_col, q.bits, q.group_size,
@@ -150,7 +166,7 @@ def distill(q: Quantized, x: torch.Tensor, ids: torch.Tensor, top: torch.Tensor,
     _tensor(ids, "ids", torch.int32, (x.shape[0], k), dev)
     _tensor(top, "top", None, (x.shape[0], k), dev)
     with _On(dev, stream) as s:
-        vocab, ldx, n, loss, dx = _head(q, x, weights, loss, dx, grad, dx_dtype)
+        vocab, ldx, n, loss, dx = _head(q, x, weights, loss, dx, grad, dx_dtype, [("ids", ids), ("top", top)])
         ws = _workspace(distill_workspace_size(n, q.d_col, vocab, k, q.group_size, grad), dev, ws)
         _check(lib.gptqt_distill(
             q.codes.data_ptr(), q.scales.data_ptr(), q.zeros.data_ptr(), vocab, q.d_col, q.bits, q.group_size,
