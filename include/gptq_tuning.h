@@ -101,7 +101,9 @@ gptq_status gptqt_linear_grouped_backward(const uint8_t* codes, const uint16_t* 
  *  dx         n_tokens x d, pitch d, dtype dx_dtype; NULL: the loss alone
  *  ws         at least gptqt_cross_entropy_workspace_size(...) bytes (with_grad: dx is not NULL),
  *             16-byte aligned
- * Errors: as gptqt_linear_grouped_backward, vocab for d_row, d for d_col.
+ * Errors: as gptqt_linear_grouped, vocab for d_row, d for d_col, n_tokens for n_rows, with no limit
+ * on tiles (tokens are taken 4096 at a time); an ldx above 2^23 -> GPTQ_ERR_UNSUPPORTED; a missing,
+ * misaligned or short workspace -> GPTQ_ERR_WORKSPACE.
  */
 size_t gptqt_cross_entropy_workspace_size(int64_t n_tokens, int64_t d, int64_t vocab, int32_t group_size,
                                           int32_t with_grad);

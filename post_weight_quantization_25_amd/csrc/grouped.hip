@@ -19,7 +19,7 @@ namespace gptq {
 // int3, 3 tokens: 44 us with one, 58 with two; 64 experts of 2816 x 2048, 8 rows: 13.6 / 16.
 // 4 waves for narrow rows, which have few chunks for each: 131072 x 2048 int3: 37 us with 4, 44 with
 // 8; 65536 x 512: 12.6 / 14; 4096 x 11008: 15.2 / 12.6; 131072 x 4096: 88 / 81; 64 experts of 2816 x
-// 2048: 13.7 / 13.6.
+// 2048: 13.7 / 13.6 (whole calls in a chain from Python; the kernel alone 10.5, replayed 10.9).
 constexpr bool few_waves(int64_t d_col) { return d_col <= 2048; }
 
 template <int X, int CB, int RUN, int TW>

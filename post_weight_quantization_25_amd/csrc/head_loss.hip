@@ -12,7 +12,9 @@
 //   logits  z of the round's words, fp32 (grouped.hip)
 //   stats   per token and span: the entries' z are picked out, the maximum m and the sum of
 //           exp(z - m) over the other words added to what the span's slot has, and exp(z - m)
-//           written in fp16 (times 2^14 and the weight row's power of two)
+//           written in fp16 (times 2^14 and the weight row's power of two): in one part, 2^-11 of
+//           it, for bfloat16 dx, whose own rounding is 2^-8 (two would be three products in place of
+//           one, the larger half of the call), in two otherwise
 //   sums    O = O exp(m_old - m) + exp(z - m) What, fp32 (back_gemm.h)
 // so the logits and the softmax are formed once, and nothing of the vocabulary's length is
 // kept beyond a round.  Then head_final_kernel joins the slots.

@@ -45,8 +45,14 @@ constexpr int64_t forward_groups(int64_t n_groups, int group) {
 // 106 / 61; 4096 x 11008, 64: 50 / 97, 128: 94 / 146; 2048 x 1024, 128: 11 / 23; 131072 x 4096, 1: 81 /
 // 104, 8: 114 / 107, 16: 158 / 107; 131072 x 2048 int3 per row, 8: 48 / 48, 16: 70 / 49; 32000 x 4096
 // 8-bit, 16: 47 / 48, 24: 77 / 49; 64 experts of 2816 x 2048, 8 rows: 14 / 24, 256: 67 / 86, 512: 81 /
-// 99, 1024: 130 / 103; 61 of 2047 x 1408 int3, 488: 33 / 45, 777: 43 / 46; 16 of 11008 x 4096, 128:
-// 155 / 155, 256: 239 / 182; 8 of 4096 x 4096, 128: 50 / 54, 256: 85 / 55.
+// 99, 1024: 130 / 103; 61 of 2047 x 1408 int3, 488: 33 / 45, 777: 43 / 46 (there the rule, which knows
+// no columns, takes the LDS kernel); 16 of 11008 x 4096, 128: 155 / 155, 256: 239 / 182; 8 of 4096 x
+// 4096, 128: 50 / 54, 256: 85 / 55.  Calls in a chain from Python, where none takes less than 10 to
+// 12; replayed from a graph 4096 x 4096, 1 / 16 / 32 / 64 / 128 tokens: 4.8 / 7.5 / 12 / 21 / 39.
+// gptq_quantized_linear, which has no experts, takes 5.1 / 8.7 / 12 / 16 / 23 for those and 32 / 62 / 121 for
+// 256 / 512 / 1024 (here 64 / 66 / 68): for one expert of 4096 x 4096 int4 it is the better call from 64
+// to 512 tokens.  At 11008 x 4096, 64 / 128 / 256: 40 / 62 / 92 (here 44 / 65 / 66); 32000 x 4096 8-bit, 16 /
+// 128: 198 / 1395 (here 47 / 87).
 constexpr int64_t likely_tiles(int64_t n, int64_t E, int per) { // of n rows spread over E experts
     if (E == 1) return ceil_div(n, per);
     const int64_t used = E < n ? E : n, t = n / per + used / 2;

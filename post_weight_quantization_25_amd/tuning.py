@@ -5,6 +5,12 @@ head with their gradients.
 Argument checks and marshalling only, as in the package's module.  Work is queued on
 ``stream`` (default: the current stream of the operands' device, which need not be the
 current device); buffers made here are allocated on that stream.
+
+Nothing here is recorded for autograd: results of operands that ask for a gradient carry no
+graph.  A program that uses autograd calls ``linear_grouped_backward``, or takes dx from the
+losses, in a ``torch.autograd.Function`` of its own.  Gradients in bfloat16 are formed from
+weights (and softmax values) in one fp16 part, 2^-11 of each; ``out_dtype`` or ``dx_dtype``
+float32 or float16 takes two, 2^-23.
 """
 from __future__ import annotations
 
