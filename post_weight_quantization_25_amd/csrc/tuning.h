@@ -72,6 +72,27 @@ GPTQ_DEV Stored expert_of(Stored L, int64_t d_row, int e) {
     return L;
 }
 
+// One weight, S (u - z).  (A 3-bit code may lie in two bytes.)
+GPTQ_DEV float weight_at(const Stored& L, int bits, int64_t r, int64_t c) {
+    const uint8_t* src = L.codes + r * L.code_ld + (c * bits >> 3);
+    const int bit = (int)(c * bits & 7);
+    uint32_t u = src[0] >> bit;
+    if (bit + bits > 8) u |= (uint32_t)src[1] << (8 - bit);
+    const int64_t at = r * L.n_groups + (L.n_groups == 1 ? 0 : c >> L.gshift);
+    return f16_bits_to_f32(L.scales[at]) * ((float)(u & ((1u << bits) - 1)) - f16_bits_to_f32(L.zeros[at]));
+}
+
+// Which of eight 16-bit elements from p on, the first m of which exist, are infinities or NaNs.
+template <int X>
+GPTQ_DEV uint32_t not_finite8(const uint16_t* p, int m) {
+    float v[8];
+    load_x8<X>(p, m, v);
+    uint32_t found = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) found |= fabsf(v[i]) < INFINITY ? 0u : 1u << i;
+    return found;
+}
+
 // ---- y[t] = What_e x[t] (grouped.hip)
 struct GroupedArgs {
     Stored L; int64_t d_row;                                    // rows of each expert
