@@ -51,6 +51,70 @@ __global__ __launch_bounds__(64 * TW, 4) void grouped_tile_kernel(GroupedArgs a)
     if (live) store_out(a.y, a.yt, (s.tok0 + m) * a.ldy + row0 + n, v);
 }
 
+// The outputs of the wave's 16 NT rows and of a tile's tokens that the wave has stored and that are
+// not finite, by the whole wave.  Elements of x that are not finite decide a token's outputs alone;
+// with none, as finite_sum.  2048 tokens x 32000 x 4096, one odd zero (690 us): 5.3 ms with an infinity
+// in each token (134 with every output summed anew), 6.3 with nothing but NaNs (29).
+template <int X, int CB, int NT>
+GPTQ_DEV void sums_again(const GroupedArgs& a, const Segment& s, int tokens, int64_t tile_row) {
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));                                // formed here, not carried through the kernel
+    const int lane = tid & 63;
+    const int64_t row0 = tile_row + 16 * NT * __builtin_amdgcn_readfirstlane(tid >> 6);
+    const Stored L = expert_of(a.L, a.d_row, s.e);
+#pragma unroll 1
+    for (int m = 0; m < tokens && s.tok0 + m < s.end; ++m) {
+        const int64_t t = s.tok0 + m;
+        const uint16_t* x = a.x + t * a.ldx;
+        bool lost[NT];                                           // the lane's own outputs: rows row0 + 16 nt + lane % 16
+        uint64_t all = 0;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int64_t r = row0 + 16 * nt + (lane & 15), at = t * a.ldy + r;
+            lost[nt] = false;
+            if ((m & 15) >> 2 == lane >> 4 && r < a.d_row)
+                lost[nt] = !(fabsf(a.yt == GPTQ_F32 ? load_as_f32<GPTQ_F32>(a.y, at) : a.yt == GPTQ_BF16 ? load_as_f32<GPTQ_BF16>(a.y, at)
+                                                                                                         : load_as_f32<GPTQ_F16>(a.y, at)) < INFINITY);
+            all |= __ballot(lost[nt]);
+        }
+        if (all == 0) continue;
+        float sum[NT] = {};
+        bool some = false;                                       // elements that are not finite
+        for (int64_t c0 = 0; c0 < L.d_col; c0 += 512) {
+            const int64_t c = c0 + 8 * lane;
+            const uint32_t found = c < L.d_col ? not_finite8<X>(x + c, (int)(L.d_col - c < 8 ? L.d_col - c : 8)) : 0;
+            uint64_t open = __ballot(found != 0);
+            some = some || open != 0;
+            for (; open != 0; open &= open - 1) {
+                const int l = __builtin_ctzll(open);
+#pragma unroll 1
+                for (uint32_t left = __builtin_amdgcn_readlane(found, l); left != 0; left &= left - 1) {
+                    const int64_t col = c0 + 8 * l + __builtin_ctz(left);
+                    const float v = X == X_BF16 ? bf16_bits_to_f32(x[col]) : f16_bits_to_f32(x[col]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        if (lost[nt]) sum[nt] = fmaf(v, weight_at(L, CB, row0 + 16 * nt + (lane & 15), col), sum[nt]);
+                }
+                bool more = false;                               // sums that are not NaN yet
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) more = more || (lost[nt] && sum[nt] == sum[nt]);
+                if (__ballot(more) == 0) { c0 = L.d_col; break; }
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            uint64_t todo = some ? 0 : __ballot(lost[nt]);
+            while (todo) {                                       // wave-uniform
+                const int l = __builtin_ctzll(todo);
+                todo &= todo - 1;
+                const float v = wave_sum<CB>(L, row0 + 16 * nt + (l & 15), [&](int64_t c, int n, float (&e)[8]) { load_x8<X>(x + c, n, e); });
+                if (lane == l) sum[nt] = v;
+            }
+            if (lost[nt]) store_out(a.y, a.yt, t * a.ldy + row0 + 16 * nt + (lane & 15), sum[nt]);
+        }
+    }
+}
+
 template <int X, int CB, int PIECE, int BM>
 __global__ __launch_bounds__(256, 2) void grouped_gemm_kernel(GroupedArgs a, int gm, int gn) {
     typedef StoredGemm<X, CB, PIECE, BM, 256> G;
@@ -76,7 +140,7 @@ __global__ __launch_bounds__(256, 2) void grouped_gemm_kernel(GroupedArgs a, int
                 if (r < a.d_row) store_out(a.y, a.yt, t * a.ldy + r, acc[mt][nt][i]);
             }
         }
-    // Outputs that are not finite, once more as finite_sum does (a zero's rest is infinity - infinity,
+    // Outputs that are not finite, once more by the definition (a zero's rest is infinity - infinity,
     // and sums of u - z may overflow where those of S (u - z) do not).  One instruction per output
     // tells whether there is any; behind the stores, whose registers the rest would take, they are
     // found in y.
@@ -87,25 +151,7 @@ __global__ __launch_bounds__(256, 2) void grouped_gemm_kernel(GroupedArgs a, int
         for (int nt = 0; nt < G::NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) none = fmaf(acc[mt][nt][i], 0.f, none);
-    if (__ballot(none != 0.f) == 0) return;                      // wave-uniform; no barrier below
-    const Stored L = expert_of(a.L, a.d_row, s.e);
-#pragma unroll 1
-    for (int k = 0; k < 4 * G::MT * G::NT; ++k) {
-        const auto token = [&](int l) { return s.tok0 + 16 * (k / (4 * G::NT)) + 4 * (l >> 4) + k / G::NT % 4; };
-        const auto row = [&](int l) { return row0 + 32 * wave + 16 * (k % G::NT) + (l & 15); };
-        const int64_t at = token(lane) * a.ldy + row(lane);
-        bool lost = false;
-        if (token(lane) < s.end && row(lane) < a.d_row)
-            lost = !(fabsf(a.yt == GPTQ_F32 ? load_as_f32<GPTQ_F32>(a.y, at) : a.yt == GPTQ_BF16 ? load_as_f32<GPTQ_BF16>(a.y, at)
-                                                                                                 : load_as_f32<GPTQ_F16>(a.y, at)) < INFINITY);
-        uint64_t todo = __ballot(lost);
-        while (todo) {                                           // wave-uniform
-            const int l = __builtin_ctzll(todo);
-            todo &= todo - 1;
-            const float v = wave_sum<CB>(L, row(l), [&](int64_t c, int m, float (&x)[8]) { load_x8<X>(a.x + token(l) * a.ldx + c, m, x); });
-            if (lane == l) store_out(a.y, a.yt, at, v);
-        }
-    }
+    if (__ballot(none != 0.f) != 0) sums_again<X, CB, G::NT>(a, s, BM, row0);   // wave-uniform; no barrier below
 }
 
 template <int X, int CB, int PIECE, int BM>
