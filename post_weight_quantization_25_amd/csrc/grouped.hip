@@ -58,7 +58,9 @@ __global__ __launch_bounds__(64 * TW, 4) void grouped_tile_kernel(GroupedArgs a)
 template <int X, int CB, int NT>
 GPTQ_DEV void sums_again(const GroupedArgs& a, const Segment& s, int tokens, int64_t tile_row) {
     int tid = threadIdx.x;
-    asm volatile("" : "+v"(tid));                                // formed here, not carried through the kernel
+    // Formed here, not carried through the kernel; and no reading of y moves above its stores, which have
+    // another type (in the hardware a lane's own accesses are in order).
+    asm volatile("" : "+v"(tid) : : "memory");
     const int lane = tid & 63;
     const int64_t row0 = tile_row + 16 * NT * __builtin_amdgcn_readfirstlane(tid >> 6);
     const Stored L = expert_of(a.L, a.d_row, s.e);
