@@ -407,7 +407,7 @@ static gptq_status launch(const MoeArgs& a, hipStream_t s) {
     GPTQ_LAUNCH_CHECK();
     const dim3 down((unsigned)((a.d + 15) / 16), (unsigned)slots);
     // Parts of the inner values: two, 2^-17 of each, are far below a 16-bit output's rounding
-    // (2^-9, 2^-12); fp32 outputs take three, which are the values themselves.
+    // (2^-8, 2^-11); fp32 outputs take three, which are the values themselves.
     if (a.yt == GPTQ_F32) moe_down_kernel<CB, RUN, 3><<<down, 64 * down_waves<3>(), 0, s>>>(a);
     else moe_down_kernel<CB, RUN, 2><<<down, 64 * down_waves<2>(), 0, s>>>(a);
     GPTQ_LAUNCH_CHECK();
